@@ -252,6 +252,69 @@ lmhead_status lmhead_quantize_nvfp4(const void *W, int64_t V, int64_t H, uint8_t
 /* Host-only: bytes of workspace lmhead_quantize_nvfp4 needs (a constant). */
 size_t lmhead_quantize_nvfp4_workspace_bytes(void);
 
+/* ---------------------------------------------------------------------------
+ * Training the head: softmax cross entropy over the vocabulary without the
+ * logits in memory, and its gradients.
+ *   t[m, v] = alpha * (hidden[m, :] . W[v, :]) + bias[v]   (as lmhead_logits_ex, fp32)
+ *   lse[m]  = log sum_v exp(t[m, v]);  loss[m] = lse[m] - t[m, target[m]]
+ * A row is left out when its target equals ignore_index or is no column of
+ * the call (target < 0 or >= V): its loss is 0 and carries no gradient; its
+ * lse is written all the same. t = -inf (a masked column, through a -inf
+ * bias) has probability 0: a target there has loss +inf, and a row of
+ * only -inf has lse -inf. +inf and NaN logits give NaN.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  LMHEAD_INDEX32 = 0, /* int32 targets or token ids */
+  LMHEAD_INDEX64 = 1  /* int64 */
+} lmhead_index;
+
+/* loss and lse.
+ *   hidden [M, H], W [V, H]  both bf16 or both fp16 (in_dtype)  (device, read)
+ *   bias        fp32 [V] or NULL                                (device, read)
+ *   target      [M] of target_type                              (device, read)
+ *   loss, lse   fp32 [M]                                        (device, written)
+ *   workspace   at least lmhead_xent_forward_workspace_bytes(M, V) bytes, 16-byte
+ *               aligned, overwritten; not in use by other work until this call's
+ *               work has finished
+ * Results do not change from run to run. Returns as lmhead_logits_ex
+ * (LMHEAD_NOT_HANDLED for fp32 inputs or H % 32 != 0). */
+lmhead_status lmhead_xent_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
+                                  float alpha, const float *bias, lmhead_dtype in_dtype,
+                                  const void *target, lmhead_index target_type,
+                                  int64_t ignore_index, float *loss, float *lse, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Host-only: bytes of workspace lmhead_xent_forward needs (0 outside the shape contract). */
+size_t lmhead_xent_forward_workspace_bytes(int64_t M, int64_t V);
+
+/* Gradients of sum_m grad_loss[m] loss[m] + grad_lse[m] lse[m]. With
+ *   G[m, v] = (grad_loss[m] + grad_lse[m]) exp(t[m, v] - lse[m]) - grad_loss[m] [v = target[m]]
+ * (grad_loss taken as 0 in rows left out):
+ *   grad_hidden = alpha G W, grad_W = alpha G^T hidden, grad_bias = sum over rows of G.
+ *   hidden .. ignore_index   as given to lmhead_xent_forward
+ *   lse         fp32 [M], as lmhead_xent_forward wrote it       (device, read)
+ *   grad_loss   fp32 [M]                                        (device, read)
+ *   grad_lse    fp32 [M], or NULL for zeros                     (device, read)
+ *   grad_hidden [M, H] of in_dtype, or NULL (not wanted)        (device, written)
+ *   grad_W      [V, H] of in_dtype, or NULL                     (device, written, every row)
+ *   grad_bias   fp32 [V], or NULL                               (device, written)
+ *   workspace   at least lmhead_xent_backward_workspace_bytes(M, H, V, grad_bias != NULL)
+ *               bytes, 256-byte aligned, overwritten; as above
+ * Sums are fp32 in a fixed order; G enters the two products rounded to the
+ * inputs' type. With M = 0, grad_W and grad_bias are zero. */
+lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
+                                   float alpha, const float *bias, lmhead_dtype in_dtype,
+                                   const void *target, lmhead_index target_type,
+                                   int64_t ignore_index, const float *lse, const float *grad_loss,
+                                   const float *grad_lse, void *grad_hidden, void *grad_W,
+                                   float *grad_bias, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Host-only: bytes of workspace lmhead_xent_backward needs: one piece of G
+ * (256 MiB, or 2 * 8192 * M bytes where that is more), fp32 sums of
+ * grad_hidden, and little else. 0 outside the shape contract or when M == 0. */
+size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias);
+
 /* Host-only shape predicate (no device access): 1 when (M, H, V) is inside the
  * shape contract of the bf16 (nvfp4 = 0) or NVFP4 (nvfp4 = 1) entry point,
  * else 0. Like the shape check the metrale page's install step runs before

@@ -10,33 +10,22 @@ LMHEAD_NOT_HANDLED the caller gets ``NotHandled`` and decides what to do.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
 from . import _lib
-from ._lib import (LMHEAD_BF16, LMHEAD_F16, LMHEAD_F32, NOT_HANDLED, OK, PATH_AUTO, PATH_NONE,
-                   PATH_NVFP4, PATH_SKINNY, PATH_TILED)
+from ._binding import (_DTYPES, LmHeadError, NotHandled, _check, _device_ctx, _need, _same_device,
+                       _stream_handle, status_string)
+from ._lib import LMHEAD_F32, PATH_AUTO, PATH_NONE, PATH_NVFP4, PATH_SKINNY, PATH_TILED
+from .training import (xent_backward, xent_backward_workspace_bytes, xent_forward,
+                       xent_forward_workspace_bytes)
 
 __all__ = ["logits", "logits_rowreduce", "logits_rowreduce_noalloc", "rowreduce_workspace_bytes", "logits_nvfp4",
            "quantize_nvfp4", "shape_ok", "path_for", "status_string", "version",
            "LmHeadError", "NotHandled", "PATH_SKINNY", "PATH_TILED", "PATH_NVFP4", "PATH_AUTO",
-           "PATH_NONE", "probe_hbm_read", "probe_mfma_bf16"]
-
-
-class LmHeadError(RuntimeError):
-    def __init__(self, status: int, where: str):
-        self.status = status
-        super().__init__(f"{where}: {status_string(status)} (status {status})")
-
-
-class NotHandled(LmHeadError):
-    """The shape lies outside the kernels' contract; nothing was launched."""
-
-
-def status_string(status: int) -> str:
-    return _lib.load().lmhead_status_string(int(status)).decode()
+           "PATH_NONE", "probe_hbm_read", "probe_mfma_bf16",
+           "xent_forward", "xent_backward", "xent_forward_workspace_bytes", "xent_backward_workspace_bytes"]
 
 
 def version() -> str:
@@ -51,52 +40,7 @@ def path_for(M: int, H: int, V: int, nvfp4: bool = False) -> int:
     return int(_lib.load().lmhead_path_for(M, H, V, int(nvfp4)))
 
 
-def _check(status: int, where: str):
-    if status == OK:
-        return
-    if status == NOT_HANDLED:
-        raise NotHandled(status, where)
-    raise LmHeadError(status, where)
-
-
-# torch's current raw HIP stream of a device index, without building a Stream
-# object per call (the public route below when this build lacks it)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_handle(device, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(device.index if device.index is not None else torch.cuda.current_device())
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _device_ctx(device):
-    """The library launches on the current device: make it `device`, switching
-    (and switching back) only when it is another one."""
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    return _NO_SWITCH if torch.cuda.current_device() == idx else torch.cuda.device(idx)
-
-
-def _need(cond: bool, msg: str):
-    if not cond:
-        raise ValueError(msg)
-
-
-def _same_device(*tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:  # the message only on failure: this runs on every call
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devs))}")
-
-
 _PATHS = {"auto": PATH_AUTO, "skinny": PATH_SKINNY, "tiled": PATH_TILED}
-
-
-_DTYPES = {torch.float32: LMHEAD_F32, torch.bfloat16: LMHEAD_BF16, torch.float16: LMHEAD_F16}
 
 
 def logits(hidden: torch.Tensor, weight: torch.Tensor, alpha: float = 1.0, bias=None,

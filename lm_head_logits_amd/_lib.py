@@ -20,6 +20,9 @@ ERR_INVALID = -1
 ERR_ALIGN = -2
 ERR_DEVICE = -3
 
+INDEX32 = 0
+INDEX64 = 1
+
 PATH_NONE = -1
 PATH_AUTO = -2
 PATH_SKINNY = 0
@@ -31,7 +34,9 @@ NOALLOC_SCRATCH_BYTES = 32 << 20  # LMHEAD_NOALLOC_SCRATCH_BYTES
 EXPORTS = ("lmhead_logits", "lmhead_logits_path", "lmhead_logits_ex", "lmhead_logits_rowreduce",
            "lmhead_rowreduce_workspace_bytes", "lmhead_logits_rowreduce_noalloc", "lmhead_logits_nvfp4", "lmhead_quantize_nvfp4",
            "lmhead_quantize_nvfp4_workspace_bytes", "lmhead_shape_ok",
-           "lmhead_path_for", "lmhead_status_string", "lmhead_version")
+           "lmhead_path_for", "lmhead_status_string", "lmhead_version",
+           "lmhead_xent_forward", "lmhead_xent_forward_workspace_bytes", "lmhead_xent_backward",
+           "lmhead_xent_backward_workspace_bytes")
 # include/lmhead_probes.h: measurement probes (not part of the projection),
 # in a library of their own
 PROBE_EXPORTS = ("lmhead_probe_grid", "lmhead_probe_hbm_read", "lmhead_probe_mfma_bf16")
@@ -85,6 +90,16 @@ def load() -> ctypes.CDLL:
     lib.lmhead_status_string.argtypes = [i32]
     lib.lmhead_version.restype = ctypes.c_char_p
     lib.lmhead_version.argtypes = []
+    sz = ctypes.c_size_t
+    lib.lmhead_xent_forward.restype = i32
+    lib.lmhead_xent_forward.argtypes = [vp, i64, i64, vp, i64, f32, vp, i32, vp, i32, i64, vp, vp, vp, sz, vp]
+    lib.lmhead_xent_forward_workspace_bytes.restype = sz
+    lib.lmhead_xent_forward_workspace_bytes.argtypes = [i64, i64]
+    lib.lmhead_xent_backward.restype = i32
+    lib.lmhead_xent_backward.argtypes = [vp, i64, i64, vp, i64, f32, vp, i32, vp, i32, i64, vp, vp, vp,
+                                         vp, vp, vp, vp, sz, vp]
+    lib.lmhead_xent_backward_workspace_bytes.restype = sz
+    lib.lmhead_xent_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
     _lib = lib
     return lib
 

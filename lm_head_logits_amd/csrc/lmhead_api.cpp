@@ -246,4 +246,64 @@ lmhead_status lmhead_logits_nvfp4(const void *hidden, int64_t M, int64_t H,
   return e == hipSuccess ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
 }
 
+size_t lmhead_xent_forward_workspace_bytes(int64_t M, int64_t V) {
+  if (check_shape(M, 32, V) == LMHEAD_ERR_INVALID) return 0;
+  return (size_t)lmhead::xent_forward_bytes(M, V);
+}
+
+size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias) {
+  if (check_shape(M, H, V) != LMHEAD_OK || M == 0) return 0;
+  return (size_t)lmhead::xent_backward_bytes(M, H, V, grad_bias != 0);
+}
+
+lmhead_status lmhead_xent_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
+                                  float alpha, const float *bias, lmhead_dtype in_dtype,
+                                  const void *target, lmhead_index target_type,
+                                  int64_t ignore_index, float *loss, float *lse, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+  lmhead_status st = check_call(M, H, V, in_dtype, LMHEAD_F32, LMHEAD_PATH_AUTO);
+  if (st != LMHEAD_OK) return st;
+  if (target_type != LMHEAD_INDEX32 && target_type != LMHEAD_INDEX64) return LMHEAD_ERR_INVALID;
+  if (M == 0) return LMHEAD_OK;
+  if (hidden == nullptr || W == nullptr || target == nullptr || loss == nullptr || lse == nullptr ||
+      workspace == nullptr || workspace_bytes < lmhead_xent_forward_workspace_bytes(M, V))
+    return LMHEAD_ERR_INVALID;
+  if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(target, target_type == LMHEAD_INDEX64 ? 8 : 4) ||
+      !aligned(loss, 4) || !aligned(lse, 4) || !aligned(bias, 4) || !aligned(workspace, 16))
+    return LMHEAD_ERR_ALIGN;
+  const lmhead::XentForward c{hidden, W, M, H, V, alpha, bias, in_dtype == LMHEAD_F16 ? 1 : 0, target,
+                              target_type == LMHEAD_INDEX64 ? 1 : 0, ignore_index, loss, lse, workspace};
+  hipError_t e = lmhead::launch_xent_forward(c, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
+}
+
+lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
+                                   float alpha, const float *bias, lmhead_dtype in_dtype,
+                                   const void *target, lmhead_index target_type,
+                                   int64_t ignore_index, const float *lse, const float *grad_loss,
+                                   const float *grad_lse, void *grad_hidden, void *grad_W,
+                                   float *grad_bias, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+  lmhead_status st = check_call(M, H, V, in_dtype, LMHEAD_F32, LMHEAD_PATH_AUTO);
+  if (st != LMHEAD_OK) return st;
+  if (target_type != LMHEAD_INDEX32 && target_type != LMHEAD_INDEX64) return LMHEAD_ERR_INVALID;
+  if (grad_hidden == nullptr && grad_W == nullptr && grad_bias == nullptr) return LMHEAD_OK;
+  if (M > 0) {
+    if (hidden == nullptr || W == nullptr || target == nullptr || lse == nullptr || grad_loss == nullptr ||
+        workspace == nullptr ||
+        workspace_bytes < lmhead_xent_backward_workspace_bytes(M, H, V, grad_bias != nullptr))
+      return LMHEAD_ERR_INVALID;
+    if (!aligned(hidden, 16) || !aligned(W, 16) ||
+        !aligned(target, target_type == LMHEAD_INDEX64 ? 8 : 4) || !aligned(lse, 4) ||
+        !aligned(grad_loss, 4) || !aligned(grad_lse, 4) || !aligned(bias, 4) || !aligned(workspace, 256))
+      return LMHEAD_ERR_ALIGN;
+  }
+  if (!aligned(grad_hidden, 16) || !aligned(grad_W, 16) || !aligned(grad_bias, 4)) return LMHEAD_ERR_ALIGN;
+  const lmhead::XentBackward c{hidden, W, M, H, V, alpha, bias, in_dtype == LMHEAD_F16 ? 1 : 0, target,
+                               target_type == LMHEAD_INDEX64 ? 1 : 0, ignore_index, lse, grad_loss,
+                               grad_lse, grad_hidden, grad_W, grad_bias, workspace};
+  hipError_t e = lmhead::launch_xent_backward(c, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? LMHEAD_OK : LMHEAD_ERR_DEVICE;
+}
+
 }  // extern "C"

@@ -1,0 +1,661 @@
+// xent.hip -- softmax cross entropy of the head's logits against target
+// tokens, and its gradients, in pieces of the vocabulary: the logits are
+// never in memory.
+//
+//   t[m, v] = alpha (hidden[m, :] . W[v, :]) + bias[v]
+//   lse[m]  = log sum_v exp t[m, v],   loss[m] = lse[m] - t[m, y_m]
+//   G[m, v] = (g_m + l_m) exp(t[m, v] - lse[m]) - g_m [v = y_m]
+//   grad_hidden = alpha G W,  grad_W = alpha G^T hidden,  grad_bias = sum_m G
+//
+// with g, l the gradients of loss and lse. A token is left out (loss 0, g
+// taken as 0) when its target is ignore_index or no column of the call.
+//
+// Forward: one matrix product (mma256.hpp) whose epilogue keeps, per row and
+// 256-column tile, the tile's largest t and its sum of exponentials, and the
+// target's t; a second kernel folds the tiles of a row in a fixed order.
+// Backward, per piece of the vocabulary: the product again, with the epilogue
+// making G of the piece (16 bits, in the workspace), then G W added to fp32
+// sums of grad_hidden, and G^T hidden, the piece's rows of grad_W. Three
+// products of 2 M H V flops: making t again costs one product and saves
+// keeping M V values from the forward pass.
+//
+// Everything is bound by the matrix pipes except for few rows, where the
+// weight's bytes bind.
+//
+// Roundings: t, the statistics, p and grad_bias are fp32. G is rounded to the
+// inputs' 16-bit type, which the matrix pipes take: a relative 2^-9 (bf16) or
+// 2^-12 (fp16) per term of sums of M or V terms, below the rounding of the
+// 16-bit gradients. fp16 G is scaled by a power of two that takes the largest
+// row's coefficient to 2^14, so that probabilities down to 2^-29 of it stay
+// normal numbers; bf16 needs no scale.
+#include "mma256.hpp"
+
+namespace lmhead {
+
+namespace {
+
+constexpr float NEG_INF = -__builtin_inff();
+
+struct XentFwdArgs {
+  const uint8_t *hidden, *W;
+  int64_t M, H, V;
+  float alpha;
+  const float *bias;
+  const void *target;
+  int target64;
+  int64_t ignore;
+  float2 *part;   // [vocabulary tile][M] {largest t, sum of exp(t - largest)}
+  float *tlogit;  // [M] t at the target (rows with one)
+};
+
+// The row's target column, or -1.
+__device__ __forceinline__ int64_t target_of(const void *target, int target64, int64_t m,
+                                             int64_t ignore, int64_t V) {
+  const int64_t y = target64 ? static_cast<const int64_t *>(target)[m]
+                             : (int64_t)static_cast<const int32_t *>(target)[m];
+  return y != ignore && y >= 0 && y < V ? y : -1;
+}
+
+// hidden W^T of tile (m0, n0): both operands K-inner, the K order of korder.hpp.
+template <int ET>
+__device__ __forceinline__ void logits_tile(MmTile<ET> &tile, const uint8_t *hidden,
+                                            const uint8_t *W, int64_t M, int64_t H, int64_t V,
+                                            int64_t m0, int64_t n0, const MmBufs &buf) {
+  const int64_t rb = H * 2;
+  const MmOperand a{hidden + m0 * rb, rb, M - m0 < MM_T ? M - m0 : MM_T, 0, rb};
+  const MmOperand b{W + n0 * rb, rb, V - n0 < MM_T ? V - n0 : MM_T, 0, rb};
+  const int64_t stages = (rb + MM_STAGE_BYTES - 1) / MM_STAGE_BYTES;
+  const int64_t rot = korder_start(n0, H) / 64;
+  mm_main<ET, false, false>(tile, a, b, stages,
+                            [&](int64_t t) { return t + rot < stages ? t + rot : t + rot - stages; },
+                            buf);
+}
+
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p) {
+  MM_SHARED();
+  const int64_t nmt = (p.M + MM_T - 1) / MM_T, nvt = (p.V + MM_T - 1) / MM_T;
+  const int64_t t = mm_tile_index(nmt * nvt);
+  const int64_t m0 = (t % nmt) * MM_T, vt = t / nmt, n0 = vt * MM_T;
+  MmTile<ET> tile;
+  logits_tile<ET>(tile, p.hidden, p.W, p.M, p.H, p.V, m0, n0, mm_buf);
+
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  const bool has_bias = p.bias != nullptr;
+  float bias[2][2][4];
+  if (has_bias) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t c = n0 + MmTile<ET>::col(wn, lg, y, j) + q;
+          bias[y][j][q] = c < p.V ? p.bias[c] : 0.0f;
+        }
+  }
+  float2 *const stat = reinterpret_cast<float2 *>(mm_buf.at(0));  // [4][256]
+  const bool ragged = n0 + MM_T > p.V;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = MmTile<ET>::row(wm, li, x, i);
+      const int64_t m = m0 + row;
+      const int64_t yt = m < p.M ? target_of(p.target, p.target64, m, p.ignore, p.V) - n0 : -1;
+      float mx = NEG_INF;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c0 = MmTile<ET>::col(wn, lg, y, j);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float v = epilogue_v(tile.c[x][y][i][j][q], p.alpha, has_bias, bias[y][j][q]);
+            if (ragged && n0 + c0 + q >= p.V) v = NEG_INF;
+            if (yt == c0 + q) p.tlogit[m] = v;
+            tile.c[x][y][i][j][q] = v;
+            mx = fmaxf(mx, v);
+          }
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      // a tile of only -inf sums nothing: its terms are taken against 0
+      const float mz = mx == NEG_INF ? 0.0f : mx;
+      float s = 0.0f;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            s = __fadd_rn(s, exp_fast(__fsub_rn(tile.c[x][y][i][j][q], mz)));
+      s = __fadd_rn(s, __shfl_xor(s, 16));
+      s = __fadd_rn(s, __shfl_xor(s, 32));
+      if (lg == 0) stat[wn * MM_T + row] = float2{mx, s};
+    }
+  __syncthreads();
+  const int row = threadIdx.x;
+  if (row < MM_T && m0 + row < p.M) {
+    float mx = NEG_INF, s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w * MM_T + row].x);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 e = stat[w * MM_T + row];
+      if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp_fast(__fsub_rn(e.x, mx))));
+    }
+    p.part[vt * p.M + m0 + row] = float2{mx, s};
+  }
+}
+
+// Folds the tiles of a row: 64 rows per work-group, 16 threads per row, each
+// thread tiles s, s + 16, ... in ascending order, then the 16 in order.
+constexpr int XC_ROWS = 64, XC_SLICES = 16;
+__device__ __forceinline__ void fold_stat(float &m, float &s, float2 e) {
+  const float n = fmaxf(m, e.x);
+  const float a = s == 0.0f ? 0.0f : __fmul_rn(s, exp_fast(__fsub_rn(m, n)));
+  const float b = e.y == 0.0f ? 0.0f : __fmul_rn(e.y, exp_fast(__fsub_rn(e.x, n)));
+  s = __fadd_rn(a, b);
+  m = n;
+}
+__global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
+    XentFwdArgs p, int64_t nvt, float *__restrict__ loss, float *__restrict__ lse) {
+  __shared__ float2 sh[XC_SLICES][XC_ROWS];
+  const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
+  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r;
+  float mx = NEG_INF, s = 0.0f;
+  if (m < p.M) {
+    for (int64_t t0 = sl; t0 < nvt; t0 += 8 * XC_SLICES) {
+      float2 e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t t = t0 + k * XC_SLICES;
+        e[k] = t < nvt ? p.part[t * p.M + m] : float2{NEG_INF, 0.0f};
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fold_stat(mx, s, e[k]);
+    }
+  }
+  sh[sl][r] = float2{mx, s};
+  __syncthreads();
+  if (sl != 0 || m >= p.M) return;
+#pragma unroll
+  for (int k = 1; k < XC_SLICES; ++k) fold_stat(mx, s, sh[k][r]);
+  // every logit -inf: log-sum-exp -inf, and a target's probability 0
+  const float l = s == 0.0f ? NEG_INF : __fadd_rn(mx, logf(s));
+  lse[m] = l;
+  float out = 0.0f;
+  if (target_of(p.target, p.target64, m, p.ignore, p.V) >= 0) {
+    const float t = p.tlogit[m];
+    out = t == NEG_INF ? __builtin_inff() : __fsub_rn(l, t);
+  }
+  loss[m] = out;
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// What the epilogue needs of a row: G = a exp(t - lse) - b [v = y].
+struct alignas(16) RowCoef {
+  float a, b, lse;
+  int32_t y;  // target column, or -1
+};
+
+// The power of two that takes the largest row coefficient to 2^14 (fp16), and
+// its inverse: one work-group, an exact maximum.
+__global__ __launch_bounds__(1024) void xent_scale_kernel(const float *__restrict__ g,
+                                                          const float *__restrict__ l,
+                                                          const void *target, int target64,
+                                                          int64_t ignore, int64_t M, int64_t V,
+                                                          float *__restrict__ scale) {
+  float mx = 0.0f;
+  for (int64_t m = threadIdx.x; m < M; m += 1024) {
+    const float b = target_of(target, target64, m, ignore, V) >= 0 ? g[m] : 0.0f;
+    const float a = l != nullptr ? __fadd_rn(b, l[m]) : b;
+    mx = fmaxf(mx, fmaxf(fabsf(a), fabsf(b)));
+  }
+  __shared__ float sh[16];
+  for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 16; ++w) mx = fmaxf(mx, sh[w]);
+    // mx <= 2^e; outside the range of useful scales (zero, infinities): 1
+    const int e = (int)((__builtin_bit_cast(uint32_t, mx) >> 23) & 255) - 126;
+    const int k = 14 - e;
+    const bool ok = mx > 0.0f && mx < __builtin_inff() && k > -120 && k < 120;
+    scale[0] = ok ? __builtin_bit_cast(float, (uint32_t)(127 + k) << 23) : 1.0f;
+    scale[1] = ok ? __builtin_bit_cast(float, (uint32_t)(127 - k) << 23) : 1.0f;
+  }
+}
+
+__global__ __launch_bounds__(256) void xent_rows_kernel(const float *__restrict__ g,
+                                                        const float *__restrict__ l,
+                                                        const float *__restrict__ lse,
+                                                        const void *target, int target64,
+                                                        int64_t ignore, int64_t M, int64_t V,
+                                                        const float *__restrict__ scale,
+                                                        RowCoef *__restrict__ rows) {
+  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (m >= M) return;
+  const int64_t y = target_of(target, target64, m, ignore, V);
+  const float s = scale != nullptr ? scale[0] : 1.0f;
+  const float b = y >= 0 ? g[m] : 0.0f;
+  const float a = l != nullptr ? __fadd_rn(b, l[m]) : b;
+  rows[m] = RowCoef{__fmul_rn(a, s), __fmul_rn(b, s), lse[m], (int32_t)y};
+}
+
+struct XentBwdArgs {
+  const uint8_t *hidden, *W;
+  int64_t M, H, V;
+  float alpha;
+  const float *bias;
+  const RowCoef *rows;
+  const float *scale;  // {s, 1 / s} (fp16), or nullptr
+  int64_t v0, vp;      // this piece's first column and its columns (a multiple of 256)
+  uint8_t *G;          // [M, vp], 16 bits
+  float *colpart;      // [row tile][vp] column sums of G, or nullptr
+  float *dh;           // [splits][M, H] fp32 sums
+  int64_t ksplit;      // columns per split of G W
+  int first;           // first piece: dh is written, not added to
+  uint16_t *dw;        // [V, H]
+};
+
+// The LDS rows (512 bytes) of a 256 x 256 tile of 16-bit values: row r in
+// stage array r / 32, its 32-byte pieces xor-ed with r so that the 16 rows one
+// store touches fall in distinct banks.
+__device__ __forceinline__ uint8_t *tile_row(const MmBufs &buf, int hi, int r) {
+  return reinterpret_cast<uint8_t *>(buf.at(hi)) + (r & 31) * 512;
+}
+
+template <int ET>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (ET == ET_F16)
+    return (uint32_t)out_bits16<_Float16>(a) | ((uint32_t)out_bits16<_Float16>(b) << 16);
+  else
+    return (uint32_t)bf16_rne(a) | ((uint32_t)bf16_rne(b) << 16);
+}
+
+// Four columns of one row of the tile, as 16-bit values, into LDS.
+template <int ET>
+__device__ __forceinline__ void stage4(const MmBufs &buf, int wm, int wn, int li, int lg,
+                                       int x, int y, int i, int j, f32x4 v) {
+  const int r = MmTile<ET>::row(wm, li, x, i);
+  uint8_t *row = wm == 0 ? tile_row(buf, x * 4 + (i >> 1), r) : tile_row(buf, x * 4 + 2 + (i >> 1), r);
+  const int piece = (y * 128 + wn * 32 + 16 * j) / 16;
+  *reinterpret_cast<u32x2 *>(row + ((piece ^ (r & 15)) * 32) + 8 * lg) =
+      u32x2{pack2<ET>(v[0], v[1]), pack2<ET>(v[2], v[3])};
+}
+
+// The staged tile to rows of `ld` bytes at `out`, `rows` rows of `bytes`
+// bytes (a multiple of 16) present.
+template <int POLICY>
+__device__ __forceinline__ void store_tile16(const MmBufs &buf, uint8_t *out, int64_t ld,
+                                             int64_t rows, int64_t bytes) {
+  const rsrc_t rs = make_rsrc(out, (uint32_t)((rows - 1) * ld + (bytes < 512 ? bytes : 512)));
+  const int c = threadIdx.x % 32, r0 = threadIdx.x / 32;
+#pragma unroll
+  for (int it = 0; it < 16; ++it) {
+    const int r = it * 16 + r0;
+    const uint8_t *row = tile_row(buf, it >> 1, r);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + (((c >> 1) ^ (r & 15)) * 32) + 16 * (c & 1));
+    const bool ok = r < rows && 16 * c < bytes;
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, ok ? (uint32_t)(r * ld + 16 * c) : OFF_NONE, 0, POLICY);
+  }
+}
+
+// G of one piece.
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  const int64_t nmt = (p.M + MM_T - 1) / MM_T;
+  const int64_t t = mm_tile_index(nmt * (p.vp / MM_T));
+  const int64_t m0 = (t % nmt) * MM_T, g0 = (t / nmt) * MM_T, n0 = p.v0 + g0;
+  MmTile<ET> tile;
+  if (n0 < p.V) {
+    logits_tile<ET>(tile, p.hidden, p.W, p.M, p.H, p.V, m0, n0, mm_buf);
+  } else {  // columns that only fill the piece up
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tile.c[x][y][i][j] = zero4();
+  }
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  const bool has_bias = p.bias != nullptr;
+  float bias[2][2][4];
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t c = n0 + MmTile<ET>::col(wn, lg, y, j) + q;
+        // columns that are not there get t = -inf, so G = 0
+        bias[y][j][q] = c < p.V ? (has_bias ? p.bias[c] : 0.0f) : NEG_INF;
+      }
+  const bool add = has_bias || n0 + MM_T > p.V;
+  float colsum[2][2][4] = {};
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + MmTile<ET>::row(wm, li, x, i);
+      // exp(-inf) = 0 in rows past the end, and where the whole row is -inf
+      const RowCoef rc = m < p.M ? p.rows[m] : RowCoef{0.0f, 0.0f, __builtin_inff(), -1};
+      const float lse = rc.lse == NEG_INF ? 0.0f : rc.lse;
+      const int64_t yt = (int64_t)rc.y - n0;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c0 = MmTile<ET>::col(wn, lg, y, j);
+          f32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float tv = epilogue_v(tile.c[x][y][i][j][q], p.alpha, add, bias[y][j][q]);
+            float gv = __fmul_rn(rc.a, exp_fast(__fsub_rn(tv, lse)));
+            if (yt == c0 + q) gv = __fsub_rn(gv, rc.b);
+            v[q] = gv;
+            colsum[y][j][q] = __fadd_rn(colsum[y][j][q], gv);
+          }
+          stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
+        }
+    }
+  __syncthreads();
+  const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
+  store_tile16<LOAD_DEFAULT>(mm_buf, p.G + (m0 * p.vp + g0) * 2, p.vp * 2, rows, 512);
+  if (p.colpart == nullptr) return;
+  __syncthreads();
+  // column sums: 16 rows of a block by lane exchanges, then the two wave rows
+  float *const cs = reinterpret_cast<float *>(mm_buf.at(0));  // [2][256]
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float s = colsum[y][j][q];
+        s = __fadd_rn(s, dpp<DPP_QUAD_SWAP1>(s));
+        s = __fadd_rn(s, dpp<DPP_QUAD_SWAP2>(s));
+        s = __fadd_rn(s, dpp<DPP_ROW_HALF_MIRROR>(s));
+        s = __fadd_rn(s, dpp<DPP_ROW_MIRROR>(s));
+        if (li == 0) cs[wm * MM_T + MmTile<ET>::col(wn, lg, y, j) + q] = s;
+      }
+  __syncthreads();
+  if (threadIdx.x < MM_T) {
+    const float s = p.scale != nullptr ? p.scale[1] : 1.0f;
+    p.colpart[(m0 / MM_T) * p.vp + g0 + threadIdx.x] =
+        __fmul_rn(s, __fadd_rn(cs[threadIdx.x], cs[MM_T + threadIdx.x]));
+  }
+}
+
+// grad_bias of one piece: the row tiles' column sums in ascending order.
+__global__ __launch_bounds__(256) void xent_bias_kernel(const float *__restrict__ colpart, int64_t nmt,
+                                                        int64_t vp, int64_t n, float *__restrict__ db) {
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (v >= n) return;
+  float s = 0.0f;
+  for (int64_t t = 0; t < nmt; ++t) s = __fadd_rn(s, colpart[t * vp + v]);
+  db[v] = s;
+}
+
+// G W of one piece, one split of its columns, into that split's fp32 sums.
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_dhidden_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  const int64_t nmt = (p.M + MM_T - 1) / MM_T, nht = (p.H + MM_T - 1) / MM_T;
+  const int64_t splits = (p.vp + p.ksplit - 1) / p.ksplit;
+  const int64_t t = mm_tile_index(nmt * nht * splits);
+  const int64_t m0 = (t % nmt) * MM_T, h0 = (t / nmt % nht) * MM_T, sp = t / (nmt * nht);
+  const int64_t k0 = sp * p.ksplit, kn = p.vp - k0 < p.ksplit ? p.vp - k0 : p.ksplit;
+  const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
+  const int64_t rb = p.H * 2;
+  // the weight rows present; a split that only fills the piece up has none
+  int64_t wrows = p.V - p.v0 - k0 < kn ? p.V - p.v0 - k0 : kn;
+  if (wrows < 0) wrows = 0;
+  const MmOperand a{p.G + (m0 * p.vp + k0) * 2, p.vp * 2, rows, 0, kn * 2};
+  const MmOperand b{p.W + (wrows > 0 ? (p.v0 + k0) * rb : 0) + h0 * 2, rb, wrows, (p.H - h0) * 2, 0};
+  MmTile<ET> tile;
+  mm_main<ET, false, true>(tile, a, b, kn / 64, [](int64_t s) { return s; }, mm_buf);
+
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  float *const out = p.dh + (sp * p.M + m0) * p.H + h0;
+  const rsrc_t rs = make_rsrc(out, (uint32_t)(((rows - 1) * p.H + (p.H - h0 < MM_T ? p.H - h0 : MM_T)) * 4));
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = MmTile<ET>::row(wm, li, x, i);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = MmTile<ET>::col(wn, lg, y, j);
+          const bool ok = r < rows && h0 + c < p.H;
+          const uint32_t off = ok ? (uint32_t)((r * p.H + c) * 4) : OFF_NONE;
+          f32x4 v = tile.c[x][y][i][j];
+          if (!p.first) {
+            const f32x4 o = __builtin_bit_cast(f32x4, load16(rs, off, 0));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = __fadd_rn(o[q], v[q]);
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, 0, LOAD_DEFAULT);
+        }
+    }
+}
+
+// grad_hidden: the splits' sums in ascending order, scaled, rounded once.
+template <int ET>
+__global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__restrict__ dh, int64_t n,
+                                                               int splits, float alpha,
+                                                               const float *__restrict__ scale,
+                                                               uint16_t *__restrict__ out) {
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (e >= n) return;
+  f32x4 s[2] = {zero4(), zero4()};
+  for (int k = 0; k < splits; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(dh + k * n + e + 4 * h);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[h][q] = __fadd_rn(s[h][q], v[q]);
+    }
+  const float f = scale != nullptr ? __fmul_rn(alpha, scale[1]) : alpha;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[h][q] = __fmul_rn(f, s[h][q]);
+  *reinterpret_cast<u32x4 *>(out + e) = u32x4{pack2<ET>(s[0][0], s[0][1]), pack2<ET>(s[0][2], s[0][3]),
+                                              pack2<ET>(s[1][0], s[1][1]), pack2<ET>(s[1][2], s[1][3])};
+}
+
+// G^T hidden of one piece: its rows of grad_W.
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_dweight_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  const int64_t nht = (p.H + MM_T - 1) / MM_T;
+  const int64_t nv = p.V - p.v0 < p.vp ? p.V - p.v0 : p.vp;
+  const int64_t t = mm_tile_index(nht * ((nv + MM_T - 1) / MM_T));
+  const int64_t h0 = (t % nht) * MM_T, g0 = (t / nht) * MM_T;
+  const MmOperand a{p.G + g0 * 2, p.vp * 2, p.M, (p.vp - g0) * 2, 0};
+  const MmOperand b{p.hidden + h0 * 2, p.H * 2, p.M, (p.H - h0) * 2, 0};
+  MmTile<ET> tile;
+  mm_main<ET, true, true>(tile, a, b, (p.M + 63) / 64, [](int64_t s) { return s; }, mm_buf);
+
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
+  const float f = p.scale != nullptr ? __fmul_rn(p.alpha, p.scale[1]) : p.alpha;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          f32x4 v = tile.c[x][y][i][j];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = __fmul_rn(f, v[q]);
+          stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
+        }
+  __syncthreads();
+  const int64_t rows = nv - g0 < MM_T ? nv - g0 : MM_T;
+  store_tile16<STORE_POLICY>(mm_buf, reinterpret_cast<uint8_t *>(p.dw + (p.v0 + g0) * p.H + h0), p.H * 2,
+                             rows, (p.H - h0) * 2);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+
+// The backward pass's plan: pieces of the vocabulary and splits of G W.
+struct BwdPlan {
+  int64_t vp, pieces, ksplit, splits;
+  int64_t off_scale, off_rows, off_col, off_dh, off_g, bytes;
+};
+BwdPlan bwd_plan(int64_t M, int64_t H, int64_t V, bool bias) {
+  BwdPlan p;
+  const int64_t vall = ceil_div(V, MM_T) * MM_T;
+  // G of a piece: 256 MiB (it then stays in the memory-side cache between the
+  // three products), but at least 8192 columns, which give the products a
+  // work-group per CU
+  int64_t most = ((int64_t)256 << 20) / (2 * M) / MM_T * MM_T;
+  if (most < 8192) most = 8192;
+  p.pieces = ceil_div(vall, most);
+  p.vp = ceil_div(ceil_div(vall, p.pieces), MM_T) * MM_T;
+  p.pieces = ceil_div(V, p.vp);
+  // G W has a tile per 256 rows and 256 of H, too few to fill the chip when M
+  // is small: K (the piece's columns) is split, at least 512 columns each,
+  // into as many splits as fill the last round of work-groups best
+  const int64_t tiles = ceil_div(M, MM_T) * ceil_div(H, MM_T), cus = 256;
+  double best = 0.0;
+  p.splits = 1;
+  for (int64_t s = 1; s <= 64 && s * 512 <= p.vp; ++s) {
+    const double use = (double)(tiles * s) / (double)(ceil_div(tiles * s, cus) * cus);
+    if (use > best * 1.05) {
+      best = use;
+      p.splits = s;
+    }
+    if (tiles * s >= cus * 4) break;
+  }
+  p.ksplit = ceil_div(ceil_div(p.vp, p.splits), 64) * 64;
+  p.splits = ceil_div(p.vp, p.ksplit);
+  p.off_scale = 0;
+  p.off_rows = 256;
+  p.off_col = p.off_rows + align256(16 * M);
+  p.off_dh = p.off_col + (bias ? align256(4 * ceil_div(M, MM_T) * p.vp) : 0);
+  p.off_g = p.off_dh + align256(4 * p.splits * M * H);
+  p.bytes = p.off_g + align256(2 * M * p.vp);
+  return p;
+}
+
+__global__ __launch_bounds__(256) void zero_kernel(uint32_t *__restrict__ p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+hipError_t zero_words(void *p, int64_t n, hipStream_t s) {
+  const int64_t blocks = ceil_div(n, 256);
+  return launch_kernel(zero_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), s,
+                       static_cast<uint32_t *>(p), n);
+}
+
+template <int ET>
+hipError_t forward(const XentFwdArgs &p, float *loss, float *lse, hipStream_t s) {
+  const int64_t nmt = ceil_div(p.M, MM_T), nvt = ceil_div(p.V, MM_T);
+  hipError_t e = launch_kernel(xent_stats_kernel<ET>, dim3((unsigned)(nmt * nvt)), dim3(MM_THREADS), s, p);
+  if (e != hipSuccess) return e;
+  return launch_kernel(xent_combine_kernel, dim3((unsigned)ceil_div(p.M, XC_ROWS)),
+                       dim3(XC_ROWS * XC_SLICES), s, p, nvt, loss, lse);
+}
+
+template <int ET>
+hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
+  const BwdPlan pl = bwd_plan(c.M, c.H, c.V, c.grad_bias != nullptr);
+  float *const scale = ET == ET_F16 ? reinterpret_cast<float *>(ws + pl.off_scale) : nullptr;
+  RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + pl.off_rows);
+  hipError_t e = hipSuccess;
+  if (scale != nullptr)
+    e = launch_kernel(xent_scale_kernel, dim3(1), dim3(1024), s, c.grad_loss, c.grad_lse, c.target,
+                      c.target64, c.ignore, c.M, c.V, scale);
+  if (e == hipSuccess)
+    e = launch_kernel(xent_rows_kernel, dim3((unsigned)ceil_div(c.M, 256)), dim3(256), s, c.grad_loss,
+                      c.grad_lse, c.lse, c.target, c.target64, c.ignore, c.M, c.V,
+                      static_cast<const float *>(scale), rows);
+  XentBwdArgs p;
+  p.hidden = static_cast<const uint8_t *>(c.hidden);
+  p.W = static_cast<const uint8_t *>(c.W);
+  p.M = c.M;
+  p.H = c.H;
+  p.V = c.V;
+  p.alpha = c.alpha;
+  p.bias = c.bias;
+  p.rows = rows;
+  p.scale = scale;
+  p.vp = pl.vp;
+  p.G = ws + pl.off_g;
+  p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + pl.off_col) : nullptr;
+  p.dh = reinterpret_cast<float *>(ws + pl.off_dh);
+  p.ksplit = pl.ksplit;
+  p.dw = static_cast<uint16_t *>(c.grad_W);
+  const int64_t nmt = ceil_div(c.M, MM_T), nht = ceil_div(c.H, MM_T);
+  for (int64_t v0 = 0; v0 < c.V && e == hipSuccess; v0 += pl.vp) {
+    p.v0 = v0;
+    p.first = v0 == 0;
+    const int64_t nv = c.V - v0 < pl.vp ? c.V - v0 : pl.vp;
+    e = launch_kernel(xent_grad_kernel<ET>, dim3((unsigned)(nmt * (pl.vp / MM_T))), dim3(MM_THREADS), s, p);
+    if (e == hipSuccess && c.grad_bias != nullptr)
+      e = launch_kernel(xent_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
+                        static_cast<const float *>(p.colpart), nmt, pl.vp, nv, c.grad_bias + v0);
+    if (e == hipSuccess && c.grad_hidden != nullptr)
+      e = launch_kernel(xent_dhidden_kernel<ET>, dim3((unsigned)(nmt * nht * pl.splits)), dim3(MM_THREADS), s, p);
+    if (e == hipSuccess && c.grad_W != nullptr)
+      e = launch_kernel(xent_dweight_kernel<ET>, dim3((unsigned)(nht * ceil_div(nv, MM_T))), dim3(MM_THREADS), s, p);
+  }
+  if (e == hipSuccess && c.grad_hidden != nullptr)
+    e = launch_kernel(xent_dhidden_out_kernel<ET>, dim3((unsigned)ceil_div(c.M * c.H, 2048)), dim3(256), s,
+                      static_cast<const float *>(p.dh), c.M * c.H, (int)pl.splits, c.alpha,
+                      static_cast<const float *>(scale), static_cast<uint16_t *>(c.grad_hidden));
+  return e;
+}
+
+}  // namespace
+
+int64_t xent_forward_bytes(int64_t M, int64_t V) { return align256(4 * M) + 8 * M * ceil_div(V, MM_T); }
+int64_t xent_backward_bytes(int64_t M, int64_t H, int64_t V, bool bias) { return bwd_plan(M, H, V, bias).bytes; }
+
+hipError_t launch_xent_forward(const XentForward &c, hipStream_t s) {
+  XentFwdArgs p;
+  p.hidden = static_cast<const uint8_t *>(c.hidden);
+  p.W = static_cast<const uint8_t *>(c.W);
+  p.M = c.M;
+  p.H = c.H;
+  p.V = c.V;
+  p.alpha = c.alpha;
+  p.bias = c.bias;
+  p.target = c.target;
+  p.target64 = c.target64;
+  p.ignore = c.ignore;
+  p.tlogit = static_cast<float *>(c.workspace);
+  p.part = reinterpret_cast<float2 *>(static_cast<uint8_t *>(c.workspace) + align256(4 * c.M));
+  return c.in_f16 ? forward<ET_F16>(p, c.loss, c.lse, s) : forward<ET_BF16>(p, c.loss, c.lse, s);
+}
+
+hipError_t launch_xent_backward(const XentBackward &c, hipStream_t s) {
+  if (c.M == 0) {  // sums over no rows
+    hipError_t e = hipSuccess;
+    if (c.grad_W != nullptr) e = zero_words(c.grad_W, c.V * c.H / 2, s);
+    if (e == hipSuccess && c.grad_bias != nullptr) e = zero_words(c.grad_bias, c.V, s);
+    return e;
+  }
+  uint8_t *const ws = static_cast<uint8_t *>(c.workspace);
+  return c.in_f16 ? backward<ET_F16>(c, ws, s) : backward<ET_BF16>(c, ws, s);
+}
+
+}  // namespace lmhead
