@@ -315,6 +315,60 @@ lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, con
  * grad_hidden, and little else. 0 outside the shape contract or when M == 0. */
 size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias);
 
+/* The embedding lookup out[m, :] = scale * W[ids[m], :], the product taken at
+ * fp32 and rounded once. An id outside [0, V) gives a row of zeros (so a
+ * vocabulary shard takes ids - v0 and the shards' results add up).
+ *   ids  [M] of ids_type                     (device, read)
+ *   W    [V, H] bf16 or fp16 (dtype)         (device, read)
+ *   out  [M, H] of dtype                     (device, written)
+ * Alignment: W and out 16 bytes. Returns as lmhead_logits_ex. */
+lmhead_status lmhead_embed(const void *ids, lmhead_index ids_type, int64_t M, const void *W, int64_t V,
+                           int64_t H, lmhead_dtype dtype, float scale, void *out, void *stream);
+
+/* Its gradient: s[v, :] = scale * sum over {m : ids[m] == v} of grad_out[m, :],
+ * summed at fp32 in an order that depends on ids only (the same bits every
+ * run). Ids outside [0, V) and ids equal to padding_index (pass a value
+ * outside [0, V) for none) have no gradient.
+ *   grad_out    [M, H] bf16 or fp16 (dtype)   (device, read)
+ *   accumulate  0: grad_W = s, every row written; else grad_W += s (one fp32
+ *               addition and one rounding; rows without an id are not touched):
+ *               the gradient of a head tied to the embedding is
+ *               lmhead_xent_backward's with this added
+ *   grad_W      [V, H] of dtype               (device, written, or read and written)
+ *   workspace   at least lmhead_embed_backward_workspace_bytes(M, H) bytes,
+ *               256-byte aligned, overwritten; not in use by other work until
+ *               this call's work has finished */
+lmhead_status lmhead_embed_backward(const void *ids, lmhead_index ids_type, int64_t M, const void *grad_out,
+                                    int64_t V, int64_t H, lmhead_dtype dtype, float scale,
+                                    int64_t padding_index, int accumulate, void *grad_W, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Host-only: bytes of workspace lmhead_embed_backward needs (0 outside the shape contract). */
+size_t lmhead_embed_backward_workspace_bytes(int64_t M, int64_t H);
+
+/* Rows to int8: scales[r] = max |x[r, :]| / 127 (1 where that is 0),
+ * codes[r, k] = x[r, k] / scales[r] rounded to nearest even, in [-127, 127];
+ * binary32 operations, the division correctly rounded. Tokens (one scale per
+ * token) and weights (one per vocabulary row) alike.
+ *   x       [rows, H] bf16 or fp16 (dtype), finite   (device, read)
+ *   codes   int8 [rows, H]                           (device, written)
+ *   scales  fp32 [rows]                              (device, written)
+ * Alignment: x and codes 16 bytes. Shapes as for the projection with M = rows. */
+lmhead_status lmhead_quantize_int8(const void *x, int64_t rows, int64_t H, lmhead_dtype dtype, int8_t *codes,
+                                   float *scales, void *stream);
+
+/* The int8 head: t = fl32(fl32(float(sum_k hidden[m, k] W[v, k]) * hidden_scale[m]) * w_scale[v]),
+ * then alpha and bias as in lmhead_logits. The integer sum is exact, so a
+ * row's logits depend on nothing but the row, whatever M.
+ *   hidden int8 [M, H], hidden_scale fp32 [M]   (device, read)
+ *   W      int8 [V, H], w_scale fp32 [V]        (device, read)
+ *   out_dtype  LMHEAD_F32, LMHEAD_BF16 or LMHEAD_F16 (rounded to nearest even)
+ *   out    [M, V] of out_dtype                  (device, written)
+ * Alignment: hidden, W and out 16 bytes. */
+lmhead_status lmhead_logits_int8(const int8_t *hidden, const float *hidden_scale, int64_t M, int64_t H,
+                                 const int8_t *W, const float *w_scale, int64_t V, float alpha,
+                                 const float *bias, lmhead_dtype out_dtype, void *out, void *stream);
+
 /* Host-only shape predicate (no device access): 1 when (M, H, V) is inside the
  * shape contract of the bf16 (nvfp4 = 0) or NVFP4 (nvfp4 = 1) entry point,
  * else 0. Like the shape check the metrale page's install step runs before

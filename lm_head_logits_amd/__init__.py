@@ -15,17 +15,20 @@ import ctypes
 import torch
 
 from . import _lib
-from ._binding import (_DTYPES, LmHeadError, NotHandled, _check, _device_ctx, _need, _same_device,
+from ._binding import (_DTYPES, LmHeadError, NotHandled, _alloc_on, _check, _device_ctx, _need, _same_device,
                        _stream_handle, status_string)
 from ._lib import LMHEAD_F32, PATH_AUTO, PATH_NONE, PATH_NVFP4, PATH_SKINNY, PATH_TILED
-from .training import (xent_backward, xent_backward_workspace_bytes, xent_forward,
+from .training import (cross_entropy, embed, embed_backward, embed_backward_workspace_bytes, embedding,
+                       xent_backward, xent_backward_workspace_bytes, xent_forward,
                        xent_forward_workspace_bytes)
 
 __all__ = ["logits", "logits_rowreduce", "logits_rowreduce_noalloc", "rowreduce_workspace_bytes", "logits_nvfp4",
            "quantize_nvfp4", "shape_ok", "path_for", "status_string", "version",
            "LmHeadError", "NotHandled", "PATH_SKINNY", "PATH_TILED", "PATH_NVFP4", "PATH_AUTO",
            "PATH_NONE", "probe_hbm_read", "probe_mfma_bf16",
-           "xent_forward", "xent_backward", "xent_forward_workspace_bytes", "xent_backward_workspace_bytes"]
+           "xent_forward", "xent_backward", "xent_forward_workspace_bytes", "xent_backward_workspace_bytes",
+           "cross_entropy", "embed", "embed_backward", "embed_backward_workspace_bytes", "embedding",
+           "quantize_int8", "logits_int8"]
 
 
 def version() -> str:
@@ -232,6 +235,58 @@ def logits_nvfp4(hidden: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
             float(alpha), bias.data_ptr() if bias is not None else None, out.data_ptr(),
             _stream_handle(hidden.device, stream))
     _check(st, "lmhead_logits_nvfp4")
+    return out
+
+
+def quantize_int8(x: torch.Tensor, *, stream=None):
+    """Rows of a bf16 or fp16 [R, H] to int8 with one scale each
+    (lmhead_quantize_int8): returns (codes int8 [R, H], scales fp32 [R]).
+    Tokens' hidden rows and vocabulary rows alike."""
+    _need(x.is_cuda and x.dtype in _DTYPES and x.dim() == 2 and x.is_contiguous(),
+          "x must be a contiguous [R, H] device tensor, float32, bfloat16 or float16")
+    R, H = x.shape
+    dev = x.device
+    with _alloc_on(stream):
+        codes = torch.empty((R, H), dtype=torch.int8, device=dev)
+        scales = torch.empty(R, dtype=torch.float32, device=dev)
+    with _device_ctx(dev):
+        st = _lib.load().lmhead_quantize_int8(x.data_ptr(), R, H, _DTYPES[x.dtype], codes.data_ptr(),
+                                              scales.data_ptr(), _stream_handle(dev, stream))
+    _check(st, "lmhead_quantize_int8")
+    return codes, scales
+
+
+def logits_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor,
+                alpha: float = 1.0, bias=None, out_dtype=torch.bfloat16, out: torch.Tensor | None = None, *,
+                stream=None) -> torch.Tensor:
+    """The int8 head (lmhead_logits_int8): int8 hidden [M, H] and weight
+    [V, H] with fp32 scales [M] and [V] (quantize_int8) -> logits [M, V] of
+    out_dtype (float32, bfloat16 or float16)."""
+    _need(hidden.is_cuda and weight.is_cuda and hidden.dtype == torch.int8 and weight.dtype == torch.int8,
+          "hidden and weight must be int8 device tensors")
+    _need(hidden.dim() == 2 and weight.dim() == 2, "hidden [M, H] and weight [V, H] are 2-D")
+    _need(hidden.is_contiguous() and weight.is_contiguous(), "inputs must be contiguous")
+    _need(out_dtype in _DTYPES, "out_dtype must be float32, bfloat16 or float16")
+    M, H = hidden.shape
+    V, H2 = weight.shape
+    if H != H2:
+        raise ValueError(f"hidden has H={H}, weight has H={H2}")
+    for t, n, name in ((hidden_scale, M, "hidden_scale"), (weight_scale, V, "weight_scale"), (bias, V, "bias")):
+        if t is not None and not (t.is_cuda and t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 device tensor [{n}]")
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty((M, V), dtype=out_dtype, device=hidden.device)
+    else:
+        _need(out.is_cuda and out.dtype == out_dtype and out.shape == (M, V) and out.is_contiguous(),
+              "out must be a contiguous [M, V] device tensor of out_dtype")
+    _same_device(hidden, hidden_scale, weight, weight_scale, bias, out)
+    with _device_ctx(hidden.device):
+        st = _lib.load().lmhead_logits_int8(
+            hidden.data_ptr(), hidden_scale.data_ptr(), M, H, weight.data_ptr(), weight_scale.data_ptr(), V,
+            float(alpha), bias.data_ptr() if bias is not None else None, _DTYPES[out_dtype], out.data_ptr(),
+            _stream_handle(hidden.device, stream))
+    _check(st, "lmhead_logits_int8")
     return out
 
 

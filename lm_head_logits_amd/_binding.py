@@ -55,6 +55,12 @@ def _device_ctx(device):
     return _NO_SWITCH if torch.cuda.current_device() == idx else torch.cuda.device(idx)
 
 
+def _alloc_on(stream):
+    """Where a call's outputs and workspace are allocated: the stream it runs
+    on, so that the allocator's reuse of their memory is ordered with it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _need(cond: bool, msg: str):
     if not cond:
         raise ValueError(msg)

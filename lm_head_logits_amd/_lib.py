@@ -36,7 +36,8 @@ EXPORTS = ("lmhead_logits", "lmhead_logits_path", "lmhead_logits_ex", "lmhead_lo
            "lmhead_quantize_nvfp4_workspace_bytes", "lmhead_shape_ok",
            "lmhead_path_for", "lmhead_status_string", "lmhead_version",
            "lmhead_xent_forward", "lmhead_xent_forward_workspace_bytes", "lmhead_xent_backward",
-           "lmhead_xent_backward_workspace_bytes")
+           "lmhead_xent_backward_workspace_bytes", "lmhead_embed", "lmhead_embed_backward",
+           "lmhead_embed_backward_workspace_bytes", "lmhead_quantize_int8", "lmhead_logits_int8")
 # include/lmhead_probes.h: measurement probes (not part of the projection),
 # in a library of their own
 PROBE_EXPORTS = ("lmhead_probe_grid", "lmhead_probe_hbm_read", "lmhead_probe_mfma_bf16")
@@ -100,6 +101,16 @@ def load() -> ctypes.CDLL:
                                          vp, vp, vp, vp, sz, vp]
     lib.lmhead_xent_backward_workspace_bytes.restype = sz
     lib.lmhead_xent_backward_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.lmhead_embed.restype = i32
+    lib.lmhead_embed.argtypes = [vp, i32, i64, vp, i64, i64, i32, f32, vp, vp]
+    lib.lmhead_embed_backward.restype = i32
+    lib.lmhead_embed_backward.argtypes = [vp, i32, i64, vp, i64, i64, i32, f32, i64, i32, vp, vp, sz, vp]
+    lib.lmhead_embed_backward_workspace_bytes.restype = sz
+    lib.lmhead_embed_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.lmhead_quantize_int8.restype = i32
+    lib.lmhead_quantize_int8.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    lib.lmhead_logits_int8.restype = i32
+    lib.lmhead_logits_int8.argtypes = [vp, vp, i64, i64, vp, vp, i64, f32, vp, i32, vp, vp]
     _lib = lib
     return lib
 

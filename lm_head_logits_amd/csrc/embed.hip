@@ -1,0 +1,547 @@
+// embed.hip -- the embedding lookup out[m, :] = scale W[ids[m], :] and its
+// gradient by sorted tokens, grad_W[v, :] = scale sum over {m : ids[m] = v}
+// of grad_out[m, :].
+//
+// Ids outside [0, V) (and, in the gradient, the padding id) have a row of
+// zeros and no gradient, so a vocabulary shard can be handed ids - v0.
+//
+// Both are bound by bytes. The gradient's fixed cost is finding each token's
+// positions: the positions are put in the order of (id, position), so that
+// the rows of one id follow each other and are summed at fp32 in ascending
+// position, the same bits every run; no float atomics. A dense gradient is
+// first filled with zeros by work-groups that ride along in the sorting
+// kernels' launches: the sort needs few CUs and the fill is what takes long.
+#include "kstep.hpp"
+#include "launch.hpp"
+
+namespace lmhead {
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
+
+__device__ __forceinline__ int64_t id_at(const void *ids, int ids64, int64_t m) {
+  return ids64 ? static_cast<const int64_t *>(ids)[m] : (int64_t)static_cast<const int32_t *>(ids)[m];
+}
+
+template <bool F16>
+__device__ __forceinline__ float from16(uint32_t bits) {
+  if constexpr (F16)
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+  else
+    return __builtin_bit_cast(float, bits << 16);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t to16(float f) {
+  if constexpr (F16)
+    return out_bits16<_Float16>(f);
+  else
+    return bf16_rne(f);
+}
+
+// ---------------------------------------------------------------------------
+// Lookup: 16 bytes (8 elements) per thread and step, EL_STEPS rows' pieces in
+// flight per thread. The product is taken at fp32 and rounded once.
+// ---------------------------------------------------------------------------
+constexpr int EL_THREADS = 256, EL_STEPS = 4;
+
+template <bool F16, typename Index>
+__global__ __launch_bounds__(EL_THREADS) void embed_kernel(const void *ids, int ids64, Index pieces,
+                                                           Index ppr, const uint16_t *__restrict__ W,
+                                                           int64_t V, float scale,
+                                                           uint16_t *__restrict__ out) {
+  const Index p0 = (Index)blockIdx.x * (EL_THREADS * EL_STEPS) + threadIdx.x;
+  u32x4 v[EL_STEPS];
+#pragma unroll
+  for (int s = 0; s < EL_STEPS; ++s) {
+    const Index p = p0 + s * EL_THREADS;
+    v[s] = u32x4{0, 0, 0, 0};
+    if (p < pieces) {
+      const Index m = p / ppr, c = p - m * ppr;
+      const int64_t id = id_at(ids, ids64, m);
+      if (id >= 0 && id < V)
+        v[s] = *reinterpret_cast<const u32x4 *>(W + ((int64_t)id * ppr + c) * 8);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < EL_STEPS; ++s) {
+    const Index p = p0 + s * EL_THREADS;
+    if (p >= pieces) break;
+    if (scale != 1.0f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[s][k] = to16<F16>(__fmul_rn(scale, from16<F16>(v[s][k] & 0xFFFFu))) |
+                  (to16<F16>(__fmul_rn(scale, from16<F16>(v[s][k] >> 16))) << 16);
+    }
+    *reinterpret_cast<u32x4 *>(out + (int64_t)p * 8) = v[s];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sorting the positions by (id, position).
+// ---------------------------------------------------------------------------
+
+// The key of position m: its id, or V where it has no gradient.
+__device__ __forceinline__ uint32_t key_of(const void *ids, int ids64, int64_t m, int64_t V,
+                                           int64_t padding) {
+  const int64_t id = id_at(ids, ids64, m);
+  return id >= 0 && id < V && id != padding ? (uint32_t)id : (uint32_t)V;
+}
+
+// A slice of the zero fill, done by the work-groups behind the sorting ones.
+struct Fill {
+  u32x4 *p;        // 16-byte words [from, to)
+  int64_t from, to;
+  int sort_blocks; // work-groups of the launch that sort
+};
+constexpr int FILL_PER_THREAD = 16;
+__device__ __forceinline__ void do_fill(const Fill &f) {
+  const int64_t b = (int64_t)blockIdx.x - f.sort_blocks;
+  const int64_t p0 = f.from + b * ((int64_t)blockDim.x * FILL_PER_THREAD) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < FILL_PER_THREAD; ++k) {
+    const int64_t p = p0 + (int64_t)k * blockDim.x;
+    if (p < f.to) f.p[p] = u32x4{0, 0, 0, 0};
+  }
+}
+int64_t fill_blocks(const Fill &f, int threads) {
+  return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * FILL_PER_THREAD) : 0;
+}
+
+// Up to RANK_MAX positions: a position's place is the number of smaller
+// (id, position) pairs, counted against every other. A work-group ranks 64
+// positions, its 16 waves splitting the others; M^2 comparisons are spread
+// over the whole chip in one launch (M = 8192: 4 µs of it).
+constexpr int RANK_THREADS = 1024, RANK_WAVES = 16, RANK_CHUNK = 8192;
+constexpr int64_t RANK_MAX = 16384;
+__global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(const void *ids, int ids64, int M,
+                                                                  int64_t V, int64_t padding,
+                                                                  uint32_t *__restrict__ keys,
+                                                                  uint32_t *__restrict__ order, Fill f) {
+  if ((int)blockIdx.x >= f.sort_blocks) return do_fill(f);
+  __shared__ alignas(16) uint32_t sk[RANK_CHUNK];
+  __shared__ uint32_t cnt[RANK_WAVES][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i = blockIdx.x * 64 + lane;
+  const uint32_t ki = i < M ? key_of(ids, ids64, i, V, padding) : 0u;
+  uint32_t n = 0;
+  for (int c0 = 0; c0 < M; c0 += RANK_CHUNK) {
+    const int cn = M - c0 < RANK_CHUNK ? M - c0 : RANK_CHUNK;
+    __syncthreads();
+    for (int j = threadIdx.x; j < RANK_CHUNK; j += RANK_THREADS)
+      sk[j] = j < cn ? key_of(ids, ids64, c0 + j, V, padding) : 0xFFFFFFFFu;
+    __syncthreads();
+    // this wave's positions of the chunk, four at a time; positions before i
+    // count with an equal id, later ones do not
+    constexpr int PER = RANK_CHUNK / RANK_WAVES;
+    const int j0 = wave * PER;
+    const int jn = cn - j0 < PER ? (cn - j0 + 3) & ~3 : PER;
+    for (int j = 0; j < jn; j += 4) {
+      const u32x4 k = *reinterpret_cast<const u32x4 *>(&sk[j0 + j]);
+      const int p = c0 + j0 + j;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) n += k[e] < ki + (p + e < i ? 1u : 0u) ? 1u : 0u;
+    }
+  }
+  cnt[wave][lane] = n;
+  __syncthreads();
+  if (wave == 0 && i < M) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int w = 0; w < RANK_WAVES; ++w) r += cnt[w][lane];
+    keys[r] = ki;
+    order[r] = (uint32_t)i;
+  }
+}
+
+// More positions: a stable radix sort, least digit first. A work-group owns a
+// contiguous tile of positions, each of its 16 waves a contiguous part of it.
+// embed_count_kernel counts the tile's digits; embed_scatter_kernel finds the
+// tile's and its waves' first place for each digit from all tiles' counts, and
+// places the positions in order (lanes of a wave with equal digits find each
+// other by ballots).
+constexpr int RX_THREADS = 1024, RX_WAVES = 16, RX_BITS = 9, RX_BINS = 1 << RX_BITS, RX_TILES = 256;
+
+struct RadixArgs {
+  const void *ids;           // first pass: keys come from here
+  int ids64;
+  int64_t V, padding;
+  const uint32_t *keys_in, *order_in;  // later passes
+  uint32_t *keys_out, *order_out;
+  uint32_t *counts;          // [tiles][RX_BINS]
+  int64_t M, tile;
+  int tiles, shift, first;
+};
+__device__ __forceinline__ uint32_t radix_key(const RadixArgs &a, int64_t m) {
+  return a.first ? key_of(a.ids, a.ids64, m, a.V, a.padding) : a.keys_in[m];
+}
+
+__global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fill f) {
+  if ((int)blockIdx.x >= f.sort_blocks) return do_fill(f);
+  __shared__ uint32_t h[RX_BINS];
+  for (int d = threadIdx.x; d < RX_BINS; d += RX_THREADS) h[d] = 0;
+  __syncthreads();
+  const int64_t m0 = blockIdx.x * a.tile, m1 = m0 + a.tile < a.M ? m0 + a.tile : a.M;
+  for (int64_t m = m0 + threadIdx.x; m < m1; m += RX_THREADS)
+    atomicAdd(&h[(radix_key(a, m) >> a.shift) & (RX_BINS - 1)], 1u);
+  __syncthreads();
+  for (int d = threadIdx.x; d < RX_BINS; d += RX_THREADS) a.counts[(int64_t)blockIdx.x * RX_BINS + d] = h[d];
+}
+
+__global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, Fill f) {
+  if ((int)blockIdx.x >= f.sort_blocks) return do_fill(f);
+  __shared__ uint32_t at[RX_WAVES][RX_BINS];  // next place of (wave, digit)
+  __shared__ uint32_t part[2][RX_BINS], sum[RX_BINS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // per digit: positions of earlier tiles, and of all tiles (two threads per
+  // digit, the even and the odd tiles)
+  {
+    const int d = tid % RX_BINS, half = tid / RX_BINS;
+    uint32_t before = 0, all = 0;
+    for (int t = half; t < a.tiles; t += 2) {
+      const uint32_t c = a.counts[(int64_t)t * RX_BINS + d];
+      all += c;
+      if (t < (int)blockIdx.x) before += c;
+    }
+    part[half][d] = all;
+    __syncthreads();
+    if (half == 0) sum[d] = part[0][d] + part[1][d];
+    __syncthreads();
+    // exclusive prefix of the totals over the digits
+    for (int s = 1; s < RX_BINS; s <<= 1) {
+      const uint32_t v = half == 0 && d >= s ? sum[d - s] : 0u;
+      __syncthreads();
+      if (half == 0) sum[d] += v;
+      __syncthreads();
+    }
+    const uint32_t first = d > 0 ? sum[d - 1] : 0u;
+    __syncthreads();
+    part[half][d] = before;
+    __syncthreads();
+    if (half == 0) sum[d] = first + part[0][d] + part[1][d];
+    for (int e = tid; e < RX_WAVES * RX_BINS; e += RX_THREADS) at[e / RX_BINS][e % RX_BINS] = 0;
+    __syncthreads();
+  }
+  const int64_t m0 = blockIdx.x * a.tile, m1 = m0 + a.tile < a.M ? m0 + a.tile : a.M;
+  const int64_t per = (a.tile + RX_WAVES * 64 - 1) / (RX_WAVES * 64) * 64;
+  const int64_t w0 = m0 + wave * per, w1 = w0 + per < m1 ? w0 + per : m1;
+  for (int64_t m = w0 + lane; m < w1; m += 64)
+    atomicAdd(&at[wave][(radix_key(a, m) >> a.shift) & (RX_BINS - 1)], 1u);
+  __syncthreads();
+  if (tid < RX_BINS) {  // counts -> first places, wave by wave
+    uint32_t p = sum[tid];
+#pragma unroll
+    for (int w = 0; w < RX_WAVES; ++w) {
+      const uint32_t c = at[w][tid];
+      at[w][tid] = p;
+      p += c;
+    }
+  }
+  __syncthreads();
+  for (int64_t b = w0; b < w1; b += 64) {
+    const int64_t m = b + lane;
+    const bool ok = m < w1;
+    const uint32_t key = ok ? radix_key(a, m) : 0u;
+    const uint32_t d = (key >> a.shift) & (RX_BINS - 1);
+    uint64_t same = __ballot(ok);
+#pragma unroll
+    for (int bit = 0; bit < RX_BITS; ++bit) {
+      const uint64_t has = __ballot((d >> bit) & 1u);
+      same &= ((d >> bit) & 1u) ? has : ~has;
+    }
+    if (ok) {
+      const int r = __popcll(same & ((1ull << lane) - 1));
+      const uint32_t place = at[wave][d] + r;
+      __builtin_amdgcn_wave_barrier();
+      if (r == 0) at[wave][d] += (uint32_t)__popcll(same);
+      a.keys_out[place] = key;
+      a.order_out[place] = a.first ? (uint32_t)m : a.order_in[m];
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Summing. The sorted positions are cut into tiles; a work-group sums a tile's
+// rows over 2048 columns, 8 per thread. An id whose positions all lie in the
+// tile is written at once; the sums of an id that began in an earlier tile
+// (slot 0) or goes on in the next (slot 1) go to the workspace, and
+// embed_join_kernel adds those of an id in tile order.
+// ---------------------------------------------------------------------------
+constexpr int ES_THREADS = 256, ES_COLS = ES_THREADS * 8, ES_AHEAD = 4;
+
+struct SumArgs {
+  const uint32_t *keys, *order;
+  int64_t M, H, V;
+  int tile;                 // positions per tile
+  const uint16_t *grad_out; // [M, H]
+  float scale;
+  int accumulate;
+  uint16_t *grad_W;         // [V, H]
+  float *part;              // [tiles][2][H]
+};
+
+template <bool F16>
+__device__ __forceinline__ void write_row(const SumArgs &a, int64_t v, int64_t c, const float (&s)[8]) {
+  u32x4 *const dst = reinterpret_cast<u32x4 *>(a.grad_W + v * a.H + c);
+  u32x4 o = u32x4{0, 0, 0, 0};
+  if (a.accumulate) o = *dst;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float lo = __fmul_rn(a.scale, s[2 * k]), hi = __fmul_rn(a.scale, s[2 * k + 1]);
+    if (a.accumulate) {
+      lo = __fadd_rn(from16<F16>(o[k] & 0xFFFFu), lo);
+      hi = __fadd_rn(from16<F16>(o[k] >> 16), hi);
+    }
+    o[k] = to16<F16>(lo) | (to16<F16>(hi) << 16);
+  }
+  *dst = o;
+}
+
+template <bool F16>
+__global__ __launch_bounds__(ES_THREADS) void embed_sum_kernel(SumArgs a) {
+  const int64_t e0 = (int64_t)blockIdx.x * a.tile;
+  const int64_t e1 = e0 + a.tile < a.M ? e0 + a.tile : a.M;
+  const int64_t c = (int64_t)blockIdx.y * ES_COLS + 8 * threadIdx.x;
+  const bool on = c < a.H;
+  const uint32_t none = (uint32_t)a.V;
+  uint32_t key = a.keys[e0];
+  if (key == none) return;  // the ids without a gradient come last
+  const bool began = e0 > 0 && a.keys[e0 - 1] == key;  // ... in an earlier tile
+  bool head = began;
+  float s[8] = {};
+  u32x4 ahead[ES_AHEAD];
+  uint32_t kahead[ES_AHEAD];
+  auto fetch = [&](int k, int64_t e) {
+    kahead[k] = e < e1 ? a.keys[e] : none;
+    if (kahead[k] != none && on)
+      ahead[k] = *reinterpret_cast<const u32x4 *>(a.grad_out + (int64_t)a.order[e] * a.H + c);
+  };
+  auto flush = [&](bool goes_on) {
+    if (!on) return;
+    if (head || goes_on) {
+      float *const p = a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.H + c;
+      *reinterpret_cast<f32x4 *>(p) = f32x4{s[0], s[1], s[2], s[3]};
+      *reinterpret_cast<f32x4 *>(p + 4) = f32x4{s[4], s[5], s[6], s[7]};
+    } else {
+      write_row<F16>(a, key, c, s);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < ES_AHEAD; ++k) fetch(k, e0 + k);
+  bool done = false;
+  for (int64_t e = e0; e < e1 && !done; e += ES_AHEAD) {
+#pragma unroll
+    for (int k = 0; k < ES_AHEAD; ++k) {
+      if (done || e + k >= e1) continue;
+      const uint32_t kk = kahead[k];  // the same in every thread
+      if (kk != key) {
+        flush(false);
+        head = false;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[q] = 0.0f;
+        key = kk;
+        if (kk == none) {
+          done = true;
+          continue;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        s[2 * q] = __fadd_rn(s[2 * q], from16<F16>(ahead[k][q] & 0xFFFFu));
+        s[2 * q + 1] = __fadd_rn(s[2 * q + 1], from16<F16>(ahead[k][q] >> 16));
+      }
+      fetch(k, e + k + ES_AHEAD);
+    }
+  }
+  if (!done) flush(e1 < a.M && a.keys[e1] == key);
+}
+
+// One work-group per tile whose last id goes on: 16 groups of 64 lanes sum 16
+// contiguous runs of the id's tiles (4 columns per lane), joined in order.
+constexpr int EJ_GROUPS = 16, EJ_COLS = 256;
+template <bool F16>
+__global__ __launch_bounds__(EJ_GROUPS * 64) void embed_join_kernel(SumArgs a, int tiles) {
+  const int t0 = blockIdx.x;
+  const int64_t last = (int64_t)(t0 + 1) * a.tile;  // first position of the next tile
+  if (last >= a.M) return;
+  const uint32_t key = a.keys[last - 1];
+  if (key == (uint32_t)a.V || a.keys[last] != key) return;
+  // began here (an id that began earlier belongs to that tile)
+  const int64_t e0 = (int64_t)t0 * a.tile;
+  if (e0 > 0 && a.keys[e0 - 1] == key) return;
+  // the id's last tile: the largest t whose first position has this key
+  int lo = t0 + 1, hi = tiles - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (a.keys[(int64_t)mid * a.tile] == key)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int n = lo - t0 + 1;  // partial sums: slot 1 of t0 (it does not begin earlier), slot 0 of the rest
+  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.y * EJ_COLS + 4 * lane;
+  const int per = (n + EJ_GROUPS - 1) / EJ_GROUPS;
+  const int k0 = g * per, k1 = k0 + per < n ? k0 + per : n;
+  f32x4 s = zero4();
+  if (c < a.H) {
+    constexpr int AH = 8;
+    for (int k = k0; k < k1; k += AH) {
+      f32x4 v[AH];
+#pragma unroll
+      for (int q = 0; q < AH; ++q) {
+        const int t = t0 + k + q;
+        v[q] = k + q < k1 ? *reinterpret_cast<const f32x4 *>(a.part + ((int64_t)t * 2 + (k + q == 0 ? 1 : 0)) * a.H + c)
+                          : zero4();
+      }
+#pragma unroll
+      for (int q = 0; q < AH; ++q)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] = __fadd_rn(s[x], v[q][x]);
+    }
+  }
+  __shared__ f32x4 sh[EJ_GROUPS][64];
+  sh[g][lane] = s;
+  __syncthreads();
+  if (g != 0 || c >= a.H) return;
+#pragma unroll
+  for (int w = 1; w < EJ_GROUPS; ++w)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s[x] = __fadd_rn(s[x], sh[w][lane][x]);
+  uint16_t *const dst = a.grad_W + (int64_t)key * a.H + c;
+  u32x2 o = u32x2{0, 0};
+  if (a.accumulate) o = *reinterpret_cast<const u32x2 *>(dst);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float x = __fmul_rn(a.scale, s[2 * k]), y = __fmul_rn(a.scale, s[2 * k + 1]);
+    if (a.accumulate) {
+      x = __fadd_rn(from16<F16>(o[k] & 0xFFFFu), x);
+      y = __fadd_rn(from16<F16>(o[k] >> 16), y);
+    }
+    o[k] = to16<F16>(x) | (to16<F16>(y) << 16);
+  }
+  *reinterpret_cast<u32x2 *>(dst) = o;
+}
+
+// Positions per tile: enough tiles to fill the chip, at most about 1024
+// (their partial sums are read back), at least 8 positions.
+int sum_tile(int64_t M) {
+  const int64_t t = ceil_div(M, 1024);
+  return (int)(t < 8 ? 8 : t);
+}
+
+struct Plan {
+  int64_t keys, order, keys2, order2, counts, part, bytes;
+};
+Plan plan(int64_t M, int64_t H) {
+  Plan p;
+  const int64_t list = align256(4 * M);
+  p.keys = 0;
+  p.order = list;
+  const bool radix = M > RANK_MAX;
+  p.keys2 = 2 * list;
+  p.order2 = p.keys2 + (radix ? list : 0);
+  p.counts = p.order2 + (radix ? list : 0);
+  p.part = p.counts + (radix ? (int64_t)RX_TILES * RX_BINS * 4 : 0);
+  p.bytes = p.part + align256(ceil_div(M, sum_tile(M)) * 2 * H * 4);
+  return p;
+}
+
+}  // namespace
+
+int64_t embed_backward_bytes(int64_t M, int64_t H) { return M > 0 ? plan(M, H).bytes : 0; }
+
+hipError_t launch_embed(const EmbedForward &c, hipStream_t s) {
+  const int64_t ppr = c.H / 8, pieces = c.M * ppr;
+  const dim3 grid((unsigned)ceil_div(pieces, EL_THREADS * EL_STEPS));
+  const uint16_t *W = static_cast<const uint16_t *>(c.W);
+  uint16_t *out = static_cast<uint16_t *>(c.out);
+  // 32-bit piece numbers where they fit (a 64-bit division per piece costs
+  // more than the piece's load)
+  if (pieces < ((int64_t)1 << 32) - EL_THREADS * EL_STEPS) {
+    auto k = c.in_f16 ? embed_kernel<true, uint32_t> : embed_kernel<false, uint32_t>;
+    return launch_kernel(k, grid, dim3(EL_THREADS), s, c.ids, c.ids64, (uint32_t)pieces, (uint32_t)ppr, W, c.V,
+                         c.scale, out);
+  }
+  auto k = c.in_f16 ? embed_kernel<true, uint64_t> : embed_kernel<false, uint64_t>;
+  return launch_kernel(k, grid, dim3(EL_THREADS), s, c.ids, c.ids64, (uint64_t)pieces, (uint64_t)ppr, W, c.V,
+                       c.scale, out);
+}
+
+hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
+  const int64_t words = c.V * c.H / 8;  // 16-byte words of grad_W
+  Fill f{static_cast<u32x4 *>(c.grad_W), 0, c.accumulate ? 0 : words, 0};
+  if (c.M == 0) {
+    if (c.accumulate) return hipSuccess;
+    return launch_kernel(embed_rank_kernel, dim3((unsigned)fill_blocks(f, RANK_THREADS)), dim3(RANK_THREADS), s,
+                         c.ids, c.ids64, 0, c.V, c.padding, static_cast<uint32_t *>(nullptr),
+                         static_cast<uint32_t *>(nullptr), f);
+  }
+  const Plan pl = plan(c.M, c.H);
+  uint8_t *const ws = static_cast<uint8_t *>(c.workspace);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(ws + pl.keys);
+  uint32_t *order = reinterpret_cast<uint32_t *>(ws + pl.order);
+  hipError_t e = hipSuccess;
+  if (c.M <= RANK_MAX) {
+    f.sort_blocks = (int)ceil_div(c.M, 64);
+    e = launch_kernel(embed_rank_kernel, dim3((unsigned)(f.sort_blocks + fill_blocks(f, RANK_THREADS))),
+                      dim3(RANK_THREADS), s, c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
+  } else {
+    RadixArgs a;
+    a.ids = c.ids;
+    a.ids64 = c.ids64;
+    a.V = c.V;
+    a.padding = c.padding;
+    a.counts = reinterpret_cast<uint32_t *>(ws + pl.counts);
+    a.M = c.M;
+    a.tile = ceil_div(c.M, RX_TILES) < RX_THREADS ? RX_THREADS : ceil_div(c.M, RX_TILES);
+    a.tiles = (int)ceil_div(c.M, a.tile);
+    int bits = 1;
+    while (((int64_t)1 << bits) <= c.V) ++bits;  // keys 0 .. V
+    const int passes = (bits + RX_BITS - 1) / RX_BITS;
+    uint32_t *ko[2] = {keys, reinterpret_cast<uint32_t *>(ws + pl.keys2)};
+    uint32_t *oo[2] = {order, reinterpret_cast<uint32_t *>(ws + pl.order2)};
+    const int64_t all = f.to;
+    for (int p = 0; p < passes && e == hipSuccess; ++p) {
+      const int to = (passes - 1 - p) & 1;  // the last pass writes (keys, order)
+      a.first = p == 0;
+      a.shift = p * RX_BITS;
+      a.keys_in = ko[1 - to];
+      a.order_in = oo[1 - to];
+      a.keys_out = ko[to];
+      a.order_out = oo[to];
+      for (int half = 0; half < 2 && e == hipSuccess; ++half) {
+        const int part = 2 * p + half;
+        f.from = all * part / (2 * passes);
+        f.to = all * (part + 1) / (2 * passes);
+        f.sort_blocks = a.tiles;
+        e = launch_kernel(half == 0 ? embed_count_kernel : embed_scatter_kernel,
+                          dim3((unsigned)(a.tiles + fill_blocks(f, RX_THREADS))), dim3(RX_THREADS), s, a, f);
+      }
+    }
+  }
+  if (e != hipSuccess) return e;
+  SumArgs a;
+  a.keys = keys;
+  a.order = order;
+  a.M = c.M;
+  a.H = c.H;
+  a.V = c.V;
+  a.tile = sum_tile(c.M);
+  a.grad_out = static_cast<const uint16_t *>(c.grad_out);
+  a.scale = c.scale;
+  a.accumulate = c.accumulate;
+  a.grad_W = static_cast<uint16_t *>(c.grad_W);
+  a.part = reinterpret_cast<float *>(ws + pl.part);
+  const int tiles = (int)ceil_div(c.M, a.tile);
+  e = launch_kernel(c.in_f16 ? embed_sum_kernel<true> : embed_sum_kernel<false>,
+                    dim3((unsigned)tiles, (unsigned)ceil_div(c.H, ES_COLS)), dim3(ES_THREADS), s, a);
+  if (e != hipSuccess || tiles < 2) return e;
+  return launch_kernel(c.in_f16 ? embed_join_kernel<true> : embed_join_kernel<false>,
+                       dim3((unsigned)(tiles - 1), (unsigned)ceil_div(c.H, EJ_COLS)), dim3(EJ_GROUPS * 64), s, a,
+                       tiles);
+}
+
+}  // namespace lmhead

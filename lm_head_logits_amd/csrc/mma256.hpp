@@ -27,27 +27,33 @@
 // half-tiles A0, A1, B0, B1 of 128 rows (16 KB), two LDS stages (128 KB).
 // Wave (wm, wn) of 2 x 4 owns rows wm 64 .. + 63 of both A halves and rows
 // wn 32 .. + 31 of both B halves: four quadrants of 64 x 32. A stage is
-// worked off in four phases of 16 MFMAs each:
-//   phase  reads into registers    MFMA      direct-to-LDS load issued
-//   0      A0(t)                   A0 B0     B0(t + 2)
-//   1      B1(t)                   A0 B1     A0(t + 2)
-//   2      A1(t)                   A1 B1     B1(t + 2)
-//   3      B0(t + 1)               A1 B0     A1(t + 2)
-// Each load refills the LDS region that the phase before has read. A phase is
+// worked off in two phases of 32 MFMAs:
+//   phase  reads into registers   MFMA            direct-to-LDS loads issued
+//   X      A0(t), B1(t)           A0 B0, A0 B1    A1(t + 1), B0(t + 2)
+//   Y      A1(t), B0(t + 1)       A1 B1, A1 B0    A0(t + 2), B1(t + 2)
+// Each load refills an LDS region that the phase before has read. A phase is
 // a read part, ended by waits and a barrier, and an MFMA part, ended by a
 // barrier; waves 4-7 run one barrier behind waves 0-3, so while one of a
 // SIMD's two waves reads and loads, the other feeds the matrix pipe.
 //
-// Why the waits suffice. (1) A region is refilled in the read part of phase
-// p + 1, after every wave's reads in phase p returned: each wave waits for its
-// own LDS reads (lgkmcnt 0) before the barrier that ends its read part, and
-// the later group's read part of phase p ends with the barrier that starts
-// the earlier group's read part of phase p + 1. (2) What phase p + 1 reads has
+// Why the waits suffice. (1) A region is refilled in the read part of the
+// phase after the one that read it, when every wave's reads have returned:
+// each wave waits for its own LDS reads (lgkmcnt 0) before the barrier that
+// ends its read part, and the later group's read part ends with the barrier
+// that starts the earlier group's next one. (2) What the next phase reads has
 // landed: each wave retires its own share of those loads before the barrier
-// that ends its read part of phase p. Loads complete in issue order and
-// exactly six half-tiles (two loads per wave each) were issued after the one
-// in question, so vmcnt(12) retires it. Stages past the last load nothing
+// that ends its read part. Loads complete in issue order and exactly four
+// half-tiles (two loads per wave each) were issued after the ones in
+// question, so vmcnt(8) retires them. Stages past the last load nothing
 // (out-of-range offsets, which leave zeros), to keep the counts exact.
+//
+// Measured (4096 x 32768 x 4096, bf16 random data, alone): K-inner operands
+// 865 µs (1.27 PFLOP/s), B K-outer 832 µs (4096 x 4096 x 32768, 1.32), both
+// K-outer 935 µs (1.18); int8 467 µs (2.35 POP/s). Four phases of 16 MFMAs
+// took 890 µs, the waves of a SIMD in step (no barrier of offset) 969 µs.
+// Loads that all hit L2: 772 µs; no loads at all: 685 µs. So what is left is
+// the loads' latency behind L2 and the tiles' starts and ends, during which
+// a CU's one work-group leaves the matrix pipes idle.
 #pragma once
 
 #include "kstep.hpp"
@@ -245,7 +251,7 @@ __device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, co
 #pragma unroll
         for (int j = 0; j < 2; ++j) tile.c[x][y][i][j] = typename MmAcc<ET>::type{0, 0, 0, 0};
 
-  u32x4 fa[4][2], fb[2][2][2];  // A half in use; B halves in use (set, block, K-step)
+  u32x4 fa[4][2], fb[3][2][2];  // A half in use; B halves in use (set, block, K-step)
   auto ms = [&](int64_t t) -> int64_t { return t < stages ? memstage(t) : -1; };
   auto readA = [&](const u32x4 *src) {
 #pragma unroll
@@ -275,59 +281,50 @@ __device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, co
   using std::integral_constant;
   using I0 = integral_constant<int, 0>;
   using I1 = integral_constant<int, 1>;
-  // ends a read part: what the next phase reads has landed, this wave's own
-  // reads have returned
   auto end_read = [&]() {
-    wait_vm<12>();
+    wait_vm<8>();
     wait_lds();
     mm_barrier();
   };
-  // stage t in LDS stage S; B0(t) is in register set S
+  using I2 = integral_constant<int, 2>;
   auto stage = [&](auto sc, int64_t t) {
     constexpr int S = decltype(sc)::value;
-    using SETA = integral_constant<int, S>;
-    using SETB = integral_constant<int, 1 - S>;
-    const int64_t m2 = ms(t + 2);
+    using SET = integral_constant<int, S>;
+    using SETN = integral_constant<int, 1 - S>;
     readA(buf.a(S, 0));
-    sb.load(0, m2, buf.b(S, 0));
+    readB(I2{}, buf.b(S, 1));
+    sa.load(1, ms(t + 1), buf.a(1 - S, 1));
+    sb.load(0, ms(t + 2), buf.b(S, 0));
     end_read();
-    mfma(I0{}, I0{}, SETA{});
+    mfma(I0{}, I0{}, SET{});
+    mfma(I0{}, I1{}, I2{});
     mm_barrier();
-
-    readB(SETB{}, buf.b(S, 1));
-    sa.load(0, m2, buf.a(S, 0));
-    end_read();
-    mfma(I0{}, I1{}, SETB{});
-    mm_barrier();
-
     readA(buf.a(S, 1));
+    readB(SETN{}, buf.b(1 - S, 0));
+    const int64_t m2 = ms(t + 2);
+    sa.load(0, m2, buf.a(S, 0));
     sb.load(1, m2, buf.b(S, 1));
     end_read();
-    mfma(I1{}, I1{}, SETB{});
-    mm_barrier();
-
-    readB(SETB{}, buf.b(1 - S, 0));
-    sa.load(1, m2, buf.a(S, 1));
-    end_read();
-    mfma(I1{}, I0{}, SETA{});
+    mfma(I1{}, I1{}, I2{});
+    mfma(I1{}, I0{}, SET{});
     mm_barrier();
   };
-
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int64_t m = ms(s);
-    sb.load(0, m, buf.b(s, 0));
-    sa.load(0, m, buf.a(s, 0));
-    sb.load(1, m, buf.b(s, 1));
-    sa.load(1, m, buf.a(s, 1));
+  {
+    const int64_t m = ms(0), n = ms(1);
+    sb.load(0, m, buf.b(0, 0));
+    sa.load(0, m, buf.a(0, 0));
+    sb.load(1, m, buf.b(0, 1));
+    sa.load(1, m, buf.a(0, 1));
+    sb.load(0, n, buf.b(1, 0));
+    sa.load(0, n, buf.a(1, 0));
+    sb.load(1, n, buf.b(1, 1));
   }
-  wait_vm<12>();  // B0(0), A0(0)
+  wait_vm<8>();
   mm_barrier();
   readB(I0{}, buf.b(0, 0));
   wait_lds();
   mm_barrier();
-  if (wave >= 4) mm_barrier();  // the second group runs one barrier behind
-  // an odd stage count ends with a stage of zeros
+  if (wave >= 4) mm_barrier();
   for (int64_t t = 0; t < stages; t += 2) {
     stage(I0{}, t);
     stage(I1{}, t + 1);
@@ -338,12 +335,67 @@ __device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, co
   mm_barrier();
 }
 
-// The tile of this work-group: XCD-aware, row tiles fastest (work-groups go
-// to the XCDs round-robin; consecutive tiles run on one XCD and share its L2).
-__device__ __forceinline__ int64_t mm_tile_index(int64_t ntiles) {
-  const int64_t b = blockIdx.x, q = ntiles / 8, r = ntiles % 8;
+// Position of a work-group among `n`: work-groups go to the eight XCDs
+// round-robin, so that consecutive positions run on one XCD and share its L2.
+__device__ __forceinline__ int64_t mm_position(int64_t n) {
+  const int64_t b = blockIdx.x, q = n / 8, r = n % 8;
   const int64_t xcd = b % 8, pos = b / 8;
   return xcd < r ? xcd * (q + 1) + pos : r * (q + 1) + (xcd - r) * q + pos;
+}
+
+// Tile (a, b) of position t among na x nb: panels of four tiles of A, walked
+// along B, so that the 32 work-groups of an XCD read 4 + 8 distinct operand
+// tiles and not 32 + 1 (4096 x 32768 x 4096: 935 -> 891 µs against one panel
+// of all of A; panels of 8: 906 µs).
+__device__ __forceinline__ void mm_tile_at(int64_t t, int64_t na, int64_t nb, int64_t &a, int64_t &b) {
+  constexpr int64_t PANEL = 4;
+  const int64_t g = t / (PANEL * nb), h = na - g * PANEL < PANEL ? na - g * PANEL : PANEL;
+  const int64_t r = t - g * PANEL * nb;
+  a = g * PANEL + r % h;
+  b = r / h;
+}
+
+// The LDS rows (512 bytes) of a 256 x 256 tile of 16-bit values: row r in
+// stage array r / 32, its 32-byte pieces xor-ed with r so that the 16 rows one
+// store touches fall in distinct banks.
+__device__ __forceinline__ uint8_t *mm_tile_row(const MmBufs &buf, int hi, int r) {
+  return reinterpret_cast<uint8_t *>(buf.at(hi)) + (r & 31) * 512;
+}
+
+template <int ET>
+__device__ __forceinline__ uint32_t mm_pack2(float a, float b) {
+  if constexpr (ET == ET_F16)
+    return (uint32_t)out_bits16<_Float16>(a) | ((uint32_t)out_bits16<_Float16>(b) << 16);
+  else
+    return (uint32_t)bf16_rne(a) | ((uint32_t)bf16_rne(b) << 16);
+}
+
+// Four columns of one row of the tile, as 16-bit values, into LDS.
+template <int ET>
+__device__ __forceinline__ void mm_stage4(const MmBufs &buf, int wm, int wn, int li, int lg,
+                                       int x, int y, int i, int j, f32x4 v) {
+  const int r = MmTile<ET>::row(wm, li, x, i);
+  uint8_t *row = wm == 0 ? mm_tile_row(buf, x * 4 + (i >> 1), r) : mm_tile_row(buf, x * 4 + 2 + (i >> 1), r);
+  const int piece = (y * 128 + wn * 32 + 16 * j) / 16;
+  *reinterpret_cast<u32x2 *>(row + ((piece ^ (r & 15)) * 32) + 8 * lg) =
+      u32x2{mm_pack2<ET>(v[0], v[1]), mm_pack2<ET>(v[2], v[3])};
+}
+
+// The staged tile to rows of `ld` bytes at `out`, `rows` rows of `bytes`
+// bytes (a multiple of 16) present.
+template <int POLICY>
+__device__ __forceinline__ void mm_store_tile16(const MmBufs &buf, uint8_t *out, int64_t ld,
+                                             int64_t rows, int64_t bytes) {
+  const rsrc_t rs = make_rsrc(out, (uint32_t)((rows - 1) * ld + (bytes < 512 ? bytes : 512)));
+  const int c = threadIdx.x % 32, r0 = threadIdx.x / 32;
+#pragma unroll
+  for (int it = 0; it < 16; ++it) {
+    const int r = it * 16 + r0;
+    const uint8_t *row = mm_tile_row(buf, it >> 1, r);
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + (((c >> 1) ^ (r & 15)) * 32) + 16 * (c & 1));
+    const bool ok = r < rows && 16 * c < bytes;
+    __builtin_amdgcn_raw_buffer_store_b128(v, rs, ok ? (uint32_t)(r * ld + 16 * c) : OFF_NONE, 0, POLICY);
+  }
 }
 
 }  // namespace lmhead

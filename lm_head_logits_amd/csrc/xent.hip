@@ -75,8 +75,9 @@ template <int ET>
 __global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p) {
   MM_SHARED();
   const int64_t nmt = (p.M + MM_T - 1) / MM_T, nvt = (p.V + MM_T - 1) / MM_T;
-  const int64_t t = mm_tile_index(nmt * nvt);
-  const int64_t m0 = (t % nmt) * MM_T, vt = t / nmt, n0 = vt * MM_T;
+  int64_t mt, vt;
+  mm_tile_at(mm_position(nmt * nvt), nmt, nvt, mt, vt);
+  const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
   MmTile<ET> tile;
   logits_tile<ET>(tile, p.hidden, p.W, p.M, p.H, p.V, m0, n0, mm_buf);
 
@@ -264,56 +265,14 @@ struct XentBwdArgs {
   uint16_t *dw;        // [V, H]
 };
 
-// The LDS rows (512 bytes) of a 256 x 256 tile of 16-bit values: row r in
-// stage array r / 32, its 32-byte pieces xor-ed with r so that the 16 rows one
-// store touches fall in distinct banks.
-__device__ __forceinline__ uint8_t *tile_row(const MmBufs &buf, int hi, int r) {
-  return reinterpret_cast<uint8_t *>(buf.at(hi)) + (r & 31) * 512;
-}
-
-template <int ET>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (ET == ET_F16)
-    return (uint32_t)out_bits16<_Float16>(a) | ((uint32_t)out_bits16<_Float16>(b) << 16);
-  else
-    return (uint32_t)bf16_rne(a) | ((uint32_t)bf16_rne(b) << 16);
-}
-
-// Four columns of one row of the tile, as 16-bit values, into LDS.
-template <int ET>
-__device__ __forceinline__ void stage4(const MmBufs &buf, int wm, int wn, int li, int lg,
-                                       int x, int y, int i, int j, f32x4 v) {
-  const int r = MmTile<ET>::row(wm, li, x, i);
-  uint8_t *row = wm == 0 ? tile_row(buf, x * 4 + (i >> 1), r) : tile_row(buf, x * 4 + 2 + (i >> 1), r);
-  const int piece = (y * 128 + wn * 32 + 16 * j) / 16;
-  *reinterpret_cast<u32x2 *>(row + ((piece ^ (r & 15)) * 32) + 8 * lg) =
-      u32x2{pack2<ET>(v[0], v[1]), pack2<ET>(v[2], v[3])};
-}
-
-// The staged tile to rows of `ld` bytes at `out`, `rows` rows of `bytes`
-// bytes (a multiple of 16) present.
-template <int POLICY>
-__device__ __forceinline__ void store_tile16(const MmBufs &buf, uint8_t *out, int64_t ld,
-                                             int64_t rows, int64_t bytes) {
-  const rsrc_t rs = make_rsrc(out, (uint32_t)((rows - 1) * ld + (bytes < 512 ? bytes : 512)));
-  const int c = threadIdx.x % 32, r0 = threadIdx.x / 32;
-#pragma unroll
-  for (int it = 0; it < 16; ++it) {
-    const int r = it * 16 + r0;
-    const uint8_t *row = tile_row(buf, it >> 1, r);
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + (((c >> 1) ^ (r & 15)) * 32) + 16 * (c & 1));
-    const bool ok = r < rows && 16 * c < bytes;
-    __builtin_amdgcn_raw_buffer_store_b128(v, rs, ok ? (uint32_t)(r * ld + 16 * c) : OFF_NONE, 0, POLICY);
-  }
-}
-
 // G of one piece.
 template <int ET>
 __global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p) {
   MM_SHARED();
   const int64_t nmt = (p.M + MM_T - 1) / MM_T;
-  const int64_t t = mm_tile_index(nmt * (p.vp / MM_T));
-  const int64_t m0 = (t % nmt) * MM_T, g0 = (t / nmt) * MM_T, n0 = p.v0 + g0;
+  int64_t mt, gt;
+  mm_tile_at(mm_position(nmt * (p.vp / MM_T)), nmt, p.vp / MM_T, mt, gt);
+  const int64_t m0 = mt * MM_T, g0 = gt * MM_T, n0 = p.v0 + g0;
   MmTile<ET> tile;
   if (n0 < p.V) {
     logits_tile<ET>(tile, p.hidden, p.W, p.M, p.H, p.V, m0, n0, mm_buf);
@@ -366,12 +325,12 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p)
             v[q] = gv;
             colsum[y][j][q] = __fadd_rn(colsum[y][j][q], gv);
           }
-          stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
+          mm_stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
         }
     }
   __syncthreads();
   const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
-  store_tile16<LOAD_DEFAULT>(mm_buf, p.G + (m0 * p.vp + g0) * 2, p.vp * 2, rows, 512);
+  mm_store_tile16<LOAD_DEFAULT>(mm_buf, p.G + (m0 * p.vp + g0) * 2, p.vp * 2, rows, 512);
   if (p.colpart == nullptr) return;
   __syncthreads();
   // column sums: 16 rows of a block by lane exchanges, then the two wave rows
@@ -413,8 +372,10 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_dhidden_kernel(XentBwdArgs
   MM_SHARED();
   const int64_t nmt = (p.M + MM_T - 1) / MM_T, nht = (p.H + MM_T - 1) / MM_T;
   const int64_t splits = (p.vp + p.ksplit - 1) / p.ksplit;
-  const int64_t t = mm_tile_index(nmt * nht * splits);
-  const int64_t m0 = (t % nmt) * MM_T, h0 = (t / nmt % nht) * MM_T, sp = t / (nmt * nht);
+  const int64_t t = mm_position(nmt * nht * splits), sp = t / (nmt * nht);
+  int64_t mt, ht;
+  mm_tile_at(t - sp * nmt * nht, nmt, nht, mt, ht);
+  const int64_t m0 = mt * MM_T, h0 = ht * MM_T;
   const int64_t k0 = sp * p.ksplit, kn = p.vp - k0 < p.ksplit ? p.vp - k0 : p.ksplit;
   const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
   const int64_t rb = p.H * 2;
@@ -474,8 +435,8 @@ __global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__re
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int q = 0; q < 4; ++q) s[h][q] = __fmul_rn(f, s[h][q]);
-  *reinterpret_cast<u32x4 *>(out + e) = u32x4{pack2<ET>(s[0][0], s[0][1]), pack2<ET>(s[0][2], s[0][3]),
-                                              pack2<ET>(s[1][0], s[1][1]), pack2<ET>(s[1][2], s[1][3])};
+  *reinterpret_cast<u32x4 *>(out + e) = u32x4{mm_pack2<ET>(s[0][0], s[0][1]), mm_pack2<ET>(s[0][2], s[0][3]),
+                                              mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
 }
 
 // G^T hidden of one piece: its rows of grad_W.
@@ -484,8 +445,10 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_dweight_kernel(XentBwdArgs
   MM_SHARED();
   const int64_t nht = (p.H + MM_T - 1) / MM_T;
   const int64_t nv = p.V - p.v0 < p.vp ? p.V - p.v0 : p.vp;
-  const int64_t t = mm_tile_index(nht * ((nv + MM_T - 1) / MM_T));
-  const int64_t h0 = (t % nht) * MM_T, g0 = (t / nht) * MM_T;
+  const int64_t ngt = (nv + MM_T - 1) / MM_T;
+  int64_t gt, ht;
+  mm_tile_at(mm_position(nht * ngt), ngt, nht, gt, ht);
+  const int64_t h0 = ht * MM_T, g0 = gt * MM_T;
   const MmOperand a{p.G + g0 * 2, p.vp * 2, p.M, (p.vp - g0) * 2, 0};
   const MmOperand b{p.hidden + h0 * 2, p.H * 2, p.M, (p.H - h0) * 2, 0};
   MmTile<ET> tile;
@@ -505,11 +468,11 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_dweight_kernel(XentBwdArgs
           f32x4 v = tile.c[x][y][i][j];
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = __fmul_rn(f, v[q]);
-          stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
+          mm_stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
         }
   __syncthreads();
   const int64_t rows = nv - g0 < MM_T ? nv - g0 : MM_T;
-  store_tile16<STORE_POLICY>(mm_buf, reinterpret_cast<uint8_t *>(p.dw + (p.v0 + g0) * p.H + h0), p.H * 2,
+  mm_store_tile16<STORE_POLICY>(mm_buf, reinterpret_cast<uint8_t *>(p.dw + (p.v0 + g0) * p.H + h0), p.H * 2,
                              rows, (p.H - h0) * 2);
 }
 
