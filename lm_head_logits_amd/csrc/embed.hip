@@ -269,7 +269,7 @@ __global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, 
 // (slot 0) or goes on in the next (slot 1) go to the workspace, and
 // embed_join_kernel adds those of an id in tile order.
 // ---------------------------------------------------------------------------
-constexpr int ES_THREADS = 256, ES_COLS = ES_THREADS * 8, ES_AHEAD = 4;
+constexpr int ES_THREADS = 256, ES_COLS = ES_THREADS * 8, ES_AHEAD = 8, ES_LIST = 256;
 
 struct SumArgs {
   const uint32_t *keys, *order;
@@ -301,76 +301,73 @@ __device__ __forceinline__ void write_row(const SumArgs &a, int64_t v, int64_t c
 
 template <bool F16>
 __global__ __launch_bounds__(ES_THREADS) void embed_sum_kernel(SumArgs a) {
-  const int64_t e0 = (int64_t)blockIdx.x * a.tile;
-  const int64_t e1 = e0 + a.tile < a.M ? e0 + a.tile : a.M;
+  // the tile's keys and positions, one load each for all of them, with the
+  // keys before the first and after the last (ES_LIST positions at a time)
+  __shared__ uint32_t sk[ES_LIST + 2], so[ES_LIST];
+  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
+  const int64_t t1 = t0 + a.tile < a.M ? t0 + a.tile : a.M;
   const int64_t c = (int64_t)blockIdx.y * ES_COLS + 8 * threadIdx.x;
   const bool on = c < a.H;
   const uint32_t none = (uint32_t)a.V;
-  uint32_t key = a.keys[e0];
-  if (key == none) return;  // the ids without a gradient come last
-  const bool began = e0 > 0 && a.keys[e0 - 1] == key;  // ... in an earlier tile
-  bool head = began;
   float s[8] = {};
-  u32x4 ahead[ES_AHEAD];
-  uint32_t kahead[ES_AHEAD];
-  auto fetch = [&](int k, int64_t e) {
-    kahead[k] = e < e1 ? a.keys[e] : none;
-    if (kahead[k] != none && on)
-      ahead[k] = *reinterpret_cast<const u32x4 *>(a.grad_out + (int64_t)a.order[e] * a.H + c);
-  };
-  auto flush = [&](bool goes_on) {
-    if (!on) return;
-    if (head || goes_on) {
-      float *const p = a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.H + c;
-      *reinterpret_cast<f32x4 *>(p) = f32x4{s[0], s[1], s[2], s[3]};
-      *reinterpret_cast<f32x4 *>(p + 4) = f32x4{s[4], s[5], s[6], s[7]};
-    } else {
-      write_row<F16>(a, key, c, s);
+  bool head = false;
+  for (int64_t e0 = t0; e0 < t1; e0 += ES_LIST) {
+    const int n = (int)(t1 - e0 < ES_LIST ? t1 - e0 : ES_LIST);
+    __syncthreads();
+    for (int i = threadIdx.x; i < n + 2; i += ES_THREADS) {
+      const int64_t e = e0 + i - 1;
+      sk[i] = e >= 0 && e < a.M ? a.keys[e] : none + 1;
+      if (i >= 1 && i <= n) so[i - 1] = a.order[e];
     }
-  };
+    __syncthreads();
+    if (e0 == t0) head = sk[0] == sk[1];  // the first id began in an earlier tile
+    if (sk[1] == none) return;            // the ids without a gradient come last
+    for (int i0 = 0; i0 < n; i0 += ES_AHEAD) {
+      u32x4 v[ES_AHEAD];
 #pragma unroll
-  for (int k = 0; k < ES_AHEAD; ++k) fetch(k, e0 + k);
-  bool done = false;
-  for (int64_t e = e0; e < e1 && !done; e += ES_AHEAD) {
+      for (int k = 0; k < ES_AHEAD; ++k)
+        if (i0 + k < n && sk[i0 + k + 1] < none && on)
+          v[k] = *reinterpret_cast<const u32x4 *>(a.grad_out + (int64_t)so[i0 + k] * a.H + c);
 #pragma unroll
-    for (int k = 0; k < ES_AHEAD; ++k) {
-      if (done || e + k >= e1) continue;
-      const uint32_t kk = kahead[k];  // the same in every thread
-      if (kk != key) {
-        flush(false);
+      for (int k = 0; k < ES_AHEAD; ++k) {
+        const int i = i0 + k;
+        if (i >= n || sk[i + 1] == none) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          s[2 * q] = __fadd_rn(s[2 * q], from16<F16>(v[k][q] & 0xFFFFu));
+          s[2 * q + 1] = __fadd_rn(s[2 * q + 1], from16<F16>(v[k][q] >> 16));
+        }
+        const bool ends = sk[i + 2] != sk[i + 1];
+        if (!ends && e0 + i + 1 < t1) continue;
+        if (on) {  // the id's last position, or the tile's
+          if (head || !ends) {
+            float *const p = a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.H + c;
+            *reinterpret_cast<f32x4 *>(p) = f32x4{s[0], s[1], s[2], s[3]};
+            *reinterpret_cast<f32x4 *>(p + 4) = f32x4{s[4], s[5], s[6], s[7]};
+          } else {
+            write_row<F16>(a, sk[i + 1], c, s);
+          }
+        }
         head = false;
 #pragma unroll
         for (int q = 0; q < 8; ++q) s[q] = 0.0f;
-        key = kk;
-        if (kk == none) {
-          done = true;
-          continue;
-        }
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        s[2 * q] = __fadd_rn(s[2 * q], from16<F16>(ahead[k][q] & 0xFFFFu));
-        s[2 * q + 1] = __fadd_rn(s[2 * q + 1], from16<F16>(ahead[k][q] >> 16));
-      }
-      fetch(k, e + k + ES_AHEAD);
     }
   }
-  if (!done) flush(e1 < a.M && a.keys[e1] == key);
 }
 
-// One work-group per tile whose last id goes on: 16 groups of 64 lanes sum 16
-// contiguous runs of the id's tiles (4 columns per lane), joined in order.
-constexpr int EJ_GROUPS = 16, EJ_COLS = 256;
+// One work-group per tile in which an id begins that goes on: EJ_GROUPS groups
+// of 256 lanes sum contiguous runs of the id's tiles (4 columns per lane),
+// joined in order. Most tiles have none, so what a work-group costs that
+// finds nothing to do counts: three loads in flight together.
+constexpr int EJ_GROUPS = 4, EJ_LANES = 256, EJ_COLS = 4 * EJ_LANES;
 template <bool F16>
-__global__ __launch_bounds__(EJ_GROUPS * 64) void embed_join_kernel(SumArgs a, int tiles) {
+__global__ __launch_bounds__(EJ_GROUPS * EJ_LANES) void embed_join_kernel(SumArgs a, int tiles) {
   const int t0 = blockIdx.x;
-  const int64_t last = (int64_t)(t0 + 1) * a.tile;  // first position of the next tile
-  if (last >= a.M) return;
-  const uint32_t key = a.keys[last - 1];
-  if (key == (uint32_t)a.V || a.keys[last] != key) return;
-  // began here (an id that began earlier belongs to that tile)
-  const int64_t e0 = (int64_t)t0 * a.tile;
-  if (e0 > 0 && a.keys[e0 - 1] == key) return;
+  const int64_t e0 = (int64_t)t0 * a.tile, last = e0 + a.tile;  // last: the next tile's first position (< M)
+  const uint32_t key = a.keys[last - 1], next = a.keys[last], prev = a.keys[e0 > 0 ? e0 - 1 : 0];
+  // an id that began in an earlier tile belongs to that one
+  if (key == (uint32_t)a.V || next != key || (e0 > 0 && prev == key)) return;
   // the id's last tile: the largest t whose first position has this key
   int lo = t0 + 1, hi = tiles - 1;
   while (lo < hi) {
@@ -381,7 +378,7 @@ __global__ __launch_bounds__(EJ_GROUPS * 64) void embed_join_kernel(SumArgs a, i
       hi = mid - 1;
   }
   const int n = lo - t0 + 1;  // partial sums: slot 1 of t0 (it does not begin earlier), slot 0 of the rest
-  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int lane = threadIdx.x % EJ_LANES, g = threadIdx.x / EJ_LANES;
   const int64_t c = (int64_t)blockIdx.y * EJ_COLS + 4 * lane;
   const int per = (n + EJ_GROUPS - 1) / EJ_GROUPS;
   const int k0 = g * per, k1 = k0 + per < n ? k0 + per : n;
@@ -402,7 +399,7 @@ __global__ __launch_bounds__(EJ_GROUPS * 64) void embed_join_kernel(SumArgs a, i
         for (int x = 0; x < 4; ++x) s[x] = __fadd_rn(s[x], v[q][x]);
     }
   }
-  __shared__ f32x4 sh[EJ_GROUPS][64];
+  __shared__ f32x4 sh[EJ_GROUPS][EJ_LANES];
   sh[g][lane] = s;
   __syncthreads();
   if (g != 0 || c >= a.H) return;
@@ -540,7 +537,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
                     dim3((unsigned)tiles, (unsigned)ceil_div(c.H, ES_COLS)), dim3(ES_THREADS), s, a);
   if (e != hipSuccess || tiles < 2) return e;
   return launch_kernel(c.in_f16 ? embed_join_kernel<true> : embed_join_kernel<false>,
-                       dim3((unsigned)(tiles - 1), (unsigned)ceil_div(c.H, EJ_COLS)), dim3(EJ_GROUPS * 64), s, a,
+                       dim3((unsigned)(tiles - 1), (unsigned)ceil_div(c.H, EJ_COLS)), dim3(EJ_GROUPS * EJ_LANES), s, a,
                        tiles);
 }
 

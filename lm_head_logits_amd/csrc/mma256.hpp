@@ -251,6 +251,11 @@ __device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, co
 #pragma unroll
         for (int j = 0; j < 2; ++j) tile.c[x][y][i][j] = typename MmAcc<ET>::type{0, 0, 0, 0};
 
+  // a tile of at most 128 rows of A leaves the second half out: half the
+  // matrix work (uniform; its loads are out of range, the counts stay). Only
+  // with both operands K-inner: with B K-outer the branch makes the compiler
+  // spill.
+  const bool tall = AOUT || BOUT || a.rows > 128;
   u32x4 fa[4][2], fb[3][2][2];  // A half in use; B halves in use (set, block, K-step)
   auto ms = [&](int64_t t) -> int64_t { return t < stages ? memstage(t) : -1; };
   auto readA = [&](const u32x4 *src) {
@@ -299,14 +304,16 @@ __device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, co
     mfma(I0{}, I0{}, SET{});
     mfma(I0{}, I1{}, I2{});
     mm_barrier();
-    readA(buf.a(S, 1));
+    if (tall) readA(buf.a(S, 1));
     readB(SETN{}, buf.b(1 - S, 0));
     const int64_t m2 = ms(t + 2);
     sa.load(0, m2, buf.a(S, 0));
     sb.load(1, m2, buf.b(S, 1));
     end_read();
-    mfma(I1{}, I1{}, I2{});
-    mfma(I1{}, I0{}, SET{});
+    if (tall) {
+      mfma(I1{}, I1{}, I2{});
+      mfma(I1{}, I0{}, SET{});
+    }
     mm_barrier();
   };
   {
@@ -362,12 +369,16 @@ __device__ __forceinline__ uint8_t *mm_tile_row(const MmBufs &buf, int hi, int r
   return reinterpret_cast<uint8_t *>(buf.at(hi)) + (r & 31) * 512;
 }
 
+// Two fp32 values to the 16-bit type, nearest even, low half first.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 template <int ET>
 __device__ __forceinline__ uint32_t mm_pack2(float a, float b) {
   if constexpr (ET == ET_F16)
-    return (uint32_t)out_bits16<_Float16>(a) | ((uint32_t)out_bits16<_Float16>(b) << 16);
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
   else
-    return (uint32_t)bf16_rne(a) | ((uint32_t)bf16_rne(b) << 16);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
 // Four columns of one row of the tile, as 16-bit values, into LDS.

@@ -23,11 +23,9 @@
 // weight's bytes bind.
 //
 // Roundings: t, the statistics, p and grad_bias are fp32. G is rounded to the
-// inputs' 16-bit type, which the matrix pipes take: a relative 2^-9 (bf16) or
-// 2^-12 (fp16) per term of sums of M or V terms, below the rounding of the
-// 16-bit gradients. fp16 G is scaled by a power of two that takes the largest
-// row's coefficient to 2^14, so that probabilities down to 2^-29 of it stay
-// normal numbers; bf16 needs no scale.
+// inputs' 16-bit type, which the matrix pipes take: at most 2^-8 (bf16) or
+// 2^-11 (fp16) of each term of sums of M or V terms, the size of the 16-bit
+// gradients' own rounding. It is kept scaled (xent_rows_kernel).
 #include "mma256.hpp"
 
 namespace lmhead {
@@ -205,48 +203,65 @@ struct alignas(16) RowCoef {
   int32_t y;  // target column, or -1
 };
 
-// The power of two that takes the largest row coefficient to 2^14 (fp16), and
-// its inverse: one work-group, an exact maximum.
-__global__ __launch_bounds__(1024) void xent_scale_kernel(const float *__restrict__ g,
-                                                          const float *__restrict__ l,
-                                                          const void *target, int target64,
-                                                          int64_t ignore, int64_t M, int64_t V,
-                                                          float *__restrict__ scale) {
-  float mx = 0.0f;
-  for (int64_t m = threadIdx.x; m < M; m += 1024) {
-    const float b = target_of(target, target64, m, ignore, V) >= 0 ? g[m] : 0.0f;
-    const float a = l != nullptr ? __fadd_rn(b, l[m]) : b;
-    mx = fmaxf(mx, fmaxf(fabsf(a), fabsf(b)));
+// G is kept scaled by f = top / mx, mx the largest |a| or |b| of the rows and
+// `top` a power of two, so that a row of that size has its largest entry, -b
+// (1 - p) at the target, just below a power of two, where the 16-bit
+// type's rounding is relatively finest: a batch's rows mostly share one size
+// (the mean's 1 / n), and this halves the worst error of the entries that
+// weigh most. top is 2^14 for fp16 (entries down to 2^-28 mx stay normal
+// numbers; |G| <= 2 top) and 1 for bf16. scale[0] = f, scale[1] = 1 / f.
+//
+// One launch: every work-group finds the maximum over all rows by itself and
+// writes its 256 rows' coefficients; M^2 / 256 reads of L2, negligible up to
+// XR_ONE rows. With more rows one work-group finds the scale in a launch of
+// its own (have_scale).
+constexpr int XR_THREADS = 256;
+constexpr int64_t XR_ONE = 32768;
+struct XentRowsArgs {
+  const float *g, *l, *lse;  // l may be nullptr
+  const void *target;
+  int target64;
+  int64_t ignore, M, V;
+  float top;
+  float *scale;
+  RowCoef *rows;
+  int have_scale, write_rows;
+};
+__global__ __launch_bounds__(XR_THREADS) void xent_rows_kernel(XentRowsArgs p) {
+  auto coef = [&](int64_t m, float &a, float &b) -> int64_t {
+    const int64_t y = target_of(p.target, p.target64, m, p.ignore, p.V);
+    b = y >= 0 ? p.g[m] : 0.0f;
+    a = p.l != nullptr ? __fadd_rn(b, p.l[m]) : b;
+    return y;
+  };
+  float f = 1.0f;
+  if (p.have_scale) {
+    f = p.scale[0];
+  } else {
+    __shared__ float sh[XR_THREADS / 64];
+    float mx = 0.0f;
+    for (int64_t m = threadIdx.x; m < p.M; m += XR_THREADS) {
+      float a, b;
+      coef(m, a, b);
+      mx = fmaxf(mx, fmaxf(fabsf(a), fabsf(b)));
+    }
+    for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < XR_THREADS / 64; ++w) mx = fmaxf(mx, sh[w]);
+    // f and 1 / f both well inside the normal range, else no scale
+    if (mx > 1e-30f && mx < 1e30f) f = __fdiv_rn(p.top, mx);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.scale[0] = f;
+      p.scale[1] = __fdiv_rn(1.0f, f);
+    }
   }
-  __shared__ float sh[16];
-  for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < 16; ++w) mx = fmaxf(mx, sh[w]);
-    // mx <= 2^e; outside the range of useful scales (zero, infinities): 1
-    const int e = (int)((__builtin_bit_cast(uint32_t, mx) >> 23) & 255) - 126;
-    const int k = 14 - e;
-    const bool ok = mx > 0.0f && mx < __builtin_inff() && k > -120 && k < 120;
-    scale[0] = ok ? __builtin_bit_cast(float, (uint32_t)(127 + k) << 23) : 1.0f;
-    scale[1] = ok ? __builtin_bit_cast(float, (uint32_t)(127 - k) << 23) : 1.0f;
-  }
-}
-
-__global__ __launch_bounds__(256) void xent_rows_kernel(const float *__restrict__ g,
-                                                        const float *__restrict__ l,
-                                                        const float *__restrict__ lse,
-                                                        const void *target, int target64,
-                                                        int64_t ignore, int64_t M, int64_t V,
-                                                        const float *__restrict__ scale,
-                                                        RowCoef *__restrict__ rows) {
-  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (m >= M) return;
-  const int64_t y = target_of(target, target64, m, ignore, V);
-  const float s = scale != nullptr ? scale[0] : 1.0f;
-  const float b = y >= 0 ? g[m] : 0.0f;
-  const float a = l != nullptr ? __fadd_rn(b, l[m]) : b;
-  rows[m] = RowCoef{__fmul_rn(a, s), __fmul_rn(b, s), lse[m], (int32_t)y};
+  const int64_t m = (int64_t)blockIdx.x * XR_THREADS + threadIdx.x;
+  if (!p.write_rows || m >= p.M) return;
+  float a, b;
+  const int64_t y = coef(m, a, b);
+  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], (int32_t)y};
 }
 
 struct XentBwdArgs {
@@ -255,7 +270,7 @@ struct XentBwdArgs {
   float alpha;
   const float *bias;
   const RowCoef *rows;
-  const float *scale;  // {s, 1 / s} (fp16), or nullptr
+  const float *scale;  // {f, 1 / f}
   int64_t v0, vp;      // this piece's first column and its columns (a multiple of 256)
   uint8_t *G;          // [M, vp], 16 bits
   float *colpart;      // [row tile][vp] column sums of G, or nullptr
@@ -350,7 +365,7 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p)
       }
   __syncthreads();
   if (threadIdx.x < MM_T) {
-    const float s = p.scale != nullptr ? p.scale[1] : 1.0f;
+    const float s = p.scale[1];
     p.colpart[(m0 / MM_T) * p.vp + g0 + threadIdx.x] =
         __fmul_rn(s, __fadd_rn(cs[threadIdx.x], cs[MM_T + threadIdx.x]));
   }
@@ -430,7 +445,7 @@ __global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__re
 #pragma unroll
       for (int q = 0; q < 4; ++q) s[h][q] = __fadd_rn(s[h][q], v[q]);
     }
-  const float f = scale != nullptr ? __fmul_rn(alpha, scale[1]) : alpha;
+  const float f = __fmul_rn(alpha, scale[1]);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -456,7 +471,7 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_dweight_kernel(XentBwdArgs
 
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  const float f = p.scale != nullptr ? __fmul_rn(p.alpha, p.scale[1]) : p.alpha;
+  const float f = __fmul_rn(p.alpha, p.scale[1]);
 #pragma unroll
   for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -541,16 +556,18 @@ hipError_t forward(const XentFwdArgs &p, float *loss, float *lse, hipStream_t s)
 template <int ET>
 hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
   const BwdPlan pl = bwd_plan(c.M, c.H, c.V, c.grad_bias != nullptr);
-  float *const scale = ET == ET_F16 ? reinterpret_cast<float *>(ws + pl.off_scale) : nullptr;
+  float *const scale = reinterpret_cast<float *>(ws + pl.off_scale);
   RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + pl.off_rows);
+  XentRowsArgs r{c.grad_loss, c.grad_lse, c.lse, c.target, c.target64, c.ignore, c.M, c.V,
+                 ET == ET_F16 ? 16384.0f : 1.0f, scale, rows, 0, 1};
   hipError_t e = hipSuccess;
-  if (scale != nullptr)
-    e = launch_kernel(xent_scale_kernel, dim3(1), dim3(1024), s, c.grad_loss, c.grad_lse, c.target,
-                      c.target64, c.ignore, c.M, c.V, scale);
+  if (c.M > XR_ONE) {
+    r.write_rows = 0;
+    e = launch_kernel(xent_rows_kernel, dim3(1), dim3(XR_THREADS), s, r);
+    r.write_rows = r.have_scale = 1;
+  }
   if (e == hipSuccess)
-    e = launch_kernel(xent_rows_kernel, dim3((unsigned)ceil_div(c.M, 256)), dim3(256), s, c.grad_loss,
-                      c.grad_lse, c.lse, c.target, c.target64, c.ignore, c.M, c.V,
-                      static_cast<const float *>(scale), rows);
+    e = launch_kernel(xent_rows_kernel, dim3((unsigned)ceil_div(c.M, XR_THREADS)), dim3(XR_THREADS), s, r);
   XentBwdArgs p;
   p.hidden = static_cast<const uint8_t *>(c.hidden);
   p.W = static_cast<const uint8_t *>(c.W);
