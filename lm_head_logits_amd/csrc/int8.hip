@@ -341,61 +341,84 @@ hipError_t stream_r(const I8Args &a, hipStream_t s) {
   return stream_split<R, NBM, OutT>(a, vsplit(ncb, a.H, 16, NBM), s);
 }
 
-// More rows: 256 x 256 tiles.
+// More rows: 256 x 256 tiles. 16-bit logits leave through LDS as whole rows in
+// 16-byte stores; rows not so aligned, and fp32 ones (whose four columns per
+// lane are 64 contiguous bytes per row already), straight from the registers.
+template <typename OutT>
+struct Int8Tiles {
+  I8Args p;
+  u32x4 *epi;
+  int64_t nmt, nvt;
+
+  __device__ __forceinline__ int64_t tiles() const { return nmt * nvt; }
+  __device__ __forceinline__ MmJob job(int32_t t) const {
+    int64_t mt, vt;
+    mm_tile_at(t, nmt, nvt, mt, vt);
+    const int64_t m0 = mt * MM_T, n0 = vt * MM_T, rows = p.M - m0, cols = p.V - n0;
+    const uint32_t rb = (uint32_t)p.H;
+    return MmJob{{p.hq + m0 * p.H, rb, (int32_t)(rows < MM_T ? rows : MM_T), rb},
+                 {p.wq + n0 * p.H, rb, (int32_t)(cols < MM_T ? cols : MM_T), rb},
+                 (int32_t)((p.H + MM_STAGE_BYTES - 1) / MM_STAGE_BYTES), 0};
+  }
+  __device__ __forceinline__ void epilogue(MmTile<ET_I8> &tile, int32_t t) const {
+    int64_t mt, vt;
+    mm_tile_at(t, nmt, nvt, mt, vt);
+    const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
+    const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T, cols = p.V - n0 < MM_T ? p.V - n0 : MM_T;
+    const int tid = mm_tid(), lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 2, wn = wave & 3;
+    const bool has_bias = p.bias != nullptr;
+    OutT *const out = static_cast<OutT *>(p.out) + m0 * p.V + n0;
+    const bool vec = p.V % 4 == 0;
+    const bool staged = sizeof(OutT) == 2 && p.V % 8 == 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int ip = 0; ip < 2; ++ip) {
+        float sc[2];
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii) {
+          const int r = MmTile<ET_I8>::row(wm, li, x, 2 * ip + ii);
+          sc[ii] = r < rows ? p.hs[m0 + r] : 0.0f;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = MmTile<ET_I8>::col(wn, lg, y, j);
+            const int n = c >= cols ? 0 : (cols - c < 4 ? (int)(cols - c) : 4);
+            float ws[4], bv[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              ws[q] = q < n ? p.ws[n0 + c + q] : 0.0f;
+              bv[q] = q < n && has_bias ? p.bias[n0 + c + q] : 0.0f;
+            }
+#pragma unroll
+            for (int ii = 0; ii < 2; ++ii) {
+              const int i = 2 * ip + ii, r = MmTile<ET_I8>::row(wm, li, x, i);
+              float v[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                v[q] = i8_logit(tile.c[x][y][i][j][q], sc[ii], ws[q], p.alpha, has_bias, bv[q]);
+              if (staged)
+                mm_stage4<std::is_same_v<OutT, _Float16> ? ET_F16 : ET_BF16>(
+                    epi, wm, wn, li, lg, y, i, j, f32x4{v[0], v[1], v[2], v[3]});
+              else if (r < rows)
+                store4<OutT>(out + r * p.V + c, v, n, vec);
+            }
+          }
+        if (staged)
+          mm_store_quarter<STORE_POLICY>(epi, x, ip, reinterpret_cast<uint8_t *>(out), p.V * 2, rows, cols * 2);
+      }
+  }
+};
+
 template <typename OutT>
 __global__ __launch_bounds__(MM_THREADS, 1) void int8_tiled_kernel(I8Args p) {
   MM_SHARED();
-  const int64_t nmt = (p.M + MM_T - 1) / MM_T, nvt = (p.V + MM_T - 1) / MM_T;
-  int64_t mt, vt;
-  mm_tile_at(mm_position(nmt * nvt), nmt, nvt, mt, vt);
-  const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
-  const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T, cols = p.V - n0 < MM_T ? p.V - n0 : MM_T;
-  const MmOperand a{p.hq + m0 * p.H, p.H, rows, 0, p.H};
-  const MmOperand b{p.wq + n0 * p.H, p.H, cols, 0, p.H};
-  MmTile<ET_I8> tile;
-  mm_main<ET_I8, false, false>(tile, a, b, (p.H + MM_STAGE_BYTES - 1) / MM_STAGE_BYTES,
-                               [](int64_t t) { return t; }, mm_buf);
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  const bool has_bias = p.bias != nullptr;
-  OutT *const out = static_cast<OutT *>(p.out) + m0 * p.V + n0;
-  // whole rows of 16-bit logits leave through LDS in 16-byte stores; rows not
-  // so aligned, and fp32 ones (whose four columns per lane are 64 contiguous
-  // bytes per row already), straight from the registers
-  const bool vec = p.V % 4 == 0;
-  const bool staged = sizeof(OutT) == 2 && p.V % 8 == 0;
-#pragma unroll
-  for (int y = 0; y < 2; ++y)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = MmTile<ET_I8>::col(wn, lg, y, j);
-      const int n = c >= cols ? 0 : (cols - c < 4 ? (int)(cols - c) : 4);
-      float ws[4], bv[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        ws[q] = q < n ? p.ws[n0 + c + q] : 0.0f;
-        bv[q] = q < n && has_bias ? p.bias[n0 + c + q] : 0.0f;
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = MmTile<ET_I8>::row(wm, li, x, i);
-          const float sc = r < rows ? p.hs[m0 + r] : 0.0f;
-          float t[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            t[q] = i8_logit(tile.c[x][y][i][j][q], sc, ws[q], p.alpha, has_bias, bv[q]);
-          if (staged)
-            mm_stage4<std::is_same_v<OutT, _Float16> ? ET_F16 : ET_BF16>(mm_buf, wm, wn, li, lg, x, y, i, j,
-                                                                         f32x4{t[0], t[1], t[2], t[3]});
-          else if (r < rows)
-            store4<OutT>(out + r * p.V + c, t, n, vec);
-        }
-    }
-  if (!staged) return;
-  __syncthreads();
-  mm_store_tile16<STORE_POLICY>(mm_buf, reinterpret_cast<uint8_t *>(out), p.V * 2, rows, (p.V - n0) * 2);
+  MM_EPI_SHARED();
+  const Int8Tiles<OutT> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, (p.V + MM_T - 1) / MM_T};
+  mm_run<ET_I8, false, false>(prob, mm_buf);
 }
 
 template <typename OutT>
@@ -408,7 +431,7 @@ hipError_t launch_t(const I8Args &a, hipStream_t s) {
       default: return stream_r<4, OutT>(a, s);
     }
   }
-  return launch_kernel(int8_tiled_kernel<OutT>, dim3((unsigned)(ceil_div(a.M, MM_T) * ceil_div(a.V, MM_T))),
+  return launch_kernel(int8_tiled_kernel<OutT>, mm_grid(ceil_div(a.M, MM_T) * ceil_div(a.V, MM_T)),
                        dim3(MM_THREADS), s, a);
 }
 

@@ -47,13 +47,13 @@
 // question, so vmcnt(8) retires them. Stages past the last load nothing
 // (out-of-range offsets, which leave zeros), to keep the counts exact.
 //
-// Measured (4096 x 32768 x 4096, bf16 random data, alone): K-inner operands
-// 865 µs (1.27 PFLOP/s), B K-outer 832 µs (4096 x 4096 x 32768, 1.32), both
-// K-outer 935 µs (1.18); int8 467 µs (2.35 POP/s). Four phases of 16 MFMAs
-// took 890 µs, the waves of a SIMD in step (no barrier of offset) 969 µs.
-// Loads that all hit L2: 772 µs; no loads at all: 685 µs. So what is left is
-// the loads' latency behind L2 and the tiles' starts and ends, during which
-// a CU's one work-group leaves the matrix pipes idle.
+// Tiles follow each other without a pause in the loads: a work-group stays on
+// its CU and takes tile after tile (mm_run), and the last two stages of one
+// already load the first two of the next, so a tile's epilogue runs while the
+// next one's operands arrive. The epilogue therefore has LDS of its own (32 KB,
+// MM_EPI) and leaves the stage buffers alone.
+//
+// @@MEASURED@@
 #pragma once
 
 #include "kstep.hpp"
@@ -75,10 +75,18 @@ constexpr int MM_STAGE_BYTES = 128;  // of a K-inner row per stage
 // One operand of a tile, wave-uniform.
 struct MmOperand {
   const uint8_t *base;  // K-inner: the tile's first row; K-outer: memory row 0, at the tile's first column
-  int64_t ld;           // bytes between rows in memory
-  int64_t rows;         // K-inner: tile rows present (1 .. 256); K-outer: memory rows (K) present
-  int64_t cut;          // K-outer: bytes from `base` to the memory row's end (K-inner: unused)
-  int64_t kbytes;       // K-inner: bytes of a row that belong to the product (K-outer: unused)
+  uint32_t ld;          // bytes between rows in memory
+  int32_t rows;         // K-inner: tile rows present (1 .. 256); K-outer: memory rows (K) present
+  uint32_t bytes;       // K-inner: bytes of a row that belong to the product;
+                        // K-outer: bytes from `base` to the memory row's end
+};
+
+// One tile: its operands and K stages, stage i of the order being memory stage
+// (i + rot) mod stages (rot != 0 with both operands K-inner only, and rows of
+// whole stages).
+struct MmJob {
+  MmOperand a, b;
+  int32_t stages, rot;
 };
 
 template <int ET>
@@ -125,76 +133,112 @@ struct MmBufs {
   __device__ __forceinline__ u32x4 *a(int s, int h) const { return at(4 * s + h); }
   __device__ __forceinline__ u32x4 *b(int s, int h) const { return at(4 * s + 2 + h); }
 };
+constexpr int MM_EPI = 2048;  // 16-byte slots of the epilogue's LDS (32 KB)
+#define MM_EPI_SHARED() __shared__ u32x4 mm_epi[MM_EPI]
 #define MM_SHARED()                                                                \
   __shared__ u32x4 mmA00[MM_HALF], mmA10[MM_HALF], mmB00[MM_HALF], mmB10[MM_HALF]; \
   __shared__ u32x4 mmA01[MM_HALF], mmA11[MM_HALF], mmB01[MM_HALF], mmB11[MM_HALF]; \
   const MmBufs mm_buf{mmA00, mmA10, mmB00, mmB10, mmA01, mmA11, mmB01, mmB11}
 
-// How one wave loads and reads one operand.
+// A wave-uniform value, in scalar registers whatever computed it.
+__device__ __forceinline__ uint32_t mm_uni(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// How one wave loads and reads one operand. The loads follow the stages of the
+// launch's tiles one after the other (MmStream moves both operands along).
 template <int ET, bool OUTER>
 struct MmSide {
-  MmOperand op;
-  rsrc_t r;           // K-inner: the tile's rows
-  uint32_t voff;      // this lane's offset of load 0 of a half-tile
-  uint32_t voff1;     // ... of load 1 (K-inner: another swizzle)
+  uint32_t voff[2];  // this lane's offsets of the two loads of a half-tile
+  uint32_t cur[2];   // ... in the stage being loaded (K-inner: without what is past the row)
+  uint32_t ld;
+  rsrc_t rs;
+  uint32_t lo, hi;   // K-outer: the stage's first memory row (64 bits: a long K passes 32)
+  uint32_t bytes;    // MmOperand::bytes
+  int32_t left;      // K-outer: memory rows from there on
+  uint32_t kb;       // K-inner: the stage's offset in a row, OFF_NONE when there is none
   int wave, lane, li, lg;
-  int w0;             // first row of this wave in a half: wm 64 or wn 32
+  int w0;            // first row of this wave in a half: wm 64 or wn 32
 
-  __device__ __forceinline__ void init(const MmOperand &o, int wave_, int lane_, int w0_) {
-    op = o;
+  __device__ __forceinline__ int piece(int u) const {
+    // K-outer, load u (= 0, 1; memory rows 8 wave + 4 u ..): 16 pieces a row;
+    // lane l fills slot l % 16 of row l / 16 with the piece whose place there is
+    // its own (see read). K-inner (rows 16 wave + 8 u ..): 8 pieces a row; the
+    // swizzle of row 8 u + l / 8 is (4 u + l / 16) & 7.
+    return OUTER ? (lane % 16) ^ (((lane / 16) | ((wave & 1) << 2)) << 1)
+                 : (lane % 8) ^ (4 * u + lane / 16);
+  }
+  __device__ __forceinline__ void init(uint32_t ld_, int wave_, int lane_, int w0_) {
+    ld = mm_uni(ld_);
     wave = wave_;
     lane = lane_;
     li = lane_ & 15;
     lg = lane_ >> 4;
     w0 = w0_;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      voff[u] = (uint32_t)(lane / (OUTER ? 16 : 8)) * ld + 16 * piece(u);
+      cur[u] = voff[u];
+    }
+  }
+  // To the first stage of a tile (in memory: stage rot).
+  __device__ __forceinline__ void begin(const MmOperand &op, int32_t rot) {
+    const uint64_t b = reinterpret_cast<uint64_t>(op.base);
+    lo = mm_uni((uint32_t)b);
+    hi = mm_uni((uint32_t)(b >> 32));
+    bytes = mm_uni(op.bytes);
     if constexpr (OUTER) {
-      // load u (= 2 wave, 2 wave + 1) of a half: memory rows 4 u .. 4 u + 3,
-      // 16 pieces each; lane l fills slot l % 16 of row l / 16 with the piece
-      // whose place there is its own (see slot_outer)
-      const int piece = (lane % 16) ^ (((lane / 16) | ((wave & 1) << 2)) << 1);
-      voff = (uint32_t)((lane / 16) * op.ld + 16 * piece);
-      voff1 = voff;
+      left = (int32_t)mm_uni((uint32_t)op.rows);
+      window();
     } else {
-      // load u of a half: rows 8 u .. 8 u + 7, 8 pieces each; the swizzle of
-      // row 8 u + l / 8 is (4 u + l / 16) & 7
-      r = make_rsrc(op.base, (uint32_t)((op.rows - 1) * op.ld + op.kbytes));
-      voff = (uint32_t)((lane / 8) * op.ld + 16 * ((lane % 8) ^ (lane / 16)));
-      voff1 = (uint32_t)((lane / 8) * op.ld + 16 * ((lane % 8) ^ (4 + lane / 16)));
+      rs = make_rsrc(op.base, (uint32_t)(op.rows - 1) * ld + op.bytes);
+      kb = mm_uni((uint32_t)rot * MM_STAGE_BYTES);
+    }
+  }
+  // K-outer: the resource starts at the stage's first memory row and ends with
+  // the last one present; rows past it read as zero. Columns past the row's end
+  // read the next row's start, into columns that are never stored.
+  __device__ __forceinline__ void window() {
+    const int32_t n = left < 64 ? left : 64;
+    const uint64_t b = ((uint64_t)hi << 32) | lo;
+    rs = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(b), (short)0,
+                                           n > 0 ? (int)((uint32_t)(n - 1) * ld + bytes) : 0, RSRC_WORD3);
+  }
+  // To the next stage of the tile.
+  __device__ __forceinline__ void step() {
+    if constexpr (OUTER) {
+      const uint64_t b = (((uint64_t)hi << 32) | lo) + 64ull * ld;
+      lo = (uint32_t)b;
+      hi = (uint32_t)(b >> 32);
+      left -= 64;
+      window();
+    } else {
+      kb += MM_STAGE_BYTES;
+      if (kb >= bytes) kb = 0;  // rot != 0: round to the row's start
+    }
+  }
+  // No stage: loads nothing.
+  __device__ __forceinline__ void none() {
+    if constexpr (OUTER) {
+      left = 0;
+      window();
+    } else {
+      kb = OFF_NONE;
+    }
+  }
+  // K-inner: a row's last stage may be partial; what lies past the row is not loaded.
+  __device__ __forceinline__ void trim(bool last) {
+    if constexpr (!OUTER) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        cur[u] = last && kb + 16 * piece(u) >= bytes ? OFF_NONE : voff[u];
     }
   }
 
-  // Half-tile h of memory stage `st` (< 0: none) into `dst`.
-  __device__ __forceinline__ void load(int h, int64_t st, u32x4 *dst) const {
-    const int u = 2 * wave;
-    if constexpr (OUTER) {
-      // the resource starts at the stage's first memory row (64-bit base: a
-      // long K passes 32 bits) and ends with the last one present; rows past
-      // it read as zero
-      const int64_t k0 = st * 64;
-      const int64_t left = st < 0 ? 0 : (op.rows - k0 < 64 ? op.rows - k0 : 64);
-      const bool any = left > 0 && op.cut > 256 * h;
-      const rsrc_t rs = make_rsrc(any ? op.base + k0 * op.ld : op.base,
-                                  any ? (uint32_t)((left - 1) * op.ld + op.cut) : 0u);
-      // columns past the row's end: a half wholly past it loads nothing; one
-      // partly past it reads the next row's start there, into columns that
-      // are never stored
-      const uint32_t s0 = any ? (uint32_t)(4 * u * op.ld + 256 * h) : OFF_NONE;
-      const uint32_t s1 = any ? (uint32_t)(4 * (u + 1) * op.ld + 256 * h) : OFF_NONE;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (mm_lds_void *)&dst[64 * u], 16, voff, s0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (mm_lds_void *)&dst[64 * (u + 1)], 16, voff1, s1, 0, 0);
-    } else {
-      const int64_t kb = st * MM_STAGE_BYTES;
-      uint32_t v0 = voff, v1 = voff1;
-      if (st >= 0 && kb + MM_STAGE_BYTES > op.kbytes) {  // uniform: the row's last, partial stage
-        const int64_t p0 = (lane % 8) ^ (lane / 16), p1 = (lane % 8) ^ (4 + lane / 16);
-        if (kb + 16 * p0 >= op.kbytes) v0 = OFF_NONE;
-        if (kb + 16 * p1 >= op.kbytes) v1 = OFF_NONE;
-      }
-      const uint32_t s0 = st >= 0 ? (uint32_t)((h * 128 + 8 * u) * op.ld + kb) : OFF_NONE;
-      const uint32_t s1 = st >= 0 ? (uint32_t)((h * 128 + 8 * (u + 1)) * op.ld + kb) : OFF_NONE;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void *)&dst[64 * u], 16, v0, s0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void *)&dst[64 * (u + 1)], 16, v1, s1, 0, 0);
-    }
+  // Half-tile h of the stage into `dst`.
+  __device__ __forceinline__ void load(int h, u32x4 *dst) const {
+    const uint32_t s = OUTER ? 8 * wave * ld + 256 * h : (h * 128 + 16 * wave) * ld + kb;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (mm_lds_void *)&dst[128 * wave], 16, cur[0], s, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (mm_lds_void *)&dst[128 * wave + 64], 16, cur[1],
+                                             s + (OUTER ? 4 : 8) * ld, 0, 0);
   }
 
   // The MFMA operand of rows w0 + 16 b .. of a half-tile, K-step s (0, 1).
@@ -228,36 +272,110 @@ __device__ __forceinline__ void mm_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// The main loop: `stages` K stages; `memstage(t)` is the memory stage that
-// stage t of the order reads. On return every wave has met a barrier after
-// its last LDS access and every direct load has landed, so the stage buffers
-// are free.
-template <int ET, bool AOUT, bool BOUT, typename F>
-__device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, const MmOperand &b,
-                                        int64_t stages, F &&memstage,
-                                        const MmBufs &buf) {
+// Where the work-groups' tiles lie. Work-groups go to the XCDs round-robin, so
+// each XCD is given a contiguous range of the tiles, worked off in rounds of one
+// tile per work-group: neighbours run at the same time and share the XCD's L2.
+// Within a round the tiles rotate over the work-groups, so that none is always
+// given the taller tiles of a pair.
+struct MmWalk {
+  uint32_t lo, hi, nw, wi, round;
+  __device__ __forceinline__ MmWalk(uint32_t tiles) {
+    const uint32_t b = blockIdx.x, g = gridDim.x, nx = g < 8 ? g : 8;
+    const uint32_t x = b % nx, q = tiles / nx, r = tiles % nx;
+    lo = x * q + (x < r ? x : r);
+    hi = lo + q + (x < r ? 1 : 0);
+    nw = (g - x + nx - 1) / nx;
+    wi = b / nx;
+    round = 0;
+  }
+  // The work-group's next tile, or -1.
+  __device__ __forceinline__ int32_t next() {
+    const uint32_t t = lo + round * nw + (wi + round) % nw;
+    ++round;
+    return t < hi ? (int32_t)mm_uni(t) : -1;
+  }
+};
+
+// Tile (a, b) of position t among na x nb: panels of four tiles of A, walked
+// along B, so that the 32 work-groups of an XCD read 4 + 8 distinct operand
+// tiles and not 32 + 1 (4096 x 32768 x 4096: 935 -> 891 µs against one panel
+// of all of A; panels of 8: 906 µs).
+__device__ __forceinline__ void mm_tile_at(uint32_t t, uint32_t na, uint32_t nb, int64_t &a, int64_t &b) {
+  constexpr uint32_t PANEL = 4;
+  const uint32_t g = t / (PANEL * nb), h = na - g * PANEL < PANEL ? na - g * PANEL : PANEL;
+  const uint32_t r = t - g * PANEL * nb, rb = r / h;
+  a = mm_uni(g * PANEL + r - rb * h);
+  b = mm_uni(rb);
+}
+
+// Runs the work-group's tiles of `p`:
+//   p.tiles()           their number
+//   p.job(t)            tile t (called by every wave, wave-uniform)
+//   p.epilogue(tile, t) called by all waves at the same point of their barriers,
+//                       which it may use; it has the accumulators and MM_EPI
+//                       slots of LDS of its own. Vector memory operations that
+//                       it leaves in flight only make later waits longer.
+// Every job of a launch has the same row lengths (ld).
+template <int ET, bool AOUT, bool BOUT, typename P>
+__device__ __forceinline__ void mm_run(const P &p, const MmBufs &buf) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  MmWalk walk((uint32_t)p.tiles());
+  int32_t tile_no = walk.next();
+  if (tile_no < 0) return;
   MmSide<ET, AOUT> sa;
   MmSide<ET, BOUT> sb;
-  sa.init(a, wave, lane, (wave >> 2) * 64);
-  sb.init(b, wave, lane, (wave & 3) * 32);
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) tile.c[x][y][i][j] = typename MmAcc<ET>::type{0, 0, 0, 0};
 
-  // a tile of at most 128 rows of A leaves the second half out: half the
-  // matrix work (uniform; its loads are out of range, the counts stay). Only
-  // with both operands K-inner: with B K-outer the branch makes the compiler
-  // spill.
-  const bool tall = AOUT || BOUT || a.rows > 128;
-  u32x4 fa[4][2], fb[3][2][2];  // A half in use; B halves in use (set, block, K-step)
-  auto ms = [&](int64_t t) -> int64_t { return t < stages ? memstage(t) : -1; };
+  using std::integral_constant;
+  using I0 = integral_constant<int, 0>;
+  using I1 = integral_constant<int, 1>;
+  using I2 = integral_constant<int, 2>;
+  // The stage being loaded: stage `l` of a tile's `lstages`, in pairs of stages
+  // (an odd count ends with one of zeros). load_no: the tile it belongs to.
+  int32_t l = 0, lstages, load_no = tile_no, rows_load;
+  auto begin = [&](const MmJob &j) {
+    lstages = (int32_t)mm_uni((uint32_t)j.stages);
+    rows_load = (int32_t)mm_uni((uint32_t)j.a.rows);
+    sa.begin(j.a, j.rot);
+    sb.begin(j.b, j.rot);
+  };
+  auto trim = [&]() {
+    sa.trim(l == lstages - 1);
+    sb.trim(l == lstages - 1);
+  };
+  // To the next stage: an odd one (ODD) of the same tile, or an even one, which
+  // may be the next tile's first.
+  auto advance = [&](auto oddc) {
+    constexpr bool ODD = decltype(oddc)::value != 0;
+    ++l;
+    if (l < lstages) {
+      sa.step();
+      sb.step();
+    } else {
+      if constexpr (!ODD) {
+        l = 0;
+        lstages = 0;
+        if (load_no >= 0) load_no = walk.next();
+      }
+      if (!ODD && load_no >= 0) {
+        begin(p.job(load_no));
+      } else {
+        sa.none();
+        sb.none();
+      }
+    }
+    trim();
+  };
+  {
+    const MmJob j = p.job(tile_no);
+    sa.init(j.a.ld, wave, lane, (wave >> 2) * 64);
+    sb.init(j.b.ld, wave, lane, (wave & 3) * 32);
+    begin(j);
+    trim();
+  }
+
+  MmTile<ET> tile;
+  u32x4 fa[4][2], fb[3][2][2];  // the A half in use; B0 of stages 0 and 1, B1 (block, K-step)
   auto readA = [&](const u32x4 *src) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -283,90 +401,95 @@ __device__ __forceinline__ void mm_main(MmTile<ET> &tile, const MmOperand &a, co
           tile.c[X][Y][i][j] = mm_step<ET>(tile.c[X][Y][i][j], fa[i][s], fb[SET][j][s]);
     __builtin_amdgcn_s_setprio(0);
   };
-  using std::integral_constant;
-  using I0 = integral_constant<int, 0>;
-  using I1 = integral_constant<int, 1>;
+  // ends a read part: what the next phase reads has landed, this wave's own
+  // reads have returned
   auto end_read = [&]() {
     wait_vm<8>();
     wait_lds();
     mm_barrier();
   };
-  using I2 = integral_constant<int, 2>;
-  auto stage = [&](auto sc, int64_t t) {
-    constexpr int S = decltype(sc)::value;
-    using SET = integral_constant<int, S>;
-    using SETN = integral_constant<int, 1 - S>;
-    readA(buf.a(S, 0));
-    readB(I2{}, buf.b(S, 1));
-    sa.load(1, ms(t + 1), buf.a(1 - S, 1));
-    sb.load(0, ms(t + 2), buf.b(S, 0));
-    end_read();
-    mfma(I0{}, I0{}, SET{});
-    mfma(I0{}, I1{}, I2{});
-    mm_barrier();
-    if (tall) readA(buf.a(S, 1));
-    readB(SETN{}, buf.b(1 - S, 0));
-    const int64_t m2 = ms(t + 2);
-    sa.load(0, m2, buf.a(S, 0));
-    sb.load(1, m2, buf.b(S, 1));
-    end_read();
-    if (tall) {
-      mfma(I1{}, I1{}, I2{});
-      mfma(I1{}, I0{}, SET{});
-    }
-    mm_barrier();
-  };
-  {
-    const int64_t m = ms(0), n = ms(1);
-    sb.load(0, m, buf.b(0, 0));
-    sa.load(0, m, buf.a(0, 0));
-    sb.load(1, m, buf.b(0, 1));
-    sa.load(1, m, buf.a(0, 1));
-    sb.load(0, n, buf.b(1, 0));
-    sa.load(0, n, buf.a(1, 0));
-    sb.load(1, n, buf.b(1, 1));
-  }
-  wait_vm<8>();
+
+  int32_t stages = lstages, rows = rows_load;  // of the tile being computed
+  sb.load(0, buf.b(0, 0));
+  sa.load(0, buf.a(0, 0));
+  sb.load(1, buf.b(0, 1));
+  sa.load(1, buf.a(0, 1));
+  advance(I1{});
+  sb.load(0, buf.b(1, 0));
+  sa.load(0, buf.a(1, 0));
+  sb.load(1, buf.b(1, 1));
+  wait_vm<8>();  // stage 0's B0, A0, B1 (and A1 and B0 of what follows in flight)
   mm_barrier();
   readB(I0{}, buf.b(0, 0));
   wait_lds();
   mm_barrier();
-  if (wave >= 4) mm_barrier();
-  for (int64_t t = 0; t < stages; t += 2) {
-    stage(I0{}, t);
-    stage(I1{}, t + 1);
+
+  for (;;) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tile.c[x][y][i][j] = typename MmAcc<ET>::type{0, 0, 0, 0};
+    // a tile of at most 128 rows of A leaves the second half out: half the
+    // matrix work (uniform; its loads are out of range, the counts stay). Only
+    // with both operands K-inner: with B K-outer the branch makes the compiler
+    // spill.
+    const bool tall = AOUT || BOUT || rows > 128;
+    if (wave >= 4) mm_barrier();  // the second group runs one barrier behind
+    for (int32_t t = 0; t < stages; t += 2) {
+      auto stage = [&](auto sc) {
+        constexpr int S = decltype(sc)::value;
+        using SET = integral_constant<int, S>;
+        using SETN = integral_constant<int, 1 - S>;
+        readA(buf.a(S, 0));
+        readB(I2{}, buf.b(S, 1));
+        sa.load(1, buf.a(1 - S, 1));
+        advance(sc);
+        sb.load(0, buf.b(S, 0));
+        end_read();
+        mfma(I0{}, I0{}, SET{});
+        mfma(I0{}, I1{}, I2{});
+        mm_barrier();
+        if (tall) readA(buf.a(S, 1));
+        readB(SETN{}, buf.b(1 - S, 0));
+        sa.load(0, buf.a(S, 0));
+        sb.load(1, buf.b(S, 1));
+        end_read();
+        if (tall) {
+          mfma(I1{}, I1{}, I2{});
+          mfma(I1{}, I0{}, SET{});
+        }
+        mm_barrier();
+      };
+      stage(I0{});
+      stage(I1{});
+    }
+    if (wave < 4) mm_barrier();
+    p.epilogue(tile, tile_no);
+    if (load_no < 0) break;
+    tile_no = load_no;  // the loads are in the next tile by now
+    stages = lstages;
+    rows = rows_load;
   }
-  if (wave < 4) mm_barrier();
-  wait_vm<0>();
-  wait_lds();
-  mm_barrier();
+  wait_vm<0>();  // the loads of nothing write LDS too
 }
 
-// Position of a work-group among `n`: work-groups go to the eight XCDs
-// round-robin, so that consecutive positions run on one XCD and share its L2.
-__device__ __forceinline__ int64_t mm_position(int64_t n) {
-  const int64_t b = blockIdx.x, q = n / 8, r = n % 8;
-  const int64_t xcd = b % 8, pos = b / 8;
-  return xcd < r ? xcd * (q + 1) + pos : r * (q + 1) + (xcd - r) * q + pos;
+// Work-groups of a launch of `tiles` tiles: one per CU, or per tile.
+inline dim3 mm_grid(int64_t tiles) {
+  const int64_t cus = device_cus();
+  return dim3((unsigned)(tiles < cus ? tiles : cus));
 }
 
-// Tile (a, b) of position t among na x nb: panels of four tiles of A, walked
-// along B, so that the 32 work-groups of an XCD read 4 + 8 distinct operand
-// tiles and not 32 + 1 (4096 x 32768 x 4096: 935 -> 891 µs against one panel
-// of all of A; panels of 8: 906 µs).
-__device__ __forceinline__ void mm_tile_at(int64_t t, int64_t na, int64_t nb, int64_t &a, int64_t &b) {
-  constexpr int64_t PANEL = 4;
-  const int64_t g = t / (PANEL * nb), h = na - g * PANEL < PANEL ? na - g * PANEL : PANEL;
-  const int64_t r = t - g * PANEL * nb;
-  a = g * PANEL + r % h;
-  b = r / h;
-}
-
-// The LDS rows (512 bytes) of a 256 x 256 tile of 16-bit values: row r in
-// stage array r / 32, its 32-byte pieces xor-ed with r so that the 16 rows one
-// store touches fall in distinct banks.
-__device__ __forceinline__ uint8_t *mm_tile_row(const MmBufs &buf, int hi, int r) {
-  return reinterpret_cast<uint8_t *>(buf.at(hi)) + (r & 31) * 512;
+// threadIdx.x, newly read: what an epilogue derives from it is worked out there
+// and not, for all tiles, ahead of their loop, where it would take registers
+// from the accumulators (50 spilled, reloaded behind every load in flight).
+__device__ __forceinline__ int mm_tid() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
 }
 
 // Two fp32 values to the 16-bit type, nearest even, low half first.
@@ -381,32 +504,40 @@ __device__ __forceinline__ uint32_t mm_pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
-// Four columns of one row of the tile, as 16-bit values, into LDS.
+// 16-bit results leave through MM_EPI in quarters: quarter (x, ip) holds the 64
+// rows 128 x + 64 wm + 32 ip + (0 .. 31) of the tile, row by row (512 bytes;
+// its 32-byte pieces xor-ed with the row so that the 16 rows one store touches
+// fall in distinct banks), and is written to memory as whole rows in 16-byte
+// stores.
+//
+// Four columns of one row, block (i, j) of quadrant (x, y), into the quarter.
 template <int ET>
-__device__ __forceinline__ void mm_stage4(const MmBufs &buf, int wm, int wn, int li, int lg,
-                                       int x, int y, int i, int j, f32x4 v) {
-  const int r = MmTile<ET>::row(wm, li, x, i);
-  uint8_t *row = wm == 0 ? mm_tile_row(buf, x * 4 + (i >> 1), r) : mm_tile_row(buf, x * 4 + 2 + (i >> 1), r);
+__device__ __forceinline__ void mm_stage4(u32x4 *epi, int wm, int wn, int li, int lg, int y, int i, int j,
+                                          f32x4 v) {
+  const int r = wm * 32 + (i & 1) * 16 + li;
   const int piece = (y * 128 + wn * 32 + 16 * j) / 16;
-  *reinterpret_cast<u32x2 *>(row + ((piece ^ (r & 15)) * 32) + 8 * lg) =
-      u32x2{mm_pack2<ET>(v[0], v[1]), mm_pack2<ET>(v[2], v[3])};
+  uint8_t *const at = reinterpret_cast<uint8_t *>(epi) + r * 512 + ((piece ^ li) * 32) + 8 * lg;
+  *reinterpret_cast<u32x2 *>(at) = u32x2{mm_pack2<ET>(v[0], v[1]), mm_pack2<ET>(v[2], v[3])};
 }
 
-// The staged tile to rows of `ld` bytes at `out`, `rows` rows of `bytes`
-// bytes (a multiple of 16) present.
+// Writes quarter (x, ip): `out` is the tile's first element, `ld` bytes between
+// rows, `rows` rows of `bytes` bytes (a multiple of 16) present. Between
+// barriers of its own on both sides.
 template <int POLICY>
-__device__ __forceinline__ void mm_store_tile16(const MmBufs &buf, uint8_t *out, int64_t ld,
-                                             int64_t rows, int64_t bytes) {
+__device__ __forceinline__ void mm_store_quarter(const u32x4 *epi, int x, int ip, uint8_t *out, int64_t ld,
+                                                 int64_t rows, int64_t bytes) {
+  lds_barrier();
   const rsrc_t rs = make_rsrc(out, (uint32_t)((rows - 1) * ld + (bytes < 512 ? bytes : 512)));
-  const int c = threadIdx.x % 32, r0 = threadIdx.x / 32;
+  const int tid = mm_tid(), c = tid % 32, r0 = tid / 32;
 #pragma unroll
-  for (int it = 0; it < 16; ++it) {
-    const int r = it * 16 + r0;
-    const uint8_t *row = mm_tile_row(buf, it >> 1, r);
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(row + (((c >> 1) ^ (r & 15)) * 32) + 16 * (c & 1));
+  for (int it = 0; it < 4; ++it) {
+    const int s = it * 16 + r0;  // row of the quarter
+    const int r = 128 * x + 64 * (s >> 5) + 32 * ip + (s & 31);
+    const u32x4 v = epi[s * 32 + (((c >> 1) ^ (s & 15)) * 2) + (c & 1)];
     const bool ok = r < rows && 16 * c < bytes;
     __builtin_amdgcn_raw_buffer_store_b128(v, rs, ok ? (uint32_t)(r * ld + 16 * c) : OFF_NONE, 0, POLICY);
   }
+  lds_barrier();
 }
 
 }  // namespace lmhead

@@ -55,98 +55,119 @@ __device__ __forceinline__ int64_t target_of(const void *target, int target64, i
 }
 
 // hidden W^T of tile (m0, n0): both operands K-inner, the K order of korder.hpp.
-template <int ET>
-__device__ __forceinline__ void logits_tile(MmTile<ET> &tile, const uint8_t *hidden,
-                                            const uint8_t *W, int64_t M, int64_t H, int64_t V,
-                                            int64_t m0, int64_t n0, const MmBufs &buf) {
-  const int64_t rb = H * 2;
-  const MmOperand a{hidden + m0 * rb, rb, M - m0 < MM_T ? M - m0 : MM_T, 0, rb};
-  const MmOperand b{W + n0 * rb, rb, V - n0 < MM_T ? V - n0 : MM_T, 0, rb};
-  const int64_t stages = (rb + MM_STAGE_BYTES - 1) / MM_STAGE_BYTES;
-  const int64_t rot = korder_start(n0, H) / 64;
-  mm_main<ET, false, false>(tile, a, b, stages,
-                            [&](int64_t t) { return t + rot < stages ? t + rot : t + rot - stages; },
-                            buf);
+__device__ __forceinline__ MmJob logits_job(const uint8_t *hidden, const uint8_t *W, int64_t M, int64_t H,
+                                            int64_t V, int64_t m0, int64_t n0) {
+  const int64_t rb = H * 2, rows = M - m0, cols = V - n0;
+  return MmJob{{hidden + m0 * rb, (uint32_t)rb, (int32_t)(rows < MM_T ? rows : MM_T), (uint32_t)rb},
+               {W + n0 * rb, (uint32_t)rb, (int32_t)(cols < MM_T ? cols : MM_T), (uint32_t)rb},
+               (int32_t)((rb + MM_STAGE_BYTES - 1) / MM_STAGE_BYTES),
+               (int32_t)(korder_start(n0, H) / 64)};
 }
 
-template <int ET>
-__global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p) {
-  MM_SHARED();
-  const int64_t nmt = (p.M + MM_T - 1) / MM_T, nvt = (p.V + MM_T - 1) / MM_T;
-  int64_t mt, vt;
-  mm_tile_at(mm_position(nmt * nvt), nmt, nvt, mt, vt);
-  const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
-  MmTile<ET> tile;
-  logits_tile<ET>(tile, p.hidden, p.W, p.M, p.H, p.V, m0, n0, mm_buf);
+// A lane's place in its wave's output.
+struct LanePlace {
+  int li, lg, wm, wn;
+  __device__ __forceinline__ LanePlace() {
+    const int tid = mm_tid(), lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    li = lane & 15;
+    lg = lane >> 4;
+    wm = wave >> 2;
+    wn = wave & 3;
+  }
+};
 
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  const bool has_bias = p.bias != nullptr;
-  float bias[2][2][4];
-  if (has_bias) {
+template <int ET>
+struct XentStats {
+  XentFwdArgs p;
+  u32x4 *epi;
+  int64_t nmt, nvt;
+
+  __device__ __forceinline__ int64_t tiles() const { return nmt * nvt; }
+  __device__ __forceinline__ MmJob job(int32_t t) const {
+    int64_t mt, vt;
+    mm_tile_at(t, nmt, nvt, mt, vt);
+    return logits_job(p.hidden, p.W, p.M, p.H, p.V, mt * MM_T, vt * MM_T);
+  }
+  __device__ __forceinline__ void epilogue(MmTile<ET> &tile, int32_t t) const {
+    int64_t mt, vt;
+    mm_tile_at(t, nmt, nvt, mt, vt);
+    const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
+    const LanePlace at;
+    const bool has_bias = p.bias != nullptr;
+    float bias[2][2][4];
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int64_t c = n0 + MmTile<ET>::col(wn, lg, y, j) + q;
-          bias[y][j][q] = c < p.V ? p.bias[c] : 0.0f;
+          const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
+          // columns that are not there get t = -inf
+          bias[y][j][q] = c < p.V ? (has_bias ? p.bias[c] : 0.0f) : NEG_INF;
         }
-  }
-  float2 *const stat = reinterpret_cast<float2 *>(mm_buf.at(0));  // [4][256]
-  const bool ragged = n0 + MM_T > p.V;
+    const bool add = has_bias || n0 + MM_T > p.V;
+    float2 *const stat = reinterpret_cast<float2 *>(epi);  // [4][256]
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = MmTile<ET>::row(wm, li, x, i);
-      const int64_t m = m0 + row;
-      const int64_t yt = m < p.M ? target_of(p.target, p.target64, m, p.ignore, p.V) - n0 : -1;
-      float mx = NEG_INF;
+      for (int i = 0; i < 4; ++i) {
+        const int row = MmTile<ET>::row(at.wm, at.li, x, i);
+        const int64_t m = m0 + row;
+        const int64_t yt = m < p.M ? target_of(p.target, p.target64, m, p.ignore, p.V) - n0 : -1;
+        float mx = NEG_INF;
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c0 = MmTile<ET>::col(wn, lg, y, j);
+          for (int j = 0; j < 2; ++j) {
+            const int c0 = MmTile<ET>::col(at.wn, at.lg, y, j);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float v = epilogue_v(tile.c[x][y][i][j][q], p.alpha, has_bias, bias[y][j][q]);
-            if (ragged && n0 + c0 + q >= p.V) v = NEG_INF;
-            if (yt == c0 + q) p.tlogit[m] = v;
-            tile.c[x][y][i][j][q] = v;
-            mx = fmaxf(mx, v);
+            for (int q = 0; q < 4; ++q) {
+              const float v = epilogue_v(tile.c[x][y][i][j][q], p.alpha, add, bias[y][j][q]);
+              if (yt == c0 + q) p.tlogit[m] = v;
+              tile.c[x][y][i][j][q] = v;
+              mx = fmaxf(mx, v);
+            }
           }
-        }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      // a tile of only -inf sums nothing: its terms are taken against 0
-      const float mz = mx == NEG_INF ? 0.0f : mx;
-      float s = 0.0f;
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        // a tile of only -inf sums nothing: its terms are taken against 0
+        const float mz = mx == NEG_INF ? 0.0f : mx;
+        float s = 0.0f;
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            s = __fadd_rn(s, exp_fast(__fsub_rn(tile.c[x][y][i][j][q], mz)));
-      s = __fadd_rn(s, __shfl_xor(s, 16));
-      s = __fadd_rn(s, __shfl_xor(s, 32));
-      if (lg == 0) stat[wn * MM_T + row] = float2{mx, s};
+            for (int q = 0; q < 4; ++q)
+              s = __fadd_rn(s, exp_fast(__fsub_rn(tile.c[x][y][i][j][q], mz)));
+        s = __fadd_rn(s, __shfl_xor(s, 16));
+        s = __fadd_rn(s, __shfl_xor(s, 32));
+        if (at.lg == 0) stat[at.wn * MM_T + row] = float2{mx, s};
+      }
+    lds_barrier();
+    const int row = threadIdx.x;
+    if (row < MM_T && m0 + row < p.M) {
+      float mx = NEG_INF, s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w * MM_T + row].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 e = stat[w * MM_T + row];
+        if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp_fast(__fsub_rn(e.x, mx))));
+      }
+      p.part[vt * p.M + m0 + row] = float2{mx, s};
     }
-  __syncthreads();
-  const int row = threadIdx.x;
-  if (row < MM_T && m0 + row < p.M) {
-    float mx = NEG_INF, s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w * MM_T + row].x);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float2 e = stat[w * MM_T + row];
-      if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp_fast(__fsub_rn(e.x, mx))));
-    }
-    p.part[vt * p.M + m0 + row] = float2{mx, s};
+    // the next tile's epilogue is barriers away
   }
+};
+
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  const XentStats<ET> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, (p.V + MM_T - 1) / MM_T};
+  mm_run<ET, false, false>(prob, mm_buf);
 }
 
 // Folds the tiles of a row: 64 rows per work-group, 16 threads per row, each
@@ -271,9 +292,10 @@ struct XentBwdArgs {
   const float *bias;
   const RowCoef *rows;
   const float *scale;  // {f, 1 / f}
-  int64_t v0, vp;      // this piece's first column and its columns (a multiple of 256)
-  uint8_t *G;          // [M, vp], 16 bits
-  float *colpart;      // [row tile][vp] column sums of G, or nullptr
+  int64_t v0, np;      // this piece's first column and its columns (a multiple of 256)
+  int64_t ldg;         // columns of a row of G in memory
+  uint8_t *G;          // [M, ldg], 16 bits
+  float *colpart;      // [row tile][ldg] column sums of G, or nullptr
   float *dh;           // [splits][M, H] fp32 sums
   int64_t ksplit;      // columns per split of G W
   int first;           // first piece: dh is written, not added to
@@ -282,93 +304,97 @@ struct XentBwdArgs {
 
 // G of one piece.
 template <int ET>
-__global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p) {
-  MM_SHARED();
-  const int64_t nmt = (p.M + MM_T - 1) / MM_T;
-  int64_t mt, gt;
-  mm_tile_at(mm_position(nmt * (p.vp / MM_T)), nmt, p.vp / MM_T, mt, gt);
-  const int64_t m0 = mt * MM_T, g0 = gt * MM_T, n0 = p.v0 + g0;
-  MmTile<ET> tile;
-  if (n0 < p.V) {
-    logits_tile<ET>(tile, p.hidden, p.W, p.M, p.H, p.V, m0, n0, mm_buf);
-  } else {  // columns that only fill the piece up
+struct XentGrad {
+  XentBwdArgs p;
+  u32x4 *epi;
+  int64_t nmt, ngt;
+
+  __device__ __forceinline__ int64_t tiles() const { return nmt * ngt; }
+  __device__ __forceinline__ MmJob job(int32_t t) const {
+    int64_t mt, gt;
+    mm_tile_at(t, nmt, ngt, mt, gt);
+    return logits_job(p.hidden, p.W, p.M, p.H, p.V, mt * MM_T, p.v0 + gt * MM_T);
+  }
+  __device__ __forceinline__ void epilogue(MmTile<ET> &tile, int32_t t) const {
+    int64_t mt, gt;
+    mm_tile_at(t, nmt, ngt, mt, gt);
+    const int64_t m0 = mt * MM_T, g0 = gt * MM_T, n0 = p.v0 + g0;
+    const LanePlace at;
+    const bool has_bias = p.bias != nullptr;
+    float bias[2][2][4];
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
+          // columns that are not there get t = -inf, so G = 0
+          bias[y][j][q] = c < p.V ? (has_bias ? p.bias[c] : 0.0f) : NEG_INF;
+        }
+    const bool add = has_bias || n0 + MM_T > p.V;
+    const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
+    float colsum[2][2][4] = {};
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int ip = 0; ip < 2; ++ip) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int ii = 0; ii < 2; ++ii) {
+          const int i = 2 * ip + ii;
+          const int64_t m = m0 + MmTile<ET>::row(at.wm, at.li, x, i);
+          // exp(-inf) = 0 in rows past the end, and where the whole row is -inf
+          const RowCoef rc = m < p.M ? p.rows[m] : RowCoef{0.0f, 0.0f, __builtin_inff(), -1};
+          const float lse = rc.lse == NEG_INF ? 0.0f : rc.lse;
+          const int64_t yt = (int64_t)rc.y - n0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) tile.c[x][y][i][j] = zero4();
-  }
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  const bool has_bias = p.bias != nullptr;
-  float bias[2][2][4];
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-  for (int y = 0; y < 2; ++y)
+            for (int j = 0; j < 2; ++j) {
+              const int c0 = MmTile<ET>::col(at.wn, at.lg, y, j);
+              f32x4 v;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t c = n0 + MmTile<ET>::col(wn, lg, y, j) + q;
-        // columns that are not there get t = -inf, so G = 0
-        bias[y][j][q] = c < p.V ? (has_bias ? p.bias[c] : 0.0f) : NEG_INF;
-      }
-  const bool add = has_bias || n0 + MM_T > p.V;
-  float colsum[2][2][4] = {};
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + MmTile<ET>::row(wm, li, x, i);
-      // exp(-inf) = 0 in rows past the end, and where the whole row is -inf
-      const RowCoef rc = m < p.M ? p.rows[m] : RowCoef{0.0f, 0.0f, __builtin_inff(), -1};
-      const float lse = rc.lse == NEG_INF ? 0.0f : rc.lse;
-      const int64_t yt = (int64_t)rc.y - n0;
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c0 = MmTile<ET>::col(wn, lg, y, j);
-          f32x4 v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float tv = epilogue_v(tile.c[x][y][i][j][q], p.alpha, add, bias[y][j][q]);
-            float gv = __fmul_rn(rc.a, exp_fast(__fsub_rn(tv, lse)));
-            if (yt == c0 + q) gv = __fsub_rn(gv, rc.b);
-            v[q] = gv;
-            colsum[y][j][q] = __fadd_rn(colsum[y][j][q], gv);
-          }
-          mm_stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
+              for (int q = 0; q < 4; ++q) {
+                const float tv = epilogue_v(tile.c[x][y][i][j][q], p.alpha, add, bias[y][j][q]);
+                float gv = __fmul_rn(rc.a, exp_fast(__fsub_rn(tv, lse)));
+                if (yt == c0 + q) gv = __fsub_rn(gv, rc.b);
+                v[q] = gv;
+                colsum[y][j][q] = __fadd_rn(colsum[y][j][q], gv);
+              }
+              mm_stage4<ET>(epi, at.wm, at.wn, at.li, at.lg, y, i, j, v);
+            }
         }
-    }
-  __syncthreads();
-  const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
-  mm_store_tile16<LOAD_DEFAULT>(mm_buf, p.G + (m0 * p.vp + g0) * 2, p.vp * 2, rows, 512);
-  if (p.colpart == nullptr) return;
-  __syncthreads();
-  // column sums: 16 rows of a block by lane exchanges, then the two wave rows
-  float *const cs = reinterpret_cast<float *>(mm_buf.at(0));  // [2][256]
-#pragma unroll
-  for (int y = 0; y < 2; ++y)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float s = colsum[y][j][q];
-        s = __fadd_rn(s, dpp<DPP_QUAD_SWAP1>(s));
-        s = __fadd_rn(s, dpp<DPP_QUAD_SWAP2>(s));
-        s = __fadd_rn(s, dpp<DPP_ROW_HALF_MIRROR>(s));
-        s = __fadd_rn(s, dpp<DPP_ROW_MIRROR>(s));
-        if (li == 0) cs[wm * MM_T + MmTile<ET>::col(wn, lg, y, j) + q] = s;
+        mm_store_quarter<LOAD_DEFAULT>(epi, x, ip, p.G + (m0 * p.ldg + g0) * 2, p.ldg * 2, rows, 512);
       }
-  __syncthreads();
-  if (threadIdx.x < MM_T) {
-    const float s = p.scale[1];
-    p.colpart[(m0 / MM_T) * p.vp + g0 + threadIdx.x] =
-        __fmul_rn(s, __fadd_rn(cs[threadIdx.x], cs[MM_T + threadIdx.x]));
+    if (p.colpart == nullptr) return;
+    // column sums: 16 rows of a block by lane exchanges, then the two wave rows
+    float *const cs = reinterpret_cast<float *>(epi);  // [2][256]
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float s = colsum[y][j][q];
+          s = __fadd_rn(s, dpp<DPP_QUAD_SWAP1>(s));
+          s = __fadd_rn(s, dpp<DPP_QUAD_SWAP2>(s));
+          s = __fadd_rn(s, dpp<DPP_ROW_HALF_MIRROR>(s));
+          s = __fadd_rn(s, dpp<DPP_ROW_MIRROR>(s));
+          if (at.li == 0) cs[at.wm * MM_T + MmTile<ET>::col(at.wn, at.lg, y, j) + q] = s;
+        }
+    lds_barrier();
+    if (threadIdx.x < MM_T)
+      p.colpart[mt * p.ldg + g0 + threadIdx.x] =
+          __fmul_rn(p.scale[1], __fadd_rn(cs[threadIdx.x], cs[MM_T + threadIdx.x]));
   }
+};
+
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  const XentGrad<ET> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
+  mm_run<ET, false, false>(prob, mm_buf);
 }
 
 // grad_bias of one piece: the row tiles' column sums in ascending order.
@@ -383,50 +409,70 @@ __global__ __launch_bounds__(256) void xent_bias_kernel(const float *__restrict_
 
 // G W of one piece, one split of its columns, into that split's fp32 sums.
 template <int ET>
+struct XentDHidden {
+  XentBwdArgs p;
+  int64_t nmt, nht, splits;
+
+  __device__ __forceinline__ int64_t tiles() const { return nmt * nht * splits; }
+  __device__ __forceinline__ void place(int32_t t, int64_t &m0, int64_t &h0, int64_t &sp) const {
+    int64_t mt, ht;
+    const uint32_t per = (uint32_t)(nmt * nht);
+    sp = mm_uni((uint32_t)t / per);
+    mm_tile_at((uint32_t)t - (uint32_t)sp * per, nmt, nht, mt, ht);
+    m0 = mt * MM_T;
+    h0 = ht * MM_T;
+  }
+  __device__ __forceinline__ MmJob job(int32_t t) const {
+    int64_t m0, h0, sp;
+    place(t, m0, h0, sp);
+    const int64_t k0 = sp * p.ksplit, kn = p.np - k0 < p.ksplit ? p.np - k0 : p.ksplit;
+    const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
+    // the weight rows present (G is 0 in columns past them)
+    int64_t wrows = p.V - p.v0 - k0 < kn ? p.V - p.v0 - k0 : kn;
+    if (wrows < 0) wrows = 0;
+    const int64_t rb = p.H * 2;
+    return MmJob{{p.G + (m0 * p.ldg + k0) * 2, (uint32_t)(p.ldg * 2), (int32_t)rows, (uint32_t)(kn * 2)},
+                 {p.W + (wrows > 0 ? (p.v0 + k0) * rb : 0) + h0 * 2, (uint32_t)rb, (int32_t)wrows,
+                  (uint32_t)((p.H - h0) * 2)},
+                 (int32_t)(kn / 64), 0};
+  }
+  __device__ __forceinline__ void epilogue(MmTile<ET> &tile, int32_t t) const {
+    int64_t m0, h0, sp;
+    place(t, m0, h0, sp);
+    const LanePlace at;
+    const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
+    float *const out = p.dh + (sp * p.M + m0) * p.H + h0;
+    const rsrc_t rs = make_rsrc(out, (uint32_t)(((rows - 1) * p.H + (p.H - h0 < MM_T ? p.H - h0 : MM_T)) * 4));
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = MmTile<ET>::row(at.wm, at.li, x, i);
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = MmTile<ET>::col(at.wn, at.lg, y, j);
+            const bool ok = r < rows && h0 + c < p.H;
+            const uint32_t off = ok ? (uint32_t)((r * p.H + c) * 4) : OFF_NONE;
+            f32x4 v = tile.c[x][y][i][j];
+            if (!p.first) {
+              const f32x4 o = __builtin_bit_cast(f32x4, load16(rs, off, 0));
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] = __fadd_rn(o[q], v[q]);
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, 0, LOAD_DEFAULT);
+          }
+      }
+  }
+};
+
+template <int ET>
 __global__ __launch_bounds__(MM_THREADS, 1) void xent_dhidden_kernel(XentBwdArgs p) {
   MM_SHARED();
-  const int64_t nmt = (p.M + MM_T - 1) / MM_T, nht = (p.H + MM_T - 1) / MM_T;
-  const int64_t splits = (p.vp + p.ksplit - 1) / p.ksplit;
-  const int64_t t = mm_position(nmt * nht * splits), sp = t / (nmt * nht);
-  int64_t mt, ht;
-  mm_tile_at(t - sp * nmt * nht, nmt, nht, mt, ht);
-  const int64_t m0 = mt * MM_T, h0 = ht * MM_T;
-  const int64_t k0 = sp * p.ksplit, kn = p.vp - k0 < p.ksplit ? p.vp - k0 : p.ksplit;
-  const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
-  const int64_t rb = p.H * 2;
-  // the weight rows present; a split that only fills the piece up has none
-  int64_t wrows = p.V - p.v0 - k0 < kn ? p.V - p.v0 - k0 : kn;
-  if (wrows < 0) wrows = 0;
-  const MmOperand a{p.G + (m0 * p.vp + k0) * 2, p.vp * 2, rows, 0, kn * 2};
-  const MmOperand b{p.W + (wrows > 0 ? (p.v0 + k0) * rb : 0) + h0 * 2, rb, wrows, (p.H - h0) * 2, 0};
-  MmTile<ET> tile;
-  mm_main<ET, false, true>(tile, a, b, kn / 64, [](int64_t s) { return s; }, mm_buf);
-
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  float *const out = p.dh + (sp * p.M + m0) * p.H + h0;
-  const rsrc_t rs = make_rsrc(out, (uint32_t)(((rows - 1) * p.H + (p.H - h0 < MM_T ? p.H - h0 : MM_T)) * 4));
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = MmTile<ET>::row(wm, li, x, i);
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c = MmTile<ET>::col(wn, lg, y, j);
-          const bool ok = r < rows && h0 + c < p.H;
-          const uint32_t off = ok ? (uint32_t)((r * p.H + c) * 4) : OFF_NONE;
-          f32x4 v = tile.c[x][y][i][j];
-          if (!p.first) {
-            const f32x4 o = __builtin_bit_cast(f32x4, load16(rs, off, 0));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = __fadd_rn(o[q], v[q]);
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, off, 0, LOAD_DEFAULT);
-        }
-    }
+  const XentDHidden<ET> prob{p, (p.M + MM_T - 1) / MM_T, (p.H + MM_T - 1) / MM_T,
+                             (p.np + p.ksplit - 1) / p.ksplit};
+  mm_run<ET, false, true>(prob, mm_buf);
 }
 
 // grad_hidden: the splits' sums in ascending order, scaled, rounded once.
@@ -456,39 +502,53 @@ __global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__re
 
 // G^T hidden of one piece: its rows of grad_W.
 template <int ET>
+struct XentDWeight {
+  XentBwdArgs p;
+  u32x4 *epi;
+  int64_t ngt, nht;
+
+  __device__ __forceinline__ int64_t tiles() const { return ngt * nht; }
+  __device__ __forceinline__ MmJob job(int32_t t) const {
+    int64_t gt, ht;
+    mm_tile_at(t, ngt, nht, gt, ht);
+    const int64_t g0 = gt * MM_T, h0 = ht * MM_T;
+    return MmJob{{p.G + g0 * 2, (uint32_t)(p.ldg * 2), (int32_t)p.M, (uint32_t)((p.ldg - g0) * 2)},
+                 {p.hidden + h0 * 2, (uint32_t)(p.H * 2), (int32_t)p.M, (uint32_t)((p.H - h0) * 2)},
+                 (int32_t)((p.M + 63) / 64), 0};
+  }
+  __device__ __forceinline__ void epilogue(MmTile<ET> &tile, int32_t t) const {
+    int64_t gt, ht;
+    mm_tile_at(t, ngt, nht, gt, ht);
+    const int64_t g0 = gt * MM_T, h0 = ht * MM_T, nv = p.V - p.v0 - g0;
+    const LanePlace at;
+    const float f = __fmul_rn(p.alpha, p.scale[1]);
+    uint8_t *const out = reinterpret_cast<uint8_t *>(p.dw + (p.v0 + g0) * p.H + h0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int ip = 0; ip < 2; ++ip) {
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              f32x4 v = tile.c[x][y][2 * ip + ii][j];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[q] = __fmul_rn(f, v[q]);
+              mm_stage4<ET>(epi, at.wm, at.wn, at.li, at.lg, y, 2 * ip + ii, j, v);
+            }
+        mm_store_quarter<STORE_POLICY>(epi, x, ip, out, p.H * 2, nv < MM_T ? nv : MM_T, (p.H - h0) * 2);
+      }
+  }
+};
+
+template <int ET>
 __global__ __launch_bounds__(MM_THREADS, 1) void xent_dweight_kernel(XentBwdArgs p) {
   MM_SHARED();
-  const int64_t nht = (p.H + MM_T - 1) / MM_T;
-  const int64_t nv = p.V - p.v0 < p.vp ? p.V - p.v0 : p.vp;
-  const int64_t ngt = (nv + MM_T - 1) / MM_T;
-  int64_t gt, ht;
-  mm_tile_at(mm_position(nht * ngt), ngt, nht, gt, ht);
-  const int64_t h0 = ht * MM_T, g0 = gt * MM_T;
-  const MmOperand a{p.G + g0 * 2, p.vp * 2, p.M, (p.vp - g0) * 2, 0};
-  const MmOperand b{p.hidden + h0 * 2, p.H * 2, p.M, (p.H - h0) * 2, 0};
-  MmTile<ET> tile;
-  mm_main<ET, true, true>(tile, a, b, (p.M + 63) / 64, [](int64_t s) { return s; }, mm_buf);
-
-  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 2, wn = wave & 3;
-  const float f = __fmul_rn(p.alpha, p.scale[1]);
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          f32x4 v = tile.c[x][y][i][j];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = __fmul_rn(f, v[q]);
-          mm_stage4<ET>(mm_buf, wm, wn, li, lg, x, y, i, j, v);
-        }
-  __syncthreads();
-  const int64_t rows = nv - g0 < MM_T ? nv - g0 : MM_T;
-  mm_store_tile16<STORE_POLICY>(mm_buf, reinterpret_cast<uint8_t *>(p.dw + (p.v0 + g0) * p.H + h0), p.H * 2,
-                             rows, (p.H - h0) * 2);
+  MM_EPI_SHARED();
+  const XentDWeight<ET> prob{p, mm_epi, p.np / MM_T, (p.H + MM_T - 1) / MM_T};
+  mm_run<ET, true, true>(prob, mm_buf);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -547,7 +607,7 @@ hipError_t zero_words(void *p, int64_t n, hipStream_t s) {
 template <int ET>
 hipError_t forward(const XentFwdArgs &p, float *loss, float *lse, hipStream_t s) {
   const int64_t nmt = ceil_div(p.M, MM_T), nvt = ceil_div(p.V, MM_T);
-  hipError_t e = launch_kernel(xent_stats_kernel<ET>, dim3((unsigned)(nmt * nvt)), dim3(MM_THREADS), s, p);
+  hipError_t e = launch_kernel(xent_stats_kernel<ET>, mm_grid(nmt * nvt), dim3(MM_THREADS), s, p);
   if (e != hipSuccess) return e;
   return launch_kernel(xent_combine_kernel, dim3((unsigned)ceil_div(p.M, XC_ROWS)),
                        dim3(XC_ROWS * XC_SLICES), s, p, nvt, loss, lse);
@@ -578,7 +638,7 @@ hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
   p.bias = c.bias;
   p.rows = rows;
   p.scale = scale;
-  p.vp = pl.vp;
+  p.ldg = pl.vp;
   p.G = ws + pl.off_g;
   p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + pl.off_col) : nullptr;
   p.dh = reinterpret_cast<float *>(ws + pl.off_dh);
@@ -589,14 +649,16 @@ hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
     p.v0 = v0;
     p.first = v0 == 0;
     const int64_t nv = c.V - v0 < pl.vp ? c.V - v0 : pl.vp;
-    e = launch_kernel(xent_grad_kernel<ET>, dim3((unsigned)(nmt * (pl.vp / MM_T))), dim3(MM_THREADS), s, p);
+    p.np = ceil_div(nv, MM_T) * MM_T;
+    e = launch_kernel(xent_grad_kernel<ET>, mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p);
     if (e == hipSuccess && c.grad_bias != nullptr)
       e = launch_kernel(xent_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
                         static_cast<const float *>(p.colpart), nmt, pl.vp, nv, c.grad_bias + v0);
     if (e == hipSuccess && c.grad_hidden != nullptr)
-      e = launch_kernel(xent_dhidden_kernel<ET>, dim3((unsigned)(nmt * nht * pl.splits)), dim3(MM_THREADS), s, p);
+      e = launch_kernel(xent_dhidden_kernel<ET>, mm_grid(nmt * nht * ceil_div(p.np, pl.ksplit)),
+                        dim3(MM_THREADS), s, p);
     if (e == hipSuccess && c.grad_W != nullptr)
-      e = launch_kernel(xent_dweight_kernel<ET>, dim3((unsigned)(nht * ceil_div(nv, MM_T))), dim3(MM_THREADS), s, p);
+      e = launch_kernel(xent_dweight_kernel<ET>, mm_grid(nht * (p.np / MM_T)), dim3(MM_THREADS), s, p);
   }
   if (e == hipSuccess && c.grad_hidden != nullptr)
     e = launch_kernel(xent_dhidden_out_kernel<ET>, dim3((unsigned)ceil_div(c.M * c.H, 2048)), dim3(256), s,
