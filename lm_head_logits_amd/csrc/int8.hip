@@ -371,45 +371,52 @@ struct Int8Tiles {
     OutT *const out = static_cast<OutT *>(p.out) + m0 * p.V + n0;
     const bool vec = p.V % 4 == 0;
     const bool staged = sizeof(OutT) == 2 && p.V % 8 == 0;
+    float sc[2][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int ip = 0; ip < 2; ++ip) {
-        float sc[2];
+      for (int i = 0; i < 4; ++i) {
+        const int r = MmTile<ET_I8>::row(wm, li, x, i);
+        sc[x][i] = r < rows ? p.hs[m0 + r] : 0.0f;
+      }
+    MmParts parts{epi, 0};
+    const rsrc_t rs = mm_out_rsrc(out, p.V * 2, rows, cols * 2);
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii) {
-          const int r = MmTile<ET_I8>::row(wm, li, x, 2 * ip + ii);
-          sc[ii] = r < rows ? p.hs[m0 + r] : 0.0f;
+    for (int y = 0; y < 2; ++y) {
+      float ws[2][4], bv[2][4];
+      int n[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = MmTile<ET_I8>::col(wn, lg, y, j);
+        n[j] = c >= cols ? 0 : (cols - c < 4 ? (int)(cols - c) : 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          ws[j][q] = q < n[j] ? p.ws[n0 + c + q] : 0.0f;
+          bv[j][q] = q < n[j] && has_bias ? p.bias[n0 + c + q] : 0.0f;
         }
+      }
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c = MmTile<ET_I8>::col(wn, lg, y, j);
-            const int n = c >= cols ? 0 : (cols - c < 4 ? (int)(cols - c) : 4);
-            float ws[4], bv[4];
+        for (int ip = 0; ip < 2; ++ip) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              ws[q] = q < n ? p.ws[n0 + c + q] : 0.0f;
-              bv[q] = q < n && has_bias ? p.bias[n0 + c + q] : 0.0f;
-            }
+          for (int i = 2 * ip; i < 2 * ip + 2; ++i)
 #pragma unroll
-            for (int ii = 0; ii < 2; ++ii) {
-              const int i = 2 * ip + ii, r = MmTile<ET_I8>::row(wm, li, x, i);
+            for (int j = 0; j < 2; ++j) {
+              const int r = MmTile<ET_I8>::row(wm, li, x, i);
               float v[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                v[q] = i8_logit(tile.c[x][y][i][j][q], sc[ii], ws[q], p.alpha, has_bias, bv[q]);
+                v[q] = i8_logit(tile.c[x][y][i][j][q], sc[x][i], ws[j][q], p.alpha, has_bias, bv[j][q]);
               if (staged)
-                mm_stage4<std::is_same_v<OutT, _Float16> ? ET_F16 : ET_BF16>(
-                    epi, wm, wn, li, lg, y, i, j, f32x4{v[0], v[1], v[2], v[3]});
+                parts.put<std::is_same_v<OutT, _Float16> ? ET_F16 : ET_BF16>(wm, wn, li, lg, i, j,
+                                                                             f32x4{v[0], v[1], v[2], v[3]});
               else if (r < rows)
-                store4<OutT>(out + r * p.V + c, v, n, vec);
+                store4<OutT>(out + r * p.V + MmTile<ET_I8>::col(wn, lg, y, j), v, n[j], vec);
             }
-          }
-        if (staged)
-          mm_store_quarter<STORE_POLICY>(epi, x, ip, reinterpret_cast<uint8_t *>(out), p.V * 2, rows, cols * 2);
-      }
+          if (staged) parts.flush<STORE_POLICY>(rs, y, x, ip, (uint32_t)p.V * 2, (int)rows, cols * 2);
+        }
+    }
   }
 };
 

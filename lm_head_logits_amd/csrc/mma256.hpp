@@ -224,12 +224,17 @@ struct MmSide {
       kb = OFF_NONE;
     }
   }
-  // K-inner: a row's last stage may be partial; what lies past the row is not loaded.
+  // K-inner: a row's last stage may be partial; what lies past the row is not
+  // loaded. A branch around both (the empty asm keeps it one), so that rows of
+  // whole stages pay no vector operations in a read part: 4% of the product.
   __device__ __forceinline__ void trim(bool last) {
     if constexpr (!OUTER) {
+      if (bytes % MM_STAGE_BYTES != 0) {
+        asm volatile("");
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        cur[u] = last && kb + 16 * piece(u) >= bytes ? OFF_NONE : voff[u];
+        for (int u = 0; u < 2; ++u)
+          cur[u] = last && kb + 16 * piece(u) >= bytes ? OFF_NONE : voff[u];
+      }
     }
   }
 
@@ -504,40 +509,44 @@ __device__ __forceinline__ uint32_t mm_pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
-// 16-bit results leave through MM_EPI in quarters: quarter (x, ip) holds the 64
-// rows 128 x + 64 wm + 32 ip + (0 .. 31) of the tile, row by row (512 bytes;
-// its 32-byte pieces xor-ed with the row so that the 16 rows one store touches
-// fall in distinct banks), and is written to memory as whole rows in 16-byte
-// stores.
-//
-// Four columns of one row, block (i, j) of quadrant (x, y), into the quarter.
-template <int ET>
-__device__ __forceinline__ void mm_stage4(u32x4 *epi, int wm, int wn, int li, int lg, int y, int i, int j,
-                                          f32x4 v) {
-  const int r = wm * 32 + (i & 1) * 16 + li;
-  const int piece = (y * 128 + wn * 32 + 16 * j) / 16;
-  uint8_t *const at = reinterpret_cast<uint8_t *>(epi) + r * 512 + ((piece ^ li) * 32) + 8 * lg;
-  *reinterpret_cast<u32x2 *>(at) = u32x2{mm_pack2<ET>(v[0], v[1]), mm_pack2<ET>(v[2], v[3])};
-}
+// 16-bit results leave through MM_EPI in eight parts: part (y, x, ip) holds the
+// 64 rows 128 x + 64 wm + 32 ip + (0 .. 31) of the tile's columns y 128 .. + 127,
+// row by row (256 bytes; its 32-byte pieces xor-ed with the row, for the
+// banks), and is written to memory as whole rows in 16-byte stores. Two buffers
+// take turns, so each part costs one barrier: a wave that writes a buffer has
+// met, since it was last read, the barrier that its readers met after reading.
+struct MmParts {
+  u32x4 *epi;
+  int n;  // parts so far
 
-// Writes quarter (x, ip): `out` is the tile's first element, `ld` bytes between
-// rows, `rows` rows of `bytes` bytes (a multiple of 16) present. Between
-// barriers of its own on both sides.
-template <int POLICY>
-__device__ __forceinline__ void mm_store_quarter(const u32x4 *epi, int x, int ip, uint8_t *out, int64_t ld,
-                                                 int64_t rows, int64_t bytes) {
-  lds_barrier();
-  const rsrc_t rs = make_rsrc(out, (uint32_t)((rows - 1) * ld + (bytes < 512 ? bytes : 512)));
-  const int tid = mm_tid(), c = tid % 32, r0 = tid / 32;
-#pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int s = it * 16 + r0;  // row of the quarter
-    const int r = 128 * x + 64 * (s >> 5) + 32 * ip + (s & 31);
-    const u32x4 v = epi[s * 32 + (((c >> 1) ^ (s & 15)) * 2) + (c & 1)];
-    const bool ok = r < rows && 16 * c < bytes;
-    __builtin_amdgcn_raw_buffer_store_b128(v, rs, ok ? (uint32_t)(r * ld + 16 * c) : OFF_NONE, 0, POLICY);
+  __device__ __forceinline__ uint8_t *buf() const { return reinterpret_cast<uint8_t *>(epi) + (n & 1) * 16384; }
+  // Four columns of one row: block (i, j) of quadrant (x, y).
+  template <int ET>
+  __device__ __forceinline__ void put(int wm, int wn, int li, int lg, int i, int j, f32x4 v) const {
+    const int r = wm * 32 + (i & 1) * 16 + li;
+    uint8_t *const at = buf() + r * 256 + (((wn * 2 + j) ^ (li & 7)) * 32) + 8 * lg;
+    *reinterpret_cast<u32x2 *>(at) = u32x2{mm_pack2<ET>(v[0], v[1]), mm_pack2<ET>(v[2], v[3])};
   }
-  lds_barrier();
+  // Writes part (y, x, ip): `rs` covers the tile from its first element, `ld`
+  // bytes between rows, `rows` rows of `bytes` bytes (a multiple of 16) present.
+  template <int POLICY>
+  __device__ __forceinline__ void flush(rsrc_t rs, int y, int x, int ip, uint32_t ld, int rows, int64_t bytes) {
+    lds_barrier();
+    const int tid = mm_tid(), c = tid % 16, r0 = tid / 16;
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+      const int r = 128 * x + 64 * it + 32 * ip + r0;
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(buf() + (it * 32 + r0) * 256 +
+                                                       (((c >> 1) ^ (r0 & 7)) * 32) + 16 * (c & 1));
+      const uint32_t at = 256 * y + 16 * c;
+      __builtin_amdgcn_raw_buffer_store_b128(v, rs, r < rows && at < bytes ? r * ld + at : OFF_NONE, 0, POLICY);
+    }
+    ++n;
+  }
+};
+// The resource of flush(): `rows` rows of `bytes` bytes at `out`.
+__device__ __forceinline__ rsrc_t mm_out_rsrc(void *out, int64_t ld, int64_t rows, int64_t bytes) {
+  return make_rsrc(out, (uint32_t)((rows - 1) * ld + (bytes < 512 ? bytes : 512)));
 }
 
 }  // namespace lmhead

@@ -33,6 +33,10 @@ namespace lmhead {
 namespace {
 
 constexpr float NEG_INF = -__builtin_inff();
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;  // log2 e, ln 2
+
+// 2^x, the hardware's (below 2^-126: 0).
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 struct XentFwdArgs {
   const uint8_t *hidden, *W;
@@ -42,7 +46,7 @@ struct XentFwdArgs {
   const void *target;
   int target64;
   int64_t ignore;
-  float2 *part;   // [vocabulary tile][M] {largest t, sum of exp(t - largest)}
+  float2 *part;   // [vocabulary tile][M] {largest u = t log2 e, sum of 2^(u - largest)}
   float *tlogit;  // [M] t at the target (rows with one)
 };
 
@@ -77,6 +81,33 @@ struct LanePlace {
   }
 };
 
+// The biases of the lane's eight columns in half y, times log2 e; columns that
+// are not there get -inf, so that their probability is 0.
+template <int ET>
+__device__ __forceinline__ void column_bias(const float *bias, int64_t V, int64_t n0, const LanePlace &at, int y,
+                                            float (&b)[2][4]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) b[j][q] = 0.0f;
+  if (bias != nullptr || n0 + MM_T > V)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
+        b[j][q] = c < V ? (bias != nullptr ? __fmul_rn(LOG2E, bias[c]) : 0.0f) : NEG_INF;
+      }
+}
+
+// Whether column c of the tile is one of the lane's in half y (columns y 128 +
+// wn 32 + j 16 + 4 lg + q). Few are, so what is done for a row's target is
+// skipped by nearly every wave instead of being a comparison per logit.
+template <int ET>
+__device__ __forceinline__ bool has_column(const LanePlace &at, int y, int32_t c) {
+  return (c >> 5) == y * 4 + at.wn && ((c >> 2) & 3) == at.lg;
+}
+
 template <int ET>
 struct XentStats {
   XentFwdArgs p;
@@ -94,19 +125,11 @@ struct XentStats {
     mm_tile_at(t, nmt, nvt, mt, vt);
     const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
     const LanePlace at;
-    const bool has_bias = p.bias != nullptr;
+    // everything in units of log 2: u = t log2 e, one multiplication per logit
+    const float k = __fmul_rn(p.alpha, LOG2E);
     float bias[2][2][4];
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
-          // columns that are not there get t = -inf
-          bias[y][j][q] = c < p.V ? (has_bias ? p.bias[c] : 0.0f) : NEG_INF;
-        }
-    const bool add = has_bias || n0 + MM_T > p.V;
+    column_bias<ET>(p.bias, p.V, n0, at, 0, bias[0]);
+    column_bias<ET>(p.bias, p.V, n0, at, 1, bias[1]);
     float2 *const stat = reinterpret_cast<float2 *>(epi);  // [4][256]
 #pragma unroll
     for (int x = 0; x < 2; ++x)
@@ -114,21 +137,30 @@ struct XentStats {
       for (int i = 0; i < 4; ++i) {
         const int row = MmTile<ET>::row(at.wm, at.li, x, i);
         const int64_t m = m0 + row;
-        const int64_t yt = m < p.M ? target_of(p.target, p.target64, m, p.ignore, p.V) - n0 : -1;
+        const int32_t yt = m < p.M ? (int32_t)target_of(p.target, p.target64, m, p.ignore, p.V) - (int32_t)n0 : -1;
         float mx = NEG_INF;
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c0 = MmTile<ET>::col(at.wn, at.lg, y, j);
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float v = epilogue_v(tile.c[x][y][i][j][q], p.alpha, add, bias[y][j][q]);
-              if (yt == c0 + q) p.tlogit[m] = v;
-              tile.c[x][y][i][j][q] = v;
-              mx = fmaxf(mx, v);
+              const float acc = tile.c[x][y][i][j][q];
+              const float u = __fmaf_rn(k, acc, bias[y][j][q]);
+              tile.c[x][y][i][j][q] = u;
+              mx = fmaxf(mx, u);
             }
-          }
+        if (has_column<ET>(at, 0, yt) || has_column<ET>(at, 1, yt)) {
+          float u = 0.0f;
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (yt == MmTile<ET>::col(at.wn, at.lg, y, j) + q) u = tile.c[x][y][i][j][q];
+          p.tlogit[m] = __fmul_rn(u, LN2);
+        }
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         // a tile of only -inf sums nothing: its terms are taken against 0
@@ -140,7 +172,7 @@ struct XentStats {
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              s = __fadd_rn(s, exp_fast(__fsub_rn(tile.c[x][y][i][j][q], mz)));
+              s = __fadd_rn(s, exp2_fast(__fsub_rn(tile.c[x][y][i][j][q], mz)));
         s = __fadd_rn(s, __shfl_xor(s, 16));
         s = __fadd_rn(s, __shfl_xor(s, 32));
         if (at.lg == 0) stat[at.wn * MM_T + row] = float2{mx, s};
@@ -154,7 +186,7 @@ struct XentStats {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 e = stat[w * MM_T + row];
-        if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp_fast(__fsub_rn(e.x, mx))));
+        if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp2_fast(__fsub_rn(e.x, mx))));
       }
       p.part[vt * p.M + m0 + row] = float2{mx, s};
     }
@@ -175,8 +207,8 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p
 constexpr int XC_ROWS = 64, XC_SLICES = 16;
 __device__ __forceinline__ void fold_stat(float &m, float &s, float2 e) {
   const float n = fmaxf(m, e.x);
-  const float a = s == 0.0f ? 0.0f : __fmul_rn(s, exp_fast(__fsub_rn(m, n)));
-  const float b = e.y == 0.0f ? 0.0f : __fmul_rn(e.y, exp_fast(__fsub_rn(e.x, n)));
+  const float a = s == 0.0f ? 0.0f : __fmul_rn(s, exp2_fast(__fsub_rn(m, n)));
+  const float b = e.y == 0.0f ? 0.0f : __fmul_rn(e.y, exp2_fast(__fsub_rn(e.x, n)));
   s = __fadd_rn(a, b);
   m = n;
 }
@@ -204,7 +236,7 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
 #pragma unroll
   for (int k = 1; k < XC_SLICES; ++k) fold_stat(mx, s, sh[k][r]);
   // every logit -inf: log-sum-exp -inf, and a target's probability 0
-  const float l = s == 0.0f ? NEG_INF : __fadd_rn(mx, logf(s));
+  const float l = s == 0.0f ? NEG_INF : __fmul_rn(LN2, __fadd_rn(mx, log2f(s)));
   lse[m] = l;
   float out = 0.0f;
   if (target_of(p.target, p.target64, m, p.ignore, p.V) >= 0) {
@@ -218,10 +250,10 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
 // Backward
 // ---------------------------------------------------------------------------
 
-// What the epilogue needs of a row: G = a exp(t - lse) - b [v = y].
+// What the epilogue needs of a row: G = a 2^(t log2 e - lse) - b [v = y].
 struct alignas(16) RowCoef {
-  float a, b, lse;
-  int32_t y;  // target column, or -1
+  float a, b, lse;  // lse times log2 e
+  int32_t y;        // target column, or -1
 };
 
 // G is kept scaled by f = top / mx, mx the largest |a| or |b| of the rows and
@@ -282,7 +314,7 @@ __global__ __launch_bounds__(XR_THREADS) void xent_rows_kernel(XentRowsArgs p) {
   if (!p.write_rows || m >= p.M) return;
   float a, b;
   const int64_t y = coef(m, a, b);
-  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], (int32_t)y};
+  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), __fmul_rn(LOG2E, p.lse[m]), (int32_t)y};
 }
 
 struct XentBwdArgs {
@@ -302,8 +334,8 @@ struct XentBwdArgs {
   uint16_t *dw;        // [V, H]
 };
 
-// G of one piece.
-template <int ET>
+// G of one piece; DB: and its column sums.
+template <int ET, bool DB>
 struct XentGrad {
   XentBwdArgs p;
   u32x4 *epi;
@@ -320,80 +352,86 @@ struct XentGrad {
     mm_tile_at(t, nmt, ngt, mt, gt);
     const int64_t m0 = mt * MM_T, g0 = gt * MM_T, n0 = p.v0 + g0;
     const LanePlace at;
-    const bool has_bias = p.bias != nullptr;
-    float bias[2][2][4];
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
-          // columns that are not there get t = -inf, so G = 0
-          bias[y][j][q] = c < p.V ? (has_bias ? p.bias[c] : 0.0f) : NEG_INF;
-        }
-    const bool add = has_bias || n0 + MM_T > p.V;
+    // p = 2^(t log2 e - lse log2 e)
+    const float k = __fmul_rn(p.alpha, LOG2E);
     const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
-    float colsum[2][2][4] = {};
+    RowCoef rc[2][4];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int ip = 0; ip < 2; ++ip) {
+      for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + MmTile<ET>::row(at.wm, at.li, x, i);
+        // 2^-inf = 0 in rows past the end, and where the whole row is -inf
+        rc[x][i] = m < p.M ? p.rows[m] : RowCoef{0.0f, 0.0f, __builtin_inff(), -1};
+        if (rc[x][i].lse == NEG_INF) rc[x][i].lse = 0.0f;
+        rc[x][i].y = rc[x][i].y < 0 ? -1 : rc[x][i].y - (int32_t)n0;
+      }
+    MmParts parts{epi, 0};
+    const rsrc_t rs = mm_out_rsrc(p.G + (m0 * p.ldg + g0) * 2, p.ldg * 2, rows, 512);
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii) {
-          const int i = 2 * ip + ii;
-          const int64_t m = m0 + MmTile<ET>::row(at.wm, at.li, x, i);
-          // exp(-inf) = 0 in rows past the end, and where the whole row is -inf
-          const RowCoef rc = m < p.M ? p.rows[m] : RowCoef{0.0f, 0.0f, __builtin_inff(), -1};
-          const float lse = rc.lse == NEG_INF ? 0.0f : rc.lse;
-          const int64_t yt = (int64_t)rc.y - n0;
+    for (int y = 0; y < 2; ++y) {
+      float bias[2][4], colsum[2][4] = {};
+      column_bias<ET>(p.bias, p.V, n0, at, y, bias);
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int ip = 0; ip < 2; ++ip) {
+#pragma unroll
+          for (int i = 2 * ip; i < 2 * ip + 2; ++i) {
+            const RowCoef &r = rc[x][i];
+            f32x4 g[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                g[j][q] = __fmul_rn(
+                    r.a, exp2_fast(__fsub_rn(__fmaf_rn(k, tile.c[x][y][i][j][q], bias[j][q]), r.lse)));
+            if (has_column<ET>(at, y, r.y))
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if (r.y == MmTile<ET>::col(at.wn, at.lg, y, j) + q) g[j][q] = __fsub_rn(g[j][q], r.b);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int c0 = MmTile<ET>::col(at.wn, at.lg, y, j);
-              f32x4 v;
+              if constexpr (DB)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float tv = epilogue_v(tile.c[x][y][i][j][q], p.alpha, add, bias[y][j][q]);
-                float gv = __fmul_rn(rc.a, exp_fast(__fsub_rn(tv, lse)));
-                if (yt == c0 + q) gv = __fsub_rn(gv, rc.b);
-                v[q] = gv;
-                colsum[y][j][q] = __fadd_rn(colsum[y][j][q], gv);
-              }
-              mm_stage4<ET>(epi, at.wm, at.wn, at.li, at.lg, y, i, j, v);
+                for (int q = 0; q < 4; ++q) colsum[j][q] = __fadd_rn(colsum[j][q], g[j][q]);
+              parts.put<ET>(at.wm, at.wn, at.li, at.lg, i, j, g[j]);
             }
+          }
+          parts.flush<LOAD_DEFAULT>(rs, y, x, ip, (uint32_t)p.ldg * 2, (int)rows, 512);
         }
-        mm_store_quarter<LOAD_DEFAULT>(epi, x, ip, p.G + (m0 * p.ldg + g0) * 2, p.ldg * 2, rows, 512);
+      if constexpr (DB) {
+        // column sums: 16 rows of a block by lane exchanges, then the two wave
+        // rows, through the buffer whose turn it is
+        float *const cs = reinterpret_cast<float *>(parts.buf());  // [2][128]
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float s = colsum[j][q];
+            s = __fadd_rn(s, dpp<DPP_QUAD_SWAP1>(s));
+            s = __fadd_rn(s, dpp<DPP_QUAD_SWAP2>(s));
+            s = __fadd_rn(s, dpp<DPP_ROW_HALF_MIRROR>(s));
+            s = __fadd_rn(s, dpp<DPP_ROW_MIRROR>(s));
+            if (at.li == 0) cs[at.wm * 128 + MmTile<ET>::col(at.wn, at.lg, 0, j) + q] = s;
+          }
+        lds_barrier();
+        ++parts.n;
+        const int c = mm_tid();
+        if (c < 128)
+          p.colpart[mt * p.ldg + g0 + y * 128 + c] = __fmul_rn(p.scale[1], __fadd_rn(cs[c], cs[128 + c]));
       }
-    if (p.colpart == nullptr) return;
-    // column sums: 16 rows of a block by lane exchanges, then the two wave rows
-    float *const cs = reinterpret_cast<float *>(epi);  // [2][256]
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float s = colsum[y][j][q];
-          s = __fadd_rn(s, dpp<DPP_QUAD_SWAP1>(s));
-          s = __fadd_rn(s, dpp<DPP_QUAD_SWAP2>(s));
-          s = __fadd_rn(s, dpp<DPP_ROW_HALF_MIRROR>(s));
-          s = __fadd_rn(s, dpp<DPP_ROW_MIRROR>(s));
-          if (at.li == 0) cs[at.wm * MM_T + MmTile<ET>::col(at.wn, at.lg, y, j) + q] = s;
-        }
-    lds_barrier();
-    if (threadIdx.x < MM_T)
-      p.colpart[mt * p.ldg + g0 + threadIdx.x] =
-          __fmul_rn(p.scale[1], __fadd_rn(cs[threadIdx.x], cs[MM_T + threadIdx.x]));
+    }
   }
 };
 
-template <int ET>
+template <int ET, bool DB>
 __global__ __launch_bounds__(MM_THREADS, 1) void xent_grad_kernel(XentBwdArgs p) {
   MM_SHARED();
   MM_EPI_SHARED();
-  const XentGrad<ET> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
+  const XentGrad<ET, DB> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
   mm_run<ET, false, false>(prob, mm_buf);
 }
 
@@ -522,24 +560,26 @@ struct XentDWeight {
     const int64_t g0 = gt * MM_T, h0 = ht * MM_T, nv = p.V - p.v0 - g0;
     const LanePlace at;
     const float f = __fmul_rn(p.alpha, p.scale[1]);
-    uint8_t *const out = reinterpret_cast<uint8_t *>(p.dw + (p.v0 + g0) * p.H + h0);
+    const int64_t rows = nv < MM_T ? nv : MM_T, bytes = (p.H - h0) * 2;
+    const rsrc_t rs = mm_out_rsrc(p.dw + (p.v0 + g0) * p.H + h0, p.H * 2, rows, bytes);
+    MmParts parts{epi, 0};
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int y = 0; y < 2; ++y)
 #pragma unroll
-      for (int ip = 0; ip < 2; ++ip) {
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii)
+        for (int ip = 0; ip < 2; ++ip) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+          for (int i = 2 * ip; i < 2 * ip + 2; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              f32x4 v = tile.c[x][y][2 * ip + ii][j];
+              f32x4 v = tile.c[x][y][i][j];
 #pragma unroll
               for (int q = 0; q < 4; ++q) v[q] = __fmul_rn(f, v[q]);
-              mm_stage4<ET>(epi, at.wm, at.wn, at.li, at.lg, y, 2 * ip + ii, j, v);
+              parts.put<ET>(at.wm, at.wn, at.li, at.lg, i, j, v);
             }
-        mm_store_quarter<STORE_POLICY>(epi, x, ip, out, p.H * 2, nv < MM_T ? nv : MM_T, (p.H - h0) * 2);
-      }
+          parts.flush<STORE_POLICY>(rs, y, x, ip, (uint32_t)p.H * 2, (int)rows, bytes);
+        }
   }
 };
 
@@ -650,7 +690,7 @@ hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
     p.first = v0 == 0;
     const int64_t nv = c.V - v0 < pl.vp ? c.V - v0 : pl.vp;
     p.np = ceil_div(nv, MM_T) * MM_T;
-    e = launch_kernel(xent_grad_kernel<ET>, mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p);
+    e = launch_kernel(c.grad_bias != nullptr ? xent_grad_kernel<ET, true> : xent_grad_kernel<ET, false>, mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p);
     if (e == hipSuccess && c.grad_bias != nullptr)
       e = launch_kernel(xent_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
                         static_cast<const float *>(p.colpart), nmt, pl.vp, nv, c.grad_bias + v0);
