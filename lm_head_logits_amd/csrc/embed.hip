@@ -95,26 +95,30 @@ struct Fill {
   int64_t from, to;
   int sort_blocks; // work-groups of the launch that sort
 };
-constexpr int FILL_PER_THREAD = 16;
+// Each fill work-group writes one contiguous part; FILL_BLOCKS of them, three
+// per CU, behind the sorting ones. Not kept in the caches (nothing reads the
+// zeros, and the rows to be summed stay there: 180 -> 160 µs for 30011
+// positions, V = 151936, H = 2048).
+constexpr int FILL_BLOCKS = 768;
 __device__ __forceinline__ void do_fill(const Fill &f) {
-  const int64_t b = (int64_t)blockIdx.x - f.sort_blocks;
-  const int64_t p0 = f.from + b * ((int64_t)blockDim.x * FILL_PER_THREAD) + threadIdx.x;
-#pragma unroll
-  for (int k = 0; k < FILL_PER_THREAD; ++k) {
-    const int64_t p = p0 + (int64_t)k * blockDim.x;
-    if (p < f.to) f.p[p] = u32x4{0, 0, 0, 0};
-  }
+  const int64_t b = (int64_t)blockIdx.x - f.sort_blocks, nb = (int64_t)gridDim.x - f.sort_blocks;
+  const int64_t n = f.to - f.from, per = (n + nb - 1) / nb;
+  const int64_t end = f.from + ((b + 1) * per < n ? (b + 1) * per : n);
+#pragma unroll 4
+  for (int64_t p = f.from + b * per + threadIdx.x; p < end; p += blockDim.x)
+    __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, f.p + p);
 }
-int64_t fill_blocks(const Fill &f, int threads) {
-  return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * FILL_PER_THREAD) : 0;
+int64_t fill_blocks(const Fill &f) {
+  const int64_t most = ceil_div(f.to - f.from, 4096);
+  return most < FILL_BLOCKS ? most : FILL_BLOCKS;
 }
 
 // Up to RANK_MAX positions: a position's place is the number of smaller
 // (id, position) pairs, counted against every other. A work-group ranks 64
 // positions, its 16 waves splitting the others; M^2 comparisons are spread
-// over the whole chip in one launch (M = 8192: 4 µs of it).
+// over the whole chip in one launch.
 constexpr int RANK_THREADS = 1024, RANK_WAVES = 16, RANK_CHUNK = 8192;
-constexpr int64_t RANK_MAX = 16384;
+constexpr int64_t RANK_MAX = 8192;
 __global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(const void *ids, int ids64, int M,
                                                                   int64_t V, int64_t padding,
                                                                   uint32_t *__restrict__ keys,
@@ -137,11 +141,18 @@ __global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(const void *id
     constexpr int PER = RANK_CHUNK / RANK_WAVES;
     const int j0 = wave * PER;
     const int jn = cn - j0 < PER ? (cn - j0 + 3) & ~3 : PER;
+    const int i0 = blockIdx.x * 64;
     for (int j = 0; j < jn; j += 4) {
       const u32x4 k = *reinterpret_cast<const u32x4 *>(&sk[j0 + j]);
       const int p = c0 + j0 + j;
+      if (p + 3 < i0 || p >= i0 + 64) {  // all four before, or all after, the 64
+        const uint32_t lim = ki + (p < i0 ? 1u : 0u);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) n += k[e] < ki + (p + e < i ? 1u : 0u) ? 1u : 0u;
+        for (int e = 0; e < 4; ++e) n += k[e] < lim ? 1u : 0u;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) n += k[e] < ki + (p + e < i ? 1u : 0u) ? 1u : 0u;
+      }
     }
   }
   cnt[wave][lane] = n;
@@ -269,7 +280,7 @@ __global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, 
 // (slot 0) or goes on in the next (slot 1) go to the workspace, and
 // embed_join_kernel adds those of an id in tile order.
 // ---------------------------------------------------------------------------
-constexpr int ES_THREADS = 256, ES_COLS = ES_THREADS * 8, ES_AHEAD = 8, ES_LIST = 256;
+constexpr int ES_THREADS = 128, ES_COLS = ES_THREADS * 8, ES_AHEAD = 8, ES_LIST = 256;
 
 struct SumArgs {
   const uint32_t *keys, *order;
@@ -282,15 +293,15 @@ struct SumArgs {
   float *part;              // [tiles][2][H]
 };
 
-template <bool F16>
+template <bool F16, bool ACC>
 __device__ __forceinline__ void write_row(const SumArgs &a, int64_t v, int64_t c, const float (&s)[8]) {
   u32x4 *const dst = reinterpret_cast<u32x4 *>(a.grad_W + v * a.H + c);
   u32x4 o = u32x4{0, 0, 0, 0};
-  if (a.accumulate) o = *dst;
+  if constexpr (ACC) o = *dst;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float lo = __fmul_rn(a.scale, s[2 * k]), hi = __fmul_rn(a.scale, s[2 * k + 1]);
-    if (a.accumulate) {
+    if constexpr (ACC) {
       lo = __fadd_rn(from16<F16>(o[k] & 0xFFFFu), lo);
       hi = __fadd_rn(from16<F16>(o[k] >> 16), hi);
     }
@@ -299,7 +310,7 @@ __device__ __forceinline__ void write_row(const SumArgs &a, int64_t v, int64_t c
   *dst = o;
 }
 
-template <bool F16>
+template <bool F16, bool ACC>
 __global__ __launch_bounds__(ES_THREADS) void embed_sum_kernel(SumArgs a) {
   // the tile's keys and positions, one load each for all of them, with the
   // keys before the first and after the last (ES_LIST positions at a time)
@@ -308,59 +319,67 @@ __global__ __launch_bounds__(ES_THREADS) void embed_sum_kernel(SumArgs a) {
   const int64_t t1 = t0 + a.tile < a.M ? t0 + a.tile : a.M;
   const int64_t c = (int64_t)blockIdx.y * ES_COLS + 8 * threadIdx.x;
   const bool on = c < a.H;
+  const uint16_t *const src = a.grad_out + (on ? c : 0);
   const uint32_t none = (uint32_t)a.V;
   float s[8] = {};
   bool head = false;
   for (int64_t e0 = t0; e0 < t1; e0 += ES_LIST) {
     const int n = (int)(t1 - e0 < ES_LIST ? t1 - e0 : ES_LIST);
     __syncthreads();
-    for (int i = threadIdx.x; i < n + 2; i += ES_THREADS) {
+    for (int i = threadIdx.x; i < ES_LIST + 2; i += ES_THREADS) {
       const int64_t e = e0 + i - 1;
       sk[i] = e >= 0 && e < a.M ? a.keys[e] : none + 1;
-      if (i >= 1 && i <= n) so[i - 1] = a.order[e];
+      if (i >= 1 && i <= ES_LIST) so[i - 1] = i <= n ? a.order[e] : 0u;
     }
     __syncthreads();
     if (e0 == t0) head = sk[0] == sk[1];  // the first id began in an earlier tile
     if (sk[1] == none) return;            // the ids without a gradient come last
     for (int i0 = 0; i0 < n; i0 += ES_AHEAD) {
+      // loads and additions without conditions (past the tile: position 0,
+      // masked to zeros): a load that only a branch uses is moved into it, and
+      // a register that a load may or may not have written is waited for,
+      // either of which puts the loads one behind the other
       u32x4 v[ES_AHEAD];
 #pragma unroll
       for (int k = 0; k < ES_AHEAD; ++k)
-        if (i0 + k < n && sk[i0 + k + 1] < none && on)
-          v[k] = *reinterpret_cast<const u32x4 *>(a.grad_out + (int64_t)so[i0 + k] * a.H + c);
+        v[k] = *reinterpret_cast<const u32x4 *>(src + (int64_t)__builtin_amdgcn_readfirstlane(so[i0 + k]) * a.H);
 #pragma unroll
       for (int k = 0; k < ES_AHEAD; ++k) {
         const int i = i0 + k;
-        if (i >= n || sk[i + 1] == none) break;
+        const uint32_t key = __builtin_amdgcn_readfirstlane(sk[i + 1]);
+        const bool valid = i < n && key < none;
+        const uint32_t mask = valid ? 0xFFFFFFFFu : 0u;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          s[2 * q] = __fadd_rn(s[2 * q], from16<F16>(v[k][q] & 0xFFFFu));
-          s[2 * q + 1] = __fadd_rn(s[2 * q + 1], from16<F16>(v[k][q] >> 16));
+          const uint32_t w = v[k][q] & mask;
+          s[2 * q] = __fadd_rn(s[2 * q], from16<F16>(w & 0xFFFFu));
+          s[2 * q + 1] = __fadd_rn(s[2 * q + 1], from16<F16>(w >> 16));
         }
-        const bool ends = sk[i + 2] != sk[i + 1];
-        if (!ends && e0 + i + 1 < t1) continue;
-        if (on) {  // the id's last position, or the tile's
-          if (head || !ends) {
-            float *const p = a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.H + c;
-            *reinterpret_cast<f32x4 *>(p) = f32x4{s[0], s[1], s[2], s[3]};
-            *reinterpret_cast<f32x4 *>(p + 4) = f32x4{s[4], s[5], s[6], s[7]};
-          } else {
-            write_row<F16>(a, sk[i + 1], c, s);
+        const bool ends = __builtin_amdgcn_readfirstlane(sk[i + 2]) != key;
+        if (valid && (ends || e0 + i + 1 >= t1)) {  // the id's last position, or the tile's
+          if (on) {
+            if (head || !ends) {
+              float *const p = a.part + ((int64_t)blockIdx.x * 2 + (head ? 0 : 1)) * a.H + c;
+              *reinterpret_cast<f32x4 *>(p) = f32x4{s[0], s[1], s[2], s[3]};
+              *reinterpret_cast<f32x4 *>(p + 4) = f32x4{s[4], s[5], s[6], s[7]};
+            } else {
+              write_row<F16, ACC>(a, key, c, s);
+            }
           }
-        }
-        head = false;
+          head = false;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s[q] = 0.0f;
+          for (int q = 0; q < 8; ++q) s[q] = 0.0f;
+        }
       }
     }
   }
 }
 
 // One work-group per tile in which an id begins that goes on: EJ_GROUPS groups
-// of 256 lanes sum contiguous runs of the id's tiles (4 columns per lane),
+// of 64 lanes sum contiguous runs of the id's tiles (4 columns per lane),
 // joined in order. Most tiles have none, so what a work-group costs that
 // finds nothing to do counts: three loads in flight together.
-constexpr int EJ_GROUPS = 4, EJ_LANES = 256, EJ_COLS = 4 * EJ_LANES;
+constexpr int EJ_GROUPS = 8, EJ_LANES = 64, EJ_COLS = 4 * EJ_LANES;
 template <bool F16>
 __global__ __launch_bounds__(EJ_GROUPS * EJ_LANES) void embed_join_kernel(SumArgs a, int tiles) {
   const int t0 = blockIdx.x;
@@ -389,9 +408,9 @@ __global__ __launch_bounds__(EJ_GROUPS * EJ_LANES) void embed_join_kernel(SumArg
       f32x4 v[AH];
 #pragma unroll
       for (int q = 0; q < AH; ++q) {
-        const int t = t0 + k + q;
-        v[q] = k + q < k1 ? *reinterpret_cast<const f32x4 *>(a.part + ((int64_t)t * 2 + (k + q == 0 ? 1 : 0)) * a.H + c)
-                          : zero4();
+        const int kk = k + q < k1 ? k + q : k1 - 1;  // (a load without a condition, as above)
+        v[q] = *reinterpret_cast<const f32x4 *>(a.part + ((int64_t)(t0 + kk) * 2 + (kk == 0 ? 1 : 0)) * a.H + c);
+        if (k + q >= k1) v[q] = zero4();
       }
 #pragma unroll
       for (int q = 0; q < AH; ++q)
@@ -425,8 +444,8 @@ __global__ __launch_bounds__(EJ_GROUPS * EJ_LANES) void embed_join_kernel(SumArg
 // Positions per tile: enough tiles to fill the chip, at most about 1024
 // (their partial sums are read back), at least 8 positions.
 int sum_tile(int64_t M) {
-  const int64_t t = ceil_div(M, 1024);
-  return (int)(t < 8 ? 8 : t);
+  const int64_t t = ceil_div(M, 512);
+  return (int)(t < 16 ? 16 : t);
 }
 
 struct Plan {
@@ -472,7 +491,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   Fill f{static_cast<u32x4 *>(c.grad_W), 0, c.accumulate ? 0 : words, 0};
   if (c.M == 0) {
     if (c.accumulate) return hipSuccess;
-    return launch_kernel(embed_rank_kernel, dim3((unsigned)fill_blocks(f, RANK_THREADS)), dim3(RANK_THREADS), s,
+    return launch_kernel(embed_rank_kernel, dim3((unsigned)fill_blocks(f)), dim3(RANK_THREADS), s,
                          c.ids, c.ids64, 0, c.V, c.padding, static_cast<uint32_t *>(nullptr),
                          static_cast<uint32_t *>(nullptr), f);
   }
@@ -483,7 +502,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (c.M <= RANK_MAX) {
     f.sort_blocks = (int)ceil_div(c.M, 64);
-    e = launch_kernel(embed_rank_kernel, dim3((unsigned)(f.sort_blocks + fill_blocks(f, RANK_THREADS))),
+    e = launch_kernel(embed_rank_kernel, dim3((unsigned)(f.sort_blocks + fill_blocks(f))),
                       dim3(RANK_THREADS), s, c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
   } else {
     RadixArgs a;
@@ -515,7 +534,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
         f.to = all * (part + 1) / (2 * passes);
         f.sort_blocks = a.tiles;
         e = launch_kernel(half == 0 ? embed_count_kernel : embed_scatter_kernel,
-                          dim3((unsigned)(a.tiles + fill_blocks(f, RX_THREADS))), dim3(RX_THREADS), s, a, f);
+                          dim3((unsigned)(a.tiles + fill_blocks(f))), dim3(RX_THREADS), s, a, f);
       }
     }
   }
@@ -533,7 +552,9 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   a.grad_W = static_cast<uint16_t *>(c.grad_W);
   a.part = reinterpret_cast<float *>(ws + pl.part);
   const int tiles = (int)ceil_div(c.M, a.tile);
-  e = launch_kernel(c.in_f16 ? embed_sum_kernel<true> : embed_sum_kernel<false>,
+  auto sum = c.in_f16 ? (c.accumulate ? embed_sum_kernel<true, true> : embed_sum_kernel<true, false>)
+                      : (c.accumulate ? embed_sum_kernel<false, true> : embed_sum_kernel<false, false>);
+  e = launch_kernel(sum,
                     dim3((unsigned)tiles, (unsigned)ceil_div(c.H, ES_COLS)), dim3(ES_THREADS), s, a);
   if (e != hipSuccess || tiles < 2) return e;
   return launch_kernel(c.in_f16 ? embed_join_kernel<true> : embed_join_kernel<false>,
