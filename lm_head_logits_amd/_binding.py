@@ -47,18 +47,22 @@ def _stream_handle(device, stream):
 
 _NO_SWITCH = contextlib.nullcontext()
 
+# torch's current device index without its lazy-initialisation check (a device
+# tensor is in hand wherever this is called)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _device_ctx(device):
     """The library launches on the current device: make it `device`, switching
     (and switching back) only when it is another one."""
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    return _NO_SWITCH if torch.cuda.current_device() == idx else torch.cuda.device(idx)
+    idx = device.index
+    return _NO_SWITCH if idx is None or _current_device() == idx else torch.cuda.device(idx)
 
 
 def _alloc_on(stream):
     """Where a call's outputs and workspace are allocated: the stream it runs
     on, so that the allocator's reuse of their memory is ordered with it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _NO_SWITCH if stream is None else torch.cuda.stream(stream)
 
 
 def _need(cond: bool, msg: str):
@@ -66,10 +70,12 @@ def _need(cond: bool, msg: str):
         raise ValueError(msg)
 
 
-def _same_device(*tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:  # the message only on failure: this runs on every call
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devs))}")
+def _same_device(first, *tensors):
+    dev = first.device
+    for t in tensors:
+        if t is not None and t.device != dev:  # the message only on failure: this runs on every call
+            devs = {str(t.device) for t in (first, *tensors) if t is not None}
+            raise ValueError(f"all tensors must be on one device, got {sorted(devs)}")
 
 
 _DTYPES = {torch.float32: LMHEAD_F32, torch.bfloat16: LMHEAD_BF16, torch.float16: LMHEAD_F16}

@@ -284,8 +284,9 @@ __device__ __forceinline__ void mm_barrier() {
 // given the taller tiles of a pair.
 struct MmWalk {
   uint32_t lo, hi, nw, wi, round;
-  __device__ __forceinline__ MmWalk(uint32_t tiles) {
-    const uint32_t b = blockIdx.x, g = gridDim.x, nx = g < 8 ? g : 8;
+  // Work-group b of g that share the tiles.
+  __device__ __forceinline__ MmWalk(uint32_t tiles, uint32_t b, uint32_t g) {
+    const uint32_t nx = g < 8 ? g : 8;
     const uint32_t x = b % nx, q = tiles / nx, r = tiles % nx;
     lo = x * q + (x < r ? x : r);
     hi = lo + q + (x < r ? 1 : 0);
@@ -320,12 +321,14 @@ __device__ __forceinline__ void mm_tile_at(uint32_t t, uint32_t na, uint32_t nb,
 //                       which it may use; it has the accumulators and MM_EPI
 //                       slots of LDS of its own. Vector memory operations that
 //                       it leaves in flight only make later waits longer.
-// Every job of a launch has the same row lengths (ld).
+// Every job of a launch has the same row lengths (ld). `b` of `g`: this
+// work-group among those that share the tiles.
 template <int ET, bool AOUT, bool BOUT, typename P>
-__device__ __forceinline__ void mm_run(const P &p, const MmBufs &buf) {
+__device__ __forceinline__ void mm_run(const P &p, const MmBufs &buf, uint32_t b = blockIdx.x,
+                                       uint32_t g = gridDim.x) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  MmWalk walk((uint32_t)p.tiles());
+  MmWalk walk((uint32_t)p.tiles(), b, g);
   int32_t tile_no = walk.next();
   if (tile_no < 0) return;
   MmSide<ET, AOUT> sa;

@@ -591,6 +591,23 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_dweight_kernel(XentBwdArgs
   mm_run<ET, true, true>(prob, mm_buf);
 }
 
+// Both products of a small piece in one launch, side by side: work-groups up to
+// `ga` make G W, the others G^T hidden (neither needs the other). 37 rows,
+// H = 256, V = 4096: two launches of 11 and 9 µs become one of 11.
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void xent_products_kernel(XentBwdArgs p, uint32_t ga) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  const int64_t nht = (p.H + MM_T - 1) / MM_T;
+  if (blockIdx.x < ga) {
+    const XentDHidden<ET> prob{p, (p.M + MM_T - 1) / MM_T, nht, (p.np + p.ksplit - 1) / p.ksplit};
+    mm_run<ET, false, true>(prob, mm_buf, blockIdx.x, ga);
+  } else {
+    const XentDWeight<ET> prob{p, mm_epi, p.np / MM_T, nht};
+    mm_run<ET, true, true>(prob, mm_buf, blockIdx.x - ga, gridDim.x - ga);
+  }
+}
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
@@ -611,12 +628,12 @@ BwdPlan bwd_plan(int64_t M, int64_t H, int64_t V, bool bias) {
   p.vp = ceil_div(ceil_div(vall, p.pieces), MM_T) * MM_T;
   p.pieces = ceil_div(V, p.vp);
   // G W has a tile per 256 rows and 256 of H, too few to fill the chip when M
-  // is small: K (the piece's columns) is split, at least 512 columns each,
+  // is small: K (the piece's columns) is split, at least 256 columns each,
   // into as many splits as fill the last round of work-groups best
   const int64_t tiles = ceil_div(M, MM_T) * ceil_div(H, MM_T), cus = 256;
   double best = 0.0;
   p.splits = 1;
-  for (int64_t s = 1; s <= 64 && s * 512 <= p.vp; ++s) {
+  for (int64_t s = 1; s <= 64 && s * 256 <= p.vp; ++s) {
     const double use = (double)(tiles * s) / (double)(ceil_div(tiles * s, cus) * cus);
     if (use > best * 1.05) {
       best = use;
@@ -694,11 +711,15 @@ hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
     if (e == hipSuccess && c.grad_bias != nullptr)
       e = launch_kernel(xent_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
                         static_cast<const float *>(p.colpart), nmt, pl.vp, nv, c.grad_bias + v0);
+    const int64_t ta = nmt * nht * ceil_div(p.np, pl.ksplit), tb = nht * (p.np / MM_T);
+    if (e == hipSuccess && c.grad_hidden != nullptr && c.grad_W != nullptr && ta + tb <= device_cus()) {
+      e = launch_kernel(xent_products_kernel<ET>, dim3((unsigned)(ta + tb)), dim3(MM_THREADS), s, p, (uint32_t)ta);
+      continue;
+    }
     if (e == hipSuccess && c.grad_hidden != nullptr)
-      e = launch_kernel(xent_dhidden_kernel<ET>, mm_grid(nmt * nht * ceil_div(p.np, pl.ksplit)),
-                        dim3(MM_THREADS), s, p);
+      e = launch_kernel(xent_dhidden_kernel<ET>, mm_grid(ta), dim3(MM_THREADS), s, p);
     if (e == hipSuccess && c.grad_W != nullptr)
-      e = launch_kernel(xent_dweight_kernel<ET>, mm_grid(nht * (p.np / MM_T)), dim3(MM_THREADS), s, p);
+      e = launch_kernel(xent_dweight_kernel<ET>, mm_grid(tb), dim3(MM_THREADS), s, p);
   }
   if (e == hipSuccess && c.grad_hidden != nullptr)
     e = launch_kernel(xent_dhidden_out_kernel<ET>, dim3((unsigned)ceil_div(c.M * c.H, 2048)), dim3(256), s,
