@@ -261,7 +261,9 @@ size_t lmhead_quantize_nvfp4_workspace_bytes(void);
  * the call (target < 0 or >= V): its loss is 0 and carries no gradient; its
  * lse is written all the same. t = -inf (a masked column, through a -inf
  * bias) has probability 0: a target there has loss +inf, and a row of
- * only -inf has lse -inf. +inf and NaN logits give NaN.
+ * only -inf has lse -inf. +inf and NaN logits give NaN (and a hidden row that
+ * is not finite makes grad_W so, even where the row is left out: it enters the
+ * product with 0).
  * ------------------------------------------------------------------------- */
 typedef enum {
   LMHEAD_INDEX32 = 0, /* int32 targets or token ids */
@@ -276,7 +278,8 @@ typedef enum {
  *   workspace   at least lmhead_xent_forward_workspace_bytes(M, V) bytes, 16-byte
  *               aligned, overwritten; not in use by other work until this call's
  *               work has finished
- * Results do not change from run to run. Returns as lmhead_logits_ex
+ * A row's results depend on that row, W, alpha and bias only, not on the call's
+ * other rows, and do not change from run to run. Returns as lmhead_logits_ex
  * (LMHEAD_NOT_HANDLED for fp32 inputs or H % 32 != 0). */
 lmhead_status lmhead_xent_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
                                   float alpha, const float *bias, lmhead_dtype in_dtype,

@@ -143,7 +143,7 @@ const char *lmhead_status_string(int status) {
   }
 }
 
-const char *lmhead_version(void) { return "0.1.0"; }
+const char *lmhead_version(void) { return "0.2.0"; }
 
 lmhead_status lmhead_logits_ex(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
                                float alpha, const float *bias, lmhead_dtype in_dtype,

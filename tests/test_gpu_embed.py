@@ -130,6 +130,11 @@ def test_gradient_added_and_padding(M):
     check_grad(go, ids, V, 0.5, padding=5, base=base)
     got = check_grad(go, ids, V, 0.5, padding=5)
     assert bool((got[5] == 0).all())
+    # counted from the end, as torch has it
+    assert torch.equal(L.embed_backward(go, ids, V, 0.5, padding_idx=5 - V), got)
+    for bad in (V, -V - 1):
+        with pytest.raises(ValueError):
+            L.embed_backward(go, ids, V, padding_idx=bad)
     # every position without a gradient
     ids.fill_(5)
     assert bool((L.embed_backward(go, ids, V, padding_idx=5) == 0).all())
