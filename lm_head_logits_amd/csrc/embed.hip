@@ -95,22 +95,22 @@ struct Fill {
   int64_t from, to;
   int sort_blocks; // work-groups of the launch that sort
 };
-// Each fill work-group writes one contiguous part; FILL_BLOCKS of them, three
-// per CU, behind the sorting ones. Not kept in the caches (nothing reads the
-// zeros, and the rows to be summed stay there: 180 -> 160 µs for 30011
-// positions, V = 151936, H = 2048).
-constexpr int FILL_BLOCKS = 768;
+// A fill work-group writes 256 KB, in steps of its width. The stores are not
+// kept in the caches: nothing reads the zeros, and what does not displace the
+// rows to be summed leaves them there (30011 positions, V = 151936, H = 2048:
+// 180 -> 161 µs; three work-groups per CU with a contiguous part each: 195 µs).
+constexpr int FILL_PER_THREAD = 16;
 __device__ __forceinline__ void do_fill(const Fill &f) {
-  const int64_t b = (int64_t)blockIdx.x - f.sort_blocks, nb = (int64_t)gridDim.x - f.sort_blocks;
-  const int64_t n = f.to - f.from, per = (n + nb - 1) / nb;
-  const int64_t end = f.from + ((b + 1) * per < n ? (b + 1) * per : n);
-#pragma unroll 4
-  for (int64_t p = f.from + b * per + threadIdx.x; p < end; p += blockDim.x)
-    __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, f.p + p);
+  const int64_t b = (int64_t)blockIdx.x - f.sort_blocks;
+  const int64_t p0 = f.from + b * ((int64_t)blockDim.x * FILL_PER_THREAD) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < FILL_PER_THREAD; ++k) {
+    const int64_t p = p0 + (int64_t)k * blockDim.x;
+    if (p < f.to) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, f.p + p);
+  }
 }
-int64_t fill_blocks(const Fill &f) {
-  const int64_t most = ceil_div(f.to - f.from, 4096);
-  return most < FILL_BLOCKS ? most : FILL_BLOCKS;
+int64_t fill_blocks(const Fill &f, int threads) {
+  return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * FILL_PER_THREAD) : 0;
 }
 
 // Up to RANK_MAX positions: a position's place is the number of smaller
@@ -491,7 +491,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   Fill f{static_cast<u32x4 *>(c.grad_W), 0, c.accumulate ? 0 : words, 0};
   if (c.M == 0) {
     if (c.accumulate) return hipSuccess;
-    return launch_kernel(embed_rank_kernel, dim3((unsigned)fill_blocks(f)), dim3(RANK_THREADS), s,
+    return launch_kernel(embed_rank_kernel, dim3((unsigned)fill_blocks(f, RANK_THREADS)), dim3(RANK_THREADS), s,
                          c.ids, c.ids64, 0, c.V, c.padding, static_cast<uint32_t *>(nullptr),
                          static_cast<uint32_t *>(nullptr), f);
   }
@@ -502,7 +502,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (c.M <= RANK_MAX) {
     f.sort_blocks = (int)ceil_div(c.M, 64);
-    e = launch_kernel(embed_rank_kernel, dim3((unsigned)(f.sort_blocks + fill_blocks(f))),
+    e = launch_kernel(embed_rank_kernel, dim3((unsigned)(f.sort_blocks + fill_blocks(f, RANK_THREADS))),
                       dim3(RANK_THREADS), s, c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
   } else {
     RadixArgs a;
@@ -534,7 +534,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
         f.to = all * (part + 1) / (2 * passes);
         f.sort_blocks = a.tiles;
         e = launch_kernel(half == 0 ? embed_count_kernel : embed_scatter_kernel,
-                          dim3((unsigned)(a.tiles + fill_blocks(f))), dim3(RX_THREADS), s, a, f);
+                          dim3((unsigned)(a.tiles + fill_blocks(f, RX_THREADS))), dim3(RX_THREADS), s, a, f);
       }
     }
   }
