@@ -12,7 +12,7 @@
 // first filled with zeros by work-groups that ride along in the sorting
 // kernels' launches: the sort needs few CUs and the fill is what takes long.
 #include "kstep.hpp"
-#include "launch.hpp"
+#include "ops_launch.hpp"
 
 namespace lmhead {
 

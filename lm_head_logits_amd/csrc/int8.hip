@@ -12,7 +12,7 @@
 // waits are those of ring.hpp) at one byte per element. Above, the 256 x 256
 // product of mma256.hpp.
 #include "mma256.hpp"
-#include "launch.hpp"
+#include "ops_launch.hpp"
 
 namespace lmhead {
 

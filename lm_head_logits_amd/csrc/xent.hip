@@ -27,6 +27,7 @@
 // 2^-11 (fp16) of each term of sums of M or V terms, the size of the 16-bit
 // gradients' own rounding. It is kept scaled (xent_rows_kernel).
 #include "mma256.hpp"
+#include "ops_launch.hpp"
 
 namespace lmhead {
 
