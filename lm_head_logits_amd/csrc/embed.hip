@@ -95,50 +95,52 @@ struct Fill {
   int64_t from, to;
   int sort_blocks; // work-groups of the launch that sort
 };
-// A fill work-group writes 256 KB, in steps of its width. The stores are not
-// kept in the caches: nothing reads the zeros, and what does not displace the
-// rows to be summed leaves them there (30011 positions, V = 151936, H = 2048:
-// 180 -> 161 µs; three work-groups per CU with a contiguous part each: 195 µs).
-constexpr int FILL_PER_THREAD = 16;
+// A fill work-group writes PER pieces per thread, in steps of its width. Small
+// work-groups in order fill fastest (1.05 GB alone: 256 threads of one piece
+// 155 µs, of four 176, 1024 of sixteen 171). The stores are not kept in the
+// caches: nothing reads the zeros, and what does not displace the rows to be
+// summed leaves them there (30011 positions, V = 151936, H = 2048: 180 -> 161 µs).
+template <int PER>
 __device__ __forceinline__ void do_fill(const Fill &f) {
   const int64_t b = (int64_t)blockIdx.x - f.sort_blocks;
-  const int64_t p0 = f.from + b * ((int64_t)blockDim.x * FILL_PER_THREAD) + threadIdx.x;
+  const int64_t p0 = f.from + b * ((int64_t)blockDim.x * PER) + threadIdx.x;
 #pragma unroll
-  for (int k = 0; k < FILL_PER_THREAD; ++k) {
+  for (int k = 0; k < PER; ++k) {
     const int64_t p = p0 + (int64_t)k * blockDim.x;
     if (p < f.to) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, f.p + p);
   }
 }
-int64_t fill_blocks(const Fill &f, int threads) {
-  return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * FILL_PER_THREAD) : 0;
+int64_t fill_blocks(const Fill &f, int threads, int per) {
+  return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * per) : 0;
 }
 
 // Up to RANK_MAX positions: a position's place is the number of smaller
 // (id, position) pairs, counted against every other. A work-group ranks 64
-// positions, its 16 waves splitting the others; M^2 comparisons are spread
-// over the whole chip in one launch.
-constexpr int RANK_THREADS = 1024, RANK_WAVES = 16, RANK_CHUNK = 8192;
+// positions, its waves splitting the others; M^2 comparisons are spread over
+// the chip in one launch. Sixteen waves where the ranking is all there is to
+// wait for; four under a dense gradient's fill, which takes longer than either
+// and is faster from small work-groups.
 constexpr int64_t RANK_MAX = 8192;
-__global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(const void *ids, int ids64, int M,
-                                                                  int64_t V, int64_t padding,
-                                                                  uint32_t *__restrict__ keys,
-                                                                  uint32_t *__restrict__ order, Fill f) {
-  if ((int)blockIdx.x >= f.sort_blocks) return do_fill(f);
-  __shared__ alignas(16) uint32_t sk[RANK_CHUNK];
-  __shared__ uint32_t cnt[RANK_WAVES][64];
+template <int WAVES, int CHUNK>
+__global__ __launch_bounds__(64 * WAVES) void embed_rank_kernel(const void *ids, int ids64, int M, int64_t V,
+                                                                int64_t padding, uint32_t *__restrict__ keys,
+                                                                uint32_t *__restrict__ order, Fill f) {
+  if ((int)blockIdx.x >= f.sort_blocks) return do_fill<1>(f);
+  __shared__ alignas(16) uint32_t sk[CHUNK];
+  __shared__ uint32_t cnt[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i = blockIdx.x * 64 + lane;
   const uint32_t ki = i < M ? key_of(ids, ids64, i, V, padding) : 0u;
   uint32_t n = 0;
-  for (int c0 = 0; c0 < M; c0 += RANK_CHUNK) {
-    const int cn = M - c0 < RANK_CHUNK ? M - c0 : RANK_CHUNK;
+  for (int c0 = 0; c0 < M; c0 += CHUNK) {
+    const int cn = M - c0 < CHUNK ? M - c0 : CHUNK;
     __syncthreads();
-    for (int j = threadIdx.x; j < RANK_CHUNK; j += RANK_THREADS)
+    for (int j = threadIdx.x; j < CHUNK; j += 64 * WAVES)
       sk[j] = j < cn ? key_of(ids, ids64, c0 + j, V, padding) : 0xFFFFFFFFu;
     __syncthreads();
     // this wave's positions of the chunk, four at a time; positions before i
     // count with an equal id, later ones do not
-    constexpr int PER = RANK_CHUNK / RANK_WAVES;
+    constexpr int PER = CHUNK / WAVES;
     const int j0 = wave * PER;
     const int jn = cn - j0 < PER ? (cn - j0 + 3) & ~3 : PER;
     const int i0 = blockIdx.x * 64;
@@ -160,7 +162,7 @@ __global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(const void *id
   if (wave == 0 && i < M) {
     uint32_t r = 0;
 #pragma unroll
-    for (int w = 0; w < RANK_WAVES; ++w) r += cnt[w][lane];
+    for (int w = 0; w < WAVES; ++w) r += cnt[w][lane];
     keys[r] = ki;
     order[r] = (uint32_t)i;
   }
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(const void *id
 // tile's and its waves' first place for each digit from all tiles' counts, and
 // places the positions in order (lanes of a wave with equal digits find each
 // other by ballots).
-constexpr int RX_THREADS = 1024, RX_WAVES = 16, RX_BITS = 9, RX_BINS = 1 << RX_BITS, RX_TILES = 256;
+constexpr int RX_THREADS = 1024, RX_WAVES = 16, RX_BITS = 9, RX_BINS = 1 << RX_BITS, RX_TILES = 256, RX_FILL = 16;
 
 struct RadixArgs {
   const void *ids;           // first pass: keys come from here
@@ -189,7 +191,7 @@ __device__ __forceinline__ uint32_t radix_key(const RadixArgs &a, int64_t m) {
 }
 
 __global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fill f) {
-  if ((int)blockIdx.x >= f.sort_blocks) return do_fill(f);
+  if ((int)blockIdx.x >= f.sort_blocks) return do_fill<RX_FILL>(f);
   __shared__ uint32_t h[RX_BINS];
   for (int d = threadIdx.x; d < RX_BINS; d += RX_THREADS) h[d] = 0;
   __syncthreads();
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fi
 }
 
 __global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, Fill f) {
-  if ((int)blockIdx.x >= f.sort_blocks) return do_fill(f);
+  if ((int)blockIdx.x >= f.sort_blocks) return do_fill<RX_FILL>(f);
   __shared__ uint32_t at[RX_WAVES][RX_BINS];  // next place of (wave, digit)
   __shared__ uint32_t part[2][RX_BINS], sum[RX_BINS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -486,14 +488,21 @@ hipError_t launch_embed(const EmbedForward &c, hipStream_t s) {
                        c.scale, out);
 }
 
+namespace {
+hipError_t launch_rank(const EmbedBackward &c, uint32_t *keys, uint32_t *order, const Fill &f, hipStream_t s) {
+  const int waves = c.accumulate ? 16 : 4;
+  auto k = c.accumulate ? embed_rank_kernel<16, 8192> : embed_rank_kernel<4, 2048>;
+  return launch_kernel(k, dim3((unsigned)(f.sort_blocks + fill_blocks(f, 64 * waves, 1))), dim3(64 * waves), s,
+                       c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
+}
+}  // namespace
+
 hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   const int64_t words = c.V * c.H / 8;  // 16-byte words of grad_W
   Fill f{static_cast<u32x4 *>(c.grad_W), 0, c.accumulate ? 0 : words, 0};
   if (c.M == 0) {
     if (c.accumulate) return hipSuccess;
-    return launch_kernel(embed_rank_kernel, dim3((unsigned)fill_blocks(f, RANK_THREADS)), dim3(RANK_THREADS), s,
-                         c.ids, c.ids64, 0, c.V, c.padding, static_cast<uint32_t *>(nullptr),
-                         static_cast<uint32_t *>(nullptr), f);
+    return launch_rank(c, nullptr, nullptr, f, s);
   }
   const Plan pl = plan(c.M, c.H);
   uint8_t *const ws = static_cast<uint8_t *>(c.workspace);
@@ -502,8 +511,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (c.M <= RANK_MAX) {
     f.sort_blocks = (int)ceil_div(c.M, 64);
-    e = launch_kernel(embed_rank_kernel, dim3((unsigned)(f.sort_blocks + fill_blocks(f, RANK_THREADS))),
-                      dim3(RANK_THREADS), s, c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
+    e = launch_rank(c, keys, order, f, s);
   } else {
     RadixArgs a;
     a.ids = c.ids;
@@ -534,7 +542,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
         f.to = all * (part + 1) / (2 * passes);
         f.sort_blocks = a.tiles;
         e = launch_kernel(half == 0 ? embed_count_kernel : embed_scatter_kernel,
-                          dim3((unsigned)(a.tiles + fill_blocks(f, RX_THREADS))), dim3(RX_THREADS), s, a, f);
+                          dim3((unsigned)(a.tiles + fill_blocks(f, RX_THREADS, RX_FILL))), dim3(RX_THREADS), s, a, f);
       }
     }
   }
