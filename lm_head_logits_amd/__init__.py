@@ -2,6 +2,11 @@
 
     logits[M, V] = alpha * (hidden[M, H] . W[V, H]^T) + bias[V]
 
+and what trains and serves the same matrix W: softmax cross entropy without
+the logits in memory (cross_entropy, xent_forward, xent_backward), the tied
+embedding (embedding, embed, embed_backward) and the head in 8-bit integers
+(quantize_int8, logits_int8).
+
 Every step of the projection runs in the library's HIP kernels. This module
 only checks tensor metadata, allocates the output through torch and passes
 device pointers and torch's current HIP stream to the C functions of

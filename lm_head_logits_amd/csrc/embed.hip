@@ -11,6 +11,10 @@
 // position, the same bits every run; no float atomics. A dense gradient is
 // first filled with zeros by work-groups that ride along in the sorting
 // kernels' launches: the sort needs few CUs and the fill is what takes long.
+//
+// Measured: the lookup of 8192 rows of H = 4096 23 µs (134 MB, 5.8 TB/s; a
+// device copy reaches 5.0). Its gradient, V = 128256: 197 µs dense (1.12 GB,
+// 5.7 TB/s; the fill alone is 154), 61 µs added to a gradient that is there.
 #include "kstep.hpp"
 #include "ops_launch.hpp"
 
