@@ -207,9 +207,10 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p
   mm_run<ET, false, false>(prob, mm_buf);
 }
 
-// Folds the tiles of a row: 64 rows per work-group, 16 threads per row, each
-// thread tiles s, s + 16, ... in ascending order, then the 16 in order.
-constexpr int XC_ROWS = 64, XC_SLICES = 16;
+// Folds the tiles of a row: 16 rows per work-group, 64 threads per row, each
+// thread tiles s, s + 64, ... in ascending order, then the 64 in eights and the
+// eights, in order.
+constexpr int XC_ROWS = 16, XC_SLICES = 64;
 __device__ __forceinline__ void fold_stat(float &m, float &s, float2 e) {
   const float n = fmaxf(m, e.x);
   const float a = s == 0.0f ? 0.0f : __fmul_rn(s, exp2_fast(__fsub_rn(m, n)));
@@ -237,9 +238,18 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
   }
   sh[sl][r] = float2{mx, s};
   __syncthreads();
+  if (sl < 8) {
+    mx = NEG_INF;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) fold_stat(mx, s, sh[8 * sl + k][r]);
+  }
+  __syncthreads();
+  if (sl < 8) sh[sl][r] = float2{mx, s};
+  __syncthreads();
   if (sl != 0 || m >= p.M) return;
 #pragma unroll
-  for (int k = 1; k < XC_SLICES; ++k) fold_stat(mx, s, sh[k][r]);
+  for (int k = 1; k < 8; ++k) fold_stat(mx, s, sh[k][r]);
   // every logit -inf: log-sum-exp -inf, and a target's probability 0
   const float l = s == 0.0f ? NEG_INF : __fmul_rn(LN2, __fadd_rn(mx, log2f(s)));
   lse[m] = l;
@@ -527,13 +537,21 @@ __global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__re
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (e >= n) return;
   f32x4 s[2] = {zero4(), zero4()};
-  for (int k = 0; k < splits; ++k)
+  for (int k0 = 0; k0 < splits; k0 += 8) {
+    f32x4 v[8][2];  // eight splits' loads in flight (past the last: the last again, not added)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 v = *reinterpret_cast<const f32x4 *>(dh + k * n + e + 4 * h);
+    for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) s[h][q] = __fadd_rn(s[h][q], v[q]);
-    }
+      for (int h = 0; h < 2; ++h)
+        v[k][h] = *reinterpret_cast<const f32x4 *>(dh + (k0 + k < splits ? k0 + k : splits - 1) * n + e + 4 * h);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          s[h][q] = k0 + k < splits ? __fadd_rn(s[h][q], v[k][h][q]) : s[h][q];
+  }
   const float f = __fmul_rn(alpha, scale[1]);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
