@@ -391,6 +391,28 @@ def test_two_streams_at_once():
             assert torch.equal(a, c)
 
 
+# at most 64 rows, where the weight's gradient walks down the vocabulary: one
+# block of columns and several a work-group, ends inside a 16-row store, a
+# block, a wave's 64 columns of H, a slab of 256
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("M,H,V", [(1, 32, 1), (1, 4128, 5000), (2, 64, 129), (17, 96, 12001), (33, 288, 70005),
+                                   (63, 2048, 15193), (64, 320, 128), (64, 224, 100003), (65, 288, 8200)])
+def test_weight_gradient_of_few_rows(M, H, V, dt):
+    say(f"xent few rows M={M} H={H} V={V} {dt}")
+    h, W, b, y, gl, gz = make(M + H + V, M, H, V, dt, False, target="ignored")
+    _, lse, dh, dw, _ = check(h, W, b, y, gl, gz, 0.5)
+    guard = torch.full((V + 2, H), 7.0, dtype=h.dtype, device=DEV)
+    _, alone, _ = L.xent_backward(gl, h, W, y, lse, 0.5, grad_lse=gz, need_hidden=False)
+    assert torch.equal(alone, dw)
+    ws = torch.empty(L.xent_backward_workspace_bytes(M, H, V), dtype=torch.uint8, device=DEV)
+    st = L._lib.load().lmhead_xent_backward(
+        h.data_ptr(), M, H, W.data_ptr(), V, 0.5, None, {"bf16": 1, "f16": 2}[dt], y.data_ptr(), 1, -100,
+        lse.data_ptr(), gl.data_ptr(), gz.data_ptr(), None, guard[1:].data_ptr(), None, ws.data_ptr(), ws.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert torch.equal(guard[1:V + 1], dw) and bool((guard[0] == 7).all()) and bool((guard[V + 1] == 7).all())
+
+
 @pytest.mark.parametrize("M,H,V", [(3, 1 << 16, 70), (5, 32, 1 << 20)])
 def test_the_contracts_maxima(M, H, V):
     say(f"xent maxima M={M} H={H} V={V}")
