@@ -261,7 +261,12 @@ size_t lmhead_quantize_nvfp4_workspace_bytes(void);
  * the call (target < 0 or >= V): its loss is 0 and carries no gradient; its
  * lse is written all the same. t = -inf (a masked column, through a -inf
  * bias) has probability 0: a target there has loss +inf, and a row of
- * only -inf has lse -inf. +inf and NaN logits give NaN (and a hidden row that
+ * only -inf has lse -inf. The type's lowest value is a number: it masks a column
+ * just as well, and a target there has the finite loss lse - t. The
+ * probabilities of the backward pass are exp(t - lse) of lse as rounded to fp32:
+ * off by 2^-24 |lse|, relatively, so good for |lse| up to thousands, and no
+ * probabilities any more past 2^24 (a row masked in every column by the lowest
+ * value). +inf and NaN logits give NaN (and a hidden row that
  * is not finite makes grad_W so, even where the row is left out: it enters the
  * product with 0).
  * ------------------------------------------------------------------------- */

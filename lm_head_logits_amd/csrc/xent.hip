@@ -38,10 +38,15 @@ namespace lmhead {
 namespace {
 
 constexpr float NEG_INF = -__builtin_inff();
-constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;  // log2 e, ln 2
+constexpr float LOG2E = 1.44269504088896340736f;  // log2 e
 
-// 2^x, the hardware's (below 2^-126: 0).
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// e^(t - ref) by the hardware's 2^x (below 2^-126: 0). The factor log2 e is
+// applied to the difference, not to t and ref: a finite t stays finite (a mask
+// of the type's lowest value times log2 e would be -inf), and the rounding of
+// the product is one of the difference. It costs a multiplication per logit.
+__device__ __forceinline__ float exp_diff(float t, float ref) {
+  return __builtin_amdgcn_exp2f(__fmul_rn(LOG2E, __fsub_rn(t, ref)));
+}
 
 struct XentFwdArgs {
   const uint8_t *hidden, *W;
@@ -51,7 +56,7 @@ struct XentFwdArgs {
   const void *target;
   int target64;
   int64_t ignore;
-  float2 *part;   // [vocabulary tile][M] {largest u = t log2 e, sum of 2^(u - largest)}
+  float2 *part;   // [vocabulary tile][M] {largest t, sum of exp(t - largest)}
   float *tlogit;  // [M] t at the target (rows with one)
 };
 
@@ -86,8 +91,8 @@ struct LanePlace {
   }
 };
 
-// The biases of the lane's eight columns in half y, times log2 e; columns that
-// are not there get -inf, so that their probability is 0.
+// The biases of the lane's eight columns in half y; columns that are not there
+// get -inf, so that their probability is 0.
 template <int ET>
 __device__ __forceinline__ void column_bias(const float *bias, int64_t V, int64_t n0, const LanePlace &at, int y,
                                             float (&b)[2][4]) {
@@ -101,7 +106,7 @@ __device__ __forceinline__ void column_bias(const float *bias, int64_t V, int64_
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
-        b[j][q] = c < V ? (bias != nullptr ? __fmul_rn(LOG2E, bias[c]) : 0.0f) : NEG_INF;
+        b[j][q] = c < V ? (bias != nullptr ? bias[c] : 0.0f) : NEG_INF;
       }
 }
 
@@ -130,8 +135,6 @@ struct XentStats {
     mm_tile_at(t, nmt, nvt, mt, vt);
     const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
     const LanePlace at;
-    // everything in units of log 2: u = t log2 e, one multiplication per logit
-    const float k = __fmul_rn(p.alpha, LOG2E);
     float bias[2][2][4];
     column_bias<ET>(p.bias, p.V, n0, at, 0, bias[0]);
     column_bias<ET>(p.bias, p.V, n0, at, 1, bias[1]);
@@ -150,21 +153,20 @@ struct XentStats {
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float acc = tile.c[x][y][i][j][q];
-              const float u = __fmaf_rn(k, acc, bias[y][j][q]);
-              tile.c[x][y][i][j][q] = u;
-              mx = fmaxf(mx, u);
+              const float v = __fmaf_rn(p.alpha, tile.c[x][y][i][j][q], bias[y][j][q]);
+              tile.c[x][y][i][j][q] = v;
+              mx = fmaxf(mx, v);
             }
         if (has_column<ET>(at, 0, yt) || has_column<ET>(at, 1, yt)) {
-          float u = 0.0f;
+          float v = 0.0f;
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                if (yt == MmTile<ET>::col(at.wn, at.lg, y, j) + q) u = tile.c[x][y][i][j][q];
-          p.tlogit[m] = __fmul_rn(u, LN2);
+                if (yt == MmTile<ET>::col(at.wn, at.lg, y, j) + q) v = tile.c[x][y][i][j][q];
+          p.tlogit[m] = v;
         }
         mx = fmaxf(mx, __shfl_xor(mx, 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -177,7 +179,7 @@ struct XentStats {
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              s = __fadd_rn(s, exp2_fast(__fsub_rn(tile.c[x][y][i][j][q], mz)));
+              s = __fadd_rn(s, exp_diff(tile.c[x][y][i][j][q], mz));
         s = __fadd_rn(s, __shfl_xor(s, 16));
         s = __fadd_rn(s, __shfl_xor(s, 32));
         if (at.lg == 0) stat[at.wn * MM_T + row] = float2{mx, s};
@@ -191,7 +193,7 @@ struct XentStats {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 e = stat[w * MM_T + row];
-        if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp2_fast(__fsub_rn(e.x, mx))));
+        if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp_diff(e.x, mx)));
       }
       p.part[vt * p.M + m0 + row] = float2{mx, s};
     }
@@ -213,8 +215,8 @@ __global__ __launch_bounds__(MM_THREADS, 1) void xent_stats_kernel(XentFwdArgs p
 constexpr int XC_ROWS = 16, XC_SLICES = 64;
 __device__ __forceinline__ void fold_stat(float &m, float &s, float2 e) {
   const float n = fmaxf(m, e.x);
-  const float a = s == 0.0f ? 0.0f : __fmul_rn(s, exp2_fast(__fsub_rn(m, n)));
-  const float b = e.y == 0.0f ? 0.0f : __fmul_rn(e.y, exp2_fast(__fsub_rn(e.x, n)));
+  const float a = s == 0.0f ? 0.0f : __fmul_rn(s, exp_diff(m, n));
+  const float b = e.y == 0.0f ? 0.0f : __fmul_rn(e.y, exp_diff(e.x, n));
   s = __fadd_rn(a, b);
   m = n;
 }
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
 #pragma unroll
   for (int k = 1; k < 8; ++k) fold_stat(mx, s, sh[k][r]);
   // every logit -inf: log-sum-exp -inf, and a target's probability 0
-  const float l = s == 0.0f ? NEG_INF : __fmul_rn(LN2, __fadd_rn(mx, log2f(s)));
+  const float l = s == 0.0f ? NEG_INF : __fadd_rn(mx, logf(s));
   lse[m] = l;
   float out = 0.0f;
   if (target_of(p.target, p.target64, m, p.ignore, p.V) >= 0) {
@@ -265,9 +267,9 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
 // Backward
 // ---------------------------------------------------------------------------
 
-// What the epilogue needs of a row: G = a 2^(t log2 e - lse) - b [v = y].
+// What the epilogue needs of a row: G = a e^(t - lse) - b [v = y].
 struct alignas(16) RowCoef {
-  float a, b, lse;  // lse times log2 e
+  float a, b, lse;
   int32_t y;        // target column, or -1
 };
 
@@ -329,7 +331,7 @@ __global__ __launch_bounds__(XR_THREADS) void xent_rows_kernel(XentRowsArgs p) {
   if (!p.write_rows || m >= p.M) return;
   float a, b;
   const int64_t y = coef(m, a, b);
-  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), __fmul_rn(LOG2E, p.lse[m]), (int32_t)y};
+  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], (int32_t)y};
 }
 
 struct XentBwdArgs {
@@ -367,8 +369,6 @@ struct XentGrad {
     mm_tile_at(t, nmt, ngt, mt, gt);
     const int64_t m0 = mt * MM_T, g0 = gt * MM_T, n0 = p.v0 + g0;
     const LanePlace at;
-    // p = 2^(t log2 e - lse log2 e)
-    const float k = __fmul_rn(p.alpha, LOG2E);
     const int64_t rows = p.M - m0 < MM_T ? p.M - m0 : MM_T;
     RowCoef rc[2][4];
 #pragma unroll
@@ -376,7 +376,7 @@ struct XentGrad {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + MmTile<ET>::row(at.wm, at.li, x, i);
-        // 2^-inf = 0 in rows past the end, and where the whole row is -inf
+        // e^-inf = 0 in rows past the end, and where the whole row is -inf
         rc[x][i] = m < p.M ? p.rows[m] : RowCoef{0.0f, 0.0f, __builtin_inff(), -1};
         if (rc[x][i].lse == NEG_INF) rc[x][i].lse = 0.0f;
         rc[x][i].y = rc[x][i].y < 0 ? -1 : rc[x][i].y - (int32_t)n0;
@@ -400,7 +400,7 @@ struct XentGrad {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 g[j][q] = __fmul_rn(
-                    r.a, exp2_fast(__fsub_rn(__fmaf_rn(k, tile.c[x][y][i][j][q], bias[j][q]), r.lse)));
+                    r.a, exp_diff(__fmaf_rn(p.alpha, tile.c[x][y][i][j][q], bias[j][q]), r.lse));
             if (has_column<ET>(at, y, r.y))
 #pragma unroll
               for (int j = 0; j < 2; ++j)
