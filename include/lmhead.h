@@ -257,6 +257,7 @@ size_t lmhead_quantize_nvfp4_workspace_bytes(void);
  * logits in memory, and its gradients.
  *   t[m, v] = alpha * (hidden[m, :] . W[v, :]) + bias[v]   (as lmhead_logits_ex, fp32)
  *   lse[m]  = log sum_v exp(t[m, v]);  loss[m] = lse[m] - t[m, target[m]]
+ * (the loss is made from the row's largest t, not from lse as rounded).
  * A row is left out when its target equals ignore_index or is no column of
  * the call (target < 0 or >= V): its loss is 0 and carries no gradient; its
  * lse is written all the same. t = -inf (a masked column, through a -inf

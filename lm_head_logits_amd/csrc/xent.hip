@@ -253,12 +253,14 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void xent_combine_kernel(
 #pragma unroll
   for (int k = 1; k < 8; ++k) fold_stat(mx, s, sh[k][r]);
   // every logit -inf: log-sum-exp -inf, and a target's probability 0
-  const float l = s == 0.0f ? NEG_INF : __fadd_rn(mx, logf(s));
-  lse[m] = l;
+  const float ls = logf(s);
+  lse[m] = s == 0.0f ? NEG_INF : __fadd_rn(mx, ls);
+  // the loss from the largest logit, not from lse as rounded: a token that is
+  // nearly certain has a loss far below half a step of its lse
   float out = 0.0f;
   if (target_of(p.target, p.target64, m, p.ignore, p.V) >= 0) {
     const float t = p.tlogit[m];
-    out = t == NEG_INF ? __builtin_inff() : __fsub_rn(l, t);
+    out = t == NEG_INF ? __builtin_inff() : __fadd_rn(__fsub_rn(mx, t), ls);
   }
   loss[m] = out;
 }

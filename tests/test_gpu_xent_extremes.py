@@ -68,6 +68,50 @@ def test_every_column_at_the_lowest_value(V):
     assert bool((lse == F.min).all()) and bool(loss.isfinite().all())
 
 
+def sum_error(V):
+    """Relative error of a row's sum of exponentials and of its fold, the
+    arguments' own errors aside: exp2 (2 u), 16 additions per lane, two lane and
+    four wave folds of two roundings and a factor, the tiles' folds."""
+    return (24 + 3 * ((V + 255) // 256 // 16 + 18)) * U
+
+
+@pytest.mark.parametrize("V", [40, 700])
+def test_loss_where_every_column_is_at_the_lowest_value(V):
+    """Equal logits: log V, though lse has no digits of that size left."""
+    say("xent loss at the lowest value", V)
+    h, W, y = grid(2, 5, 32, V, "bf16")
+    loss, _ = L.xent_forward(h, W, y, 1.0, torch.full((V,), F.min, device=DEV))
+    assert bool(((loss.double() - math.log(V)).abs() <= sum_error(V) + 4 * U * math.log(V)).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("top", [64.0, 4096.0])
+def test_loss_of_a_confident_token(top, dt):
+    """A largest logit of `top`, two columns 3 and 6 below it, the others 40 and
+    more below: the loss is log(1 + e^-3 + e^-6 + ...), or that plus 3, in an
+    lse whose half step is 2^-24 top. Exact logits: every one is the bias."""
+    H, V = 32, 520
+    say("xent confident", top, dt)
+    h, W, _ = grid(4, 3, H, V, dt)
+    h.zero_()
+    b = torch.full((V,), top - 40.0, device=DEV)
+    b[:7] = 0.0
+    b[300], b[310], b[5] = top, top - 3, top - 6
+    y = torch.tensor([300, 310, 300], device=DEV)
+    loss, lse = L.xent_forward(h, W, y, 1.0, b)
+    s = torch.exp(b.double() - top).sum()
+    want = torch.log(s) + (top - b.double()[y])
+    # the sum's terms past the largest weigh e^-3 and less; their arguments are
+    # off by the product's and the constant's rounding, 2 u x relatively
+    terms = torch.exp(b.double() - top)
+    arg = 2 * U * float(((top - b.double()) * terms).sum() / s)
+    tol = sum_error(V) + arg + 4 * U * want
+    err = (loss.double() - want).abs()
+    say(f"  worst {float((err / tol).max()):.3f} of the bound")
+    assert bool((err <= tol).all())
+    assert bool(((lse.double() - top - torch.log(s)).abs() <= U * top + sum_error(V) + arg + 4 * U).all())
+
+
 def test_logits_near_the_largest_value():
     """A finite logit of 3e38 (its product with log2 e would be inf): certainty."""
     M, H, V = 6, 32, 300
