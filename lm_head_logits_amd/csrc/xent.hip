@@ -275,7 +275,7 @@ struct alignas(16) RowCoef {
   int32_t y;        // target column, or -1
 };
 
-// G is kept scaled by f = top / mx, mx the largest |a| or |b| of the rows and
+// G is kept scaled by f = top / mx, mx the largest finite |a| or |b| of the rows and
 // `top` a power of two, so that a row of that size has its largest entry, -b
 // (1 - p) at the target, just below a power of two, where the 16-bit
 // type's rounding is relatively finest: a batch's rows mostly share one size
@@ -315,7 +315,10 @@ __global__ __launch_bounds__(XR_THREADS) void xent_rows_kernel(XentRowsArgs p) {
     for (int64_t m = threadIdx.x; m < p.M; m += XR_THREADS) {
       float a, b;
       coef(m, a, b);
-      mx = fmaxf(mx, fmaxf(fabsf(a), fabsf(b)));
+      // of the finite ones: a row of inf or NaN is lost, the others are not
+      a = fabsf(a);
+      b = fabsf(b);
+      mx = fmaxf(mx, fmaxf(a < __builtin_inff() ? a : 0.0f, b < __builtin_inff() ? b : 0.0f));
     }
     for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;

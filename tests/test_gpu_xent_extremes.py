@@ -132,3 +132,27 @@ def test_logits_near_the_largest_value():
     assert torch.equal(dh[3:], d.to(torch.bfloat16).expand(3, H))
     s = h[3:].double().sum(0)
     assert torch.equal(dw[7], s.to(torch.bfloat16)) and torch.equal(dw[200], (-s).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_other_rows_of_an_infinite_upstream_gradient(bad, dt):
+    """An overflowed row's upstream gradient leaves the other rows' grad_hidden
+    as they are without it (fp16: G of 2^-16 / V unscaled would be lost)."""
+    M, H, V = 20, 64, 700
+    say("xent infinite upstream gradient", bad, dt)
+    h, W, y = grid(5, M, H, V, dt)
+    gl = torch.full((M,), 2.0 ** -16, device=DEV)
+    gz = torch.zeros(M, device=DEV)
+    _, lse = L.xent_forward(h, W, y, 0.25)
+    for into in (gl, gz):
+        keep = float(into[7])
+        into[7] = 0.0
+        want = L.xent_backward(gl, h, W, y, lse, 0.25, grad_lse=gz)[0]
+        into[7] = bad
+        got = L.xent_backward(gl, h, W, y, lse, 0.25, grad_lse=gz)[0]
+        into[7] = keep
+        assert not bool(got[7].isfinite().all())
+        rows = torch.arange(M, device=DEV) != 7
+        assert bool(want[rows].isfinite().all()) and bool((want[rows] != 0).any(1).all())
+        assert torch.equal(got[rows], want[rows])
