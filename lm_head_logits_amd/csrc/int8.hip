@@ -45,10 +45,11 @@ __device__ __forceinline__ float elem(u32x4 v, int k) {
 }
 
 template <bool F16>
-__global__ __launch_bounds__(Q_THREADS) void quantize_int8_kernel(const uint16_t *__restrict__ x, int64_t H,
-                                                                  int8_t *__restrict__ q,
+__global__ __launch_bounds__(Q_THREADS) void quantize_int8_kernel(const uint16_t *__restrict__ x, int64_t rows,
+                                                                  int64_t H, int8_t *__restrict__ q,
                                                                   float *__restrict__ scale) {
-  const int64_t row = blockIdx.x;
+  const int64_t row = group_number();
+  if (row >= rows) return;
   const u32x4 *const src = reinterpret_cast<const u32x4 *>(x + row * H);
   const int pieces = (int)(H / 8);
   u32x4 keep[Q_KEEP];
@@ -453,8 +454,8 @@ hipError_t launch_t(const I8Args &a, hipStream_t s) {
 
 hipError_t launch_quantize_int8(const void *x, int64_t rows, int64_t H, int in_f16, int8_t *q, float *scale,
                                 hipStream_t s) {
-  return launch_kernel(in_f16 ? quantize_int8_kernel<true> : quantize_int8_kernel<false>, dim3((unsigned)rows),
-                       dim3(Q_THREADS), s, static_cast<const uint16_t *>(x), H, q, scale);
+  return launch_kernel(in_f16 ? quantize_int8_kernel<true> : quantize_int8_kernel<false>, numbered_grid(rows),
+                       dim3(Q_THREADS), s, static_cast<const uint16_t *>(x), rows, H, q, scale);
 }
 
 hipError_t launch_int8(const Int8Args &c, hipStream_t s) {
