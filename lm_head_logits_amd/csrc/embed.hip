@@ -55,7 +55,7 @@ __global__ __launch_bounds__(EL_THREADS) void embed_kernel(const void *ids, int 
                                                            Index ppr, const uint16_t *__restrict__ W,
                                                            int64_t V, float scale,
                                                            uint16_t *__restrict__ out) {
-  const Index p0 = (Index)blockIdx.x * (EL_THREADS * EL_STEPS) + threadIdx.x;
+  const Index p0 = (Index)group_number() * (EL_THREADS * EL_STEPS) + threadIdx.x;
   u32x4 v[EL_STEPS];
 #pragma unroll
   for (int s = 0; s < EL_STEPS; ++s) {
@@ -106,7 +106,7 @@ struct Fill {
 // summed leaves them there (30011 positions, V = 151936, H = 2048: 180 -> 161 µs).
 template <int PER>
 __device__ __forceinline__ void do_fill(const Fill &f) {
-  const int64_t b = (int64_t)blockIdx.x - f.sort_blocks;
+  const int64_t b = group_number() - f.sort_blocks;
   const int64_t p0 = f.from + b * ((int64_t)blockDim.x * PER) + threadIdx.x;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -129,7 +129,7 @@ template <int WAVES, int CHUNK>
 __global__ __launch_bounds__(64 * WAVES) void embed_rank_kernel(const void *ids, int ids64, int M, int64_t V,
                                                                 int64_t padding, uint32_t *__restrict__ keys,
                                                                 uint32_t *__restrict__ order, Fill f) {
-  if ((int)blockIdx.x >= f.sort_blocks) return do_fill<1>(f);
+  if (group_number() >= f.sort_blocks) return do_fill<1>(f);
   __shared__ alignas(16) uint32_t sk[CHUNK];
   __shared__ uint32_t cnt[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -195,7 +195,7 @@ __device__ __forceinline__ uint32_t radix_key(const RadixArgs &a, int64_t m) {
 }
 
 __global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fill f) {
-  if ((int)blockIdx.x >= f.sort_blocks) return do_fill<RX_FILL>(f);
+  if (group_number() >= f.sort_blocks) return do_fill<RX_FILL>(f);
   __shared__ uint32_t h[RX_BINS];
   for (int d = threadIdx.x; d < RX_BINS; d += RX_THREADS) h[d] = 0;
   __syncthreads();
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fi
 }
 
 __global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, Fill f) {
-  if ((int)blockIdx.x >= f.sort_blocks) return do_fill<RX_FILL>(f);
+  if (group_number() >= f.sort_blocks) return do_fill<RX_FILL>(f);
   __shared__ uint32_t at[RX_WAVES][RX_BINS];  // next place of (wave, digit)
   __shared__ uint32_t part[2][RX_BINS], sum[RX_BINS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -477,7 +477,7 @@ int64_t embed_backward_bytes(int64_t M, int64_t H) { return M > 0 ? plan(M, H).b
 
 hipError_t launch_embed(const EmbedForward &c, hipStream_t s) {
   const int64_t ppr = c.H / 8, pieces = c.M * ppr;
-  const dim3 grid((unsigned)ceil_div(pieces, EL_THREADS * EL_STEPS));
+  const dim3 grid = numbered_grid(ceil_div(pieces, EL_THREADS * EL_STEPS));
   const uint16_t *W = static_cast<const uint16_t *>(c.W);
   uint16_t *out = static_cast<uint16_t *>(c.out);
   // 32-bit piece numbers where they fit (a 64-bit division per piece costs
@@ -496,7 +496,7 @@ namespace {
 hipError_t launch_rank(const EmbedBackward &c, uint32_t *keys, uint32_t *order, const Fill &f, hipStream_t s) {
   const int waves = c.accumulate ? 16 : 4;
   auto k = c.accumulate ? embed_rank_kernel<16, 8192> : embed_rank_kernel<4, 2048>;
-  return launch_kernel(k, dim3((unsigned)(f.sort_blocks + fill_blocks(f, 64 * waves, 1))), dim3(64 * waves), s,
+  return launch_kernel(k, numbered_grid(f.sort_blocks + fill_blocks(f, 64 * waves, 1)), dim3(64 * waves), s,
                        c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
 }
 }  // namespace
@@ -546,7 +546,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
         f.to = all * (part + 1) / (2 * passes);
         f.sort_blocks = a.tiles;
         e = launch_kernel(half == 0 ? embed_count_kernel : embed_scatter_kernel,
-                          dim3((unsigned)(a.tiles + fill_blocks(f, RX_THREADS, RX_FILL))), dim3(RX_THREADS), s, a, f);
+                          numbered_grid(a.tiles + fill_blocks(f, RX_THREADS, RX_FILL)), dim3(RX_THREADS), s, a, f);
       }
     }
   }

@@ -24,3 +24,38 @@ def test_quantiser_of_all_rows():
         scale = f.abs().amax(1) / torch.full((1,), 127.0, device=DEV)
         assert torch.equal(s[r:r + (1 << 20)], scale)
         assert torch.equal(q[r:r + (1 << 20)].float(), torch.round(f / scale[:, None]))
+
+
+@pytest.mark.parametrize("M,H", [((1 << 20) + 5, (1 << 14) + 32), ((1 << 20) + 3, 1 << 15)])
+def test_lookup_of_many_rows(M, H):
+    """More than 2^21 work-groups, with 32-bit and with 64-bit piece numbers."""
+    V = 40
+    say(f"embed M={M} H={H}")
+    g = torch.Generator(device=DEV).manual_seed(2)
+    W = torch.randn(V, H, generator=g, device=DEV).half()
+    ids = torch.randint(-1, V + 1, (M,), generator=g, device=DEV, dtype=torch.int32)
+    out = L.embed(ids, W, 0.5)
+    Wz = torch.cat([W * 0.5, torch.zeros(1, H, dtype=W.dtype, device=DEV)])  # halves are exact
+    at = torch.where((ids >= 0) & (ids < V), ids, torch.full_like(ids, V)).long()
+    for r in range(0, M, 1 << 16):
+        assert torch.equal(out[r:r + (1 << 16)], Wz[at[r:r + (1 << 16)]]), r
+    del out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M", [0, 3, 9000])
+def test_dense_gradient_of_2_35_elements(M):
+    """A gradient of 64 GiB, filled behind either sort and alone."""
+    V, H = 1 << 20, 1 << 15
+    say(f"embed grad M={M} V={V} H={H}")
+    ids = torch.tensor([V - 1, 0, V - 1, (1 << 19) + 1], device=DEV).repeat(M // 4 + 1)[:M]
+    go = torch.ones(M, H, dtype=torch.bfloat16, device=DEV)
+    gw = torch.empty(V, H, dtype=torch.bfloat16, device=DEV).fill_(7.0)  # what the call's own may reuse
+    del gw
+    gw = L.embed_backward(go, ids, V)
+    want = torch.zeros(V, device=DEV).index_add_(0, ids, torch.ones(M, device=DEV)).to(torch.bfloat16)  # whole numbers
+    for r in range(0, V, 1 << 15):
+        part = gw[r:r + (1 << 15)]
+        assert bool((part == want[r:r + (1 << 15), None]).all()), r
+    del gw, part
+    torch.cuda.empty_cache()

@@ -114,3 +114,24 @@ int main(int, char **v) {{ auto g = lmhead::group_grid(atoll(v[1])); printf("%u 
         x, y = map(int, subprocess.run([str(exe), str(n)], capture_output=True, text=True, check=True).stdout.split())
         assert x * 1024 < 1 << 32 and y < 1 << 16 and x * y >= n > x * (y - 1)
         assert y == 1 or x == 1 << 21
+
+
+# the contract's maxima (M 2^24, H 2^16, V 2^20, M V 2^42), and either side of
+# what 2^32 threads in one dimension would cover
+SHAPES = [(1, 1 << 16, 1 << 20), (8192, 1 << 16, 1 << 20), (8192, 1 << 15, 1 << 20), (8192, (1 << 15) - 32, 1 << 20),
+          (1 << 24, 8192, 1), (1 << 24, 2048, 5), (1 << 24, 1 << 16, 1 << 18), (1 << 22, 1 << 16, 1 << 20)]
+
+
+@pytest.mark.parametrize("M,H,V", SHAPES)
+def test_embedding(calls, M, H, V):
+    st, launches = calls("lmhead_embed", "p", 1, M, "p", V, H, 1, 1.0, "p", None)
+    taken(st, launches)
+    assert groups(launches[0]) * 256 * 4 >= M * H // 8
+
+
+@pytest.mark.parametrize("accumulate", [0, 1])
+@pytest.mark.parametrize("M,H,V", [(0, 1 << 16, 1 << 20), *SHAPES])
+def test_embedding_gradient(calls, M, H, V, accumulate):
+    st, launches = calls("lmhead_embed_backward", "p", 1, M, "p", V, H, 1, 1.0, -1, accumulate, "p", "p", "max", None)
+    if M or not accumulate:
+        taken(st, launches)
