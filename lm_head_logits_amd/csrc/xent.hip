@@ -539,7 +539,7 @@ __global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__re
                                                                int splits, float alpha,
                                                                const float *__restrict__ scale,
                                                                uint16_t *__restrict__ out) {
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t e = (group_number() * 256 + threadIdx.x) * 8;
   if (e >= n) return;
   f32x4 s[2] = {zero4(), zero4()};
   for (int k0 = 0; k0 < splits; k0 += 8) {
@@ -861,7 +861,7 @@ hipError_t backward(const XentBackward &c, uint8_t *ws, hipStream_t s) {
     }
   }
   if (e == hipSuccess && c.grad_hidden != nullptr)
-    e = launch_kernel(xent_dhidden_out_kernel<ET>, dim3((unsigned)ceil_div(c.M * c.H, 2048)), dim3(256), s,
+    e = launch_kernel(xent_dhidden_out_kernel<ET>, numbered_grid(ceil_div(c.M * c.H, 2048)), dim3(256), s,
                       static_cast<const float *>(p.dh), c.M * c.H, (int)pl.splits, c.alpha,
                       static_cast<const float *>(scale), static_cast<uint16_t *>(c.grad_hidden));
   return e;

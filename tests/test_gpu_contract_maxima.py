@@ -59,3 +59,28 @@ def test_dense_gradient_of_2_35_elements(M):
         assert bool((part == want[r:r + (1 << 15), None]).all()), r
     del gw, part
     torch.cuda.empty_cache()
+
+
+def test_hidden_gradient_of_more_than_2_32_elements():
+    """The last kernel of the backward pass with more than 2^21 work-groups;
+    rows from the beginning, either side of the 2^32nd element and the end,
+    with the bounds of the smaller sizes' tests."""
+    from test_gpu_xent import TINY16, U, close, reference
+    M, H, V = (1 << 18) + 300, (1 << 14) + 32, 5
+    say(f"xent M={M} H={H} V={V}")
+    g = torch.Generator(device=DEV).manual_seed(3)
+    h = torch.randn(M, H, generator=g, device=DEV, dtype=torch.bfloat16).mul_(0.25)
+    W = torch.randn(V, H, generator=g, device=DEV).mul_(0.02).bfloat16()
+    y = torch.randint(0, V, (M,), generator=g, device=DEV)
+    gl = torch.full((M,), 2.0 ** -18, device=DEV)
+    _, lse = L.xent_forward(h, W, y, 1.0)
+    dh = L.xent_backward(gl, h, W, y, lse, 1.0, need_weight=False)[0]
+    at = (1 << 32) // H
+    for r0 in (0, at - 200, M - 400):
+        rows = slice(r0, r0 + 400)
+        r = reference(h[rows], W, None, y[rows], gl[rows], None, 1.0)
+        t = r["dh_tol"]
+        close(f"dh {r0}", dh[rows], r["dh"], t + r["h16"] * (r["dh"].abs() + t) * (1 + 4 * U) + 4 * U * r["dh"].abs()
+              + TINY16["bf16"])
+    del h, dh
+    torch.cuda.empty_cache()

@@ -135,3 +135,10 @@ def test_embedding_gradient(calls, M, H, V, accumulate):
     st, launches = calls("lmhead_embed_backward", "p", 1, M, "p", V, H, 1, 1.0, -1, accumulate, "p", "p", "max", None)
     if M or not accumulate:
         taken(st, launches)
+
+
+@pytest.mark.parametrize("M,H,V", SHAPES)
+def test_cross_entropy(calls, M, H, V):
+    taken(*calls("lmhead_xent_forward", "p", M, H, "p", V, 1.0, "p", 1, "p", 1, -100, "p", "p", "p", "max", None))
+    taken(*calls("lmhead_xent_backward", "p", M, H, "p", V, 1.0, "p", 1, "p", 1, -100, "p", "p", "p", "p", "p", "p",
+                 "p", "max", None))
