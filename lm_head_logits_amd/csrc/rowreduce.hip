@@ -74,9 +74,10 @@ __device__ __forceinline__ RowAcc row16_fold(RowAcc a) {
 constexpr RowAcc EMPTY{-__builtin_inff(), 0.0f, 0x7FFFFFFF};
 
 __global__ __launch_bounds__(RC_THREADS) void row_combine_kernel(
-    const RowPart *__restrict__ part, int64_t ncb, float *__restrict__ row_max,
+    const RowPart *__restrict__ part, int64_t rows, int64_t ncb, float *__restrict__ row_max,
     int32_t *__restrict__ row_argmax, float *__restrict__ row_sumexp) {
-  const int64_t row = blockIdx.x;
+  const int64_t row = group_number();
+  if (row >= rows) return;
   const RowPart *p = part + row * ncb;
   RowAcc a = EMPTY;
   for (int64_t c0 = threadIdx.x; c0 < ncb; c0 += (int64_t)RC_BATCH * RC_THREADS) {
@@ -112,8 +113,8 @@ __global__ __launch_bounds__(RC_THREADS) void row_combine_kernel(
 
 hipError_t launch_row_combine(const void *part, int64_t M, int64_t V, float *row_max,
                               int32_t *row_argmax, float *row_sumexp, hipStream_t stream) {
-  return launch_kernel(row_combine_kernel, dim3((unsigned)M), dim3(RC_THREADS), stream,
-                       static_cast<const RowPart *>(part), (V + 15) / 16, row_max, row_argmax,
+  return launch_kernel(row_combine_kernel, numbered_grid(M), dim3(RC_THREADS), stream,
+                       static_cast<const RowPart *>(part), M, (V + 15) / 16, row_max, row_argmax,
                        row_sumexp);
 }
 

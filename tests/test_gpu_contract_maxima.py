@@ -84,3 +84,18 @@ def test_hidden_gradient_of_more_than_2_32_elements():
               + TINY16["bf16"])
     del h, dh
     torch.cuda.empty_cache()
+
+
+def test_row_reduction_of_many_rows():
+    """Just over 2^22 rows, one work-group each in the combining kernel: every
+    row as in a call of few rows, which the other tests check."""
+    M, H, V = (1 << 22) + 5, 32, 40
+    say(f"rowreduce M={M}")
+    g = torch.Generator(device=DEV).manual_seed(4)
+    few = torch.randn(61, H, generator=g, device=DEV).bfloat16()
+    W = torch.randn(V, H, generator=g, device=DEV).bfloat16()
+    at = torch.arange(M, device=DEV) % 61
+    want = L.logits_rowreduce(few, W, 0.5)
+    got = L.logits_rowreduce(few[at].contiguous(), W, 0.5)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a, b[at])

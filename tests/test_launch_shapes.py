@@ -142,3 +142,17 @@ def test_cross_entropy(calls, M, H, V):
     taken(*calls("lmhead_xent_forward", "p", M, H, "p", V, 1.0, "p", 1, "p", 1, -100, "p", "p", "p", "max", None))
     taken(*calls("lmhead_xent_backward", "p", M, H, "p", V, 1.0, "p", 1, "p", 1, -100, "p", "p", "p", "p", "p", "p",
                  "p", "max", None))
+
+
+# the other heads at sizes whose outputs (the row reduction's scratch) the
+# card's memory holds: M V up to 2^37
+@pytest.mark.parametrize("M,H,V", [(1, 1 << 16, 1 << 20), (1 << 17, 1 << 16, 1 << 20), (1 << 24, 8192, 1),
+                                   ((1 << 22) + 1, 2048, 5), (1 << 24, 32, 1 << 13)])
+def test_heads(calls, M, H, V):
+    for name, *args in (("lmhead_logits_int8", "p", "p", M, H, "p", "p", V, 1.0, "p", 1, "p", None),
+                        ("lmhead_logits", "p", M, H, "p", V, 1.0, "p", 1, "p", None),
+                        ("lmhead_logits_nvfp4", "p", M, H, "p", "p", 1.0, V, 1.0, "p", "p", None),
+                        ("lmhead_quantize_nvfp4", "p", V, H, "p", "p", "p", "p", "max", None),
+                        ("lmhead_logits_rowreduce", "p", M, H, "p", V, 1.0, "p", 1, 1, None, "p", "p", "p", "p", "max",
+                         None, -2)):
+        taken(*calls(name, *args))
