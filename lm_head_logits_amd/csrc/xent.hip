@@ -100,14 +100,18 @@ __device__ __forceinline__ void column_bias(const float *bias, int64_t V, int64_
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) b[j][q] = 0.0f;
-  if (bias != nullptr || n0 + MM_T > V)
+  // 32-bit columns of the tile: 64-bit ones cost registers that the epilogues lack
+  const int32_t cols = (int32_t)(V - n0 < MM_T ? V - n0 : MM_T);
+  if (bias != nullptr || cols < MM_T) {
+    const float *const first = bias + n0;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t c = n0 + MmTile<ET>::col(at.wn, at.lg, y, j) + q;
-        b[j][q] = c < V ? (bias != nullptr ? bias[c] : 0.0f) : NEG_INF;
+        const uint32_t c = MmTile<ET>::col(at.wn, at.lg, y, j) + q;
+        b[j][q] = (int32_t)c < cols ? (bias != nullptr ? first[c] : 0.0f) : NEG_INF;
       }
+  }
 }
 
 // Whether column c of the tile is one of the lane's in half y (columns y 128 +
