@@ -22,7 +22,8 @@ import torch
 from . import _lib
 from ._binding import (_DTYPES, LmHeadError, NotHandled, _alloc_on, _check, _device_ctx, _need, _same_device,
                        _stream_handle, status_string)
-from ._lib import LMHEAD_F32, PATH_AUTO, PATH_NONE, PATH_NVFP4, PATH_SKINNY, PATH_TILED
+from ._lib import (LMHEAD_BF16, LMHEAD_F16, LMHEAD_F32, NOT_HANDLED, OK, PATH_AUTO, PATH_NONE, PATH_NVFP4,
+                   PATH_SKINNY, PATH_TILED)
 from .training import (cross_entropy, embed, embed_backward, embed_backward_workspace_bytes, embedding,
                        xent_backward, xent_backward_workspace_bytes, xent_forward,
                        xent_forward_workspace_bytes)
