@@ -118,13 +118,12 @@ int64_t fill_blocks(const Fill &f, int threads, int per) {
   return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * per) : 0;
 }
 
-// Up to RANK_MAX positions: a position's place is the number of smaller
-// (id, position) pairs, counted against every other. A work-group ranks 64
-// positions, its waves splitting the others; M^2 comparisons are spread over
-// the chip in one launch. Sixteen waves where the ranking is all there is to
-// wait for; four under a dense gradient's fill, which takes longer than either
-// and is faster from small work-groups.
-constexpr int64_t RANK_MAX = 8192;
+// Few positions: a position's place is the number of smaller (id, position)
+// pairs, counted against every other. A work-group ranks 64 positions, its
+// waves splitting the others; M^2 comparisons are spread over the chip in one
+// launch. Sixteen waves where the ranking is all there is to wait for; four
+// under a dense gradient's fill, which takes longer than either and is faster
+// from small work-groups. How few: see ranks().
 template <int WAVES, int CHUNK>
 __global__ __launch_bounds__(64 * WAVES) void embed_rank_kernel(const void *ids, int ids64, int M, int64_t V,
                                                                 int64_t padding, uint32_t *__restrict__ keys,
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(64 * WAVES) void embed_rank_kernel(const void *ids,
   }
 }
 
-// More positions: a stable radix sort, least digit first. A work-group owns a
+// Else a stable radix sort, least digit first. A work-group owns a
 // contiguous tile of positions, each of its 16 waves a contiguous part of it.
 // embed_count_kernel counts the tile's digits; embed_scatter_kernel finds the
 // tile's and its waves' first place for each digit from all tiles' counts, and
@@ -454,6 +453,22 @@ int sum_tile(int64_t M) {
   return (int)(t < 16 ? 16 : t);
 }
 
+// Which sort. Ranking is one launch against two per nine bits of the ids, and
+// 8 ns per position while each work-group has a place of its own on the chip.
+// Added to a gradient (µs, ranked / radix; H = 4096, V = 128256, and H = 2048, V
+// = 64000): 4500 positions 37 / 38 (the second), 6144 53.2 / 51.8 and 42.8 / 41.6,
+// 8192 62 / 59 and 49.9 / 46.5. Dense, it is hidden as long as the fill takes
+// longer, about M ranks in the time of 30000 M elements (dense, µs): 64000 x 2048
+// 3500 positions 58 / 67, 4500 71 / 67; 128256 x 2048 8192 105 / 117, 10240 121 /
+// 120; 128256 x 4096 16384 210 / 233, 32768 336 / 261; 32000 x 2048 2048 36.5 /
+// 41.5, 8192 86 / 52; and up to 2048 positions whatever the table: 4096 x 256 30.0
+// / 32.2, at 4096 positions 43 / 33.
+constexpr int64_t RANK_ALWAYS = 2048, RANK_ADDED = 5120, RANK_DENSE = 16384, RANK_FILL = 30000;
+bool ranks(int64_t M, int64_t H, int64_t V, bool accumulate) {
+  if (accumulate) return M <= RANK_ADDED;
+  return M <= RANK_ALWAYS || (M <= RANK_DENSE && M * RANK_FILL <= V * H);
+}
+
 struct Plan {
   int64_t keys, order, keys2, order2, counts, part, bytes;
 };
@@ -462,7 +477,7 @@ Plan plan(int64_t M, int64_t H) {
   const int64_t list = align256(4 * M);
   p.keys = 0;
   p.order = list;
-  const bool radix = M > RANK_MAX;
+  const bool radix = M > RANK_ALWAYS;  // for some table, or added
   p.keys2 = 2 * list;
   p.order2 = p.keys2 + (radix ? list : 0);
   p.counts = p.order2 + (radix ? list : 0);
@@ -513,7 +528,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
   uint32_t *keys = reinterpret_cast<uint32_t *>(ws + pl.keys);
   uint32_t *order = reinterpret_cast<uint32_t *>(ws + pl.order);
   hipError_t e = hipSuccess;
-  if (c.M <= RANK_MAX) {
+  if (ranks(c.M, c.H, c.V, c.accumulate)) {
     f.sort_blocks = (int)ceil_div(c.M, 64);
     e = launch_rank(c, keys, order, f, s);
   } else {

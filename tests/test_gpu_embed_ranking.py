@@ -44,3 +44,30 @@ def test_order_is_that_of_positions(M):
     for gw, want in ((None, 7.0), (torch.ones(V, H, dtype=torch.bfloat16, device=DEV), 8.0)):
         out = L.embed_backward(go, ids, V, grad_weight=gw)
         assert bool((out[3] == want).all())
+
+
+# a table large enough for its fill to hide the ranking of 16384 positions; one
+# position more and a smaller table take the radix sort
+@pytest.mark.parametrize("M,V,H", [(8192, 120000, 2080), (16384, 240000, 2080), (16385, 240000, 2080),
+                                   (16384, 235000, 2080), (5120, 75000, 2080), (5121, 70000, 2080)])
+def test_large_tables(M, V, H):
+    say(f"embed ranking M={M} V={V} H={H}")
+    ids = tokens(M, M, V, "padded", torch.int32)
+    go = table(M + 1, M, H, "f16") * 0.01
+    for base in (None, table(M + 2, V, H, "f16")):
+        got = check_grad(go, ids, V, 0.5, base=base)
+        assert torch.equal(got, L.embed_backward(go, ids, V, 0.5, grad_weight=None if base is None else base.clone()))
+        del got
+    torch.cuda.empty_cache()
+
+
+def test_both_sorts_give_the_same_bits():
+    """The sums' order is that of (id, position), whichever sort found it."""
+    M, H = 3000, 64
+    ids = tokens(5, M, 600, "padded")
+    go = table(6, M, H, "bf16")
+    ranked = L.embed_backward(go, ids, 600, grad_weight=torch.zeros(600, H, dtype=torch.bfloat16, device=DEV))
+    small = L.embed_backward(go, ids, 600)        # V H = 38400: the radix sort
+    large = L.embed_backward(go, ids, 1 << 20)    # V H = 2^26 < 3000 * 30000, radix; the same rows
+    huge = L.embed_backward(go, ids, 1 << 20, grad_weight=torch.zeros(1 << 20, H, dtype=torch.bfloat16, device=DEV))
+    assert torch.equal(ranked, small) and torch.equal(large[:600], small) and torch.equal(huge[:600], small)
