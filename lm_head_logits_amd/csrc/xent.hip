@@ -546,6 +546,11 @@ __global__ __launch_bounds__(256) void xent_dhidden_out_kernel(const float *__re
   const int64_t e = (group_number() * 256 + threadIdx.x) * 8;
   if (e >= n) return;
   f32x4 s[2] = {zero4(), zero4()};
+  if (splits == 1) {  // many rows: the loop would load the one sum eight times
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = *reinterpret_cast<const f32x4 *>(dh + e + 4 * h);
+    splits = 0;
+  }
   for (int k0 = 0; k0 < splits; k0 += 8) {
     f32x4 v[8][2];  // eight splits' loads in flight (past the last: the last again, not added)
 #pragma unroll
