@@ -13,8 +13,8 @@
 // kernels' launches: the sort needs few CUs and the fill is what takes long.
 //
 // Measured: the lookup of 8192 rows of H = 4096 23 µs (134 MB, 5.8 TB/s; a
-// device copy reaches 5.0). Its gradient, V = 128256: 197 µs dense (1.12 GB,
-// 5.7 TB/s; the fill alone is 154), 61 µs added to a gradient that is there.
+// device copy reaches 4.7-5.0). Its gradient, V = 128256: 195 µs dense (1.12 GB,
+// 5.7 TB/s; the fill alone is 154), 59 µs added to a gradient that is there.
 #include "kstep.hpp"
 #include "ops_launch.hpp"
 
@@ -99,24 +99,18 @@ struct Fill {
   int64_t from, to;
   int sort_blocks; // work-groups of the launch that sort
 };
-// A fill work-group writes PER pieces per thread, in steps of its width. Small
-// work-groups in order fill fastest (1.05 GB alone: 256 threads of one piece
-// 155 µs, of four 176, 1024 of sixteen 171). The stores are not kept in the
-// caches: nothing reads the zeros, and what does not displace the rows to be
-// summed leaves them there (30011 positions, V = 151936, H = 2048: 180 -> 161 µs).
-template <int PER>
+// A thread writes one piece: small work-groups in order fill fastest (1.05 GB
+// alone: 256 threads of one piece 155 µs, of four 176, 1024 of sixteen 171).
+// The stores are not kept in the caches: nothing reads the zeros, and what does
+// not displace the rows to be summed leaves them there. In the sorting launches
+// the work-groups have 1024 threads all the same (30011 positions, V = 151936, H
+// = 2048, the whole call: one piece a thread 145 µs, four 160, sixteen 152; V =
+// 262144, H = 8192 1030, 1186, 1124; V = 32000, H = 2048 77, 78, 76).
 __device__ __forceinline__ void do_fill(const Fill &f) {
-  const int64_t b = group_number() - f.sort_blocks;
-  const int64_t p0 = f.from + b * ((int64_t)blockDim.x * PER) + threadIdx.x;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int64_t p = p0 + (int64_t)k * blockDim.x;
-    if (p < f.to) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, f.p + p);
-  }
+  const int64_t p = f.from + (group_number() - f.sort_blocks) * blockDim.x + threadIdx.x;
+  if (p < f.to) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, f.p + p);
 }
-int64_t fill_blocks(const Fill &f, int threads, int per) {
-  return f.to > f.from ? ceil_div(f.to - f.from, (int64_t)threads * per) : 0;
-}
+int64_t fill_blocks(const Fill &f, int threads) { return f.to > f.from ? ceil_div(f.to - f.from, threads) : 0; }
 
 // Few positions: a position's place is the number of smaller (id, position)
 // pairs, counted against every other. A work-group ranks 64 positions, its
@@ -128,7 +122,7 @@ template <int WAVES, int CHUNK>
 __global__ __launch_bounds__(64 * WAVES) void embed_rank_kernel(const void *ids, int ids64, int M, int64_t V,
                                                                 int64_t padding, uint32_t *__restrict__ keys,
                                                                 uint32_t *__restrict__ order, Fill f) {
-  if (group_number() >= f.sort_blocks) return do_fill<1>(f);
+  if (group_number() >= f.sort_blocks) return do_fill(f);
   __shared__ alignas(16) uint32_t sk[CHUNK];
   __shared__ uint32_t cnt[WAVES][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -177,7 +171,7 @@ __global__ __launch_bounds__(64 * WAVES) void embed_rank_kernel(const void *ids,
 // tile's and its waves' first place for each digit from all tiles' counts, and
 // places the positions in order (lanes of a wave with equal digits find each
 // other by ballots).
-constexpr int RX_THREADS = 1024, RX_WAVES = 16, RX_BITS = 9, RX_BINS = 1 << RX_BITS, RX_TILES = 256, RX_FILL = 16;
+constexpr int RX_THREADS = 1024, RX_WAVES = 16, RX_BITS = 9, RX_BINS = 1 << RX_BITS, RX_TILES = 256;
 
 struct RadixArgs {
   const void *ids;           // first pass: keys come from here
@@ -194,7 +188,7 @@ __device__ __forceinline__ uint32_t radix_key(const RadixArgs &a, int64_t m) {
 }
 
 __global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fill f) {
-  if (group_number() >= f.sort_blocks) return do_fill<RX_FILL>(f);
+  if (group_number() >= f.sort_blocks) return do_fill(f);
   __shared__ uint32_t h[RX_BINS];
   for (int d = threadIdx.x; d < RX_BINS; d += RX_THREADS) h[d] = 0;
   __syncthreads();
@@ -206,7 +200,7 @@ __global__ __launch_bounds__(RX_THREADS) void embed_count_kernel(RadixArgs a, Fi
 }
 
 __global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, Fill f) {
-  if (group_number() >= f.sort_blocks) return do_fill<RX_FILL>(f);
+  if (group_number() >= f.sort_blocks) return do_fill(f);
   __shared__ uint32_t at[RX_WAVES][RX_BINS];  // next place of (wave, digit)
   __shared__ uint32_t part[2][RX_BINS], sum[RX_BINS];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -280,7 +274,7 @@ __global__ __launch_bounds__(RX_THREADS) void embed_scatter_kernel(RadixArgs a, 
 
 // ---------------------------------------------------------------------------
 // Summing. The sorted positions are cut into tiles; a work-group sums a tile's
-// rows over 2048 columns, 8 per thread. An id whose positions all lie in the
+// rows over 1024 columns, 8 per thread. An id whose positions all lie in the
 // tile is written at once; the sums of an id that began in an earlier tile
 // (slot 0) or goes on in the next (slot 1) go to the workspace, and
 // embed_join_kernel adds those of an id in tile order.
@@ -446,8 +440,8 @@ __global__ __launch_bounds__(EJ_GROUPS * EJ_LANES) void embed_join_kernel(SumArg
   *reinterpret_cast<u32x2 *>(dst) = o;
 }
 
-// Positions per tile: enough tiles to fill the chip, at most about 1024
-// (their partial sums are read back), at least 8 positions.
+// Positions per tile: enough tiles to fill the chip, at most 512 (their partial
+// sums are read back), at least 16 positions.
 int sum_tile(int64_t M) {
   const int64_t t = ceil_div(M, 512);
   return (int)(t < 16 ? 16 : t);
@@ -455,14 +449,14 @@ int sum_tile(int64_t M) {
 
 // Which sort. Ranking is one launch against two per nine bits of the ids, and
 // 8 ns per position while each work-group has a place of its own on the chip.
-// Added to a gradient (µs, ranked / radix; H = 4096, V = 128256, and H = 2048, V
-// = 64000): 4500 positions 37 / 38 (the second), 6144 53.2 / 51.8 and 42.8 / 41.6,
-// 8192 62 / 59 and 49.9 / 46.5. Dense, it is hidden as long as the fill takes
-// longer, about M ranks in the time of 30000 M elements (dense, µs): 64000 x 2048
-// 3500 positions 58 / 67, 4500 71 / 67; 128256 x 2048 8192 105 / 117, 10240 121 /
-// 120; 128256 x 4096 16384 210 / 233, 32768 336 / 261; 32000 x 2048 2048 36.5 /
-// 41.5, 8192 86 / 52; and up to 2048 positions whatever the table: 4096 x 256 30.0
-// / 32.2, at 4096 positions 43 / 33.
+// Added to a gradient (µs, ranked / radix): H = 4096, V = 128256 4500 positions
+// 46 / 47, 6144 53.5 / 51.9, 8192 63 / 59; H = 2048, V = 64000 37.4 / 38.3, 42.8 /
+// 41.3, 49.9 / 46.5. Dense, it is hidden as long as the fill takes longer, about
+// M ranks in the time of 30000 M elements (the whole call, V x H): 64000 x 2048
+// 3500 positions 58 / 62, 4500 71 / 63; 128256 x 2048 8192 105 / 114, 10240 121 /
+// 117; 128256 x 4096 16384 209 / 235, 32768 336 / 258; 32000 x 2048 2048 36 / 41,
+// 8192 87 / 52; and up to 2048 positions whatever the table: 4096 x 256 29.5 / 31,
+// at 4096 positions 43 / 32.
 constexpr int64_t RANK_ALWAYS = 2048, RANK_ADDED = 5120, RANK_DENSE = 16384, RANK_FILL = 30000;
 bool ranks(int64_t M, int64_t H, int64_t V, bool accumulate) {
   if (accumulate) return M <= RANK_ADDED;
@@ -511,7 +505,7 @@ namespace {
 hipError_t launch_rank(const EmbedBackward &c, uint32_t *keys, uint32_t *order, const Fill &f, hipStream_t s) {
   const int waves = c.accumulate ? 16 : 4;
   auto k = c.accumulate ? embed_rank_kernel<16, 8192> : embed_rank_kernel<4, 2048>;
-  return launch_kernel(k, numbered_grid(f.sort_blocks + fill_blocks(f, 64 * waves, 1)), dim3(64 * waves), s,
+  return launch_kernel(k, numbered_grid(f.sort_blocks + fill_blocks(f, 64 * waves)), dim3(64 * waves), s,
                        c.ids, c.ids64, (int)c.M, c.V, c.padding, keys, order, f);
 }
 }  // namespace
@@ -561,7 +555,7 @@ hipError_t launch_embed_backward(const EmbedBackward &c, hipStream_t s) {
         f.to = all * (part + 1) / (2 * passes);
         f.sort_blocks = a.tiles;
         e = launch_kernel(half == 0 ? embed_count_kernel : embed_scatter_kernel,
-                          numbered_grid(a.tiles + fill_blocks(f, RX_THREADS, RX_FILL)), dim3(RX_THREADS), s, a, f);
+                          numbered_grid(a.tiles + fill_blocks(f, RX_THREADS)), dim3(RX_THREADS), s, a, f);
       }
     }
   }
