@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include "../../include/lmhead.h"
-#include "groups.hpp"
 #include "korder.hpp"
 
 namespace lmhead {
@@ -50,16 +49,6 @@ hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_
                          typename arg_of<P>::type... args) {
   void *ptrs[] = {static_cast<void *>(&args)...};
   return hipLaunchKernel(reinterpret_cast<const void *>(kernel), grid, block, ptrs, 0, stream);
-}
-
-// The grid of n numbered work-groups (groups.hpp), and a work-group's number in
-// it: n and above for the last ones, where n passes one dimension.
-inline dim3 numbered_grid(int64_t n) {
-  const GroupGrid g = group_grid(n);
-  return dim3(g.x, g.y);
-}
-__device__ __forceinline__ int64_t group_number() {
-  return ((int64_t)blockIdx.y << GROUPS_X_BITS) + blockIdx.x;
 }
 
 // Compute units of the current device (queried once per device).

@@ -3,6 +3,7 @@
 // before any of these runs.
 #pragma once
 
+#include "group_launch.hpp"
 #include "launch.hpp"
 
 namespace lmhead {

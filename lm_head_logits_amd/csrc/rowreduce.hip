@@ -18,6 +18,7 @@
 // symmetric (both partners of a butterfly
 // step compute the same bits), and the order depends only on V, so a row's
 // result does not depend on M or on which GEMM kernel wrote the partials.
+#include "group_launch.hpp"
 #include "kstep.hpp"
 #include "launch.hpp"
 
