@@ -310,7 +310,12 @@ size_t lmhead_xent_forward_workspace_bytes(int64_t M, int64_t V);
  *   workspace   at least lmhead_xent_backward_workspace_bytes(M, H, V, grad_bias != NULL)
  *               bytes, 256-byte aligned, overwritten; as above
  * Sums are fp32 in a fixed order; G enters the two products rounded to the
- * inputs' type. With M = 0, grad_W and grad_bias are zero. */
+ * inputs' type. It is rounded after scaling by one factor for the whole call,
+ * made from the largest finite upstream gradient of its rows: unlike the forward
+ * pass's results, the last bits of a row's grad_hidden depend on the other rows'
+ * upstream gradients, and with fp16 the entries of G below 2^-28 of the largest
+ * lose digits, those below 2^-39 vanish. With M = 0, grad_W and grad_bias are
+ * zero. */
 lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V,
                                    float alpha, const float *bias, lmhead_dtype in_dtype,
                                    const void *target, lmhead_index target_type,
@@ -319,9 +324,11 @@ lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, con
                                    float *grad_bias, void *workspace, size_t workspace_bytes,
                                    void *stream);
 
-/* Host-only: bytes of workspace lmhead_xent_backward needs: one piece of G
- * (256 MiB, or 2 * 8192 * M bytes where that is more), fp32 sums of
- * grad_hidden, and little else. 0 outside the shape contract or when M == 0. */
+/* Host-only: bytes of workspace lmhead_xent_backward needs: one piece of G (at
+ * most 256 MiB, or 2 * 8192 * M bytes where that is more), the fp32 [M, H] sum of
+ * grad_hidden, once per split of the vocabulary (up to 64 where M H is small; the
+ * same whether grad_hidden is wanted or not), and little else. 0 outside the
+ * shape contract or when M == 0. */
 size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias);
 
 /* The embedding lookup out[m, :] = scale * W[ids[m], :], the product taken at

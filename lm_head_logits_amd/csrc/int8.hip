@@ -14,10 +14,13 @@
 //
 // Measured with the quantisation of the hidden rows, H = 4096, V = 128256: one
 // row 83 µs (526 MB, 6.3 TB/s), 48 rows with fp32 logits 91 µs (550 MB); 2048
-// rows, V = 151936: 1.0 ms (2.5 POP/s). 130 rows, H = 2048, V = 151936: 91 µs
-// (351 MB, 3.9 TB/s): 594 tiles are 2.3 rounds of the 256 work-groups, and half
-// of what a stage loads is the hidden rows again; tiles of the last round cut
-// in two took 90 µs, K starts spread over the weight's rows the same.
+// rows, V = 151936: 0.97-1.05 ms by card (2.4-2.6 POP/s). 130 rows, H = 2048, V =
+// 151936: 91-105 µs by card (351 MB, 3.3-3.9 TB/s): 594 tiles are 2.3 rounds of
+// the 256 work-groups, and half of what a stage loads is the hidden rows again;
+// tiles of the last round cut in two took 90 µs where whole ones took 91, K
+// starts spread over the weight's rows the same. The quantiser: 2048 rows of H =
+// 4096 12 µs, a head of V = 128256 310-430 µs (1.58 GB read and written, up to 5.0
+// TB/s; a device copy reaches 4.7-5.0).
 #include "mma256.hpp"
 #include "ops_launch.hpp"
 

@@ -53,17 +53,18 @@
 // next one's operands arrive. The epilogue therefore has LDS of its own (32 KB,
 // MM_EPI) and leaves the stage buffers alone.
 //
-// Measured (bf16 random data, one kernel alone, 16-bit results written):
-// K-inner operands 4096 x 32768 x 4096 803 µs (1.37 PFLOP/s), 4096 x 4096 x
-// 32768 709 µs (1.55), B K-outer 711 µs (1.55), both K-outer (32768 x 4096 x
-// 4096) 788 µs (1.40), int8 4096 x 32768 x 4096 410 µs (2.68 POP/s). On the
-// way there, same shapes: four phases of 16 MFMAs 890 µs, two of 32 865; the
-// waves of a SIMD in step, without the barrier of offset, 969; a work-group
-// per tile instead of tile after tile 865 (both K-outer 935 against 788); the
-// 32x32x16 MFMA 907, in fewer cycles but at a lower clock. That is what bounds
-// it now: the matrix pipes are busy 76-80% of the cycles (67% with both
-// operands K-outer) and the card lowers its clock to 1.8-1.95 GHz under them;
-// a copy whose loads all hit L2 ran 11% faster, one that loaded nothing 20%.
+// Measured, with the epilogues of the kernels built on it (from card to card;
+// rows of A x rows of B x K): K-inner operands 4096 x 32256 x 4096 730-770 µs
+// (1.40-1.48 PFLOP/s), B K-outer 4096 x 4096 x 32256 680-720 µs (1.50-1.59), both
+// K-outer 32256 x 4096 x 4096 790-850 µs (1.28-1.37), int8 2048 x 151936 x 4096 0.96-1.04
+// ms (2.5-2.65 POP/s). Steps on the way, on a bench of the core alone with 32768
+// columns, whose K-inner product then took 803 µs: four phases of 16 MFMAs 890,
+// two of 32 865; the waves of a SIMD in step, without the barrier of offset, 969;
+// a work-group per tile instead of tile after tile 865 (both K-outer 935 against
+// 788); the 32x32x16 MFMA 907, in fewer cycles but at a lower clock. That is what
+// bounds it now: the matrix pipes are busy 74-79% of the cycles (65% with both
+// operands K-outer) and the card lowers its clock to 1.7-1.95 GHz under them; a
+// copy whose loads all hit L2 ran 11% faster, one that loaded nothing 20%.
 #pragma once
 
 #include "kstep.hpp"

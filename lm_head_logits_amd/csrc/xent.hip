@@ -20,11 +20,12 @@
 // keeping M V values from the forward pass.
 //
 // Everything is bound by the matrix pipes (mma256.hpp) except for few rows,
-// where the weight's bytes bind, and for the smallest heads, where the launches
-// do. 4096 rows, H = 4096, V = 128256: forward 2.9 ms (1.49 PFLOP/s, its
-// epilogue included), per piece of 32064 columns G 0.73 ms (1.47), G W 0.68 ms
-// (1.58), G^T hidden 0.79 ms (1.36); 11.7 ms in all, of which the fourth
-// product, t made again, is 2.9.
+// where the weight's bytes bind, and for the smallest heads, where six short
+// kernels follow each other. 4096 rows, H = 4096, V = 128256, from card to card:
+// forward 2.9-3.1 ms (1.4-1.5 PFLOP/s, its epilogue included), per piece of 32256
+// columns G 0.73-0.77 ms (1.40-1.48), G W 0.68-0.72 ms (1.50-1.59), G^T hidden
+// 0.79-0.85 ms (1.28-1.37); 12.0-12.4 ms in all, of which the fourth product, t
+// made again, is 2.9-3.1.
 //
 // Roundings: t, the statistics, p and grad_bias are fp32. G is rounded to the
 // inputs' 16-bit type, which the matrix pipes take: at most 2^-8 (bf16) or
