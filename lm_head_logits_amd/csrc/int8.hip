@@ -14,7 +14,7 @@
 //
 // Measured with the quantisation of the hidden rows, H = 4096, V = 128256: one
 // row 83 µs (526 MB, 6.3 TB/s), 48 rows with fp32 logits 91 µs (550 MB); 2048
-// rows, V = 151936: 0.97-1.05 ms by card (2.4-2.6 POP/s). 130 rows, H = 2048, V =
+// rows, V = 151936: 0.97-1.08 ms by card (2.4-2.6 POP/s). 130 rows, H = 2048, V =
 // 151936: 91-105 µs by card (351 MB, 3.3-3.9 TB/s): 594 tiles are 2.3 rounds of
 // the 256 work-groups, and half of what a stage loads is the hidden rows again;
 // tiles of the last round cut in two took 90 µs where whole ones took 91, K

@@ -104,13 +104,13 @@ __device__ __forceinline__ void column_bias(const float *bias, int64_t V, int64_
   // 32-bit columns of the tile: 64-bit ones cost registers that the epilogues lack
   const int32_t cols = (int32_t)(V - n0 < MM_T ? V - n0 : MM_T);
   if (bias != nullptr || cols < MM_T) {
-    const float *const first = bias + n0;
+    const float *const first = bias != nullptr ? bias + n0 : nullptr;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t c = MmTile<ET>::col(at.wn, at.lg, y, j) + q;
-        b[j][q] = (int32_t)c < cols ? (bias != nullptr ? first[c] : 0.0f) : NEG_INF;
+        b[j][q] = (int32_t)c < cols ? (first != nullptr ? first[c] : 0.0f) : NEG_INF;
       }
   }
 }
