@@ -24,7 +24,7 @@
 // kernels follow each other. 4096 rows, H = 4096, V = 128256, from card to card:
 // forward 2.9-3.1 ms (1.4-1.5 PFLOP/s, its epilogue included), per piece of 32256
 // columns G 0.73-0.77 ms (1.40-1.48), G W 0.68-0.72 ms (1.50-1.59), G^T hidden
-// 0.79-0.85 ms (1.28-1.37); 12.0-12.4 ms in all, of which the fourth product, t
+// 0.79-0.85 ms (1.28-1.37); 12.0-12.7 ms in all, of which the fourth product, t
 // made again, is 2.9-3.1.
 //
 // Roundings: t, the statistics, p and grad_bias are fp32. G is rounded to the
