@@ -331,6 +331,103 @@ lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, con
  * shape contract or when M == 0. */
 size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias);
 
+/* ---------------------------------------------------------------------------
+ * Further losses of the head's logits, which are never whole in memory:
+ *   t[m, v] = (alpha * (hidden[m, :] . W[v, :]) + bias[v]) / temperature,
+ *   lse[m] = log sum_v exp(t[m, v]),  log q[m, v] = t[m, v] - lse[m]
+ * (alpha / temperature and bias[v] / temperature are taken at fp32 each).
+ * A forward call makes the rows' losses and, where `state` is given, leaves
+ * there what lmhead_loss_backward needs; that call may be made more than once on
+ * one state, and the state belongs to the call's hidden, W and bias.
+ *   temperature > 0
+ *   state       at least lmhead_loss_state_bytes(M, H, V, K) bytes, 256-byte aligned
+ *               (device, written), or NULL when no backward pass follows
+ *   workspace   at least lmhead_loss_forward_workspace_bytes(M, H, V, K, state != NULL)
+ *               bytes, 256-byte aligned, overwritten; not in use by other work
+ *               until this call's work has finished
+ * K is the teacher's logits per row for lmhead_distill_forward and 0 for the others. What
+ * is said of lmhead_xent_forward about -inf, the lowest value, +inf and NaN
+ * holds, as does its independence of the call's other rows (preference: of the
+ * other pairs). Returns as lmhead_xent_forward.
+ * ------------------------------------------------------------------------- */
+
+/* The divergence from a teacher's top logits. A row's entries k are those whose
+ * id is a column of the call and whose logit is not -inf; the others are absent.
+ *   p_k = exp(teacher_logits[m, k] / temperature - n),
+ *   n = teacher_lse[m], or (NULL) the log-sum-exp over the row's entries
+ *   loss[m] = sum_k p_k (log p_k - log q[m, id_k])
+ * With teacher_lse, the log-sum-exp of the teacher's logits / temperature over its
+ * whole vocabulary, the entries' mass P = sum p_k is below 1 and what lies
+ * outside them is left out of the sum. A row without entries has loss 0 and no
+ * gradient. An id that a row has twice counts twice.
+ *   teacher_ids     [M, K] of ids_type                          (device, read)
+ *   teacher_logits  [M, K] of logits_dtype, any order           (device, read)
+ *   teacher_lse     fp32 [M] or NULL                            (device, read)
+ *   loss            fp32 [M]                                    (device, written)
+ *   1 <= K <= LMHEAD_MAX_TEACHER */
+#define LMHEAD_MAX_TEACHER ((int64_t)1024)
+lmhead_status lmhead_distill_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
+                                     const float *bias, lmhead_dtype in_dtype, float temperature,
+                                     const void *teacher_ids, lmhead_index ids_type, const void *teacher_logits,
+                                     lmhead_dtype logits_dtype, int64_t K, const float *teacher_lse, float *loss,
+                                     void *state, size_t state_bytes, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/* The clipped policy loss with a KL term of the tokens target[m]:
+ *   logp[m] = log q[m, target[m]],  r = exp(logp - old_logp) (NULL: 1),
+ *   d = ref_logp - logp,
+ *   loss[m] = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_coef (exp(d) - d - 1)
+ * with A = advantage[m]; the first term is 0 where A is 0, the second where ref_logp
+ * is NULL or kl_coef is 0. Its derivative by logp is -r A where the minimum is r A
+ * (ties included) and 0 elsewhere, and kl_coef (1 - exp(d)). Rows whose target is
+ * ignore_index or no column of the call have loss and logp 0 and no gradient.
+ *   target     [M] of target_type; advantage, old_logp, ref_logp fp32 [M]  (device, read)
+ *   loss, logp fp32 [M]                                                    (device, written) */
+lmhead_status lmhead_policy_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
+                                    const float *bias, lmhead_dtype in_dtype, float temperature, const void *target,
+                                    lmhead_index target_type, int64_t ignore_index, const float *advantage,
+                                    const float *old_logp, const float *ref_logp, float clip_low, float clip_high,
+                                    float kl_coef, float *loss, float *logp, void *state, size_t state_bytes,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The logistic loss of preferred pairs. Sequence s is rows starts[s] ..
+ * starts[s + 1] - 1 (ascending, within [0, M]; rows in none of them are left out);
+ * sequence i is the preferred one of pair i, sequence pairs + i the other.
+ *   logp[s] = sum of log q[m, target[m]] over the sequence's rows that are not left
+ *             out (as above), or (average != 0) their mean; 0 without any
+ *   z = beta ((logp[i] - ref_logp[i]) - (logp[pairs + i] - ref_logp[pairs + i])) - margin
+ *   loss[i] = -(1 - label_smoothing) log sigma(z) - label_smoothing log sigma(-z)
+ * with ref_logp taken as 0 where NULL; sums and z are fp64.
+ *   starts      [2 pairs + 1] of starts_type                    (device, read)
+ *   ref_logp    fp32 [2 pairs] or NULL                          (device, read)
+ *   loss, logp  fp32 [pairs], [2 pairs]                         (device, written)
+ *   0 <= label_smoothing <= 1 */
+lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
+                                        const float *bias, lmhead_dtype in_dtype, float temperature, const void *target,
+                                        lmhead_index target_type, int64_t ignore_index, const void *starts,
+                                        lmhead_index starts_type, int64_t pairs, const float *ref_logp, float beta,
+                                        float margin, float label_smoothing, int average, float *loss, float *logp,
+                                        void *state, size_t state_bytes, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/* Gradients of sum_m grad_loss[m] loss[m] (preference: over the pairs) of one of the
+ * three calls above, whose state is given and whose other arguments are the same
+ * (K: 0 but for lmhead_distill_forward).
+ *   grad_loss   fp32 [M], or [pairs]                            (device, read)
+ *   grad_hidden, grad_W, grad_bias, workspace   as in lmhead_xent_backward, with
+ *               lmhead_loss_backward_workspace_bytes(M, H, V, K, grad_bias != NULL) bytes
+ * Rounded and scaled as there. */
+lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
+                                   const float *bias, lmhead_dtype in_dtype, float temperature, int64_t K,
+                                   const float *grad_loss, const void *state, size_t state_bytes, void *grad_hidden,
+                                   void *grad_W, float *grad_bias, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Host-only: bytes of the state and of the workspaces (0 outside the shape contract or when M == 0). */
+size_t lmhead_loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K);
+size_t lmhead_loss_forward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int with_state);
+size_t lmhead_loss_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int grad_bias);
+
 /* The embedding lookup out[m, :] = scale * W[ids[m], :], the product taken at
  * fp32 and rounded once. An id outside [0, V) gives a row of zeros (so a
  * vocabulary shard takes ids - v0 and the shards' results add up).

@@ -37,7 +37,9 @@ EXPORTS = ("lmhead_logits", "lmhead_logits_path", "lmhead_logits_ex", "lmhead_lo
            "lmhead_path_for", "lmhead_status_string", "lmhead_version",
            "lmhead_xent_forward", "lmhead_xent_forward_workspace_bytes", "lmhead_xent_backward",
            "lmhead_xent_backward_workspace_bytes", "lmhead_embed", "lmhead_embed_backward",
-           "lmhead_embed_backward_workspace_bytes", "lmhead_quantize_int8", "lmhead_logits_int8")
+           "lmhead_embed_backward_workspace_bytes", "lmhead_quantize_int8", "lmhead_logits_int8",
+           "lmhead_distill_forward", "lmhead_policy_forward", "lmhead_preference_forward", "lmhead_loss_backward",
+           "lmhead_loss_state_bytes", "lmhead_loss_forward_workspace_bytes", "lmhead_loss_backward_workspace_bytes")
 # include/lmhead_probes.h: measurement probes (not part of the projection),
 # in a library of their own
 PROBE_EXPORTS = ("lmhead_probe_grid", "lmhead_probe_hbm_read", "lmhead_probe_mfma_bf16")
@@ -111,6 +113,22 @@ def load() -> ctypes.CDLL:
     lib.lmhead_quantize_int8.argtypes = [vp, i64, i64, i32, vp, vp, vp]
     lib.lmhead_logits_int8.restype = i32
     lib.lmhead_logits_int8.argtypes = [vp, vp, i64, i64, vp, vp, i64, f32, vp, i32, vp, vp]
+    head = [vp, i64, i64, vp, i64, f32, vp, i32, f32]  # hidden .. temperature
+    memory = [vp, sz, vp, sz, vp]  # state, workspace, stream
+    lib.lmhead_distill_forward.restype = i32
+    lib.lmhead_distill_forward.argtypes = [*head, vp, i32, vp, i32, i64, vp, vp, *memory]
+    lib.lmhead_policy_forward.restype = i32
+    lib.lmhead_policy_forward.argtypes = [*head, vp, i32, i64, vp, vp, vp, f32, f32, f32, vp, vp, *memory]
+    lib.lmhead_preference_forward.restype = i32
+    lib.lmhead_preference_forward.argtypes = [*head, vp, i32, i64, vp, i32, i64, vp, f32, f32, f32, i32, vp, vp, *memory]
+    lib.lmhead_loss_backward.restype = i32
+    lib.lmhead_loss_backward.argtypes = [*head, i64, vp, vp, sz, vp, vp, vp, vp, sz, vp]
+    lib.lmhead_loss_state_bytes.restype = sz
+    lib.lmhead_loss_state_bytes.argtypes = [i64, i64, i64, i64]
+    lib.lmhead_loss_forward_workspace_bytes.restype = sz
+    lib.lmhead_loss_forward_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    lib.lmhead_loss_backward_workspace_bytes.restype = sz
+    lib.lmhead_loss_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
     _lib = lib
     return lib
 

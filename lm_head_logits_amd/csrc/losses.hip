@@ -1,0 +1,1004 @@
+// losses.hip -- losses of the head's logits beyond the cross entropy against
+// tokens (xent.hip): the divergence from a teacher's top logits, the clipped
+// policy loss with a KL term, the logistic loss of preferred pairs; and their
+// gradients.
+//
+//   t[m, v] = (alpha (hidden[m, :] . W[v, :]) + bias[v]) / T
+//   lse[m] = log sum_v e^t[m, v],  q = e^(t - lse)
+//   distill      p_k = e^(s_k / T - n) over the teacher's entries present, n their
+//                log-sum-exp or the teacher's own
+//                loss[m] = sum_k p_k (log p_k - log q[id_k])
+//                G[m, v] = g_m (P q[v] - sum_k p_k [v = id_k]),  P = sum_k p_k
+//   token losses logp[m] = t[m, y_m] - lse[m], c[m] = d loss / d logp[m],
+//                G[m, v] = g c_m ([v = y_m] - q[v])
+//   policy       r = e^(logp - old), d = ref - logp
+//                loss[m] = -min(r A, clip(r) A) + kl (e^d - d - 1)
+//                c = -r A [r A <= clip(r) A] + kl (1 - e^d)
+//   preference   S = sum or mean of logp over a sequence,
+//                z = beta ((S_w - ref_w) - (S_l - ref_l)) - margin
+//                loss = -(1 - e) log sigma(z) - e log sigma(-z)
+//   grad_hidden = alpha / T G W,  grad_W = alpha / T G^T hidden,  grad_bias = 1 / T sum_m G
+//
+// Forward: one matrix product whose epilogue keeps, per row and 256-column
+// tile, the largest t and the sum of exponentials, and the t that the loss
+// asks for (the target's, or the teacher's entries'); a second kernel folds a
+// row's tiles and makes its loss and c. Backward: the pieces of xent.hip.
+//
+// 1 / T: alpha / T and a copy of the bias divided by T go into the products.
+#include "losses_launch.hpp"
+#include "xent_core.hpp"
+
+namespace lmhead {
+
+namespace {
+
+constexpr int32_t NO_ID = 0x7FFFFFFF;
+
+// What the forward pass leaves for the backward pass, in one buffer.
+struct StateLayout {
+  int64_t y, lse, coef, up, bias, ids, p, tk, bytes;
+};
+StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) {
+  StateLayout s;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t b = at;
+    at += align256(bytes);
+    return b;
+  };
+  s.y = take(4 * M);
+  s.lse = take(4 * M);
+  s.coef = take(4 * M);
+  s.up = take(4 * M);
+  s.bias = take(4 * V);
+  s.ids = take(4 * M * K);
+  s.p = take(4 * M * K);
+  s.tk = take(4 * M * K);
+  s.bytes = at;
+  (void)H;
+  (void)keep;
+  return s;
+}
+struct State {
+  int32_t *y;      // [M] target column or -1
+  float *lse;      // [M]
+  float *coef;     // [M] d loss / d logp; distill: P
+  int32_t *up;     // [M] which element of the upstream gradient is the row's
+  float *bias;     // [V] bias / T, where T != 1
+  int32_t *ids;    // [M, K] the teacher's tokens in ascending order, NO_ID behind the last
+  float *p, *tk;   // [M, K] their probabilities and the head's t
+};
+State state_at(void *base, const StateLayout &l) {
+  uint8_t *const b = static_cast<uint8_t *>(base);
+  return State{reinterpret_cast<int32_t *>(b + l.y),    reinterpret_cast<float *>(b + l.lse),
+               reinterpret_cast<float *>(b + l.coef),   reinterpret_cast<int32_t *>(b + l.up),
+               reinterpret_cast<float *>(b + l.bias),   reinterpret_cast<int32_t *>(b + l.ids),
+               reinterpret_cast<float *>(b + l.p),      reinterpret_cast<float *>(b + l.tk)};
+}
+
+struct ForwardLayout {
+  int64_t part, tlogit, rowlogp, ent, ptr, state, bytes;
+};
+ForwardLayout forward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool with_state) {
+  ForwardLayout f;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t b = at;
+    at += align256(bytes);
+    return b;
+  };
+  const int64_t nvt = ceil_div(V, MM_T);
+  f.part = take(8 * M * nvt);
+  f.tlogit = take(4 * M);
+  f.rowlogp = take(4 * M);
+  f.ent = take(K ? 4 * M : 0);
+  f.ptr = take(K ? 2 * M * (nvt + 1) : 0);
+  f.state = take(with_state ? 0 : state_layout(M, H, V, K, false).bytes);
+  f.bytes = at;
+  return f;
+}
+
+// ---------------------------------------------------------------------------
+// Before the product
+// ---------------------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void loss_bias_scale_kernel(const float *__restrict__ bias, int64_t V, float T,
+                                                              float *__restrict__ out) {
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (v < V) out[v] = __fdiv_rn(bias[v], T);
+}
+
+// A row of the teacher's entries, one wave each: their probabilities, and the
+// entries in the order of their tokens (by counting for each the smaller pairs
+// (token, place)), with the first entry of every 256-column tile. An entry
+// whose token is no column of the call, or whose logit is -inf, is absent.
+constexpr int DP_WAVES = 4;
+struct DistillPrep {
+  const void *ids;
+  int ids64;
+  int64_t M, V, K;
+  const void *logits;
+  OutType type;
+  const float *teacher_lse;
+  float T;
+  int32_t *sid;    // [M, K]
+  float *sp;       // [M, K]
+  uint16_t *ptr;   // [M, nvt + 1] entries before each tile
+  float *ent;      // [M] sum p log p
+  float *P;        // [M] sum p
+};
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x = __fadd_rn(x, __shfl_xor(x, d));
+  return x;
+}
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    const float o = __shfl_xor(x, d);
+    x = x != x || o != o ? __builtin_nanf("") : fmaxf(x, o);
+  }
+  return x;
+}
+// E: entries a lane, at least K / 64
+template <int E>
+__global__ __launch_bounds__(64 * DP_WAVES) void distill_prep_kernel(DistillPrep c) {
+  __shared__ int32_t id_sh[DP_WAVES][64 * E], sorted_sh[DP_WAVES][64 * E];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = group_number() * DP_WAVES + wave;
+  if (m >= c.M) return;  // waves work alone
+  int32_t *const id_w = id_sh[wave], *const sorted = sorted_sh[wave];
+  const int K = (int)c.K;
+  int32_t id[E];
+  float v[E];
+  float mx = NEG_INF;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int k = lane + 64 * e;
+    id[e] = NO_ID;
+    v[e] = NEG_INF;
+    if (k < K) {
+      const int64_t at = m * c.K + k;
+      const int64_t i = c.ids64 ? static_cast<const int64_t *>(c.ids)[at] : (int64_t)static_cast<const int32_t *>(c.ids)[at];
+      const float s = c.type == OUT_F32    ? static_cast<const float *>(c.logits)[at]
+                      : c.type == OUT_BF16 ? (float)static_cast<const __bf16 *>(c.logits)[at]
+                                           : (float)static_cast<const _Float16 *>(c.logits)[at];
+      if (i >= 0 && i < c.V && s != NEG_INF) {
+        id[e] = (int32_t)i;
+        v[e] = __fdiv_rn(s, c.T);
+        mx = mx != mx || v[e] != v[e] ? __builtin_nanf("") : fmaxf(mx, v[e]);
+      }
+      id_w[k] = id[e];
+    }
+  }
+  mx = wave_max(mx);
+  float s = 0.0f;
+  const float lse_t = c.teacher_lse != nullptr ? c.teacher_lse[m] : 0.0f;
+  if (c.teacher_lse == nullptr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (id[e] != NO_ID) s = __fadd_rn(s, expf(__fsub_rn(v[e], mx)));
+    s = wave_sum(s);
+  }
+  const float ls = logf(s);
+  float p[E], ent = 0.0f, P = 0.0f;
+  int count = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    p[e] = 0.0f;
+    if (id[e] != NO_ID) {
+      const float lp = c.teacher_lse != nullptr ? __fsub_rn(v[e], lse_t) : __fsub_rn(__fsub_rn(v[e], mx), ls);
+      p[e] = expf(lp);
+      if (p[e] != 0.0f) ent = __fadd_rn(ent, __fmul_rn(p[e], lp));
+      P = __fadd_rn(P, p[e]);
+      ++count;
+    }
+  }
+  ent = wave_sum(ent);
+  P = wave_sum(P);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) count += __shfl_xor(count, d);
+  sched_fence();  // other lanes' values: LDS keeps a wave's order
+  int rank[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) rank[e] = 0;
+  for (int j = 0; j < K; ++j) {
+    const int32_t other = id_w[j];
+#pragma unroll
+    for (int e = 0; e < E; ++e) rank[e] += other < id[e] || (other == id[e] && j < lane + 64 * e) ? 1 : 0;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (lane + 64 * e < K) {
+      sorted[rank[e]] = id[e];
+      c.sid[m * c.K + rank[e]] = id[e];
+      c.sp[m * c.K + rank[e]] = p[e];
+    }
+  sched_fence();
+  const int64_t nvt = (c.V + MM_T - 1) / MM_T;
+  for (int64_t t = lane; t <= nvt; t += 64) {
+    int lo = 0, hi = count;  // the first of the present entries at or past the tile's first column
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (sorted[mid] < t * MM_T) lo = mid + 1;
+      else hi = mid;
+    }
+    c.ptr[m * (nvt + 1) + t] = (uint16_t)lo;
+  }
+  if (lane == 0) {
+    c.ent[m] = ent;
+    c.P[m] = c.teacher_lse == nullptr && count > 0 ? (P != P ? P : 1.0f) : P;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The product's epilogue
+// ---------------------------------------------------------------------------
+
+struct LossFwdArgs {
+  const uint8_t *hidden, *W;
+  int64_t M, H, V;
+  float alpha;
+  const float *bias;
+  const void *target;  // target losses
+  int target64;
+  int64_t ignore;
+  float2 *part;        // [vocabulary tile][M] {largest t, sum of exp(t - largest)}
+  float *tlogit;       // [M] t at the target (rows with one)
+  const int32_t *sid;  // PICK: the teacher's entries (distill_prep_kernel)
+  const uint16_t *ptr;
+  float *tk;           // [M, K] t at the entries
+  int64_t K;
+};
+
+// PICK: t at the rows' entries in the tile instead of at one target. Through
+// LDS, 32 rows at a time: all 256 columns of the rows are written, then 16
+// threads a row take that row's entries from it. Groups of rows without an
+// entry are left out.
+template <int ET, bool PICK>
+struct LossStats {
+  LossFwdArgs p;
+  u32x4 *epi;
+  int64_t nmt, nvt;
+
+  __device__ __forceinline__ int64_t tiles() const { return nmt * nvt; }
+  __device__ __forceinline__ MmJob job(int32_t t) const {
+    int64_t mt, vt;
+    mm_tile_at(t, nmt, nvt, mt, vt);
+    return logits_job(p.hidden, p.W, p.M, p.H, p.V, mt * MM_T, vt * MM_T);
+  }
+  __device__ __forceinline__ void epilogue(MmTile<ET> &tile, int32_t t) const {
+    int64_t mt, vt;
+    mm_tile_at(t, nmt, nvt, mt, vt);
+    const int64_t m0 = mt * MM_T, n0 = vt * MM_T;
+    const LanePlace at;
+    float bias[2][2][4];
+    column_bias<ET>(p.bias, p.V, n0, at, 0, bias[0]);
+    column_bias<ET>(p.bias, p.V, n0, at, 1, bias[1]);
+    float2 *const stat = reinterpret_cast<float2 *>(epi);  // [4][256]
+    uint32_t *const groups = reinterpret_cast<uint32_t *>(epi) + 4 * MM_T * 2;
+    if (PICK && threadIdx.x == 0) *groups = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = MmTile<ET>::row(at.wm, at.li, x, i);
+        const int64_t m = m0 + row;
+        float mx = NEG_INF;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float v = __fmaf_rn(p.alpha, tile.c[x][y][i][j][q], bias[y][j][q]);
+              tile.c[x][y][i][j][q] = v;
+              mx = fmaxf(mx, v);
+            }
+        if constexpr (!PICK) {
+          const int32_t yt = m < p.M ? (int32_t)target_of(p.target, p.target64, m, p.ignore, p.V) - (int32_t)n0 : -1;
+          if (has_column<ET>(at, 0, yt) || has_column<ET>(at, 1, yt)) {
+            float v = 0.0f;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  if (yt == MmTile<ET>::col(at.wn, at.lg, y, j) + q) v = tile.c[x][y][i][j][q];
+            p.tlogit[m] = v;
+          }
+        }
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        // a tile of only -inf sums nothing: its terms are taken against 0
+        const float mz = mx == NEG_INF ? 0.0f : mx;
+        float s = 0.0f;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s = __fadd_rn(s, exp_diff(tile.c[x][y][i][j][q], mz));
+        s = __fadd_rn(s, __shfl_xor(s, 16));
+        s = __fadd_rn(s, __shfl_xor(s, 32));
+        if (at.lg == 0) stat[at.wn * MM_T + row] = float2{mx, s};
+      }
+    lds_barrier();
+    const int tid = mm_tid();
+    if (tid < MM_T && m0 + tid < p.M) {
+      float mx = NEG_INF, s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mx = fmaxf(mx, stat[w * MM_T + tid].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 e = stat[w * MM_T + tid];
+        if (e.y != 0.0f) s = __fadd_rn(s, __fmul_rn(e.y, exp_diff(e.x, mx)));
+      }
+      p.part[vt * p.M + m0 + tid] = float2{mx, s};
+    }
+    if constexpr (PICK) {
+      // thread (row tid / 16 of a group, entry tid % 16): the entries of the
+      // row of each of the eight groups
+      const int pr = tid >> 4, pe = tid & 15;
+      uint32_t range[8];
+      uint32_t some = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t m = m0 + 128 * (k >> 2) + 64 * (pr >> 4) + 16 * (k & 3) + (pr & 15);
+        range[k] = 0;
+        if (m < p.M) {
+          const uint16_t *const r = p.ptr + m * (nvt + 1) + vt;
+          range[k] = r[0] | (uint32_t)r[1] << 16;
+          if (r[0] < r[1]) some |= 1u << k;
+        }
+      }
+      if (some != 0 && pe == 0) atomicOr(groups, some);
+      lds_barrier();
+      const uint32_t mask = mm_uni(*groups);
+      lds_barrier();  // the flags are read: their place may be written
+      float *const box = reinterpret_cast<float *>(epi);  // [32][256], 16-byte pieces xor-ed with the row
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = x * 4 + i;
+          if ((mask >> k & 1) == 0) continue;
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int piece = MmTile<ET>::col(at.wn, at.lg, y, j) >> 2;
+              *reinterpret_cast<f32x4 *>(box + (at.wm * 16 + at.li) * MM_T + 4 * (piece ^ at.li)) = tile.c[x][y][i][j];
+            }
+          lds_barrier();
+          const int64_t m = m0 + 128 * x + 64 * (pr >> 4) + 16 * i + (pr & 15);
+          for (uint32_t e = (range[k] & 0xFFFF) + pe; e < range[k] >> 16; e += 16) {
+            const uint32_t c = (uint32_t)(p.sid[m * p.K + e] - (int32_t)n0) & (MM_T - 1);
+            p.tk[m * p.K + e] = box[pr * MM_T + 4 * ((c >> 2) ^ (pr & 15)) + (c & 3)];
+          }
+          lds_barrier();
+        }
+    }
+    // the next tile's epilogue is barriers away
+  }
+};
+
+template <int ET, bool PICK>
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_stats_kernel(LossFwdArgs p) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  const LossStats<ET, PICK> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, (p.V + MM_T - 1) / MM_T};
+  mm_run<ET, false, false>(prob, mm_buf);
+}
+
+// ---------------------------------------------------------------------------
+// The rows' losses
+// ---------------------------------------------------------------------------
+
+// Folds the tiles of row m, as xent.hip does: 16 rows per work-group, 64
+// threads per row, each thread tiles s, s + 64, ... in ascending order, then the
+// 64 in eights and the eights, in order. Every thread of the row returns with
+// the result: the largest t and the log of the sum of exp(t - largest).
+__device__ __forceinline__ float2 fold_row(const float2 *part, int64_t M, int64_t nvt, int64_t m, bool ok,
+                                           float2 (&sh)[XC_SLICES][XC_ROWS]) {
+  const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
+  float mx = NEG_INF, s = 0.0f;
+  if (ok) {
+    for (int64_t t0 = sl; t0 < nvt; t0 += 8 * XC_SLICES) {
+      float2 e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t t = t0 + k * XC_SLICES;
+        e[k] = t < nvt ? part[t * M + m] : float2{NEG_INF, 0.0f};
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fold_stat(mx, s, e[k]);
+    }
+  }
+  sh[sl][r] = float2{mx, s};
+  __syncthreads();
+  if (sl < 8) {
+    mx = NEG_INF;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) fold_stat(mx, s, sh[8 * sl + k][r]);
+  }
+  __syncthreads();
+  if (sl < 8) sh[sl][r] = float2{mx, s};
+  __syncthreads();
+  mx = NEG_INF;
+  s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) fold_stat(mx, s, sh[k][r]);
+  __syncthreads();
+  return float2{mx, s};
+}
+// every logit -inf: log-sum-exp -inf
+__device__ __forceinline__ float row_lse(float2 f, float ls) { return f.y == 0.0f ? NEG_INF : __fadd_rn(f.x, ls); }
+// log q of a column from the largest logit, not from lse as rounded: that of a
+// token that is nearly certain is far below half a step of its lse
+__device__ __forceinline__ float log_q(float t, float2 f, float ls) {
+  return t == NEG_INF ? NEG_INF : __fsub_rn(__fsub_rn(t, f.x), ls);
+}
+
+struct DistillRows {
+  const float2 *part;
+  int64_t M, nvt, K;
+  const int32_t *sid;
+  const float *p, *tk, *ent, *P;
+  float *loss, *lse;
+  int32_t *y, *up;
+};
+__global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(DistillRows c) {
+  __shared__ float2 sh[XC_SLICES][XC_ROWS];
+  const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
+  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r;
+  const float2 f = fold_row(c.part, c.M, c.nvt, m, m < c.M, sh);
+  const float ls = logf(f.y);
+  float sum = 0.0f;
+  if (m < c.M)
+    for (int64_t k = sl; k < c.K; k += XC_SLICES) {
+      const float p = c.p[m * c.K + k];
+      if (p != 0.0f) sum = __fadd_rn(sum, __fmul_rn(p, log_q(c.tk[m * c.K + k], f, ls)));
+    }
+  sh[sl][r].x = sum;
+  __syncthreads();
+  if (sl != 0 || m >= c.M) return;
+  for (int k = 1; k < XC_SLICES; ++k) sum = __fadd_rn(sum, sh[k][r].x);
+  c.lse[m] = row_lse(f, ls);
+  c.y[m] = -1;
+  c.up[m] = (int32_t)m;
+  c.loss[m] = c.P[m] == 0.0f ? 0.0f : __fsub_rn(c.ent[m], sum);
+}
+
+struct TokenRows {
+  const float2 *part;
+  int64_t M, nvt, V;
+  const float *tlogit;
+  const void *target;
+  int target64;
+  int64_t ignore;
+  float *lse, *coef;
+  int32_t *y, *up;
+  float *logp;     // [M]
+  // policy
+  const float *advantage, *old_logp, *ref_logp;
+  float low, high, kl;
+  float *loss;
+};
+// The clipped loss and the KL term of one token, and their derivative.
+__device__ __forceinline__ void policy_token(const TokenRows &c, int64_t m, float logp, float &loss, float &coef) {
+  const float A = c.advantage[m];
+  const float r = c.old_logp != nullptr ? expf(__fsub_rn(logp, c.old_logp[m])) : 1.0f;
+  const float held = fminf(fmaxf(r, __fsub_rn(1.0f, c.low)), __fadd_rn(1.0f, c.high));
+  const float ra = __fmul_rn(r, A), ca = __fmul_rn(held, A);
+  loss = coef = 0.0f;
+  if (A != 0.0f) {  // else 0, also where the ratio has overflowed
+    const bool free = ra <= ca;
+    loss = free ? -ra : r != r ? r : -ca;
+    coef = free ? -ra : r != r ? r : 0.0f;
+  }
+  if (c.ref_logp != nullptr && c.kl != 0.0f) {
+    const float d = __fsub_rn(c.ref_logp[m], logp), e = expm1f(d);
+    loss = __fadd_rn(loss, __fmul_rn(c.kl, d == __builtin_inff() ? d : __fsub_rn(e, d)));
+    coef = __fsub_rn(coef, __fmul_rn(c.kl, e));
+  }
+}
+template <bool POLICY>
+__global__ __launch_bounds__(XC_ROWS * XC_SLICES) void token_rows_kernel(TokenRows c) {
+  __shared__ float2 sh[XC_SLICES][XC_ROWS];
+  const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
+  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r;
+  const float2 f = fold_row(c.part, c.M, c.nvt, m, m < c.M, sh);
+  if (sl != 0 || m >= c.M) return;
+  const float ls = logf(f.y);
+  const int64_t y = target_of(c.target, c.target64, m, c.ignore, c.V);
+  const float logp = y >= 0 ? log_q(c.tlogit[m], f, ls) : 0.0f;
+  c.lse[m] = row_lse(f, ls);
+  c.y[m] = (int32_t)y;
+  c.logp[m] = logp;
+  float loss = 0.0f, coef = 0.0f;
+  if constexpr (POLICY) {
+    if (y >= 0) policy_token(c, m, logp, loss, coef);
+    c.loss[m] = loss;
+    c.up[m] = (int32_t)m;
+  } else {
+    c.up[m] = 0;  // preference_pairs_kernel knows the rows' pairs
+  }
+  c.coef[m] = coef;
+}
+
+// One pair of sequences, one work-group: their sums in 64 bits in a fixed
+// order (differences of sums over thousands of tokens are wanted), the loss,
+// and the derivative for every row of theirs.
+constexpr int PP_THREADS = 256;
+struct Pairs {
+  const void *starts;
+  int starts64;
+  int64_t pairs, M, V;
+  const void *target;
+  int target64;
+  int64_t ignore;
+  const float *rowlogp, *ref;
+  float beta, margin, smoothing;
+  int average;
+  float *loss, *logp, *coef;
+  int32_t *up;
+};
+__global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
+  __shared__ double sh[2][PP_THREADS];
+  __shared__ float der[2];
+  const int tid = threadIdx.x;
+  const int64_t pair = blockIdx.x;
+  auto bound = [&](int64_t i) {
+    const int64_t b = c.starts64 ? static_cast<const int64_t *>(c.starts)[i] : (int64_t)static_cast<const int32_t *>(c.starts)[i];
+    return b < 0 ? (int64_t)0 : b > c.M ? c.M : b;
+  };
+  double total[2], size[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int64_t q = pair + w * c.pairs, lo = bound(q), hi = bound(q + 1);
+    double s = 0.0, n = 0.0;
+    for (int64_t m = lo + tid; m < hi; m += PP_THREADS)
+      if (target_of(c.target, c.target64, m, c.ignore, c.V) >= 0) {
+        s += c.rowlogp[m];
+        n += 1.0;
+      }
+    sh[0][tid] = s;
+    sh[1][tid] = n;
+    __syncthreads();
+    for (int d = PP_THREADS / 2; d; d >>= 1) {
+      if (tid < d) {
+        sh[0][tid] += sh[0][tid + d];
+        sh[1][tid] += sh[1][tid + d];
+      }
+      __syncthreads();
+    }
+    total[w] = sh[0][0];
+    size[w] = c.average && sh[1][0] > 0.0 ? sh[1][0] : 1.0;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    double lead[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      total[w] /= size[w];
+      c.logp[pair + w * c.pairs] = (float)total[w];
+      lead[w] = total[w] - (c.ref != nullptr ? (double)c.ref[pair + w * c.pairs] : 0.0);
+    }
+    const double z = (double)c.beta * (lead[0] - lead[1]) - (double)c.margin, e = c.smoothing;
+    // -log sigma(z) = max(-z, 0) + log(1 + e^-|z|)
+    const double soft = log1p(exp(-fabs(z)));
+    // infinite on one side only, where that side has weight
+    const double neg = fmax(-z, 0.0) + soft, pos = fmax(z, 0.0) + soft;
+    c.loss[pair] = (float)(z != z ? z : (e != 1.0 ? (1.0 - e) * neg : 0.0) + (e != 0.0 ? e * pos : 0.0));
+    const double dz = (e - 1.0 / (1.0 + exp(z))) * (double)c.beta;
+    der[0] = (float)(dz / size[0]);
+    der[1] = (float)(-dz / size[1]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int64_t q = pair + w * c.pairs, lo = bound(q), hi = bound(q + 1);
+    for (int64_t m = lo + tid; m < hi; m += PP_THREADS)
+      if (target_of(c.target, c.target64, m, c.ignore, c.V) >= 0) {
+        c.coef[m] = der[w];
+        c.up[m] = (int32_t)pair;
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// The rows' coefficients of G, scaled as in xent.hip: by f = top / the largest
+// finite one. Target losses: a = b = -g c. Distill: a = g P, b = g (the factor of
+// the entries), no target. Every work-group finds the maximum by itself up to
+// LC_ONE rows; with more, one work-group finds it in a launch of its own.
+constexpr int LC_THREADS = 256;
+constexpr int64_t LC_ONE = 32768;
+struct LossCoef {
+  const float *g;
+  int64_t M;
+  const float *lse, *coef;
+  const int32_t *y, *up;
+  int distill;
+  float top;
+  float *scale;
+  RowCoef *rows;
+  int have_scale, write_rows;
+};
+__global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
+  auto coef = [&](int64_t m, float &a, float &b) {
+    const float c = p.coef[m];
+    a = b = 0.0f;
+    if (c == 0.0f) return;  // also rows of no sequence: they have no upstream gradient
+    const float g = p.g[p.up[m]];
+    a = __fmul_rn(p.distill ? c : -c, g);
+    b = p.distill ? g : a;
+  };
+  float f = 1.0f;
+  if (p.have_scale) {
+    f = p.scale[0];
+  } else {
+    __shared__ float sh[LC_THREADS / 64];
+    float mx = 0.0f;
+    for (int64_t m = threadIdx.x; m < p.M; m += LC_THREADS) {
+      float a, b;
+      coef(m, a, b);
+      a = fabsf(a);
+      b = fabsf(b);
+      mx = fmaxf(mx, fmaxf(a < __builtin_inff() ? a : 0.0f, b < __builtin_inff() ? b : 0.0f));
+    }
+    for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < LC_THREADS / 64; ++w) mx = fmaxf(mx, sh[w]);
+    // f and 1 / f both well inside the normal range, else no scale
+    if (mx > 1e-30f && mx < 1e30f) f = __fdiv_rn(p.top, mx);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.scale[0] = f;
+      p.scale[1] = __fdiv_rn(1.0f, f);
+    }
+  }
+  const int64_t m = (int64_t)blockIdx.x * LC_THREADS + threadIdx.x;
+  if (!p.write_rows || m >= p.M) return;
+  float a, b;
+  coef(m, a, b);
+  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], p.distill ? -1 : p.y[m]};
+}
+
+template <int ET, bool DB>
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  const XentGrad<ET, DB> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
+  mm_run<ET, false, false>(prob, mm_buf);
+}
+
+// G at the teacher's entries of a piece, over what the product's epilogue left
+// there: a q - b p from the entry's t, the dense value's own fp32 operations,
+// rounded once. An id that a row has more than once is written by each of them
+// with the sum of their p.
+//
+// grad_bias: what the entries add to it, as whole numbers of 2^-shift of the
+// largest coefficient, so that the order of the additions does not matter.
+struct DistillEntries {
+  XentBwdArgs b;
+  int64_t K;
+  const int32_t *sid;
+  const float *p, *tk;
+  unsigned long long *bias;  // [V] or nullptr
+  double unit;               // 2^shift / top
+};
+template <int ET>
+__global__ __launch_bounds__(256) void distill_entries_kernel(DistillEntries c) {
+  const int64_t e = group_number() * 256 + threadIdx.x;
+  if (e >= c.b.M * c.K) return;
+  const int32_t id = c.sid[e];
+  if (id == NO_ID || id < c.b.v0 || id >= c.b.v0 + c.b.np) return;
+  const int64_t m = e / c.K, k = e - m * c.K;
+  const RowCoef r = c.b.rows[m];
+  const float lse = r.lse == NEG_INF ? 0.0f : r.lse;
+  int64_t first = k;
+  while (first > 0 && c.sid[e - k + first - 1] == id) --first;
+  float p = 0.0f;
+  for (int64_t j = first; j < c.K && c.sid[e - k + j] == id; ++j) p = __fadd_rn(p, c.p[e - k + j]);
+  const float g = __fsub_rn(__fmul_rn(r.a, exp_diff(c.tk[e], lse)), __fmul_rn(r.b, p));
+  reinterpret_cast<uint16_t *>(c.b.G)[m * c.b.ldg + (id - c.b.v0)] = (uint16_t)mm_pack2<ET>(g, 0.0f);
+  if (c.bias != nullptr) {
+    const double x = -(double)r.b * (double)c.p[e] * c.unit;
+    // what is not finite makes the whole row of G so, and with it every sum
+    if (fabs(x) < 0x1p62) atomicAdd(c.bias + id, (unsigned long long)llrint(x));
+  }
+}
+
+__global__ __launch_bounds__(256) void loss_zero_kernel(uint32_t *__restrict__ p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+hipError_t zero_words(void *p, int64_t n, hipStream_t s) {
+  const int64_t blocks = ceil_div(n, 256);
+  return launch_kernel(loss_zero_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), s,
+                       static_cast<uint32_t *>(p), n);
+}
+
+// grad_bias of one piece: the row tiles' column sums in ascending order, the
+// entries' share, and 1 / T.
+__global__ __launch_bounds__(256) void loss_bias_kernel(const float *__restrict__ colpart, int64_t nmt, int64_t vp,
+                                                        int64_t n, const long long *__restrict__ entries,
+                                                        const float *__restrict__ scale, double unit, float T,
+                                                        float *__restrict__ db) {
+  const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (v >= n) return;
+  float s = 0.0f;
+  for (int64_t t = 0; t < nmt; ++t) s = __fadd_rn(s, colpart[t * vp + v]);
+  if (entries != nullptr) s = (float)((double)s + (double)entries[v] / unit * (double)scale[1]);
+  db[v] = __fdiv_rn(s, T);
+}
+
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_dhidden_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  const XentDHidden<ET> prob{p, (p.M + MM_T - 1) / MM_T, (p.H + MM_T - 1) / MM_T,
+                             (p.np + p.ksplit - 1) / p.ksplit};
+  mm_run<ET, false, true>(prob, mm_buf);
+}
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_dweight_kernel(XentBwdArgs p) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  const XentDWeight<ET> prob{p, mm_epi, p.np / MM_T, (p.H + MM_T - 1) / MM_T};
+  mm_run<ET, true, true>(prob, mm_buf);
+}
+
+// grad_hidden: the splits' sums in ascending order, scaled, rounded once.
+template <int ET>
+__global__ __launch_bounds__(256) void loss_dhidden_out_kernel(const float *__restrict__ dh, int64_t n, int splits,
+                                                               float alpha, const float *__restrict__ scale,
+                                                               uint16_t *__restrict__ out) {
+  const int64_t e = (group_number() * 256 + threadIdx.x) * 8;
+  if (e >= n) return;
+  f32x4 s[2] = {zero4(), zero4()};
+  for (int k = 0; k < splits; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(dh + k * n + e + 4 * h);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s[h][q] = __fadd_rn(s[h][q], v[q]);
+    }
+  const float f = __fmul_rn(alpha, scale[1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[h][q] = __fmul_rn(f, s[h][q]);
+  *reinterpret_cast<u32x4 *>(out + e) = u32x4{mm_pack2<ET>(s[0][0], s[0][1]), mm_pack2<ET>(s[0][2], s[0][3]),
+                                              mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
+}
+
+struct BackwardLayout {
+  BwdPlan plan;
+  int64_t entries, bytes;
+};
+BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool bias) {
+  BackwardLayout b;
+  b.plan = bwd_plan(M, H, V, bias);
+  b.entries = b.plan.bytes;
+  b.bytes = b.entries + (bias && K ? align256(8 * V) : 0);
+  return b;
+}
+
+// What the three forward passes begin with: the memory's places, the bias.
+struct Setup {
+  State st;
+  ForwardLayout lay;
+  uint8_t *ws;
+  LossFwdArgs a;
+};
+hipError_t set_up(const LossHead &h, const LossMemory &mem, int64_t K, hipStream_t s, Setup &u) {
+  u.lay = forward_layout(h.M, h.H, h.V, K, mem.state != nullptr);
+  u.ws = static_cast<uint8_t *>(mem.workspace);
+  u.st = state_at(mem.state != nullptr ? mem.state : u.ws + u.lay.state, state_layout(h.M, h.H, h.V, K, mem.keep != 0));
+  u.a = LossFwdArgs{};
+  u.a.hidden = static_cast<const uint8_t *>(h.hidden);
+  u.a.W = static_cast<const uint8_t *>(h.W);
+  u.a.M = h.M;
+  u.a.H = h.H;
+  u.a.V = h.V;
+  u.a.alpha = (float)((double)h.alpha / (double)h.temperature);
+  u.a.bias = h.bias;
+  u.a.part = reinterpret_cast<float2 *>(u.ws + u.lay.part);
+  u.a.tlogit = reinterpret_cast<float *>(u.ws + u.lay.tlogit);
+  u.a.K = K;
+  if (h.M == 0 || h.bias == nullptr || h.temperature == 1.0f) return hipSuccess;
+  u.a.bias = u.st.bias;
+  return launch_kernel(loss_bias_scale_kernel, dim3((unsigned)ceil_div(h.V, 256)), dim3(256), s, h.bias, h.V,
+                       h.temperature, u.st.bias);
+}
+template <bool PICK>
+hipError_t stats(const LossHead &h, const LossFwdArgs &a, hipStream_t s) {
+  const int64_t tiles = ceil_div(h.M, MM_T) * ceil_div(h.V, MM_T);
+  return launch_kernel(h.in_f16 ? loss_stats_kernel<ET_F16, PICK> : loss_stats_kernel<ET_BF16, PICK>, mm_grid(tiles),
+                       dim3(MM_THREADS), s, a);
+}
+void set_targets(LossFwdArgs &a, const LossTargets &y) {
+  a.target = y.target;
+  a.target64 = y.wide;
+  a.ignore = y.ignore;
+}
+TokenRows token_rows(const Setup &u, const LossTargets &y) {
+  TokenRows r{};
+  r.part = u.a.part;
+  r.M = u.a.M;
+  r.nvt = ceil_div(u.a.V, MM_T);
+  r.V = u.a.V;
+  r.tlogit = u.a.tlogit;
+  r.target = y.target;
+  r.target64 = y.wide;
+  r.ignore = y.ignore;
+  r.lse = u.st.lse;
+  r.coef = u.st.coef;
+  r.y = u.st.y;
+  r.up = u.st.up;
+  return r;
+}
+dim3 rows_grid(int64_t M) { return dim3((unsigned)ceil_div(M, XC_ROWS)); }
+
+template <int ET>
+hipError_t backward(const LossBackward &c, hipStream_t s) {
+  const LossHead &h = c.head;
+  const BackwardLayout lay = backward_layout(h.M, h.H, h.V, c.K, c.grad_bias != nullptr);
+  const BwdPlan &pl = lay.plan;
+  uint8_t *const ws = static_cast<uint8_t *>(c.mem.workspace);
+  const State st = state_at(c.mem.state, state_layout(h.M, h.H, h.V, c.K, c.mem.keep != 0));
+  float *const scale = reinterpret_cast<float *>(ws + pl.off_scale);
+  RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + pl.off_rows);
+  const float top = ET == ET_F16 ? 16384.0f : 1.0f;
+  LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, c.K > 0, top, scale, rows, 0, 1};
+  hipError_t e = hipSuccess;
+  if (h.M > LC_ONE) {
+    r.write_rows = 0;
+    e = launch_kernel(loss_coef_kernel, dim3(1), dim3(LC_THREADS), s, r);
+    r.write_rows = r.have_scale = 1;
+  }
+  if (e == hipSuccess)
+    e = launch_kernel(loss_coef_kernel, dim3((unsigned)ceil_div(h.M, LC_THREADS)), dim3(LC_THREADS), s, r);
+  XentBwdArgs p{};
+  p.hidden = static_cast<const uint8_t *>(h.hidden);
+  p.W = static_cast<const uint8_t *>(h.W);
+  p.M = h.M;
+  p.H = h.H;
+  p.V = h.V;
+  p.alpha = (float)((double)h.alpha / (double)h.temperature);
+  p.bias = h.bias == nullptr || h.temperature == 1.0f ? h.bias : st.bias;
+  p.rows = rows;
+  p.scale = scale;
+  p.ldg = pl.vp;
+  p.G = ws + pl.off_g;
+  p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + pl.off_col) : nullptr;
+  p.dh = reinterpret_cast<float *>(ws + pl.off_dh);
+  p.ksplit = pl.ksplit;
+  p.dw = static_cast<uint16_t *>(c.grad_W);
+  const int64_t nmt = ceil_div(h.M, MM_T), nht = ceil_div(h.H, MM_T);
+  // whole numbers of 2^-shift: their sum over all rows stays below 2^62
+  int shift = 61;
+  for (int64_t k = h.M * (c.K > 0 ? c.K : 1); k > 0; k >>= 1) --shift;
+  if (shift > 44) shift = 44;
+  const double unit = (double)((int64_t)1 << shift) / (double)top;
+  const bool sums = c.grad_bias != nullptr && c.K > 0;
+  unsigned long long *const entries = sums ? reinterpret_cast<unsigned long long *>(ws + lay.entries) : nullptr;
+  if (e == hipSuccess && sums) e = zero_words(entries, 2 * h.V, s);
+  for (int64_t v0 = 0; v0 < h.V && e == hipSuccess; v0 += pl.vp) {
+    p.v0 = v0;
+    p.first = v0 == 0;
+    const int64_t nv = h.V - v0 < pl.vp ? h.V - v0 : pl.vp;
+    p.np = ceil_div(nv, MM_T) * MM_T;
+    e = launch_kernel(c.grad_bias != nullptr ? loss_grad_kernel<ET, true> : loss_grad_kernel<ET, false>,
+                      mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p);
+    if (e == hipSuccess && c.K > 0)
+      e = launch_kernel(distill_entries_kernel<ET>, numbered_grid(ceil_div(h.M * c.K, 256)), dim3(256), s,
+                        DistillEntries{p, c.K, st.ids, st.p, st.tk, entries, unit});
+    if (e == hipSuccess && c.grad_bias != nullptr)
+      e = launch_kernel(loss_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
+                        static_cast<const float *>(p.colpart), nmt, pl.vp, nv,
+                        sums ? reinterpret_cast<const long long *>(entries) + v0 : nullptr, static_cast<const float *>(scale),
+                        unit, h.temperature, c.grad_bias + v0);
+    if (e == hipSuccess && c.grad_hidden != nullptr)
+      e = launch_kernel(loss_dhidden_kernel<ET>, mm_grid(nmt * nht * ceil_div(p.np, pl.ksplit)), dim3(MM_THREADS), s, p);
+    if (e == hipSuccess && c.grad_W != nullptr)
+      e = launch_kernel(loss_dweight_kernel<ET>, mm_grid(nht * (p.np / MM_T)), dim3(MM_THREADS), s, p);
+  }
+  if (e == hipSuccess && c.grad_hidden != nullptr)
+    e = launch_kernel(loss_dhidden_out_kernel<ET>, numbered_grid(ceil_div(h.M * h.H, 2048)), dim3(256), s,
+                      static_cast<const float *>(p.dh), h.M * h.H, (int)pl.splits, p.alpha,
+                      static_cast<const float *>(scale), static_cast<uint16_t *>(c.grad_hidden));
+  return e;
+}
+
+}  // namespace
+
+int64_t loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) {
+  return state_layout(M, H, V, K, keep).bytes;
+}
+int64_t loss_forward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool with_state) {
+  return forward_layout(M, H, V, K, with_state).bytes;
+}
+int64_t loss_backward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool bias) {
+  return backward_layout(M, H, V, K, bias).bytes;
+}
+
+hipError_t launch_distill_forward(const DistillForward &c, hipStream_t s) {
+  const LossHead &h = c.head;
+  Setup u;
+  hipError_t e = set_up(h, c.mem, c.K, s, u);
+  if (e != hipSuccess) return e;
+  uint16_t *const ptr = reinterpret_cast<uint16_t *>(u.ws + u.lay.ptr);
+  float *const ent = reinterpret_cast<float *>(u.ws + u.lay.ent);
+  const DistillPrep d{c.ids, c.ids64, h.M, h.V, c.K, c.logits, c.logits_type, c.teacher_lse, h.temperature,
+                      u.st.ids, u.st.p, ptr, ent, u.st.coef};
+  e = launch_kernel(c.K <= 64 ? distill_prep_kernel<1> : c.K <= 256 ? distill_prep_kernel<4> : distill_prep_kernel<16>,
+                    numbered_grid(ceil_div(h.M, DP_WAVES)), dim3(64 * DP_WAVES), s, d);
+  u.a.sid = u.st.ids;
+  u.a.ptr = ptr;
+  u.a.tk = u.st.tk;
+  if (e == hipSuccess) e = stats<true>(h, u.a, s);
+  if (e == hipSuccess)
+    e = launch_kernel(distill_rows_kernel, rows_grid(h.M), dim3(XC_ROWS * XC_SLICES), s,
+                      DistillRows{u.a.part, h.M, ceil_div(h.V, MM_T), c.K, u.st.ids, u.st.p, u.st.tk, ent, u.st.coef,
+                                  c.loss, u.st.lse, u.st.y, u.st.up});
+  return e;
+}
+
+hipError_t launch_policy_forward(const PolicyForward &c, hipStream_t s) {
+  Setup u;
+  hipError_t e = set_up(c.head, c.mem, 0, s, u);
+  if (e != hipSuccess) return e;
+  set_targets(u.a, c.y);
+  e = stats<false>(c.head, u.a, s);
+  TokenRows r = token_rows(u, c.y);
+  r.logp = c.logp;
+  r.advantage = c.advantage;
+  r.old_logp = c.old_logp;
+  r.ref_logp = c.ref_logp;
+  r.low = c.clip_low;
+  r.high = c.clip_high;
+  r.kl = c.kl_coef;
+  r.loss = c.loss;
+  if (e == hipSuccess)
+    e = launch_kernel(token_rows_kernel<true>, rows_grid(c.head.M), dim3(XC_ROWS * XC_SLICES), s, r);
+  return e;
+}
+
+hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t s) {
+  Setup u;
+  hipError_t e = set_up(c.head, c.mem, 0, s, u);
+  if (e != hipSuccess) return e;
+  set_targets(u.a, c.y);
+  if (c.head.M > 0) {
+    e = stats<false>(c.head, u.a, s);
+    TokenRows r = token_rows(u, c.y);
+    r.logp = reinterpret_cast<float *>(u.ws + u.lay.rowlogp);
+    if (e == hipSuccess)
+      e = launch_kernel(token_rows_kernel<false>, rows_grid(c.head.M), dim3(XC_ROWS * XC_SLICES), s, r);
+  }
+  if (e == hipSuccess && c.pairs > 0)
+    e = launch_kernel(preference_pairs_kernel, dim3((unsigned)c.pairs), dim3(PP_THREADS), s,
+                      Pairs{c.starts, c.starts64, c.pairs, c.head.M, c.head.V, c.y.target, c.y.wide, c.y.ignore,
+                            reinterpret_cast<float *>(u.ws + u.lay.rowlogp), c.ref_logp, c.beta, c.margin, c.smoothing,
+                            c.average, c.loss, c.logp, u.st.coef, u.st.up});
+  return e;
+}
+
+hipError_t launch_loss_backward(const LossBackward &c, hipStream_t s) {
+  if (c.head.M == 0) {  // sums over no rows
+    hipError_t e = hipSuccess;
+    if (c.grad_W != nullptr) e = zero_words(c.grad_W, c.head.V * c.head.H / 2, s);
+    if (e == hipSuccess && c.grad_bias != nullptr) e = zero_words(c.grad_bias, c.head.V, s);
+    return e;
+  }
+  return c.head.in_f16 ? backward<ET_F16>(c, s) : backward<ET_BF16>(c, s);
+}
+
+}  // namespace lmhead

@@ -1,0 +1,287 @@
+"""Further losses of the head's logits, which are never whole in memory: the
+divergence from a teacher's top logits (lmhead_distill_forward), the clipped
+policy loss with a KL term (lmhead_policy_forward) and the logistic loss of
+preferred pairs (lmhead_preference_forward), each with its gradients
+(lmhead_loss_backward).
+
+``distill_forward``, ``policy_forward``, ``preference_forward`` and
+``loss_backward`` are the C calls with torch tensors; ``distillation``,
+``policy_loss`` and ``preference_loss`` are the same as differentiable
+functions.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import _lib
+from ._binding import _DTYPES, _alloc_on, _check, _device_ctx, _need, _same_device, _stream_handle
+from .training import _f32_arg, _head_args, _index_arg, _ptr, _Total, _total, _workspace
+
+
+class LossState(NamedTuple):
+    """What a forward call leaves for loss_backward."""
+    state: torch.Tensor   # bytes, the library's own layout
+    hidden: torch.Tensor
+    bias: torch.Tensor | None
+    alpha: float
+    temperature: float
+    K: int                # the teacher's logits a row; 0 for the losses of targets
+    elements: int         # of the loss, and so of its upstream gradient
+
+
+def loss_state_bytes(M: int, H: int, V: int, K: int = 0) -> int:
+    return int(_lib.load().lmhead_loss_state_bytes(M, H, V, K))
+
+
+def loss_forward_workspace_bytes(M: int, H: int, V: int, K: int = 0, train: bool = True) -> int:
+    return int(_lib.load().lmhead_loss_forward_workspace_bytes(M, H, V, K, int(train)))
+
+
+def loss_backward_workspace_bytes(M: int, H: int, V: int, K: int = 0, grad_bias: bool = False) -> int:
+    return int(_lib.load().lmhead_loss_backward_workspace_bytes(M, H, V, K, int(grad_bias)))
+
+
+def _memory(M, H, V, K, train, workspace, dev):
+    state = torch.empty(loss_state_bytes(M, H, V, K), dtype=torch.uint8, device=dev) if train else None
+    return state, _workspace(workspace, loss_forward_workspace_bytes(M, H, V, K, train), dev)
+
+
+def _memory_args(state, workspace):
+    return (state.data_ptr() if state is not None and state.numel() else None, state.numel() if state is not None else 0,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _optional_f32(t, M, name):
+    if t is not None:
+        _f32_arg(t, M, name)
+
+
+def distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                    alpha: float = 1.0, bias=None, *, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                    train: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """Divergence of the head's distribution at `temperature` from a teacher's,
+    given by its top logits (lmhead_distill_forward): returns (loss fp32 [M],
+    saved). teacher_ids [M, K] (int32 or int64) and teacher_logits [M, K]
+    (float32, bfloat16 or float16) in any order, as logits_topk gives them;
+    entries whose id is no row of weight, or whose logit is -inf, are absent, and
+    a row without entries has loss 0. The teacher's probabilities are normalised
+    over the entries, or, with teacher_lse (fp32 [M], the log-sum-exp of its
+    logits / temperature over its whole vocabulary), are those of its whole
+    distribution. saved is what loss_backward takes (None where train is
+    false)."""
+    M, H, V, code = _head_args(hidden, weight, bias)
+    _need(teacher_ids.dim() == 2 and teacher_ids.shape[0] == M and teacher_ids.shape[1] >= 1,
+          "teacher_ids must be [M, K]")
+    K = teacher_ids.shape[1]
+    itype = _index_arg(teacher_ids, (M, K), "teacher_ids")
+    if not (teacher_logits.is_cuda and teacher_logits.dtype in _DTYPES and teacher_logits.shape == (M, K)
+            and teacher_logits.is_contiguous()):
+        raise ValueError("teacher_logits must be a contiguous device tensor [M, K], float32, bfloat16 or float16")
+    _optional_f32(teacher_lse, M, "teacher_lse")
+    dev = hidden.device
+    with _alloc_on(stream):
+        loss = torch.empty(M, dtype=torch.float32, device=dev)
+        state, workspace = _memory(M, H, V, K, train, workspace, dev)
+    _same_device(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, workspace)
+    with _device_ctx(dev):
+        st = _lib.load().lmhead_distill_forward(
+            hidden.data_ptr(), M, H, weight.data_ptr(), V, float(alpha), _ptr(bias), code, float(temperature),
+            teacher_ids.data_ptr(), itype, teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K,
+            _ptr(teacher_lse), loss.data_ptr(), *_memory_args(state, workspace), _stream_handle(dev, stream))
+    _check(st, "lmhead_distill_forward")
+    return loss, LossState(state, hidden, bias, float(alpha), float(temperature), K, M) if train else None
+
+
+def policy_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, advantage: torch.Tensor,
+                   old_logp: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None, alpha: float = 1.0,
+                   bias=None, *, temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2,
+                   kl_coef: float = 0.0, ignore_index: int = -100, train: bool = True,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """Clipped policy loss of the tokens target [M] with a KL term
+    (lmhead_policy_forward): returns (loss fp32 [M], logp fp32 [M], saved), logp
+    being the tokens' log-probabilities. advantage, old_logp (None: logp itself,
+    the first step after a rollout) and ref_logp (None: no KL term) are fp32 [M].
+    Rows whose target is ignore_index or no row of weight have loss and logp 0."""
+    M, H, V, code = _head_args(hidden, weight, bias)
+    itype = _index_arg(target, (M,), "target")
+    _f32_arg(advantage, M, "advantage")
+    _optional_f32(old_logp, M, "old_logp")
+    _optional_f32(ref_logp, M, "ref_logp")
+    dev = hidden.device
+    with _alloc_on(stream):
+        loss = torch.empty(M, dtype=torch.float32, device=dev)
+        logp = torch.empty(M, dtype=torch.float32, device=dev)
+        state, workspace = _memory(M, H, V, 0, train, workspace, dev)
+    _same_device(hidden, weight, bias, target, advantage, old_logp, ref_logp, workspace)
+    with _device_ctx(dev):
+        st = _lib.load().lmhead_policy_forward(
+            hidden.data_ptr(), M, H, weight.data_ptr(), V, float(alpha), _ptr(bias), code, float(temperature),
+            target.data_ptr(), itype, int(ignore_index), advantage.data_ptr(), _ptr(old_logp), _ptr(ref_logp),
+            float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), logp.data_ptr(),
+            *_memory_args(state, workspace), _stream_handle(dev, stream))
+    _check(st, "lmhead_policy_forward")
+    return loss, logp, LossState(state, hidden, bias, float(alpha), float(temperature), 0, M) if train else None
+
+
+def preference_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, starts: torch.Tensor,
+                       ref_logp: torch.Tensor | None = None, alpha: float = 1.0, bias=None, *, beta: float = 0.1,
+                       margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False,
+                       temperature: float = 1.0, ignore_index: int = -100, train: bool = True,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Logistic loss of P preferred pairs of sequences
+    (lmhead_preference_forward): returns (loss fp32 [P], logp fp32 [2 P], saved).
+    Sequence s is rows starts[s] .. starts[s + 1] - 1 of the batch (starts: int32
+    or int64 [2 P + 1], ascending); sequences 0 .. P - 1 are the preferred ones,
+    P .. 2 P - 1 the others. logp is the sum (average: the mean) of the log-
+    probabilities of a sequence's targets, without those left out; ref_logp
+    (None: zeros), fp32 [2 P], is a reference model's, as this function returns it."""
+    M, H, V, code = _head_args(hidden, weight, bias)
+    itype = _index_arg(target, (M,), "target")
+    _need(starts.dim() == 1 and starts.shape[0] % 2 == 1, "starts must be [2 P + 1]")
+    stype = _index_arg(starts, starts.shape, "starts")
+    P = starts.shape[0] // 2
+    if ref_logp is not None and not (ref_logp.is_cuda and ref_logp.dtype == torch.float32 and ref_logp.shape == (2 * P,)
+                                     and ref_logp.is_contiguous()):
+        raise ValueError("ref_logp must be a contiguous fp32 device tensor [2 P]")
+    dev = hidden.device
+    with _alloc_on(stream):
+        loss = torch.empty(P, dtype=torch.float32, device=dev)
+        logp = torch.empty(2 * P, dtype=torch.float32, device=dev)
+        state, workspace = _memory(M, H, V, 0, train, workspace, dev)
+    _same_device(hidden, weight, bias, target, starts, ref_logp, workspace)
+    with _device_ctx(dev):
+        st = _lib.load().lmhead_preference_forward(
+            hidden.data_ptr(), M, H, weight.data_ptr(), V, float(alpha), _ptr(bias), code, float(temperature),
+            target.data_ptr(), itype, int(ignore_index), starts.data_ptr(), stype, P, _ptr(ref_logp), float(beta),
+            float(margin), float(label_smoothing), int(average), loss.data_ptr(), logp.data_ptr(),
+            *_memory_args(state, workspace), _stream_handle(dev, stream))
+    _check(st, "lmhead_preference_forward")
+    return loss, logp, LossState(state, hidden, bias, float(alpha), float(temperature), 0, P) if train else None
+
+
+def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossState, *, need_hidden: bool = True,
+                  need_weight: bool = True, need_bias: bool | None = None, workspace: torch.Tensor | None = None,
+                  stream=None):
+    """Gradients of distill_forward, policy_forward or preference_forward
+    (lmhead_loss_backward): returns (grad_hidden, grad_weight, grad_bias), of the
+    inputs' types, None where not needed (need_bias: by default when there is a
+    bias). grad_loss is fp32, of the loss's shape; saved is what the forward call
+    returned, weight what it was given."""
+    _need(isinstance(saved, LossState), "saved must be what a forward call with train=True returned")
+    hidden, bias = saved.hidden, saved.bias
+    M, H, V, code = _head_args(hidden, weight, bias)
+    if not (grad_loss.is_cuda and grad_loss.dtype == torch.float32 and grad_loss.shape == (saved.elements,)
+            and grad_loss.is_contiguous()):
+        raise ValueError(f"grad_loss must be a contiguous fp32 device tensor [{saved.elements}]")
+    if need_bias is None:
+        need_bias = bias is not None
+    _need(not need_bias or bias is not None, "there is no bias to differentiate")
+    dev = hidden.device
+    with _alloc_on(stream):
+        dh = torch.empty_like(hidden) if need_hidden else None
+        dw = torch.empty_like(weight) if need_weight else None
+        db = torch.empty_like(bias) if need_bias else None
+        workspace = _workspace(workspace, loss_backward_workspace_bytes(M, H, V, saved.K, need_bias), dev)
+    _same_device(hidden, weight, bias, grad_loss, saved.state, workspace)
+    with _device_ctx(dev):
+        st = _lib.load().lmhead_loss_backward(
+            hidden.data_ptr(), M, H, weight.data_ptr(), V, saved.alpha, _ptr(bias), code, saved.temperature, saved.K,
+            grad_loss.data_ptr(), saved.state.data_ptr(), saved.state.numel(), _ptr(dh), _ptr(dw), _ptr(db),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(dev, stream))
+    _check(st, "lmhead_loss_backward")
+    return dh, dw, db
+
+
+class _HeadLoss(torch.autograd.Function):
+    """forward(hidden, weight, bias, call): call(hidden, weight, bias, train) is
+    one of the forward calls above with its other arguments bound."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, bias, call):
+        *out, saved = call(hidden, weight, bias, any(ctx.needs_input_grad))
+        if saved is not None:
+            ctx.save_for_backward(hidden, weight, bias, saved.state)
+            ctx.rest = saved[3:]
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*out[1:])
+        return tuple(out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss, *_):
+        if grad_loss is None:
+            return None, None, None, None
+        hidden, weight, bias, state = ctx.saved_tensors
+        dh, dw, db = loss_backward(grad_loss.contiguous(), weight, LossState(state, hidden, bias, *ctx.rest),
+                                   need_hidden=ctx.needs_input_grad[0], need_weight=ctx.needs_input_grad[1],
+                                   need_bias=ctx.needs_input_grad[2])
+        return dh, dw, db, None
+
+
+def _reduce(loss, reduction, kept):
+    """kept(): which elements the mean is over."""
+    if reduction == "mean":
+        return _Total.apply(loss) / _total(kept())
+    return _Total.apply(loss) if reduction == "sum" else loss
+
+
+def _check_reduction(reduction):
+    _need(reduction in ("none", "sum", "mean"), "reduction must be none, sum or mean")
+
+
+def distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+                 alpha: float = 1.0, bias=None, *, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                 reduction: str = "mean") -> torch.Tensor:
+    """Differentiable distill_forward. reduction: "none" (fp32 [M]), "sum", or
+    "mean" over the rows that have entries (NaN when there are none). Losses at a
+    temperature T are usually weighted by T * T; that is left to the caller."""
+    _check_reduction(reduction)
+
+    def call(h, w, b, train):
+        return distill_forward(h, w, teacher_ids, teacher_logits, alpha, b, temperature=temperature,
+                               teacher_lse=teacher_lse, train=train)
+
+    (loss,) = _HeadLoss.apply(hidden, weight, bias, call)
+    return _reduce(loss, reduction, lambda: ((teacher_ids >= 0) & (teacher_ids < weight.shape[0])
+                                             & (teacher_logits != -torch.inf)).any(1))
+
+
+def policy_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, advantage: torch.Tensor,
+                old_logp: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None, alpha: float = 1.0, bias=None,
+                *, temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                ignore_index: int = -100, reduction: str = "mean", return_logp: bool = False):
+    """Differentiable policy_forward. reduction: "none" (fp32 [M]), "sum", or
+    "mean" over the rows that are not left out. With return_logp also the tokens'
+    log-probabilities [M], without a gradient (for the ratio's and the KL's
+    statistics)."""
+    _check_reduction(reduction)
+
+    def call(h, w, b, train):
+        return policy_forward(h, w, target, advantage, old_logp, ref_logp, alpha, b, temperature=temperature,
+                              clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, ignore_index=ignore_index,
+                              train=train)
+
+    loss, logp = _HeadLoss.apply(hidden, weight, bias, call)
+    loss = _reduce(loss, reduction, lambda: (target != ignore_index) & (target >= 0) & (target < weight.shape[0]))
+    return (loss, logp) if return_logp else loss
+
+
+def preference_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, starts: torch.Tensor,
+                    ref_logp: torch.Tensor | None = None, alpha: float = 1.0, bias=None, *, beta: float = 0.1,
+                    margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False, temperature: float = 1.0,
+                    ignore_index: int = -100, reduction: str = "mean", return_logp: bool = False):
+    """Differentiable preference_forward. reduction: "none" (fp32 [P]), "sum",
+    or "mean" over the pairs. With return_logp also the sequences'
+    log-probabilities [2 P], without a gradient (for the implicit rewards)."""
+    _check_reduction(reduction)
+
+    def call(h, w, b, train):
+        return preference_forward(h, w, target, starts, ref_logp, alpha, b, beta=beta, margin=margin,
+                                  label_smoothing=label_smoothing, average=average, temperature=temperature,
+                                  ignore_index=ignore_index, train=train)
+
+    loss, logp = _HeadLoss.apply(hidden, weight, bias, call)
+    loss = _reduce(loss, reduction, lambda: torch.ones_like(loss))
+    return (loss, logp) if return_logp else loss
