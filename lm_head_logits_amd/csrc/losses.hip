@@ -34,9 +34,15 @@ namespace {
 
 constexpr int32_t NO_ID = 0x7FFFFFFF;
 
+// Rows that are not trained on are left out of the work. With more than
+// LR_DIRECT rows, one row tile, the others' hidden rows are copied one behind
+// the other and their number stays on the device, where every kernel reads it;
+// with fewer nothing would be saved by it.
+constexpr int64_t LR_DIRECT = MM_T;
+
 // What the forward pass leaves for the backward pass, in one buffer.
 struct StateLayout {
-  int64_t y, lse, coef, up, bias, ids, p, tk, bytes;
+  int64_t count, rows, inv, hidden, y, lse, coef, up, bias, ids, p, tk, bytes;
 };
 StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) {
   StateLayout s;
@@ -46,6 +52,11 @@ StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
     at += align256(bytes);
     return b;
   };
+  const bool packed = M > LR_DIRECT;
+  s.count = take(4);
+  s.rows = take(packed ? 4 * M : 0);
+  s.inv = take(packed ? 4 * M : 0);
+  s.hidden = take(packed ? 2 * M * H : 0);
   s.y = take(4 * M);
   s.lse = take(4 * M);
   s.coef = take(4 * M);
@@ -55,29 +66,37 @@ StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
   s.p = take(4 * M * K);
   s.tk = take(4 * M * K);
   s.bytes = at;
-  (void)H;
   (void)keep;
   return s;
 }
+// Rows of the work ("packed") are numbered 0 .. n - 1; without packing they are the call's.
 struct State {
-  int32_t *y;      // [M] target column or -1
-  float *lse;      // [M]
-  float *coef;     // [M] d loss / d logp; distill: P
-  int32_t *up;     // [M] which element of the upstream gradient is the row's
+  int32_t *count;  // n; nullptr without packing
+  int32_t *rows;   // [n] the call's row; nullptr
+  int32_t *inv;    // [M] the packed row, -1 where left out; nullptr
+  uint16_t *hidden;  // [n, H]; nullptr
+  int32_t *y;      // [n] target column or -1
+  float *lse;      // [n]
+  float *coef;     // [n] d loss / d logp; distill: P
+  int32_t *up;     // [n] which element of the upstream gradient is the row's
   float *bias;     // [V] bias / T, where T != 1
   int32_t *ids;    // [M, K] the teacher's tokens in ascending order, NO_ID behind the last
   float *p, *tk;   // [M, K] their probabilities and the head's t
 };
-State state_at(void *base, const StateLayout &l) {
+State state_at(void *base, const StateLayout &l, int64_t M) {
   uint8_t *const b = static_cast<uint8_t *>(base);
-  return State{reinterpret_cast<int32_t *>(b + l.y),    reinterpret_cast<float *>(b + l.lse),
+  const bool packed = M > LR_DIRECT;
+  auto ints = [&](int64_t at) { return packed ? reinterpret_cast<int32_t *>(b + at) : nullptr; };
+  return State{ints(l.count), ints(l.rows), ints(l.inv), packed ? reinterpret_cast<uint16_t *>(b + l.hidden) : nullptr,
+               reinterpret_cast<int32_t *>(b + l.y),    reinterpret_cast<float *>(b + l.lse),
                reinterpret_cast<float *>(b + l.coef),   reinterpret_cast<int32_t *>(b + l.up),
                reinterpret_cast<float *>(b + l.bias),   reinterpret_cast<int32_t *>(b + l.ids),
                reinterpret_cast<float *>(b + l.p),      reinterpret_cast<float *>(b + l.tk)};
 }
 
+constexpr int64_t LR_CHUNK = 4096;  // rows counted at a time
 struct ForwardLayout {
-  int64_t part, tlogit, rowlogp, ent, ptr, state, bytes;
+  int64_t part, tlogit, rowlogp, ent, P, ptr, chunks, state, bytes;
 };
 ForwardLayout forward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool with_state) {
   ForwardLayout f;
@@ -92,6 +111,8 @@ ForwardLayout forward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool wi
   f.tlogit = take(4 * M);
   f.rowlogp = take(4 * M);
   f.ent = take(K ? 4 * M : 0);
+  f.P = take(K ? 4 * M : 0);
+  f.chunks = take(4 * ceil_div(M, LR_CHUNK));
   f.ptr = take(K ? 2 * M * (nvt + 1) : 0);
   f.state = take(with_state ? 0 : state_layout(M, H, V, K, false).bytes);
   f.bytes = at;
@@ -231,6 +252,105 @@ __global__ __launch_bounds__(64 * DP_WAVES) void distill_prep_kernel(DistillPrep
   }
 }
 
+// Which rows are worked on: those of a teacher with entries; those with a
+// target, within the sequences where there are any.
+struct Select {
+  const float *P;      // distill: [M] mass of the entries
+  const void *target;  // else
+  int target64;
+  int64_t ignore, M, V;
+  const void *starts;  // preference: [bounds]
+  int starts64;
+  int64_t last;        // the last bound's place
+  __device__ __forceinline__ int64_t bound(int64_t i) const {
+    return starts64 ? static_cast<const int64_t *>(starts)[i] : (int64_t)static_cast<const int32_t *>(starts)[i];
+  }
+  // (column of the target, or 0 where a row has none of its own; -1: left out)
+  __device__ __forceinline__ int64_t column(int64_t m, int64_t lo, int64_t hi) const {
+    if (P != nullptr) return P[m] == 0.0f ? -1 : 0;
+    return m >= lo && m < hi ? target_of(target, target64, m, ignore, V) : -1;
+  }
+};
+constexpr int LR_THREADS = 256, LR_ROWS = 16;
+__device__ __forceinline__ int block_sum(int x, int (&sh)[LR_THREADS / 64]) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = sh[0] + sh[1] + sh[2] + sh[3];
+  __syncthreads();
+  return x;
+}
+// Rows worked on in each chunk of LR_CHUNK (only where there are several).
+__global__ __launch_bounds__(LR_THREADS) void loss_count_kernel(Select c, int32_t *chunks) {
+  __shared__ int sh[LR_THREADS / 64];
+  const int64_t lo = c.starts != nullptr ? c.bound(0) : 0, hi = c.starts != nullptr ? c.bound(c.last) : c.M;
+  const int64_t m0 = (int64_t)blockIdx.x * LR_CHUNK;
+  int n = 0;
+  for (int64_t m = m0 + threadIdx.x; m < m0 + LR_CHUNK && m < c.M; m += LR_THREADS) n += c.column(m, lo, hi) >= 0 ? 1 : 0;
+  n = block_sum(n, sh);
+  if (threadIdx.x == 0) chunks[blockIdx.x] = n;
+}
+// 16 rows a work-group, which counts the rows before them by itself; copies
+// the hidden rows that are worked on, clears the outputs of the others.
+struct Gather {
+  Select sel;
+  const int32_t *chunks;
+  const uint16_t *hidden;
+  int64_t H;
+  State st;
+  float *zero0, *zero1;  // [M] outputs of rows left out, or nullptr
+};
+__global__ __launch_bounds__(LR_THREADS) void loss_gather_kernel(Gather c) {
+  __shared__ int sh[LR_THREADS / 64];
+  __shared__ int32_t list[LR_ROWS];
+  const Select &s = c.sel;
+  const int tid = threadIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.x * LR_ROWS, chunk = r0 / LR_CHUNK;
+  const int64_t lo = s.starts != nullptr ? s.bound(0) : 0, hi = s.starts != nullptr ? s.bound(s.last) : s.M;
+  int n = 0;
+  for (int64_t k = tid; k < chunk; k += LR_THREADS) n += c.chunks[k];
+  for (int64_t m = chunk * LR_CHUNK + tid; m < r0; m += LR_THREADS) n += s.column(m, lo, hi) >= 0 ? 1 : 0;
+  const int before = block_sum(n, sh);
+  if (tid < 64) {  // one wave: the ballot is its own
+    const int64_t m = r0 + tid;
+    const bool mine = tid < LR_ROWS && m < s.M;
+    const int64_t y = mine ? s.column(m, lo, hi) : -1;
+    const uint64_t set = __ballot(y >= 0);
+    const int place = __popcll(set & ((1ull << tid) - 1)), kept = __popcll(set);
+    if (mine) {
+      c.st.inv[m] = y >= 0 ? before + place : -1;
+      if (y >= 0) {
+        list[place] = (int32_t)m;
+        c.st.rows[before + place] = (int32_t)m;
+        c.st.y[before + place] = s.P != nullptr ? -1 : (int32_t)y;
+      } else {
+        if (c.zero0 != nullptr) c.zero0[m] = 0.0f;
+        if (c.zero1 != nullptr) c.zero1[m] = 0.0f;
+      }
+    }
+    if (tid == 0) {
+      sh[0] = kept;
+      if (r0 + LR_ROWS >= s.M) *c.st.count = before + kept;
+    }
+  }
+  __syncthreads();
+  const uint32_t per = (uint32_t)(c.H / 8), total = (uint32_t)sh[0] * per;  // 16-byte pieces
+  const u32x4 *const from = reinterpret_cast<const u32x4 *>(c.hidden);
+  u32x4 *const to = reinterpret_cast<u32x4 *>(c.st.hidden) + (int64_t)before * per;
+  for (uint32_t e0 = tid; e0 < total; e0 += 4 * LR_THREADS) {
+    u32x4 v[4];
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t e = e0 + k * LR_THREADS < total ? e0 + k * LR_THREADS : e0, r = e / per;
+      v[k] = from[(int64_t)list[r] * per + (e - r * per)];
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k)
+      if (e0 + k * LR_THREADS < total) to[e0 + k * LR_THREADS] = v[k];
+  }
+}
+
 // ---------------------------------------------------------------------------
 // The product's epilogue
 // ---------------------------------------------------------------------------
@@ -240,7 +360,10 @@ struct LossFwdArgs {
   int64_t M, H, V;
   float alpha;
   const float *bias;
-  const void *target;  // target losses
+  const int32_t *count;  // packed rows (State): their number, in the place of M
+  const int32_t *rows;
+  const int32_t *y;      // ... and their targets
+  const void *target;    // else
   int target64;
   int64_t ignore;
   float2 *part;        // [vocabulary tile][M] {largest t, sum of exp(t - largest)}
@@ -249,6 +372,13 @@ struct LossFwdArgs {
   const uint16_t *ptr;
   float *tk;           // [M, K] t at the entries
   int64_t K;
+  __device__ __forceinline__ void set_rows() {
+    if (count != nullptr) M = mm_uni(*count);
+  }
+  __device__ __forceinline__ int64_t row(int64_t m) const { return rows != nullptr ? rows[m] : m; }
+  __device__ __forceinline__ int32_t column(int64_t m) const {
+    return y != nullptr ? y[m] : (int32_t)target_of(target, target64, m, ignore, V);
+  }
 };
 
 // PICK: t at the rows' entries in the tile instead of at one target. Through
@@ -296,7 +426,7 @@ struct LossStats {
               mx = fmaxf(mx, v);
             }
         if constexpr (!PICK) {
-          const int32_t yt = m < p.M ? (int32_t)target_of(p.target, p.target64, m, p.ignore, p.V) - (int32_t)n0 : -1;
+          const int32_t yt = m < p.M ? p.column(m) - (int32_t)n0 : -1;
           if (has_column<ET>(at, 0, yt) || has_column<ET>(at, 1, yt)) {
             float v = 0.0f;
 #pragma unroll
@@ -348,7 +478,7 @@ struct LossStats {
         const int64_t m = m0 + 128 * (k >> 2) + 64 * (pr >> 4) + 16 * (k & 3) + (pr & 15);
         range[k] = 0;
         if (m < p.M) {
-          const uint16_t *const r = p.ptr + m * (nvt + 1) + vt;
+          const uint16_t *const r = p.ptr + p.row(m) * (nvt + 1) + vt;
           range[k] = r[0] | (uint32_t)r[1] << 16;
           if (r[0] < r[1]) some |= 1u << k;
         }
@@ -374,8 +504,9 @@ struct LossStats {
           lds_barrier();
           const int64_t m = m0 + 128 * x + 64 * (pr >> 4) + 16 * i + (pr & 15);
           for (uint32_t e = (range[k] & 0xFFFF) + pe; e < range[k] >> 16; e += 16) {
-            const uint32_t c = (uint32_t)(p.sid[m * p.K + e] - (int32_t)n0) & (MM_T - 1);
-            p.tk[m * p.K + e] = box[pr * MM_T + 4 * ((c >> 2) ^ (pr & 15)) + (c & 3)];
+            const int64_t at_e = p.row(m) * p.K + e;
+            const uint32_t c = (uint32_t)(p.sid[at_e] - (int32_t)n0) & (MM_T - 1);
+            p.tk[at_e] = box[pr * MM_T + 4 * ((c >> 2) ^ (pr & 15)) + (c & 3)];
           }
           lds_barrier();
         }
@@ -388,6 +519,7 @@ template <int ET, bool PICK>
 __global__ __launch_bounds__(MM_THREADS, 1) void loss_stats_kernel(LossFwdArgs p) {
   MM_SHARED();
   MM_EPI_SHARED();
+  p.set_rows();
   const LossStats<ET, PICK> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, (p.V + MM_T - 1) / MM_T};
   mm_run<ET, false, false>(prob, mm_buf);
 }
@@ -442,45 +574,52 @@ __device__ __forceinline__ float log_q(float t, float2 f, float ls) {
   return t == NEG_INF ? NEG_INF : __fsub_rn(__fsub_rn(t, f.x), ls);
 }
 
-struct DistillRows {
+// What the kernels that make the rows' losses share.
+struct RowsArgs {
   const float2 *part;
-  int64_t M, nvt, K;
-  const int32_t *sid;
-  const float *p, *tk, *ent, *P;
-  float *loss, *lse;
-  int32_t *y, *up;
+  int64_t M, nvt;
+  State st;
+  __device__ __forceinline__ int64_t rows() const { return st.count != nullptr ? *st.count : M; }
+  __device__ __forceinline__ int64_t row(int64_t m) const { return st.rows != nullptr ? st.rows[m] : m; }
+};
+struct DistillRows {
+  RowsArgs r;
+  int64_t K;
+  const float *ent, *P;
+  float *loss;
 };
 __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(DistillRows c) {
   __shared__ float2 sh[XC_SLICES][XC_ROWS];
   const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
-  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r;
-  const float2 f = fold_row(c.part, c.M, c.nvt, m, m < c.M, sh);
+  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r, n = c.r.rows();
+  if (m - r >= n) return;  // the whole work-group
+  const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
   const float ls = logf(f.y);
+  const int64_t row = m < n ? c.r.row(m) : 0;
   float sum = 0.0f;
-  if (m < c.M)
+  if (m < n)
     for (int64_t k = sl; k < c.K; k += XC_SLICES) {
-      const float p = c.p[m * c.K + k];
-      if (p != 0.0f) sum = __fadd_rn(sum, __fmul_rn(p, log_q(c.tk[m * c.K + k], f, ls)));
+      const float p = c.r.st.p[row * c.K + k];
+      if (p != 0.0f) sum = __fadd_rn(sum, __fmul_rn(p, log_q(c.r.st.tk[row * c.K + k], f, ls)));
     }
   sh[sl][r].x = sum;
   __syncthreads();
-  if (sl != 0 || m >= c.M) return;
+  if (sl != 0 || m >= n) return;
   for (int k = 1; k < XC_SLICES; ++k) sum = __fadd_rn(sum, sh[k][r].x);
-  c.lse[m] = row_lse(f, ls);
-  c.y[m] = -1;
-  c.up[m] = (int32_t)m;
-  c.loss[m] = c.P[m] == 0.0f ? 0.0f : __fsub_rn(c.ent[m], sum);
+  c.r.st.lse[m] = row_lse(f, ls);
+  c.r.st.y[m] = -1;
+  c.r.st.up[m] = (int32_t)row;
+  c.r.st.coef[m] = c.P[row];
+  c.loss[row] = c.P[row] == 0.0f ? 0.0f : __fsub_rn(c.ent[row], sum);
 }
 
 struct TokenRows {
-  const float2 *part;
-  int64_t M, nvt, V;
+  RowsArgs r;
+  int64_t V;
   const float *tlogit;
-  const void *target;
+  const void *target;  // without packing
   int target64;
   int64_t ignore;
-  float *lse, *coef;
-  int32_t *y, *up;
   float *logp;     // [M]
   // policy
   const float *advantage, *old_logp, *ref_logp;
@@ -509,24 +648,27 @@ template <bool POLICY>
 __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void token_rows_kernel(TokenRows c) {
   __shared__ float2 sh[XC_SLICES][XC_ROWS];
   const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
-  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r;
-  const float2 f = fold_row(c.part, c.M, c.nvt, m, m < c.M, sh);
-  if (sl != 0 || m >= c.M) return;
+  const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r, n = c.r.rows();
+  if (m - r >= n) return;  // the whole work-group
+  const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
+  if (sl != 0 || m >= n) return;
   const float ls = logf(f.y);
-  const int64_t y = target_of(c.target, c.target64, m, c.ignore, c.V);
+  const int64_t row = c.r.row(m);
+  const bool packed = c.r.st.rows != nullptr;
+  const int64_t y = packed ? c.r.st.y[m] : target_of(c.target, c.target64, m, c.ignore, c.V);
   const float logp = y >= 0 ? log_q(c.tlogit[m], f, ls) : 0.0f;
-  c.lse[m] = row_lse(f, ls);
-  c.y[m] = (int32_t)y;
-  c.logp[m] = logp;
+  c.r.st.lse[m] = row_lse(f, ls);
+  if (!packed) c.r.st.y[m] = (int32_t)y;
+  c.logp[row] = logp;
   float loss = 0.0f, coef = 0.0f;
   if constexpr (POLICY) {
-    if (y >= 0) policy_token(c, m, logp, loss, coef);
-    c.loss[m] = loss;
-    c.up[m] = (int32_t)m;
+    if (y >= 0) policy_token(c, row, logp, loss, coef);
+    c.loss[row] = loss;
+    c.r.st.up[m] = (int32_t)row;
   } else {
-    c.up[m] = 0;  // preference_pairs_kernel knows the rows' pairs
+    c.r.st.up[m] = 0;  // preference_pairs_kernel knows the rows' pairs
   }
-  c.coef[m] = coef;
+  c.r.st.coef[m] = coef;
 }
 
 // One pair of sequences, one work-group: their sums in 64 bits in a fixed
@@ -545,6 +687,7 @@ struct Pairs {
   int average;
   float *loss, *logp, *coef;
   int32_t *up;
+  const int32_t *inv;  // State
 };
 __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
   __shared__ double sh[2][PP_THREADS];
@@ -603,8 +746,10 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
     const int64_t q = pair + w * c.pairs, lo = bound(q), hi = bound(q + 1);
     for (int64_t m = lo + tid; m < hi; m += PP_THREADS)
       if (target_of(c.target, c.target64, m, c.ignore, c.V) >= 0) {
-        c.coef[m] = der[w];
-        c.up[m] = (int32_t)pair;
+        const int64_t at = c.inv != nullptr ? c.inv[m] : m;
+        if (at < 0) continue;  // bounds that do not ascend
+        c.coef[at] = der[w];
+        c.up[at] = (int32_t)pair;
       }
   }
 }
@@ -617,20 +762,54 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // finite one. Target losses: a = b = -g c. Distill: a = g P, b = g (the factor of
 // the entries), no target. Every work-group finds the maximum by itself up to
 // LC_ONE rows; with more, one work-group finds it in a launch of its own.
+// The splits of G W's K (the piece's columns) that fill the last round of
+// work-groups best, at least 256 columns each; chosen as bwd_plan does, from the
+// rows worked on, by one wave. `cap`: row tiles times splits that the sums have
+// room for.
+struct SplitPlan {
+  int64_t ksplit;
+  int32_t splits;
+};
+__device__ __forceinline__ void plan_splits(int64_t n, int64_t H, int64_t vp, int64_t cap, SplitPlan *out) {
+  const int lane = threadIdx.x;
+  const int64_t nmt = (n + MM_T - 1) / MM_T, tiles = nmt * ((H + MM_T - 1) / MM_T), cus = 256;
+  const int64_t s = lane + 1;
+  const bool ok = s == 1 || (s * 256 <= vp && s * nmt <= cap && tiles * (s - 1) < cus * 4);
+  const float use = ok && tiles > 0 ? (float)(tiles * s) / (float)((tiles * s + cus - 1) / cus * cus) : 0.0f;
+  float best = 0.0f;
+  int64_t splits = 1;
+  for (int k = 0; k < 64; ++k) {
+    const float u = __shfl(use, k);
+    if (u > best * 1.05f) {
+      best = u;
+      splits = k + 1;
+    }
+  }
+  if (lane == 0) {
+    const int64_t ksplit = ((vp + splits - 1) / splits + 63) / 64 * 64;
+    out->ksplit = ksplit;
+    out->splits = (int32_t)((vp + ksplit - 1) / ksplit);
+  }
+}
+
 constexpr int LC_THREADS = 256;
 constexpr int64_t LC_ONE = 32768;
 struct LossCoef {
   const float *g;
   int64_t M;
   const float *lse, *coef;
-  const int32_t *y, *up;
+  const int32_t *y, *up, *count;
   int distill;
   float top;
   float *scale;
   RowCoef *rows;
   int have_scale, write_rows;
+  SplitPlan *plan;
+  int64_t H, vp, cap;
 };
 __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
+  if (p.count != nullptr) p.M = *p.count;
+  if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale) plan_splits(p.M, p.H, p.vp, p.cap, p.plan);
   auto coef = [&](int64_t m, float &a, float &b) {
     const float c = p.coef[m];
     a = b = 0.0f;
@@ -671,10 +850,21 @@ __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
   p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], p.distill ? -1 : p.y[m]};
 }
 
+// Packed rows: their number is known on the device.
+struct OnDevice {
+  const int32_t *count;
+  const SplitPlan *plan;
+  __device__ __forceinline__ void apply(XentBwdArgs &p) const {
+    if (count != nullptr) p.M = mm_uni(*count);
+    p.ksplit = (int64_t)mm_uni((uint32_t)plan->ksplit);
+  }
+};
+
 template <int ET, bool DB>
-__global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p) {
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p, OnDevice dev) {
   MM_SHARED();
   MM_EPI_SHARED();
+  dev.apply(p);
   const XentGrad<ET, DB> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
   mm_run<ET, false, false>(prob, mm_buf);
 }
@@ -689,7 +879,7 @@ __global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p)
 struct DistillEntries {
   XentBwdArgs b;
   int64_t K;
-  const int32_t *sid;
+  const int32_t *sid, *inv;
   const float *p, *tk;
   unsigned long long *bias;  // [V] or nullptr
   double unit;               // 2^shift / top
@@ -700,7 +890,8 @@ __global__ __launch_bounds__(256) void distill_entries_kernel(DistillEntries c) 
   if (e >= c.b.M * c.K) return;
   const int32_t id = c.sid[e];
   if (id == NO_ID || id < c.b.v0 || id >= c.b.v0 + c.b.np) return;
-  const int64_t m = e / c.K, k = e - m * c.K;
+  const int64_t row = e / c.K, k = e - row * c.K, m = c.inv != nullptr ? c.inv[row] : row;
+  if (m < 0) return;
   const RowCoef r = c.b.rows[m];
   const float lse = r.lse == NEG_INF ? 0.0f : r.lse;
   int64_t first = k;
@@ -727,66 +918,111 @@ hipError_t zero_words(void *p, int64_t n, hipStream_t s) {
 
 // grad_bias of one piece: the row tiles' column sums in ascending order, the
 // entries' share, and 1 / T.
-__global__ __launch_bounds__(256) void loss_bias_kernel(const float *__restrict__ colpart, int64_t nmt, int64_t vp,
-                                                        int64_t n, const long long *__restrict__ entries,
+__global__ __launch_bounds__(256) void loss_bias_kernel(const float *__restrict__ colpart, int64_t M,
+                                                        const int32_t *__restrict__ count, int64_t vp, int64_t n, const long long *__restrict__ entries,
                                                         const float *__restrict__ scale, double unit, float T,
                                                         float *__restrict__ db) {
   const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (v >= n) return;
   float s = 0.0f;
+  const int64_t nmt = ((count != nullptr ? *count : M) + MM_T - 1) / MM_T;
   for (int64_t t = 0; t < nmt; ++t) s = __fadd_rn(s, colpart[t * vp + v]);
   if (entries != nullptr) s = (float)((double)s + (double)entries[v] / unit * (double)scale[1]);
   db[v] = __fdiv_rn(s, T);
 }
 
 template <int ET>
-__global__ __launch_bounds__(MM_THREADS, 1) void loss_dhidden_kernel(XentBwdArgs p) {
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_dhidden_kernel(XentBwdArgs p, OnDevice dev) {
   MM_SHARED();
+  dev.apply(p);
   const XentDHidden<ET> prob{p, (p.M + MM_T - 1) / MM_T, (p.H + MM_T - 1) / MM_T,
                              (p.np + p.ksplit - 1) / p.ksplit};
   mm_run<ET, false, true>(prob, mm_buf);
 }
 template <int ET>
-__global__ __launch_bounds__(MM_THREADS, 1) void loss_dweight_kernel(XentBwdArgs p) {
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_dweight_kernel(XentBwdArgs p, OnDevice dev) {
   MM_SHARED();
   MM_EPI_SHARED();
+  dev.apply(p);
   const XentDWeight<ET> prob{p, mm_epi, p.np / MM_T, (p.H + MM_T - 1) / MM_T};
   mm_run<ET, true, true>(prob, mm_buf);
 }
 
-// grad_hidden: the splits' sums in ascending order, scaled, rounded once.
+// grad_hidden: the splits' sums in ascending order, scaled, rounded once; 0 in
+// the rows left out.
+struct DHiddenOut {
+  const float *dh;  // [splits][n, H]
+  int64_t M, H;
+  const int32_t *count, *inv;
+  const SplitPlan *plan;
+  float alpha;
+  const float *scale;
+  uint16_t *out;
+};
 template <int ET>
-__global__ __launch_bounds__(256) void loss_dhidden_out_kernel(const float *__restrict__ dh, int64_t n, int splits,
-                                                               float alpha, const float *__restrict__ scale,
-                                                               uint16_t *__restrict__ out) {
+__global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
   const int64_t e = (group_number() * 256 + threadIdx.x) * 8;
-  if (e >= n) return;
-  f32x4 s[2] = {zero4(), zero4()};
-  for (int k = 0; k < splits; ++k)
+  if (e >= c.M * c.H) return;
+  const int64_t row = e / c.H, m = c.inv != nullptr ? c.inv[row] : row;
+  if (m < 0) {
+    *reinterpret_cast<u32x4 *>(c.out + e) = u32x4{0, 0, 0, 0};
+    return;
+  }
+  const int64_t n = (c.count != nullptr ? *c.count : c.M) * c.H, at = m * c.H + (e - row * c.H);
+  const int splits = c.plan->splits;
+  f32x4 s[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4 v = *reinterpret_cast<const f32x4 *>(dh + k * n + e + 4 * h);
+  for (int h = 0; h < 2; ++h) s[h] = *reinterpret_cast<const f32x4 *>(c.dh + at + 4 * h);
+  for (int k0 = 1; k0 < splits; k0 += 8) {
+    f32x4 v[8][2];  // eight splits' loads in flight (past the last: the last again, not added)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) s[h][q] = __fadd_rn(s[h][q], v[q]);
-    }
-  const float f = __fmul_rn(alpha, scale[1]);
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[k][h] = *reinterpret_cast<const f32x4 *>(c.dh + (k0 + k < splits ? k0 + k : splits - 1) * n + at + 4 * h);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[h][q] = k0 + k < splits ? __fadd_rn(s[h][q], v[k][h][q]) : s[h][q];
+  }
+  const float f = __fmul_rn(c.alpha, c.scale[1]);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int q = 0; q < 4; ++q) s[h][q] = __fmul_rn(f, s[h][q]);
-  *reinterpret_cast<u32x4 *>(out + e) = u32x4{mm_pack2<ET>(s[0][0], s[0][1]), mm_pack2<ET>(s[0][2], s[0][3]),
-                                              mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
+  *reinterpret_cast<u32x4 *>(c.out + e) = u32x4{mm_pack2<ET>(s[0][0], s[0][1]), mm_pack2<ET>(s[0][2], s[0][3]),
+                                                mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
 }
 
+// bwd_plan's pieces, with room for the sums of grad_hidden whatever the rows
+// worked on are: splits times row tiles as for all rows.
 struct BackwardLayout {
-  BwdPlan plan;
-  int64_t entries, bytes;
+  int64_t vp, splits, cap;
+  int64_t scale, plan, rows, col, dh, G, entries, bytes;
 };
 BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool bias) {
   BackwardLayout b;
-  b.plan = bwd_plan(M, H, V, bias);
-  b.entries = b.plan.bytes;
-  b.bytes = b.entries + (bias && K ? align256(8 * V) : 0);
+  const BwdPlan pl = bwd_plan(M, H, V, bias);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += align256(bytes);
+    return o;
+  };
+  const int64_t nmt = ceil_div(M, MM_T);
+  b.vp = pl.vp;
+  b.splits = pl.splits;
+  b.cap = pl.splits * nmt;
+  b.scale = take(8);
+  b.plan = take(sizeof(SplitPlan));
+  b.rows = take(16 * M);
+  b.col = take(bias ? 4 * nmt * b.vp : 0);
+  b.dh = take(4 * H * (M > LR_DIRECT ? b.cap * MM_T : pl.splits * M));
+  b.G = take(2 * M * b.vp);
+  b.entries = take(bias && K ? 8 * V : 0);
+  b.bytes = at;
   return b;
 }
 
@@ -800,15 +1036,19 @@ struct Setup {
 hipError_t set_up(const LossHead &h, const LossMemory &mem, int64_t K, hipStream_t s, Setup &u) {
   u.lay = forward_layout(h.M, h.H, h.V, K, mem.state != nullptr);
   u.ws = static_cast<uint8_t *>(mem.workspace);
-  u.st = state_at(mem.state != nullptr ? mem.state : u.ws + u.lay.state, state_layout(h.M, h.H, h.V, K, mem.keep != 0));
+  u.st = state_at(mem.state != nullptr ? mem.state : u.ws + u.lay.state, state_layout(h.M, h.H, h.V, K, mem.keep != 0),
+                  h.M);
   u.a = LossFwdArgs{};
-  u.a.hidden = static_cast<const uint8_t *>(h.hidden);
+  u.a.hidden = u.st.hidden != nullptr ? reinterpret_cast<const uint8_t *>(u.st.hidden) : static_cast<const uint8_t *>(h.hidden);
   u.a.W = static_cast<const uint8_t *>(h.W);
   u.a.M = h.M;
   u.a.H = h.H;
   u.a.V = h.V;
   u.a.alpha = (float)((double)h.alpha / (double)h.temperature);
   u.a.bias = h.bias;
+  u.a.count = u.st.count;
+  u.a.rows = u.st.rows;
+  u.a.y = u.st.rows != nullptr ? u.st.y : nullptr;
   u.a.part = reinterpret_cast<float2 *>(u.ws + u.lay.part);
   u.a.tlogit = reinterpret_cast<float *>(u.ws + u.lay.tlogit);
   u.a.K = K;
@@ -816,6 +1056,18 @@ hipError_t set_up(const LossHead &h, const LossMemory &mem, int64_t K, hipStream
   u.a.bias = u.st.bias;
   return launch_kernel(loss_bias_scale_kernel, dim3((unsigned)ceil_div(h.V, 256)), dim3(256), s, h.bias, h.V,
                        h.temperature, u.st.bias);
+}
+// The rows worked on, one behind the other.
+hipError_t gather(const LossHead &h, const Setup &u, const Select &sel, float *zero0, float *zero1, hipStream_t s) {
+  if (u.st.rows == nullptr) return hipSuccess;
+  int32_t *const chunks = reinterpret_cast<int32_t *>(u.ws + u.lay.chunks);
+  hipError_t e = hipSuccess;
+  if (h.M > LR_CHUNK)
+    e = launch_kernel(loss_count_kernel, dim3((unsigned)ceil_div(h.M, LR_CHUNK)), dim3(LR_THREADS), s, sel, chunks);
+  if (e == hipSuccess)
+    e = launch_kernel(loss_gather_kernel, dim3((unsigned)ceil_div(h.M, LR_ROWS)), dim3(LR_THREADS), s,
+                      Gather{sel, chunks, static_cast<const uint16_t *>(h.hidden), h.H, u.st, zero0, zero1});
+  return e;
 }
 template <bool PICK>
 hipError_t stats(const LossHead &h, const LossFwdArgs &a, hipStream_t s) {
@@ -828,20 +1080,15 @@ void set_targets(LossFwdArgs &a, const LossTargets &y) {
   a.target64 = y.wide;
   a.ignore = y.ignore;
 }
+RowsArgs rows_args(const Setup &u) { return RowsArgs{u.a.part, u.a.M, ceil_div(u.a.V, MM_T), u.st}; }
 TokenRows token_rows(const Setup &u, const LossTargets &y) {
   TokenRows r{};
-  r.part = u.a.part;
-  r.M = u.a.M;
-  r.nvt = ceil_div(u.a.V, MM_T);
+  r.r = rows_args(u);
   r.V = u.a.V;
   r.tlogit = u.a.tlogit;
   r.target = y.target;
   r.target64 = y.wide;
   r.ignore = y.ignore;
-  r.lse = u.st.lse;
-  r.coef = u.st.coef;
-  r.y = u.st.y;
-  r.up = u.st.up;
   return r;
 }
 dim3 rows_grid(int64_t M) { return dim3((unsigned)ceil_div(M, XC_ROWS)); }
@@ -850,13 +1097,14 @@ template <int ET>
 hipError_t backward(const LossBackward &c, hipStream_t s) {
   const LossHead &h = c.head;
   const BackwardLayout lay = backward_layout(h.M, h.H, h.V, c.K, c.grad_bias != nullptr);
-  const BwdPlan &pl = lay.plan;
   uint8_t *const ws = static_cast<uint8_t *>(c.mem.workspace);
-  const State st = state_at(c.mem.state, state_layout(h.M, h.H, h.V, c.K, c.mem.keep != 0));
-  float *const scale = reinterpret_cast<float *>(ws + pl.off_scale);
-  RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + pl.off_rows);
+  const State st = state_at(c.mem.state, state_layout(h.M, h.H, h.V, c.K, c.mem.keep != 0), h.M);
+  float *const scale = reinterpret_cast<float *>(ws + lay.scale);
+  SplitPlan *const plan = reinterpret_cast<SplitPlan *>(ws + lay.plan);
+  RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + lay.rows);
   const float top = ET == ET_F16 ? 16384.0f : 1.0f;
-  LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, c.K > 0, top, scale, rows, 0, 1};
+  LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, st.count, c.K > 0, top, scale, rows, 0, 1,
+             plan, h.H, lay.vp, lay.cap};
   hipError_t e = hipSuccess;
   if (h.M > LC_ONE) {
     r.write_rows = 0;
@@ -866,7 +1114,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   if (e == hipSuccess)
     e = launch_kernel(loss_coef_kernel, dim3((unsigned)ceil_div(h.M, LC_THREADS)), dim3(LC_THREADS), s, r);
   XentBwdArgs p{};
-  p.hidden = static_cast<const uint8_t *>(h.hidden);
+  p.hidden = st.hidden != nullptr ? reinterpret_cast<const uint8_t *>(st.hidden) : static_cast<const uint8_t *>(h.hidden);
   p.W = static_cast<const uint8_t *>(h.W);
   p.M = h.M;
   p.H = h.H;
@@ -875,12 +1123,12 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   p.bias = h.bias == nullptr || h.temperature == 1.0f ? h.bias : st.bias;
   p.rows = rows;
   p.scale = scale;
-  p.ldg = pl.vp;
-  p.G = ws + pl.off_g;
-  p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + pl.off_col) : nullptr;
-  p.dh = reinterpret_cast<float *>(ws + pl.off_dh);
-  p.ksplit = pl.ksplit;
+  p.ldg = lay.vp;
+  p.G = ws + lay.G;
+  p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + lay.col) : nullptr;
+  p.dh = reinterpret_cast<float *>(ws + lay.dh);
   p.dw = static_cast<uint16_t *>(c.grad_W);
+  const OnDevice dev{st.count, plan};
   const int64_t nmt = ceil_div(h.M, MM_T), nht = ceil_div(h.H, MM_T);
   // whole numbers of 2^-shift: their sum over all rows stays below 2^62
   int shift = 61;
@@ -890,30 +1138,31 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   const bool sums = c.grad_bias != nullptr && c.K > 0;
   unsigned long long *const entries = sums ? reinterpret_cast<unsigned long long *>(ws + lay.entries) : nullptr;
   if (e == hipSuccess && sums) e = zero_words(entries, 2 * h.V, s);
-  for (int64_t v0 = 0; v0 < h.V && e == hipSuccess; v0 += pl.vp) {
+  for (int64_t v0 = 0; v0 < h.V && e == hipSuccess; v0 += lay.vp) {
     p.v0 = v0;
     p.first = v0 == 0;
-    const int64_t nv = h.V - v0 < pl.vp ? h.V - v0 : pl.vp;
+    const int64_t nv = h.V - v0 < lay.vp ? h.V - v0 : lay.vp;
     p.np = ceil_div(nv, MM_T) * MM_T;
     e = launch_kernel(c.grad_bias != nullptr ? loss_grad_kernel<ET, true> : loss_grad_kernel<ET, false>,
-                      mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p);
+                      mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
     if (e == hipSuccess && c.K > 0)
       e = launch_kernel(distill_entries_kernel<ET>, numbered_grid(ceil_div(h.M * c.K, 256)), dim3(256), s,
-                        DistillEntries{p, c.K, st.ids, st.p, st.tk, entries, unit});
+                        DistillEntries{p, c.K, st.ids, st.inv, st.p, st.tk, entries, unit});
     if (e == hipSuccess && c.grad_bias != nullptr)
       e = launch_kernel(loss_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
-                        static_cast<const float *>(p.colpart), nmt, pl.vp, nv,
+                        static_cast<const float *>(p.colpart), h.M, static_cast<const int32_t *>(st.count), lay.vp, nv,
                         sums ? reinterpret_cast<const long long *>(entries) + v0 : nullptr, static_cast<const float *>(scale),
                         unit, h.temperature, c.grad_bias + v0);
+    // the last piece may have fewer splits with work in them; `cap` tiles is the most there are
+    const int64_t ta = nht * (st.count != nullptr ? lay.cap : lay.splits);
     if (e == hipSuccess && c.grad_hidden != nullptr)
-      e = launch_kernel(loss_dhidden_kernel<ET>, mm_grid(nmt * nht * ceil_div(p.np, pl.ksplit)), dim3(MM_THREADS), s, p);
+      e = launch_kernel(loss_dhidden_kernel<ET>, mm_grid(ta), dim3(MM_THREADS), s, p, dev);
     if (e == hipSuccess && c.grad_W != nullptr)
-      e = launch_kernel(loss_dweight_kernel<ET>, mm_grid(nht * (p.np / MM_T)), dim3(MM_THREADS), s, p);
+      e = launch_kernel(loss_dweight_kernel<ET>, mm_grid(nht * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
   }
   if (e == hipSuccess && c.grad_hidden != nullptr)
     e = launch_kernel(loss_dhidden_out_kernel<ET>, numbered_grid(ceil_div(h.M * h.H, 2048)), dim3(256), s,
-                      static_cast<const float *>(p.dh), h.M * h.H, (int)pl.splits, p.alpha,
-                      static_cast<const float *>(scale), static_cast<uint16_t *>(c.grad_hidden));
+                      DHiddenOut{p.dh, h.M, h.H, st.count, st.inv, plan, p.alpha, scale, static_cast<uint16_t *>(c.grad_hidden)});
   return e;
 }
 
@@ -935,19 +1184,22 @@ hipError_t launch_distill_forward(const DistillForward &c, hipStream_t s) {
   hipError_t e = set_up(h, c.mem, c.K, s, u);
   if (e != hipSuccess) return e;
   uint16_t *const ptr = reinterpret_cast<uint16_t *>(u.ws + u.lay.ptr);
-  float *const ent = reinterpret_cast<float *>(u.ws + u.lay.ent);
+  float *const ent = reinterpret_cast<float *>(u.ws + u.lay.ent), *const P = reinterpret_cast<float *>(u.ws + u.lay.P);
   const DistillPrep d{c.ids, c.ids64, h.M, h.V, c.K, c.logits, c.logits_type, c.teacher_lse, h.temperature,
-                      u.st.ids, u.st.p, ptr, ent, u.st.coef};
+                      u.st.ids, u.st.p, ptr, ent, P};
   e = launch_kernel(c.K <= 64 ? distill_prep_kernel<1> : c.K <= 256 ? distill_prep_kernel<4> : distill_prep_kernel<16>,
                     numbered_grid(ceil_div(h.M, DP_WAVES)), dim3(64 * DP_WAVES), s, d);
+  Select sel{};
+  sel.P = P;
+  sel.M = h.M;
+  if (e == hipSuccess) e = gather(h, u, sel, c.loss, nullptr, s);
   u.a.sid = u.st.ids;
   u.a.ptr = ptr;
   u.a.tk = u.st.tk;
   if (e == hipSuccess) e = stats<true>(h, u.a, s);
   if (e == hipSuccess)
     e = launch_kernel(distill_rows_kernel, rows_grid(h.M), dim3(XC_ROWS * XC_SLICES), s,
-                      DistillRows{u.a.part, h.M, ceil_div(h.V, MM_T), c.K, u.st.ids, u.st.p, u.st.tk, ent, u.st.coef,
-                                  c.loss, u.st.lse, u.st.y, u.st.up});
+                      DistillRows{rows_args(u), c.K, ent, P, c.loss});
   return e;
 }
 
@@ -956,7 +1208,9 @@ hipError_t launch_policy_forward(const PolicyForward &c, hipStream_t s) {
   hipError_t e = set_up(c.head, c.mem, 0, s, u);
   if (e != hipSuccess) return e;
   set_targets(u.a, c.y);
-  e = stats<false>(c.head, u.a, s);
+  Select sel{nullptr, c.y.target, c.y.wide, c.y.ignore, c.head.M, c.head.V, nullptr, 0, 0};
+  e = gather(c.head, u, sel, c.loss, c.logp, s);
+  if (e == hipSuccess) e = stats<false>(c.head, u.a, s);
   TokenRows r = token_rows(u, c.y);
   r.logp = c.logp;
   r.advantage = c.advantage;
@@ -976,18 +1230,23 @@ hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t s) 
   hipError_t e = set_up(c.head, c.mem, 0, s, u);
   if (e != hipSuccess) return e;
   set_targets(u.a, c.y);
+  float *const rowlogp = reinterpret_cast<float *>(u.ws + u.lay.rowlogp);
   if (c.head.M > 0) {
-    e = stats<false>(c.head, u.a, s);
+    // without pairs there are no bounds, and no row is worked on
+    Select sel{nullptr, c.y.target, c.y.wide, c.y.ignore, c.head.M, c.pairs > 0 ? c.head.V : 0, c.pairs > 0 ? c.starts : nullptr,
+               c.starts64, 2 * c.pairs};
+    e = gather(c.head, u, sel, nullptr, nullptr, s);
+    if (e == hipSuccess) e = stats<false>(c.head, u.a, s);
     TokenRows r = token_rows(u, c.y);
-    r.logp = reinterpret_cast<float *>(u.ws + u.lay.rowlogp);
+    r.logp = rowlogp;
     if (e == hipSuccess)
       e = launch_kernel(token_rows_kernel<false>, rows_grid(c.head.M), dim3(XC_ROWS * XC_SLICES), s, r);
   }
   if (e == hipSuccess && c.pairs > 0)
     e = launch_kernel(preference_pairs_kernel, dim3((unsigned)c.pairs), dim3(PP_THREADS), s,
                       Pairs{c.starts, c.starts64, c.pairs, c.head.M, c.head.V, c.y.target, c.y.wide, c.y.ignore,
-                            reinterpret_cast<float *>(u.ws + u.lay.rowlogp), c.ref_logp, c.beta, c.margin, c.smoothing,
-                            c.average, c.loss, c.logp, u.st.coef, u.st.up});
+                            rowlogp, c.ref_logp, c.beta, c.margin, c.smoothing, c.average, c.loss, c.logp, u.st.coef,
+                            u.st.up, u.st.inv});
   return e;
 }
 
