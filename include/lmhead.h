@@ -332,7 +332,7 @@ lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, con
 size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias);
 
 /* ---------------------------------------------------------------------------
- * Further losses of the head's logits, which are never whole in memory:
+ * Further losses of the head's logits, which need not be whole in memory:
  *   t[m, v] = (alpha * (hidden[m, :] . W[v, :]) + bias[v]) / temperature,
  *   lse[m] = log sum_v exp(t[m, v]),  log q[m, v] = t[m, v] - lse[m]
  * (alpha / temperature and bias[v] / temperature are taken at fp32 each).
@@ -340,8 +340,14 @@ size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int
  * there what lmhead_loss_backward needs; that call may be made more than once on
  * one state, and the state belongs to the call's hidden, W and bias.
  *   temperature > 0
- *   state       at least lmhead_loss_state_bytes(M, H, V, K) bytes, 256-byte aligned
- *               (device, written), or NULL when no backward pass follows
+ *   state       at least lmhead_loss_state_bytes(M, H, V, K, keep_logits) bytes,
+ *               256-byte aligned (device, written), or NULL when no backward pass
+ *               follows
+ *   keep_logits 0, or 1: the forward call leaves every t it works on in the state (fp32,
+ *               4 M V bytes and the ends of tiles; room for all rows), and the backward
+ *               call reads them instead of making them again, which is one of its three
+ *               products. The gradients are the same, bit for bit; grad_bias up to the
+ *               order of its fp32 sums. The backward call is given what the forward call was
  *   workspace   at least lmhead_loss_forward_workspace_bytes(M, H, V, K, state != NULL)
  *               bytes, 256-byte aligned, overwritten; not in use by other work
  *               until this call's work has finished
@@ -370,7 +376,7 @@ lmhead_status lmhead_distill_forward(const void *hidden, int64_t M, int64_t H, c
                                      const float *bias, lmhead_dtype in_dtype, float temperature,
                                      const void *teacher_ids, lmhead_index ids_type, const void *teacher_logits,
                                      lmhead_dtype logits_dtype, int64_t K, const float *teacher_lse, float *loss,
-                                     void *state, size_t state_bytes, void *workspace, size_t workspace_bytes,
+                                     void *state, size_t state_bytes, int keep_logits, void *workspace, size_t workspace_bytes,
                                      void *stream);
 
 /* The clipped policy loss with a KL term of the tokens target[m]:
@@ -387,7 +393,7 @@ lmhead_status lmhead_policy_forward(const void *hidden, int64_t M, int64_t H, co
                                     const float *bias, lmhead_dtype in_dtype, float temperature, const void *target,
                                     lmhead_index target_type, int64_t ignore_index, const float *advantage,
                                     const float *old_logp, const float *ref_logp, float clip_low, float clip_high,
-                                    float kl_coef, float *loss, float *logp, void *state, size_t state_bytes,
+                                    float kl_coef, float *loss, float *logp, void *state, size_t state_bytes, int keep_logits,
                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* The logistic loss of preferred pairs. Sequence s is rows starts[s] ..
@@ -407,7 +413,7 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
                                         lmhead_index target_type, int64_t ignore_index, const void *starts,
                                         lmhead_index starts_type, int64_t pairs, const float *ref_logp, float beta,
                                         float margin, float label_smoothing, int average, float *loss, float *logp,
-                                        void *state, size_t state_bytes, void *workspace, size_t workspace_bytes,
+                                        void *state, size_t state_bytes, int keep_logits, void *workspace, size_t workspace_bytes,
                                         void *stream);
 
 /* Gradients of sum_m grad_loss[m] loss[m] (preference: over the pairs) of one of the
@@ -415,18 +421,20 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
  * (K: 0 but for lmhead_distill_forward).
  *   grad_loss   fp32 [M], or [pairs]                            (device, read)
  *   grad_hidden, grad_W, grad_bias, workspace   as in lmhead_xent_backward, with
- *               lmhead_loss_backward_workspace_bytes(M, H, V, K, grad_bias != NULL) bytes
+ *               lmhead_loss_backward_workspace_bytes(M, H, V, K, keep_logits, grad_bias != NULL)
+ *               bytes
  * Rounded and scaled as there. */
 lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
                                    const float *bias, lmhead_dtype in_dtype, float temperature, int64_t K,
-                                   const float *grad_loss, const void *state, size_t state_bytes, void *grad_hidden,
+                                   const float *grad_loss, const void *state, size_t state_bytes, int keep_logits, void *grad_hidden,
                                    void *grad_W, float *grad_bias, void *workspace, size_t workspace_bytes,
                                    void *stream);
 
 /* Host-only: bytes of the state and of the workspaces (0 outside the shape contract or when M == 0). */
-size_t lmhead_loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K);
+size_t lmhead_loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int keep_logits);
 size_t lmhead_loss_forward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int with_state);
-size_t lmhead_loss_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int grad_bias);
+size_t lmhead_loss_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int keep_logits,
+                                            int grad_bias);
 
 /* The embedding lookup out[m, :] = scale * W[ids[m], :], the product taken at
  * fp32 and rounded once. An id outside [0, V) gives a row of zeros (so a

@@ -114,7 +114,7 @@ def load() -> ctypes.CDLL:
     lib.lmhead_logits_int8.restype = i32
     lib.lmhead_logits_int8.argtypes = [vp, vp, i64, i64, vp, vp, i64, f32, vp, i32, vp, vp]
     head = [vp, i64, i64, vp, i64, f32, vp, i32, f32]  # hidden .. temperature
-    memory = [vp, sz, vp, sz, vp]  # state, workspace, stream
+    memory = [vp, sz, i32, vp, sz, vp]  # state, workspace, stream
     lib.lmhead_distill_forward.restype = i32
     lib.lmhead_distill_forward.argtypes = [*head, vp, i32, vp, i32, i64, vp, vp, *memory]
     lib.lmhead_policy_forward.restype = i32
@@ -122,13 +122,13 @@ def load() -> ctypes.CDLL:
     lib.lmhead_preference_forward.restype = i32
     lib.lmhead_preference_forward.argtypes = [*head, vp, i32, i64, vp, i32, i64, vp, f32, f32, f32, i32, vp, vp, *memory]
     lib.lmhead_loss_backward.restype = i32
-    lib.lmhead_loss_backward.argtypes = [*head, i64, vp, vp, sz, vp, vp, vp, vp, sz, vp]
+    lib.lmhead_loss_backward.argtypes = [*head, i64, vp, vp, sz, i32, vp, vp, vp, vp, sz, vp]
     lib.lmhead_loss_state_bytes.restype = sz
-    lib.lmhead_loss_state_bytes.argtypes = [i64, i64, i64, i64]
+    lib.lmhead_loss_state_bytes.argtypes = [i64, i64, i64, i64, i32]
     lib.lmhead_loss_forward_workspace_bytes.restype = sz
     lib.lmhead_loss_forward_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
     lib.lmhead_loss_backward_workspace_bytes.restype = sz
-    lib.lmhead_loss_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i32]
+    lib.lmhead_loss_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i32, i32]
     _lib = lib
     return lib
 

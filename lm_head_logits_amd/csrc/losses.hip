@@ -22,7 +22,9 @@
 // Forward: one matrix product whose epilogue keeps, per row and 256-column
 // tile, the largest t and the sum of exponentials, and the t that the loss
 // asks for (the target's, or the teacher's entries'); a second kernel folds a
-// row's tiles and makes its loss and c. Backward: the pieces of xent.hip.
+// row's tiles and makes its loss and c. Backward: the pieces of xent.hip; G of a
+// piece either by the product again or, where the forward pass kept t (fp32),
+// from memory.
 //
 // 1 / T: alpha / T and a copy of the bias divided by T go into the products.
 #include "losses_launch.hpp"
@@ -42,8 +44,9 @@ constexpr int64_t LR_DIRECT = MM_T;
 
 // What the forward pass leaves for the backward pass, in one buffer.
 struct StateLayout {
-  int64_t count, rows, inv, hidden, y, lse, coef, up, bias, ids, p, tk, bytes;
+  int64_t count, rows, inv, hidden, y, lse, coef, up, bias, ids, p, tk, t, bytes;
 };
+int64_t padded(int64_t V) { return ceil_div(V, MM_T) * MM_T; }
 StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) {
   StateLayout s;
   int64_t at = 0;
@@ -65,8 +68,8 @@ StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
   s.ids = take(4 * M * K);
   s.p = take(4 * M * K);
   s.tk = take(4 * M * K);
+  s.t = take(keep ? 4 * M * padded(V) : 0);
   s.bytes = at;
-  (void)keep;
   return s;
 }
 // Rows of the work ("packed") are numbered 0 .. n - 1; without packing they are the call's.
@@ -82,6 +85,7 @@ struct State {
   float *bias;     // [V] bias / T, where T != 1
   int32_t *ids;    // [M, K] the teacher's tokens in ascending order, NO_ID behind the last
   float *p, *tk;   // [M, K] their probabilities and the head's t
+  float *t;        // [n, V in whole tiles] every t (-inf behind the last), where they are kept
 };
 State state_at(void *base, const StateLayout &l, int64_t M) {
   uint8_t *const b = static_cast<uint8_t *>(base);
@@ -91,7 +95,8 @@ State state_at(void *base, const StateLayout &l, int64_t M) {
                reinterpret_cast<int32_t *>(b + l.y),    reinterpret_cast<float *>(b + l.lse),
                reinterpret_cast<float *>(b + l.coef),   reinterpret_cast<int32_t *>(b + l.up),
                reinterpret_cast<float *>(b + l.bias),   reinterpret_cast<int32_t *>(b + l.ids),
-               reinterpret_cast<float *>(b + l.p),      reinterpret_cast<float *>(b + l.tk)};
+               reinterpret_cast<float *>(b + l.p),      reinterpret_cast<float *>(b + l.tk),
+               reinterpret_cast<float *>(b + l.t)};
 }
 
 constexpr int64_t LR_CHUNK = 4096;  // rows counted at a time
@@ -372,6 +377,7 @@ struct LossFwdArgs {
   const uint16_t *ptr;
   float *tk;           // [M, K] t at the entries
   int64_t K;
+  float *t;            // KEEP: [M, padded V]
   __device__ __forceinline__ void set_rows() {
     if (count != nullptr) M = mm_uni(*count);
   }
@@ -385,7 +391,9 @@ struct LossFwdArgs {
 // LDS, 32 rows at a time: all 256 columns of the rows are written, then 16
 // threads a row take that row's entries from it. Groups of rows without an
 // entry are left out.
-template <int ET, bool PICK>
+//
+// KEEP: t of the whole tile to memory, for the backward pass.
+template <int ET, bool PICK, bool KEEP>
 struct LossStats {
   LossFwdArgs p;
   u32x4 *epi;
@@ -408,6 +416,10 @@ struct LossStats {
     float2 *const stat = reinterpret_cast<float2 *>(epi);  // [4][256]
     uint32_t *const groups = reinterpret_cast<uint32_t *>(epi) + 4 * MM_T * 2;
     if (PICK && threadIdx.x == 0) *groups = 0;
+    const int rows = (int)(p.M - m0 < MM_T ? p.M - m0 : MM_T);
+    const uint32_t ldt = (uint32_t)(nvt * MM_T);
+    rsrc_t rs;
+    if constexpr (KEEP) rs = make_rsrc(p.t + m0 * ldt + n0, ((rows - 1) * ldt + MM_T) * 4);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -425,6 +437,15 @@ struct LossStats {
               tile.c[x][y][i][j][q] = v;
               mx = fmaxf(mx, v);
             }
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  __builtin_bit_cast(u32x4, tile.c[x][y][i][j]), rs,
+                  row < rows ? (uint32_t)((row * ldt + MmTile<ET>::col(at.wn, at.lg, y, j)) * 4) : OFF_NONE, 0, LOAD_DEFAULT);
+        }
         if constexpr (!PICK) {
           const int32_t yt = m < p.M ? p.column(m) - (int32_t)n0 : -1;
           if (has_column<ET>(at, 0, yt) || has_column<ET>(at, 1, yt)) {
@@ -515,12 +536,12 @@ struct LossStats {
   }
 };
 
-template <int ET, bool PICK>
+template <int ET, bool PICK, bool KEEP>
 __global__ __launch_bounds__(MM_THREADS, 1) void loss_stats_kernel(LossFwdArgs p) {
   MM_SHARED();
   MM_EPI_SHARED();
   p.set_rows();
-  const LossStats<ET, PICK> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, (p.V + MM_T - 1) / MM_T};
+  const LossStats<ET, PICK, KEEP> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, (p.V + MM_T - 1) / MM_T};
   mm_run<ET, false, false>(prob, mm_buf);
 }
 
@@ -869,6 +890,66 @@ __global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p,
   mm_run<ET, false, false>(prob, mm_buf);
 }
 
+// G of a piece from the kept t: the same operations on the same values as the
+// product's epilogue, so the same bits. 2048 columns and R rows a work-group,
+// eight columns a thread; four rows' loads in flight. grad_bias: the column sums
+// of R rows.
+template <int ET, bool DB, int R>
+__global__ __launch_bounds__(256) void loss_kept_kernel(XentBwdArgs p, OnDevice dev, const float *t, int64_t ldt) {
+  if (dev.count != nullptr) p.M = mm_uni(*dev.count);
+  const int64_t chunks = (p.np + 2047) / 2048, g = group_number(), rt = g / chunks;
+  const int64_t m0 = rt * R, c = (g - rt * chunks) * 2048 + 8 * threadIdx.x;
+  if (m0 >= p.M || c >= p.np) return;  // np is a multiple of 256
+  const int rows = (int)(p.M - m0 < R ? p.M - m0 : R);
+  float sum[8] = {};
+  const float *at = t + m0 * ldt + p.v0 + c;
+  uint16_t *out = reinterpret_cast<uint16_t *>(p.G) + m0 * p.ldg + c;
+  for (int r0 = 0; r0 < rows; r0 += 4) {
+    f32x4 v[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[k][h] = __builtin_nontemporal_load(
+            reinterpret_cast<const f32x4 *>(at + (r0 + k < rows ? r0 + k : rows - 1) * ldt + 4 * h));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (r0 + k >= rows) break;
+      RowCoef r = p.rows[m0 + r0 + k];
+      if (r.lse == NEG_INF) r.lse = 0.0f;
+      float g8[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) g8[q] = __fmul_rn(r.a, exp_diff(v[k][q >> 2][q & 3], r.lse));
+      const int64_t y = r.y - p.v0 - c;
+      if (y >= 0 && y < 8)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (y == q) g8[q] = __fsub_rn(g8[q], r.b);
+      if constexpr (DB)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] = __fadd_rn(sum[q], g8[q]);
+      *reinterpret_cast<u32x4 *>(out + (r0 + k) * p.ldg) =
+          u32x4{mm_pack2<ET>(g8[0], g8[1]), mm_pack2<ET>(g8[2], g8[3]), mm_pack2<ET>(g8[4], g8[5]), mm_pack2<ET>(g8[6], g8[7])};
+    }
+  }
+  if constexpr (DB) {
+    const float f = p.scale[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<f32x4 *>(p.colpart + rt * p.ldg + c + 4 * h) =
+          f32x4{__fmul_rn(f, sum[4 * h]), __fmul_rn(f, sum[4 * h + 1]), __fmul_rn(f, sum[4 * h + 2]), __fmul_rn(f, sum[4 * h + 3])};
+  }
+}
+// rows a work-group of it: few where there are few, for the sake of work-groups
+constexpr int KEPT_FEW = 4, KEPT_MANY = 32;
+int kept_rows(int64_t M) { return M <= MM_T ? KEPT_FEW : KEPT_MANY; }
+template <int ET, bool DB>
+hipError_t kept_grad(const XentBwdArgs &p, const OnDevice &dev, const float *t, int64_t ldt, hipStream_t s) {
+  const int R = kept_rows(p.M);
+  return launch_kernel(R == KEPT_FEW ? loss_kept_kernel<ET, DB, KEPT_FEW> : loss_kept_kernel<ET, DB, KEPT_MANY>,
+                       numbered_grid(ceil_div(p.M, R) * ceil_div(p.np, 2048)), dim3(256), s, p, dev, t, ldt);
+}
+
 // G at the teacher's entries of a piece, over what the product's epilogue left
 // there: a q - b p from the entry's t, the dense value's own fp32 operations,
 // rounded once. An id that a row has more than once is written by each of them
@@ -916,16 +997,17 @@ hipError_t zero_words(void *p, int64_t n, hipStream_t s) {
                        static_cast<uint32_t *>(p), n);
 }
 
-// grad_bias of one piece: the row tiles' column sums in ascending order, the
-// entries' share, and 1 / T.
+// grad_bias of one piece: the column sums of the row tiles (of `tile` rows) in
+// ascending order, the entries' share, and 1 / T.
 __global__ __launch_bounds__(256) void loss_bias_kernel(const float *__restrict__ colpart, int64_t M,
-                                                        const int32_t *__restrict__ count, int64_t vp, int64_t n, const long long *__restrict__ entries,
+                                                        const int32_t *__restrict__ count, int tile, int64_t vp, int64_t n, const long long *__restrict__ entries,
                                                         const float *__restrict__ scale, double unit, float T,
                                                         float *__restrict__ db) {
   const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (v >= n) return;
   float s = 0.0f;
-  const int64_t nmt = ((count != nullptr ? *count : M) + MM_T - 1) / MM_T;
+  const int64_t nmt = ((count != nullptr ? *count : M) + tile - 1) / tile;
+#pragma unroll 8
   for (int64_t t = 0; t < nmt; ++t) s = __fadd_rn(s, colpart[t * vp + v]);
   if (entries != nullptr) s = (float)((double)s + (double)entries[v] / unit * (double)scale[1]);
   db[v] = __fdiv_rn(s, T);
@@ -1002,7 +1084,7 @@ struct BackwardLayout {
   int64_t vp, splits, cap;
   int64_t scale, plan, rows, col, dh, G, entries, bytes;
 };
-BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool bias) {
+BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep, bool bias) {
   BackwardLayout b;
   const BwdPlan pl = bwd_plan(M, H, V, bias);
   int64_t at = 0;
@@ -1018,7 +1100,7 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
   b.scale = take(8);
   b.plan = take(sizeof(SplitPlan));
   b.rows = take(16 * M);
-  b.col = take(bias ? 4 * nmt * b.vp : 0);
+  b.col = take(bias ? 4 * (keep ? ceil_div(M, kept_rows(M)) : nmt) * b.vp : 0);
   b.dh = take(4 * H * (M > LR_DIRECT ? b.cap * MM_T : pl.splits * M));
   b.G = take(2 * M * b.vp);
   b.entries = take(bias && K ? 8 * V : 0);
@@ -1052,6 +1134,7 @@ hipError_t set_up(const LossHead &h, const LossMemory &mem, int64_t K, hipStream
   u.a.part = reinterpret_cast<float2 *>(u.ws + u.lay.part);
   u.a.tlogit = reinterpret_cast<float *>(u.ws + u.lay.tlogit);
   u.a.K = K;
+  u.a.t = u.st.t;
   if (h.M == 0 || h.bias == nullptr || h.temperature == 1.0f) return hipSuccess;
   u.a.bias = u.st.bias;
   return launch_kernel(loss_bias_scale_kernel, dim3((unsigned)ceil_div(h.V, 256)), dim3(256), s, h.bias, h.V,
@@ -1069,11 +1152,15 @@ hipError_t gather(const LossHead &h, const Setup &u, const Select &sel, float *z
                       Gather{sel, chunks, static_cast<const uint16_t *>(h.hidden), h.H, u.st, zero0, zero1});
   return e;
 }
-template <bool PICK>
+template <bool PICK, bool KEEP>
 hipError_t stats(const LossHead &h, const LossFwdArgs &a, hipStream_t s) {
   const int64_t tiles = ceil_div(h.M, MM_T) * ceil_div(h.V, MM_T);
-  return launch_kernel(h.in_f16 ? loss_stats_kernel<ET_F16, PICK> : loss_stats_kernel<ET_BF16, PICK>, mm_grid(tiles),
-                       dim3(MM_THREADS), s, a);
+  return launch_kernel(h.in_f16 ? loss_stats_kernel<ET_F16, PICK, KEEP> : loss_stats_kernel<ET_BF16, PICK, KEEP>,
+                       mm_grid(tiles), dim3(MM_THREADS), s, a);
+}
+template <bool PICK>
+hipError_t stats(const LossHead &h, const LossFwdArgs &a, bool keep, hipStream_t s) {
+  return keep ? stats<PICK, true>(h, a, s) : stats<PICK, false>(h, a, s);
 }
 void set_targets(LossFwdArgs &a, const LossTargets &y) {
   a.target = y.target;
@@ -1096,7 +1183,7 @@ dim3 rows_grid(int64_t M) { return dim3((unsigned)ceil_div(M, XC_ROWS)); }
 template <int ET>
 hipError_t backward(const LossBackward &c, hipStream_t s) {
   const LossHead &h = c.head;
-  const BackwardLayout lay = backward_layout(h.M, h.H, h.V, c.K, c.grad_bias != nullptr);
+  const BackwardLayout lay = backward_layout(h.M, h.H, h.V, c.K, c.mem.keep != 0, c.grad_bias != nullptr);
   uint8_t *const ws = static_cast<uint8_t *>(c.mem.workspace);
   const State st = state_at(c.mem.state, state_layout(h.M, h.H, h.V, c.K, c.mem.keep != 0), h.M);
   float *const scale = reinterpret_cast<float *>(ws + lay.scale);
@@ -1143,14 +1230,19 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
     p.first = v0 == 0;
     const int64_t nv = h.V - v0 < lay.vp ? h.V - v0 : lay.vp;
     p.np = ceil_div(nv, MM_T) * MM_T;
-    e = launch_kernel(c.grad_bias != nullptr ? loss_grad_kernel<ET, true> : loss_grad_kernel<ET, false>,
-                      mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
+    if (c.mem.keep)
+      e = c.grad_bias != nullptr ? kept_grad<ET, true>(p, dev, st.t, padded(h.V), s)
+                                 : kept_grad<ET, false>(p, dev, st.t, padded(h.V), s);
+    else
+      e = launch_kernel(c.grad_bias != nullptr ? loss_grad_kernel<ET, true> : loss_grad_kernel<ET, false>,
+                        mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
     if (e == hipSuccess && c.K > 0)
       e = launch_kernel(distill_entries_kernel<ET>, numbered_grid(ceil_div(h.M * c.K, 256)), dim3(256), s,
                         DistillEntries{p, c.K, st.ids, st.inv, st.p, st.tk, entries, unit});
     if (e == hipSuccess && c.grad_bias != nullptr)
       e = launch_kernel(loss_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
-                        static_cast<const float *>(p.colpart), h.M, static_cast<const int32_t *>(st.count), lay.vp, nv,
+                        static_cast<const float *>(p.colpart), h.M, static_cast<const int32_t *>(st.count),
+                        c.mem.keep ? kept_rows(h.M) : (int)MM_T, lay.vp, nv,
                         sums ? reinterpret_cast<const long long *>(entries) + v0 : nullptr, static_cast<const float *>(scale),
                         unit, h.temperature, c.grad_bias + v0);
     // the last piece may have fewer splits with work in them; `cap` tiles is the most there are
@@ -1174,8 +1266,8 @@ int64_t loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
 int64_t loss_forward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool with_state) {
   return forward_layout(M, H, V, K, with_state).bytes;
 }
-int64_t loss_backward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool bias) {
-  return backward_layout(M, H, V, K, bias).bytes;
+int64_t loss_backward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool keep, bool bias) {
+  return backward_layout(M, H, V, K, keep, bias).bytes;
 }
 
 hipError_t launch_distill_forward(const DistillForward &c, hipStream_t s) {
@@ -1196,7 +1288,7 @@ hipError_t launch_distill_forward(const DistillForward &c, hipStream_t s) {
   u.a.sid = u.st.ids;
   u.a.ptr = ptr;
   u.a.tk = u.st.tk;
-  if (e == hipSuccess) e = stats<true>(h, u.a, s);
+  if (e == hipSuccess) e = stats<true>(h, u.a, c.mem.keep != 0, s);
   if (e == hipSuccess)
     e = launch_kernel(distill_rows_kernel, rows_grid(h.M), dim3(XC_ROWS * XC_SLICES), s,
                       DistillRows{rows_args(u), c.K, ent, P, c.loss});
@@ -1210,7 +1302,7 @@ hipError_t launch_policy_forward(const PolicyForward &c, hipStream_t s) {
   set_targets(u.a, c.y);
   Select sel{nullptr, c.y.target, c.y.wide, c.y.ignore, c.head.M, c.head.V, nullptr, 0, 0};
   e = gather(c.head, u, sel, c.loss, c.logp, s);
-  if (e == hipSuccess) e = stats<false>(c.head, u.a, s);
+  if (e == hipSuccess) e = stats<false>(c.head, u.a, c.mem.keep != 0, s);
   TokenRows r = token_rows(u, c.y);
   r.logp = c.logp;
   r.advantage = c.advantage;
@@ -1236,7 +1328,7 @@ hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t s) 
     Select sel{nullptr, c.y.target, c.y.wide, c.y.ignore, c.head.M, c.pairs > 0 ? c.head.V : 0, c.pairs > 0 ? c.starts : nullptr,
                c.starts64, 2 * c.pairs};
     e = gather(c.head, u, sel, nullptr, nullptr, s);
-    if (e == hipSuccess) e = stats<false>(c.head, u.a, s);
+    if (e == hipSuccess) e = stats<false>(c.head, u.a, c.mem.keep != 0, s);
     TokenRows r = token_rows(u, c.y);
     r.logp = rowlogp;
     if (e == hipSuccess)

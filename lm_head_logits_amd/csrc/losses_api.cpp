@@ -40,10 +40,11 @@ lmhead::LossHead head_of(const void *hidden, int64_t M, int64_t H, const void *W
 
 // The memory of a forward pass over M > 0 rows.
 lmhead_status check_forward(const lmhead::LossHead &h, int64_t K, const void *state, size_t state_bytes,
-                            const void *workspace, size_t workspace_bytes) {
+                            int keep_logits, const void *workspace, size_t workspace_bytes) {
   if (h.hidden == nullptr || h.W == nullptr || workspace == nullptr ||
       workspace_bytes < (size_t)lmhead::loss_forward_bytes(h.M, h.H, h.V, K, state != nullptr) ||
-      (state != nullptr && state_bytes < (size_t)lmhead::loss_state_bytes(h.M, h.H, h.V, K, false)))
+      (state != nullptr && state_bytes < (size_t)lmhead::loss_state_bytes(h.M, h.H, h.V, K, keep_logits != 0)) ||
+      (state == nullptr && keep_logits != 0))
     return LMHEAD_ERR_INVALID;
   if (!aligned(h.hidden, 16) || !aligned(h.W, 16) || !aligned(h.bias, 4) || !aligned(state, 256) ||
       !aligned(workspace, 256))
@@ -59,9 +60,9 @@ lmhead_status done(hipError_t e) { return e == hipSuccess ? LMHEAD_OK : LMHEAD_E
 
 extern "C" {
 
-size_t lmhead_loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K) {
+size_t lmhead_loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int keep_logits) {
   if (check_shape(M, H, V) != LMHEAD_OK || M == 0 || !teacher_count_ok(K)) return 0;
-  return (size_t)lmhead::loss_state_bytes(M, H, V, K, false);
+  return (size_t)lmhead::loss_state_bytes(M, H, V, K, keep_logits != 0);
 }
 
 size_t lmhead_loss_forward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int with_state) {
@@ -69,30 +70,31 @@ size_t lmhead_loss_forward_workspace_bytes(int64_t M, int64_t H, int64_t V, int6
   return (size_t)lmhead::loss_forward_bytes(M, H, V, K, with_state != 0);
 }
 
-size_t lmhead_loss_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int grad_bias) {
+size_t lmhead_loss_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int keep_logits,
+                                            int grad_bias) {
   if (check_shape(M, H, V) != LMHEAD_OK || M == 0 || !teacher_count_ok(K)) return 0;
-  return (size_t)lmhead::loss_backward_bytes(M, H, V, K, grad_bias != 0);
+  return (size_t)lmhead::loss_backward_bytes(M, H, V, K, keep_logits != 0, grad_bias != 0);
 }
 
 lmhead_status lmhead_distill_forward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
                                      const float *bias, lmhead_dtype in_dtype, float temperature,
                                      const void *teacher_ids, lmhead_index ids_type, const void *teacher_logits,
                                      lmhead_dtype logits_dtype, int64_t K, const float *teacher_lse, float *loss,
-                                     void *state, size_t state_bytes, void *workspace, size_t workspace_bytes,
+                                     void *state, size_t state_bytes, int keep_logits, void *workspace, size_t workspace_bytes,
                                      void *stream) {
   lmhead_status st = check_head(M, H, V, in_dtype, temperature);
   if (st != LMHEAD_OK) return st;
   if (!known_index(ids_type) || !known_dtype(logits_dtype) || K < 1 || !teacher_count_ok(K)) return LMHEAD_ERR_INVALID;
   if (M == 0) return LMHEAD_OK;
   const lmhead::LossHead h = head_of(hidden, M, H, W, V, alpha, bias, in_dtype, temperature);
-  st = check_forward(h, K, state, state_bytes, workspace, workspace_bytes);
+  st = check_forward(h, K, state, state_bytes, keep_logits, workspace, workspace_bytes);
   if (st == LMHEAD_ERR_INVALID || teacher_ids == nullptr || teacher_logits == nullptr || loss == nullptr)
     return LMHEAD_ERR_INVALID;
   if (st != LMHEAD_OK || !aligned(teacher_ids, index_size(ids_type)) ||
       !aligned(teacher_logits, logits_dtype == LMHEAD_F32 ? 4 : 2) || !aligned(teacher_lse, 4) || !aligned(loss, 4))
     return LMHEAD_ERR_ALIGN;
   return done(lmhead::launch_distill_forward(
-      lmhead::DistillForward{h, lmhead::LossMemory{state, 0, workspace}, teacher_ids, ids_type == LMHEAD_INDEX64 ? 1 : 0, K,
+      lmhead::DistillForward{h, lmhead::LossMemory{state, keep_logits != 0, workspace}, teacher_ids, ids_type == LMHEAD_INDEX64 ? 1 : 0, K,
                              teacher_logits,
                              logits_dtype == LMHEAD_F32    ? lmhead::OUT_F32
                              : logits_dtype == LMHEAD_BF16 ? lmhead::OUT_BF16
@@ -105,7 +107,7 @@ lmhead_status lmhead_policy_forward(const void *hidden, int64_t M, int64_t H, co
                                     const float *bias, lmhead_dtype in_dtype, float temperature, const void *target,
                                     lmhead_index target_type, int64_t ignore_index, const float *advantage,
                                     const float *old_logp, const float *ref_logp, float clip_low, float clip_high,
-                                    float kl_coef, float *loss, float *logp, void *state, size_t state_bytes,
+                                    float kl_coef, float *loss, float *logp, void *state, size_t state_bytes, int keep_logits,
                                     void *workspace, size_t workspace_bytes, void *stream) {
   lmhead_status st = check_head(M, H, V, in_dtype, temperature);
   if (st != LMHEAD_OK) return st;
@@ -113,14 +115,14 @@ lmhead_status lmhead_policy_forward(const void *hidden, int64_t M, int64_t H, co
     return LMHEAD_ERR_INVALID;
   if (M == 0) return LMHEAD_OK;
   const lmhead::LossHead h = head_of(hidden, M, H, W, V, alpha, bias, in_dtype, temperature);
-  st = check_forward(h, 0, state, state_bytes, workspace, workspace_bytes);
+  st = check_forward(h, 0, state, state_bytes, keep_logits, workspace, workspace_bytes);
   if (st == LMHEAD_ERR_INVALID || target == nullptr || advantage == nullptr || loss == nullptr || logp == nullptr)
     return LMHEAD_ERR_INVALID;
   if (st != LMHEAD_OK || !aligned(target, index_size(target_type)) || !aligned(advantage, 4) || !aligned(old_logp, 4) ||
       !aligned(ref_logp, 4) || !aligned(loss, 4) || !aligned(logp, 4))
     return LMHEAD_ERR_ALIGN;
   return done(lmhead::launch_policy_forward(
-      lmhead::PolicyForward{h, lmhead::LossMemory{state, 0, workspace},
+      lmhead::PolicyForward{h, lmhead::LossMemory{state, keep_logits != 0, workspace},
                             lmhead::LossTargets{target, target_type == LMHEAD_INDEX64 ? 1 : 0, ignore_index}, advantage,
                             old_logp, ref_logp, clip_low, clip_high, kl_coef, loss, logp},
       static_cast<hipStream_t>(stream)));
@@ -131,7 +133,7 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
                                         lmhead_index target_type, int64_t ignore_index, const void *starts,
                                         lmhead_index starts_type, int64_t pairs, const float *ref_logp, float beta,
                                         float margin, float label_smoothing, int average, float *loss, float *logp,
-                                        void *state, size_t state_bytes, void *workspace, size_t workspace_bytes,
+                                        void *state, size_t state_bytes, int keep_logits, void *workspace, size_t workspace_bytes,
                                         void *stream) {
   lmhead_status st = check_head(M, H, V, in_dtype, temperature);
   if (st != LMHEAD_OK) return st;
@@ -142,14 +144,14 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
   if (pairs > 0 && (starts == nullptr || loss == nullptr || logp == nullptr)) return LMHEAD_ERR_INVALID;
   if (M > 0) {
     if (target == nullptr) return LMHEAD_ERR_INVALID;
-    st = check_forward(h, 0, state, state_bytes, workspace, workspace_bytes);
+    st = check_forward(h, 0, state, state_bytes, keep_logits, workspace, workspace_bytes);
     if (st != LMHEAD_OK) return st;
   }
   if (!aligned(target, index_size(target_type)) || !aligned(starts, index_size(starts_type)) || !aligned(ref_logp, 4) ||
       !aligned(loss, 4) || !aligned(logp, 4))
     return LMHEAD_ERR_ALIGN;
   return done(lmhead::launch_preference_forward(
-      lmhead::PreferenceForward{h, lmhead::LossMemory{state, 0, workspace},
+      lmhead::PreferenceForward{h, lmhead::LossMemory{state, keep_logits != 0, workspace},
                                 lmhead::LossTargets{target, target_type == LMHEAD_INDEX64 ? 1 : 0, ignore_index}, starts,
                                 starts_type == LMHEAD_INDEX64 ? 1 : 0, pairs, ref_logp, beta, margin, label_smoothing,
                                 average != 0, loss, logp},
@@ -158,7 +160,7 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
 
 lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
                                    const float *bias, lmhead_dtype in_dtype, float temperature, int64_t K,
-                                   const float *grad_loss, const void *state, size_t state_bytes, void *grad_hidden,
+                                   const float *grad_loss, const void *state, size_t state_bytes, int keep_logits, void *grad_hidden,
                                    void *grad_W, float *grad_bias, void *workspace, size_t workspace_bytes,
                                    void *stream) {
   lmhead_status st = check_head(M, H, V, in_dtype, temperature);
@@ -168,8 +170,8 @@ lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, con
   if (M > 0) {
     // grad_loss may be NULL where there is no pair: then no row reads it
     if (hidden == nullptr || W == nullptr || state == nullptr ||
-        state_bytes < lmhead_loss_state_bytes(M, H, V, K) || workspace == nullptr ||
-        workspace_bytes < lmhead_loss_backward_workspace_bytes(M, H, V, K, grad_bias != nullptr))
+        state_bytes < lmhead_loss_state_bytes(M, H, V, K, keep_logits) || workspace == nullptr ||
+        workspace_bytes < lmhead_loss_backward_workspace_bytes(M, H, V, K, keep_logits, grad_bias != nullptr))
       return LMHEAD_ERR_INVALID;
     if (!aligned(hidden, 16) || !aligned(W, 16) || !aligned(bias, 4) || !aligned(grad_loss, 4) || !aligned(state, 256) ||
         !aligned(workspace, 256))
@@ -178,7 +180,7 @@ lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, con
   if (!aligned(grad_hidden, 16) || !aligned(grad_W, 16) || !aligned(grad_bias, 4)) return LMHEAD_ERR_ALIGN;
   return done(lmhead::launch_loss_backward(
       lmhead::LossBackward{head_of(hidden, M, H, W, V, alpha, bias, in_dtype, temperature),
-                           lmhead::LossMemory{const_cast<void *>(state), 0, workspace}, K, grad_loss, grad_hidden, grad_W,
+                           lmhead::LossMemory{const_cast<void *>(state), keep_logits != 0, workspace}, K, grad_loss, grad_hidden, grad_W,
                            grad_bias},
       static_cast<hipStream_t>(stream)));
 }

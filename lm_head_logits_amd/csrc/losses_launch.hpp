@@ -20,7 +20,7 @@ struct LossHead {
 // ... and of memory. state: nullptr when no backward pass follows.
 struct LossMemory {
   void *state;
-  int keep;                // the logits are kept in the state
+  int keep;                // t is kept in the state (there is one)
   void *workspace;
 };
 struct LossTargets {
@@ -70,7 +70,7 @@ struct LossBackward {
 };
 int64_t loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool keep);
 int64_t loss_forward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool with_state);
-int64_t loss_backward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool bias);
+int64_t loss_backward_bytes(int64_t M, int64_t H, int64_t V, int64_t K, bool keep, bool bias);
 hipError_t launch_distill_forward(const DistillForward &c, hipStream_t stream);
 hipError_t launch_policy_forward(const PolicyForward &c, hipStream_t stream);
 hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t stream);

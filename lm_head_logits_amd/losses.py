@@ -1,4 +1,4 @@
-"""Further losses of the head's logits, which are never whole in memory: the
+"""Further losses of the head's logits, which need not be whole in memory: the
 divergence from a teacher's top logits (lmhead_distill_forward), the clipped
 policy loss with a KL term (lmhead_policy_forward) and the logistic loss of
 preferred pairs (lmhead_preference_forward), each with its gradients
@@ -29,28 +29,46 @@ class LossState(NamedTuple):
     temperature: float
     K: int                # the teacher's logits a row; 0 for the losses of targets
     elements: int         # of the loss, and so of its upstream gradient
+    keep_logits: bool     # the logits are in the state
 
 
-def loss_state_bytes(M: int, H: int, V: int, K: int = 0) -> int:
-    return int(_lib.load().lmhead_loss_state_bytes(M, H, V, K))
+# Up to this many bytes of fp32 logits a forward call for training keeps them for
+# the backward pass by default: a quarter of the pass's products saved (4096 rows,
+# H = 4096, V = 128256: 12.6 -> 10.0 ms) for a small share of the card's 288 GB.
+KEEP_BYTES = 16 << 30
+
+
+def loss_state_bytes(M: int, H: int, V: int, K: int = 0, keep_logits: bool = False) -> int:
+    return int(_lib.load().lmhead_loss_state_bytes(M, H, V, K, int(keep_logits)))
 
 
 def loss_forward_workspace_bytes(M: int, H: int, V: int, K: int = 0, train: bool = True) -> int:
     return int(_lib.load().lmhead_loss_forward_workspace_bytes(M, H, V, K, int(train)))
 
 
-def loss_backward_workspace_bytes(M: int, H: int, V: int, K: int = 0, grad_bias: bool = False) -> int:
-    return int(_lib.load().lmhead_loss_backward_workspace_bytes(M, H, V, K, int(grad_bias)))
+def loss_backward_workspace_bytes(M: int, H: int, V: int, K: int = 0, keep_logits: bool = False,
+                                  grad_bias: bool = False) -> int:
+    return int(_lib.load().lmhead_loss_backward_workspace_bytes(M, H, V, K, int(keep_logits), int(grad_bias)))
 
 
-def _memory(M, H, V, K, train, workspace, dev):
-    state = torch.empty(loss_state_bytes(M, H, V, K), dtype=torch.uint8, device=dev) if train else None
-    return state, _workspace(workspace, loss_forward_workspace_bytes(M, H, V, K, train), dev)
+class _Memory:
+    """State and workspace of a forward call."""
 
+    def __init__(self, M, H, V, K, train, keep_logits, workspace, dev):
+        self.keep = train and (4 * M * V <= KEEP_BYTES if keep_logits is None else bool(keep_logits))
+        self.state = (torch.empty(loss_state_bytes(M, H, V, K, self.keep), dtype=torch.uint8, device=dev) if train
+                      else None)
+        self.workspace = _workspace(workspace, loss_forward_workspace_bytes(M, H, V, K, train), dev)
 
-def _memory_args(state, workspace):
-    return (state.data_ptr() if state is not None and state.numel() else None, state.numel() if state is not None else 0,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    def args(self):
+        st, ws = self.state, self.workspace
+        return (st.data_ptr() if st is not None and st.numel() else None, st.numel() if st is not None else 0,
+                int(self.keep), ws.data_ptr(), ws.numel() * ws.element_size())
+
+    def saved(self, hidden, bias, alpha, temperature, K, elements):
+        if self.state is None:
+            return None
+        return LossState(self.state, hidden, bias, float(alpha), float(temperature), K, elements, self.keep)
 
 
 def _optional_f32(t, M, name):
@@ -60,7 +78,8 @@ def _optional_f32(t, M, name):
 
 def distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                     alpha: float = 1.0, bias=None, *, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
-                    train: bool = True, workspace: torch.Tensor | None = None, stream=None):
+                    train: bool = True, keep_logits: bool | None = None, workspace: torch.Tensor | None = None,
+                    stream=None):
     """Divergence of the head's distribution at `temperature` from a teacher's,
     given by its top logits (lmhead_distill_forward): returns (loss fp32 [M],
     saved). teacher_ids [M, K] (int32 or int64) and teacher_logits [M, K]
@@ -70,7 +89,8 @@ def distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: tor
     over the entries, or, with teacher_lse (fp32 [M], the log-sum-exp of its
     logits / temperature over its whole vocabulary), are those of its whole
     distribution. saved is what loss_backward takes (None where train is
-    false)."""
+    false); keep_logits: it holds the logits too, fp32 [M, V], which saves making
+    them again there (None: up to 16 GB of them)."""
     M, H, V, code = _head_args(hidden, weight, bias)
     _need(teacher_ids.dim() == 2 and teacher_ids.shape[0] == M and teacher_ids.shape[1] >= 1,
           "teacher_ids must be [M, K]")
@@ -83,27 +103,28 @@ def distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: tor
     dev = hidden.device
     with _alloc_on(stream):
         loss = torch.empty(M, dtype=torch.float32, device=dev)
-        state, workspace = _memory(M, H, V, K, train, workspace, dev)
-    _same_device(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, workspace)
+        mem = _Memory(M, H, V, K, train, keep_logits, workspace, dev)
+    _same_device(hidden, weight, bias, teacher_ids, teacher_logits, teacher_lse, mem.workspace)
     with _device_ctx(dev):
         st = _lib.load().lmhead_distill_forward(
             hidden.data_ptr(), M, H, weight.data_ptr(), V, float(alpha), _ptr(bias), code, float(temperature),
             teacher_ids.data_ptr(), itype, teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K,
-            _ptr(teacher_lse), loss.data_ptr(), *_memory_args(state, workspace), _stream_handle(dev, stream))
+            _ptr(teacher_lse), loss.data_ptr(), *mem.args(), _stream_handle(dev, stream))
     _check(st, "lmhead_distill_forward")
-    return loss, LossState(state, hidden, bias, float(alpha), float(temperature), K, M) if train else None
+    return loss, mem.saved(hidden, bias, alpha, temperature, K, M)
 
 
 def policy_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, advantage: torch.Tensor,
                    old_logp: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None, alpha: float = 1.0,
                    bias=None, *, temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2,
                    kl_coef: float = 0.0, ignore_index: int = -100, train: bool = True,
-                   workspace: torch.Tensor | None = None, stream=None):
+                   keep_logits: bool | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Clipped policy loss of the tokens target [M] with a KL term
     (lmhead_policy_forward): returns (loss fp32 [M], logp fp32 [M], saved), logp
     being the tokens' log-probabilities. advantage, old_logp (None: logp itself,
     the first step after a rollout) and ref_logp (None: no KL term) are fp32 [M].
-    Rows whose target is ignore_index or no row of weight have loss and logp 0."""
+    Rows whose target is ignore_index or no row of weight have loss and logp 0.
+    saved and keep_logits are distill_forward's."""
     M, H, V, code = _head_args(hidden, weight, bias)
     itype = _index_arg(target, (M,), "target")
     _f32_arg(advantage, M, "advantage")
@@ -113,30 +134,31 @@ def policy_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Ten
     with _alloc_on(stream):
         loss = torch.empty(M, dtype=torch.float32, device=dev)
         logp = torch.empty(M, dtype=torch.float32, device=dev)
-        state, workspace = _memory(M, H, V, 0, train, workspace, dev)
-    _same_device(hidden, weight, bias, target, advantage, old_logp, ref_logp, workspace)
+        mem = _Memory(M, H, V, 0, train, keep_logits, workspace, dev)
+    _same_device(hidden, weight, bias, target, advantage, old_logp, ref_logp, mem.workspace)
     with _device_ctx(dev):
         st = _lib.load().lmhead_policy_forward(
             hidden.data_ptr(), M, H, weight.data_ptr(), V, float(alpha), _ptr(bias), code, float(temperature),
             target.data_ptr(), itype, int(ignore_index), advantage.data_ptr(), _ptr(old_logp), _ptr(ref_logp),
             float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), logp.data_ptr(),
-            *_memory_args(state, workspace), _stream_handle(dev, stream))
+            *mem.args(), _stream_handle(dev, stream))
     _check(st, "lmhead_policy_forward")
-    return loss, logp, LossState(state, hidden, bias, float(alpha), float(temperature), 0, M) if train else None
+    return loss, logp, mem.saved(hidden, bias, alpha, temperature, 0, M)
 
 
 def preference_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, starts: torch.Tensor,
                        ref_logp: torch.Tensor | None = None, alpha: float = 1.0, bias=None, *, beta: float = 0.1,
                        margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False,
                        temperature: float = 1.0, ignore_index: int = -100, train: bool = True,
-                       workspace: torch.Tensor | None = None, stream=None):
+                       keep_logits: bool | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Logistic loss of P preferred pairs of sequences
     (lmhead_preference_forward): returns (loss fp32 [P], logp fp32 [2 P], saved).
     Sequence s is rows starts[s] .. starts[s + 1] - 1 of the batch (starts: int32
     or int64 [2 P + 1], ascending); sequences 0 .. P - 1 are the preferred ones,
     P .. 2 P - 1 the others. logp is the sum (average: the mean) of the log-
     probabilities of a sequence's targets, without those left out; ref_logp
-    (None: zeros), fp32 [2 P], is a reference model's, as this function returns it."""
+    (None: zeros), fp32 [2 P], is a reference model's, as this function returns it.
+    saved and keep_logits are distill_forward's."""
     M, H, V, code = _head_args(hidden, weight, bias)
     itype = _index_arg(target, (M,), "target")
     _need(starts.dim() == 1 and starts.shape[0] % 2 == 1, "starts must be [2 P + 1]")
@@ -149,16 +171,16 @@ def preference_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch
     with _alloc_on(stream):
         loss = torch.empty(P, dtype=torch.float32, device=dev)
         logp = torch.empty(2 * P, dtype=torch.float32, device=dev)
-        state, workspace = _memory(M, H, V, 0, train, workspace, dev)
-    _same_device(hidden, weight, bias, target, starts, ref_logp, workspace)
+        mem = _Memory(M, H, V, 0, train, keep_logits, workspace, dev)
+    _same_device(hidden, weight, bias, target, starts, ref_logp, mem.workspace)
     with _device_ctx(dev):
         st = _lib.load().lmhead_preference_forward(
             hidden.data_ptr(), M, H, weight.data_ptr(), V, float(alpha), _ptr(bias), code, float(temperature),
             target.data_ptr(), itype, int(ignore_index), starts.data_ptr(), stype, P, _ptr(ref_logp), float(beta),
             float(margin), float(label_smoothing), int(average), loss.data_ptr(), logp.data_ptr(),
-            *_memory_args(state, workspace), _stream_handle(dev, stream))
+            *mem.args(), _stream_handle(dev, stream))
     _check(st, "lmhead_preference_forward")
-    return loss, logp, LossState(state, hidden, bias, float(alpha), float(temperature), 0, P) if train else None
+    return loss, logp, mem.saved(hidden, bias, alpha, temperature, 0, P)
 
 
 def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossState, *, need_hidden: bool = True,
@@ -183,12 +205,13 @@ def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossStat
         dh = torch.empty_like(hidden) if need_hidden else None
         dw = torch.empty_like(weight) if need_weight else None
         db = torch.empty_like(bias) if need_bias else None
-        workspace = _workspace(workspace, loss_backward_workspace_bytes(M, H, V, saved.K, need_bias), dev)
+        workspace = _workspace(workspace, loss_backward_workspace_bytes(M, H, V, saved.K, saved.keep_logits, need_bias), dev)
     _same_device(hidden, weight, bias, grad_loss, saved.state, workspace)
     with _device_ctx(dev):
         st = _lib.load().lmhead_loss_backward(
             hidden.data_ptr(), M, H, weight.data_ptr(), V, saved.alpha, _ptr(bias), code, saved.temperature, saved.K,
-            grad_loss.data_ptr(), saved.state.data_ptr(), saved.state.numel(), _ptr(dh), _ptr(dw), _ptr(db),
+            grad_loss.data_ptr(), saved.state.data_ptr(), saved.state.numel(), int(saved.keep_logits), _ptr(dh), _ptr(dw),
+            _ptr(db),
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(dev, stream))
     _check(st, "lmhead_loss_backward")
     return dh, dw, db

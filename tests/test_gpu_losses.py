@@ -115,8 +115,16 @@ def check(c, alpha=0.5, kw=None):
     assert alone[-1] is None
     for a, b in zip(alone, got):
         assert torch.equal(a, b)
+    assert saved.keep_logits
     d = L.loss_backward(c["grad"], c["weight"], saved)
     check_grads(d, grads, c["hidden"].dtype, c["bias"] is not None)
+    # the logits made again instead of kept: the same bits but for grad_bias, whose sums have another order
+    *again, lean = call(c, alpha, kw, keep_logits=False)
+    assert all(torch.equal(a, b) for a, b in zip(again, got)) and not lean.keep_logits
+    e = L.loss_backward(c["grad"], c["weight"], lean)
+    assert torch.equal(d[0], e[0]) and torch.equal(d[1], e[1])
+    if c["bias"] is not None:
+        close("bias", e[2], *grads["bias"])
     return got, d
 
 
@@ -433,17 +441,19 @@ def test_two_streams_at_once(op):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("keep", [0, 1])
+@pytest.mark.parametrize("M", [90, 290])
 @pytest.mark.parametrize("op", OPS)
-def test_nothing_outside_the_outputs_is_written(op):
+def test_nothing_outside_the_outputs_is_written(op, M, keep):
     """Exact sizes of state and workspace, guards around every output."""
-    M, H, V, K, P, pad = 290, 96, 333, 9, 2, 64
+    H, V, K, P, pad = 96, 333, 9, 2, 64
     c = make(op, 59, M, H, V, "bf16", True, K=K, pairs=P)
     reference(c, 0.5, KW[op])
     from lm_head_logits_amd import _lib
     lib, s = _lib.load(), torch.cuda.current_stream().cuda_stream
     K = K if op == "distill" else 0
-    ns, nf, nb = (L.loss_state_bytes(M, H, V, K), L.loss_forward_workspace_bytes(M, H, V, K),
-                  L.loss_backward_workspace_bytes(M, H, V, K, True))
+    ns, nf, nb = (L.loss_state_bytes(M, H, V, K, keep), L.loss_forward_workspace_bytes(M, H, V, K),
+                  L.loss_backward_workspace_bytes(M, H, V, K, keep, True))
     n = dict(loss=P if op == "preference" else M, logp=2 * P if op == "preference" else M)
     buf = {k: torch.full((m + 2 * pad,), 123.0, dtype=d, device=DEV) for k, m, d in
            (("loss", n["loss"], torch.float32), ("logp", n["logp"], torch.float32), ("dh", M * H, torch.bfloat16),
@@ -452,7 +462,7 @@ def test_nothing_outside_the_outputs_is_written(op):
     ws = torch.full((max(nf, nb) + 512,), 77, dtype=torch.uint8, device=DEV)
     at = {k: v.data_ptr() + pad * v.element_size() for k, v in buf.items()}
     head = (c["hidden"].data_ptr(), M, H, c["weight"].data_ptr(), V, 0.5, c["bias"].data_ptr(), _lib.LMHEAD_BF16, 1.25)
-    mem = (state.data_ptr(), ns, ws.data_ptr(), nf, s)
+    mem = (state.data_ptr(), ns, keep, ws.data_ptr(), nf, s)
     if op == "distill":
         st = lib.lmhead_distill_forward(*head, c["teacher_ids"].data_ptr(), 1, c["teacher_logits"].data_ptr(), 0, K, None,
                                         at["loss"], *mem)
@@ -466,7 +476,8 @@ def test_nothing_outside_the_outputs_is_written(op):
     assert st == _lib.OK
     torch.cuda.synchronize()
     assert bool((ws[nf:] == 77).all()) and bool((state[ns:] == 77).all())
-    st = lib.lmhead_loss_backward(*head, K, c["grad"].data_ptr(), state.data_ptr(), ns, at["dh"], at["dw"], at["db"],
+    st = lib.lmhead_loss_backward(*head, K, c["grad"].data_ptr(), state.data_ptr(), ns, keep, at["dh"], at["dw"],
+                                  at["db"],
                                   ws.data_ptr(), nb, s)
     assert st == _lib.OK
     torch.cuda.synchronize()
