@@ -331,6 +331,31 @@ lmhead_status lmhead_xent_backward(const void *hidden, int64_t M, int64_t H, con
  * shape contract or when M == 0. */
 size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int grad_bias);
 
+/* The K largest logits of each row, their columns, and the row's log-sum-exp at a
+ * temperature: what a token is sampled from, and what lmhead_distill_forward takes of a
+ * teacher.
+ *   values[m, k], ids[m, k]  the k-th of row m's logits in descending order, and its
+ *               column; equal logits (zeros of both signs too) by ascending column, NaN
+ *               before all others. values are the logits' own bits.
+ *   lse[m]      log sum_v exp(logits[m, v] / temperature): -inf for a row of only -inf, NaN
+ *               for one with +inf or NaN
+ *   logits      [M, V] of dtype, rows row_stride elements apart (row_stride >= V), any
+ *               alignment of an element                          (device, read)
+ *   values      [M, K] of dtype; ids int32 [M, K]; lse fp32 [M]  (device, written)
+ *   workspace   at least lmhead_logits_topk_workspace_bytes(M, V, K) bytes, 16-byte aligned,
+ *               overwritten; as above (NULL where that is 0)
+ *   1 <= K <= V, K <= LMHEAD_MAX_TOPK; temperature > 0
+ * A row's results depend on that row alone but for lse's last bits, whose order of sums
+ * depends on M, V and K; they do not change from run to run. Returns LMHEAD_OK or an error. */
+#define LMHEAD_MAX_TOPK ((int64_t)1024)
+lmhead_status lmhead_logits_topk(const void *logits, int64_t M, int64_t V, int64_t row_stride, lmhead_dtype dtype, int64_t K,
+                                 float temperature, void *values, int32_t *ids, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* Host-only: bytes of workspace lmhead_logits_topk needs (0 outside the contract, and
+ * where it needs none). */
+size_t lmhead_logits_topk_workspace_bytes(int64_t M, int64_t V, int64_t K);
+
 /* ---------------------------------------------------------------------------
  * Further losses of the head's logits, which need not be whole in memory:
  *   t[m, v] = (alpha * (hidden[m, :] . W[v, :]) + bias[v]) / temperature,

@@ -2,11 +2,12 @@
 
     logits[M, V] = alpha * (hidden[M, H] . W[V, H]^T) + bias[V]
 
-and what trains and serves the same matrix W: softmax cross entropy without
-the logits in memory (cross_entropy, xent_forward, xent_backward), the losses
-of tuning it against a teacher, a reward or preferences (distillation,
-policy_loss, preference_loss), the tied embedding (embedding, embed,
-embed_backward) and the head in 8-bit integers (quantize_int8, logits_int8).
+the largest of them (logits_topk), and what trains and serves the same matrix
+W: softmax cross entropy without the logits in memory (cross_entropy,
+xent_forward, xent_backward), the losses of tuning it against a teacher, a
+reward or preferences (distillation, policy_loss, preference_loss), the tied
+embedding (embedding, embed, embed_backward) and the head in 8-bit integers
+(quantize_int8, logits_int8).
 
 Every step of the projection runs in the library's HIP kernels. This module
 only checks tensor metadata, allocates the output through torch and passes
@@ -25,9 +26,9 @@ from ._binding import (_DTYPES, LmHeadError, NotHandled, _alloc_on, _check, _dev
                        _stream_handle, status_string)
 from ._lib import (LMHEAD_BF16, LMHEAD_F16, LMHEAD_F32, NOT_HANDLED, OK, PATH_AUTO, PATH_NONE, PATH_NVFP4,
                    PATH_SKINNY, PATH_TILED)
-from .losses import (LossState, distill_forward, distillation, loss_backward, loss_backward_workspace_bytes,
-                     loss_forward_workspace_bytes, loss_state_bytes, policy_forward, policy_loss, preference_forward,
-                     preference_loss)
+from .losses import (LossState, distill_forward, distillation, logits_topk, logits_topk_workspace_bytes,
+                     loss_backward, loss_backward_workspace_bytes, loss_forward_workspace_bytes, loss_state_bytes,
+                     policy_forward, policy_loss, preference_forward, preference_loss)
 from .training import (cross_entropy, embed, embed_backward, embed_backward_workspace_bytes, embedding,
                        xent_backward, xent_backward_workspace_bytes, xent_forward,
                        xent_forward_workspace_bytes)
@@ -41,7 +42,7 @@ __all__ = ["logits", "logits_rowreduce", "logits_rowreduce_noalloc", "rowreduce_
            "quantize_int8", "logits_int8",
            "distill_forward", "policy_forward", "preference_forward", "loss_backward", "LossState", "distillation",
            "policy_loss", "preference_loss", "loss_state_bytes", "loss_forward_workspace_bytes",
-           "loss_backward_workspace_bytes"]
+           "loss_backward_workspace_bytes", "logits_topk", "logits_topk_workspace_bytes"]
 
 
 def version() -> str:

@@ -38,6 +38,7 @@ EXPORTS = ("lmhead_logits", "lmhead_logits_path", "lmhead_logits_ex", "lmhead_lo
            "lmhead_xent_forward", "lmhead_xent_forward_workspace_bytes", "lmhead_xent_backward",
            "lmhead_xent_backward_workspace_bytes", "lmhead_embed", "lmhead_embed_backward",
            "lmhead_embed_backward_workspace_bytes", "lmhead_quantize_int8", "lmhead_logits_int8",
+           "lmhead_logits_topk", "lmhead_logits_topk_workspace_bytes",
            "lmhead_distill_forward", "lmhead_policy_forward", "lmhead_preference_forward", "lmhead_loss_backward",
            "lmhead_loss_state_bytes", "lmhead_loss_forward_workspace_bytes", "lmhead_loss_backward_workspace_bytes")
 # include/lmhead_probes.h: measurement probes (not part of the projection),
@@ -113,6 +114,10 @@ def load() -> ctypes.CDLL:
     lib.lmhead_quantize_int8.argtypes = [vp, i64, i64, i32, vp, vp, vp]
     lib.lmhead_logits_int8.restype = i32
     lib.lmhead_logits_int8.argtypes = [vp, vp, i64, i64, vp, vp, i64, f32, vp, i32, vp, vp]
+    lib.lmhead_logits_topk.restype = i32
+    lib.lmhead_logits_topk.argtypes = [vp, i64, i64, i64, i32, i64, f32, vp, vp, vp, vp, sz, vp]
+    lib.lmhead_logits_topk_workspace_bytes.restype = sz
+    lib.lmhead_logits_topk_workspace_bytes.argtypes = [i64, i64, i64]
     head = [vp, i64, i64, vp, i64, f32, vp, i32, f32]  # hidden .. temperature
     memory = [vp, sz, i32, vp, sz, vp]  # state, workspace, stream
     lib.lmhead_distill_forward.restype = i32

@@ -54,11 +54,41 @@ lmhead_status check_forward(const lmhead::LossHead &h, int64_t K, const void *st
 
 bool teacher_count_ok(int64_t K) { return K >= 0 && K <= LMHEAD_MAX_TEACHER; }
 
+lmhead::OutType out_type(int dtype) {
+  return dtype == LMHEAD_F32 ? lmhead::OUT_F32 : dtype == LMHEAD_BF16 ? lmhead::OUT_BF16 : lmhead::OUT_F16;
+}
+
 lmhead_status done(hipError_t e) { return e == hipSuccess ? LMHEAD_OK : LMHEAD_ERR_DEVICE; }
 
 }  // namespace
 
 extern "C" {
+
+size_t lmhead_logits_topk_workspace_bytes(int64_t M, int64_t V, int64_t K) {
+  if (check_shape(M, 32, V) != LMHEAD_OK || M == 0 || K < 1 || K > LMHEAD_MAX_TOPK || K > V) return 0;
+  return (size_t)lmhead::topk_bytes(M, V, K);
+}
+
+lmhead_status lmhead_logits_topk(const void *logits, int64_t M, int64_t V, int64_t row_stride, lmhead_dtype dtype, int64_t K,
+                                 float temperature, void *values, int32_t *ids, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  const lmhead_status st = check_shape(M, 32, V);
+  if (st != LMHEAD_OK) return st;
+  if (!known_dtype(dtype) || K < 1 || K > LMHEAD_MAX_TOPK || K > V || row_stride < V || row_stride > (int64_t)1 << 40 ||
+      !(temperature > 0.0f) || isinf(temperature))
+    return LMHEAD_ERR_INVALID;
+  if (M == 0) return LMHEAD_OK;
+  const size_t need = lmhead_logits_topk_workspace_bytes(M, V, K);
+  if (logits == nullptr || values == nullptr || ids == nullptr || lse == nullptr ||
+      (need > 0 && (workspace == nullptr || workspace_bytes < need)))
+    return LMHEAD_ERR_INVALID;
+  const uintptr_t size = dtype == LMHEAD_F32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(values, size) || !aligned(ids, 4) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return LMHEAD_ERR_ALIGN;
+  return done(lmhead::launch_topk(lmhead::TopkArgs{logits, M, V, row_stride, K, out_type(dtype), temperature, values, ids,
+                                                   lse, workspace},
+                                  static_cast<hipStream_t>(stream)));
+}
 
 size_t lmhead_loss_state_bytes(int64_t M, int64_t H, int64_t V, int64_t K, int keep_logits) {
   if (check_shape(M, H, V) != LMHEAD_OK || M == 0 || !teacher_count_ok(K)) return 0;
@@ -96,10 +126,7 @@ lmhead_status lmhead_distill_forward(const void *hidden, int64_t M, int64_t H, c
   return done(lmhead::launch_distill_forward(
       lmhead::DistillForward{h, lmhead::LossMemory{state, keep_logits != 0, workspace}, teacher_ids, ids_type == LMHEAD_INDEX64 ? 1 : 0, K,
                              teacher_logits,
-                             logits_dtype == LMHEAD_F32    ? lmhead::OUT_F32
-                             : logits_dtype == LMHEAD_BF16 ? lmhead::OUT_BF16
-                                                           : lmhead::OUT_F16,
-                             teacher_lse, loss},
+                             out_type(logits_dtype), teacher_lse, loss},
       static_cast<hipStream_t>(stream)));
 }
 

@@ -2,10 +2,11 @@
 divergence from a teacher's top logits (lmhead_distill_forward), the clipped
 policy loss with a KL term (lmhead_policy_forward) and the logistic loss of
 preferred pairs (lmhead_preference_forward), each with its gradients
-(lmhead_loss_backward).
+(lmhead_loss_backward). And the rows' top logits (lmhead_logits_topk), which a
+teacher hands down and a token is sampled from.
 
-``distill_forward``, ``policy_forward``, ``preference_forward`` and
-``loss_backward`` are the C calls with torch tensors; ``distillation``,
+``logits_topk``, ``distill_forward``, ``policy_forward``, ``preference_forward``
+and ``loss_backward`` are the C calls with torch tensors; ``distillation``,
 ``policy_loss`` and ``preference_loss`` are the same as differentiable
 functions.
 """
@@ -69,6 +70,41 @@ class _Memory:
         if self.state is None:
             return None
         return LossState(self.state, hidden, bias, float(alpha), float(temperature), K, elements, self.keep)
+
+
+def logits_topk_workspace_bytes(M: int, V: int, k: int) -> int:
+    return int(_lib.load().lmhead_logits_topk_workspace_bytes(M, V, k))
+
+
+def logits_topk(logits: torch.Tensor, k: int, temperature: float = 1.0, *, workspace: torch.Tensor | None = None,
+                stream=None):
+    """The k largest logits of each row of logits [M, V] (float32, bfloat16 or
+    float16; rows may be further apart than V, as in a slice of padded columns)
+    in descending order, equal ones by ascending column (lmhead_logits_topk):
+    returns (values [M, k] of the logits' type, ids int32 [M, k], lse fp32 [M]),
+    lse being the log-sum-exp of the whole row of logits / temperature, so that
+    values / temperature - lse are the candidates' log-probabilities."""
+    _need(logits.is_cuda and logits.dtype in _DTYPES and logits.dim() == 2,
+          "logits must be a device tensor [M, V], float32, bfloat16 or float16")
+    M, V = logits.shape
+    _need(V == 1 or logits.stride(1) == 1, "a row's logits must be next to each other")
+    ld = logits.stride(0) if M > 1 else V
+    _need(ld >= V, "rows must not overlap")
+    _need(1 <= k <= V, "k must be 1 .. V")
+    dev = logits.device
+    with _alloc_on(stream):
+        values = torch.empty((M, k), dtype=logits.dtype, device=dev)
+        ids = torch.empty((M, k), dtype=torch.int32, device=dev)
+        lse = torch.empty(M, dtype=torch.float32, device=dev)
+        workspace = _workspace(workspace, logits_topk_workspace_bytes(M, V, k), dev)
+    _same_device(logits, workspace)
+    with _device_ctx(dev):
+        st = _lib.load().lmhead_logits_topk(
+            logits.data_ptr(), M, V, ld, _DTYPES[logits.dtype], k, float(temperature), values.data_ptr(), ids.data_ptr(),
+            lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream_handle(dev, stream))
+    _check(st, "lmhead_logits_topk")
+    return values, ids, lse
 
 
 def _optional_f32(t, M, name):
