@@ -292,6 +292,7 @@ __global__ __launch_bounds__(LR_THREADS) void loss_count_kernel(Select c, int32_
   const int64_t lo = c.starts != nullptr ? c.bound(0) : 0, hi = c.starts != nullptr ? c.bound(c.last) : c.M;
   const int64_t m0 = (int64_t)blockIdx.x * LR_CHUNK;
   int n = 0;
+#pragma unroll 8
   for (int64_t m = m0 + threadIdx.x; m < m0 + LR_CHUNK && m < c.M; m += LR_THREADS) n += c.column(m, lo, hi) >= 0 ? 1 : 0;
   n = block_sum(n, sh);
   if (threadIdx.x == 0) chunks[blockIdx.x] = n;
@@ -315,6 +316,7 @@ __global__ __launch_bounds__(LR_THREADS) void loss_gather_kernel(Gather c) {
   const int64_t lo = s.starts != nullptr ? s.bound(0) : 0, hi = s.starts != nullptr ? s.bound(s.last) : s.M;
   int n = 0;
   for (int64_t k = tid; k < chunk; k += LR_THREADS) n += c.chunks[k];
+#pragma unroll 8
   for (int64_t m = chunk * LR_CHUNK + tid; m < r0; m += LR_THREADS) n += s.column(m, lo, hi) >= 0 ? 1 : 0;
   const int before = block_sum(n, sh);
   if (tid < 64) {  // one wave: the ballot is its own
@@ -492,17 +494,24 @@ struct LossStats {
       // thread (row tid / 16 of a group, entry tid % 16): the entries of the
       // row of each of the eight groups
       const int pr = tid >> 4, pe = tid & 15;
-      uint32_t range[8];
-      uint32_t some = 0;
+      // (every load for all eight groups before the first is used)
+      uint32_t range[8], some = 0;
+      int32_t at_row[8], id[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int64_t m = m0 + 128 * (k >> 2) + 64 * (pr >> 4) + 16 * (k & 3) + (pr & 15);
-        range[k] = 0;
-        if (m < p.M) {
-          const uint16_t *const r = p.ptr + p.row(m) * (nvt + 1) + vt;
-          range[k] = r[0] | (uint32_t)r[1] << 16;
-          if (r[0] < r[1]) some |= 1u << k;
-        }
+        at_row[k] = m < p.M ? (int32_t)p.row(m) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint16_t *const r = p.ptr + (at_row[k] < 0 ? 0 : at_row[k]) * (nvt + 1) + vt;
+        range[k] = at_row[k] < 0 ? 0u : r[0] | (uint32_t)r[1] << 16;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t e = (range[k] & 0xFFFF) + pe, end = range[k] >> 16;
+        id[k] = e < end ? p.sid[at_row[k] * p.K + e] : 0;
+        if ((range[k] & 0xFFFF) < end) some |= 1u << k;
       }
       if (some != 0 && pe == 0) atomicOr(groups, some);
       lds_barrier();
@@ -523,11 +532,12 @@ struct LossStats {
               *reinterpret_cast<f32x4 *>(box + (at.wm * 16 + at.li) * MM_T + 4 * (piece ^ at.li)) = tile.c[x][y][i][j];
             }
           lds_barrier();
-          const int64_t m = m0 + 128 * x + 64 * (pr >> 4) + 16 * i + (pr & 15);
-          for (uint32_t e = (range[k] & 0xFFFF) + pe; e < range[k] >> 16; e += 16) {
-            const int64_t at_e = p.row(m) * p.K + e;
-            const uint32_t c = (uint32_t)(p.sid[at_e] - (int32_t)n0) & (MM_T - 1);
-            p.tk[at_e] = box[pr * MM_T + 4 * ((c >> 2) ^ (pr & 15)) + (c & 3)];
+          int32_t col = id[k];
+          for (uint32_t e = (range[k] & 0xFFFF) + pe; e < range[k] >> 16;) {
+            const uint32_t c = (uint32_t)(col - (int32_t)n0) & (MM_T - 1);
+            p.tk[at_row[k] * p.K + e] = box[pr * MM_T + 4 * ((c >> 2) ^ (pr & 15)) + (c & 3)];
+            e += 16;
+            if (e < range[k] >> 16) col = p.sid[at_row[k] * p.K + e];
           }
           lds_barrier();
         }
@@ -788,28 +798,26 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // rows worked on, by one wave. `cap`: row tiles times splits that the sums have
 // room for.
 struct SplitPlan {
-  int64_t ksplit;
-  int32_t splits;
+  int32_t ksplit, splits;
 };
-__device__ __forceinline__ void plan_splits(int64_t n, int64_t H, int64_t vp, int64_t cap, SplitPlan *out) {
-  const int lane = threadIdx.x;
-  const int64_t nmt = (n + MM_T - 1) / MM_T, tiles = nmt * ((H + MM_T - 1) / MM_T), cus = 256;
-  const int64_t s = lane + 1;
-  const bool ok = s == 1 || (s * 256 <= vp && s * nmt <= cap && tiles * (s - 1) < cus * 4);
+__device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, int32_t cap, SplitPlan *out) {
+  const uint32_t nmt = (n + MM_T - 1) / MM_T, tiles = nmt * ((H + MM_T - 1) / MM_T), cus = 256;
+  const uint32_t s = threadIdx.x + 1;
+  const bool ok = s == 1 || (s * 256 <= (uint32_t)vp && s * nmt <= (uint32_t)cap && tiles * (s - 1) < cus * 4);
   const float use = ok && tiles > 0 ? (float)(tiles * s) / (float)((tiles * s + cus - 1) / cus * cus) : 0.0f;
   float best = 0.0f;
-  int64_t splits = 1;
+  int32_t splits = 1;
+#pragma unroll
   for (int k = 0; k < 64; ++k) {
-    const float u = __shfl(use, k);
-    if (u > best * 1.05f) {
+    const float u = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, use), k));
+    if (u > best * 1.06f) {
       best = u;
       splits = k + 1;
     }
   }
-  if (lane == 0) {
-    const int64_t ksplit = ((vp + splits - 1) / splits + 63) / 64 * 64;
-    out->ksplit = ksplit;
-    out->splits = (int32_t)((vp + ksplit - 1) / ksplit);
+  if (threadIdx.x == 0) {
+    out->ksplit = ((vp + splits - 1) / splits + 63) / 64 * 64;
+    out->splits = (vp + out->ksplit - 1) / out->ksplit;
   }
 }
 
@@ -830,14 +838,11 @@ struct LossCoef {
 };
 __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
   if (p.count != nullptr) p.M = *p.count;
-  if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale) plan_splits(p.M, p.H, p.vp, p.cap, p.plan);
-  auto coef = [&](int64_t m, float &a, float &b) {
-    const float c = p.coef[m];
-    a = b = 0.0f;
-    if (c == 0.0f) return;  // also rows of no sequence: they have no upstream gradient
-    const float g = p.g[p.up[m]];
-    a = __fmul_rn(p.distill ? c : -c, g);
-    b = p.distill ? g : a;
+  if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale) plan_splits((int32_t)p.M, (int32_t)p.H, (int32_t)p.vp, (int32_t)p.cap, p.plan);
+  // c = 0: nothing, whatever g is (rows of no sequence have no upstream gradient)
+  auto coef_of = [&](float c, float g, float &a, float &b) {
+    a = c == 0.0f ? 0.0f : __fmul_rn(p.distill ? c : -c, g);
+    b = p.distill && c != 0.0f ? g : a;
   };
   float f = 1.0f;
   if (p.have_scale) {
@@ -845,12 +850,25 @@ __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
   } else {
     __shared__ float sh[LC_THREADS / 64];
     float mx = 0.0f;
-    for (int64_t m = threadIdx.x; m < p.M; m += LC_THREADS) {
-      float a, b;
-      coef(m, a, b);
-      a = fabsf(a);
-      b = fabsf(b);
-      mx = fmaxf(mx, fmaxf(a < __builtin_inff() ? a : 0.0f, b < __builtin_inff() ? b : 0.0f));
+    for (int64_t m0 = threadIdx.x; m0 < p.M; m0 += 8 * LC_THREADS) {
+      float c[8], g[8];
+      int32_t u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {  // past the last: the last again
+        const int64_t m = m0 + k * LC_THREADS < p.M ? m0 + k * LC_THREADS : p.M - 1;
+        c[k] = p.coef[m];
+        u[k] = p.up[m];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] = c[k] == 0.0f ? 0.0f : p.g[u[k]];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float a, b;
+        coef_of(c[k], g[k], a, b);
+        a = fabsf(a);
+        b = fabsf(b);
+        mx = fmaxf(mx, fmaxf(a < __builtin_inff() ? a : 0.0f, b < __builtin_inff() ? b : 0.0f));
+      }
     }
     for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
@@ -867,7 +885,8 @@ __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
   const int64_t m = (int64_t)blockIdx.x * LC_THREADS + threadIdx.x;
   if (!p.write_rows || m >= p.M) return;
   float a, b;
-  coef(m, a, b);
+  const float c = p.coef[m];
+  coef_of(c, c == 0.0f ? 0.0f : p.g[p.up[m]], a, b);
   p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], p.distill ? -1 : p.y[m]};
 }
 
@@ -1030,6 +1049,28 @@ __global__ __launch_bounds__(MM_THREADS, 1) void loss_dweight_kernel(XentBwdArgs
   mm_run<ET, true, true>(prob, mm_buf);
 }
 
+// Both products of a small piece in one launch, as in xent.hip.
+template <int ET>
+__global__ __launch_bounds__(MM_THREADS, 1) void loss_products_kernel(XentBwdArgs p, OnDevice dev, uint32_t ga) {
+  MM_SHARED();
+  MM_EPI_SHARED();
+  dev.apply(p);
+  const int64_t nht = (p.H + MM_T - 1) / MM_T;
+  if (blockIdx.x < ga) {
+    const XentDHidden<ET> prob{p, (p.M + MM_T - 1) / MM_T, nht, (p.np + p.ksplit - 1) / p.ksplit};
+    mm_run<ET, false, true>(prob, mm_buf, blockIdx.x, ga);
+  } else {
+    const XentDWeight<ET> prob{p, mm_epi, p.np / MM_T, nht};
+    mm_run<ET, true, true>(prob, mm_buf, blockIdx.x - ga, gridDim.x - ga);
+  }
+}
+// At most 64 rows: G^T hidden without the core (xent_core.hpp).
+template <int ET>
+__global__ __launch_bounds__(64 * XO_WAVES, 3) void loss_outer_kernel(XentBwdArgs p, int64_t per_slab) {
+  XO_SHARED();
+  xent_outer<ET>(p, per_slab, xo_g0, xo_g1, xo_stage);
+}
+
 // grad_hidden: the splits' sums in ascending order, scaled, rounded once; 0 in
 // the rows left out.
 struct DHiddenOut {
@@ -1055,20 +1096,24 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
   f32x4 s[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) s[h] = *reinterpret_cast<const f32x4 *>(c.dh + at + 4 * h);
-  for (int k0 = 1; k0 < splits; k0 += 8) {
-    f32x4 v[8][2];  // eight splits' loads in flight (past the last: the last again, not added)
+  auto more = [&](auto nc, int k0) {  // that many splits' loads in flight
+    constexpr int N = decltype(nc)::value;
+    f32x4 v[N][2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[k][h] = *reinterpret_cast<const f32x4 *>(c.dh + (k0 + k) * n + at + 4 * h);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        v[k][h] = *reinterpret_cast<const f32x4 *>(c.dh + (k0 + k < splits ? k0 + k : splits - 1) * n + at + 4 * h);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) s[h][q] = k0 + k < splits ? __fadd_rn(s[h][q], v[k][h][q]) : s[h][q];
-  }
+        for (int q = 0; q < 4; ++q) s[h][q] = __fadd_rn(s[h][q], v[k][h][q]);
+  };
+  int k0 = 1;
+  for (; k0 + 8 <= splits; k0 += 8) more(std::integral_constant<int, 8>{}, k0);
+  for (; k0 + 2 <= splits; k0 += 2) more(std::integral_constant<int, 2>{}, k0);
+  if (k0 < splits) more(std::integral_constant<int, 1>{}, k0);
   const float f = __fmul_rn(c.alpha, c.scale[1]);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -1078,10 +1123,10 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
                                                 mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
 }
 
-// bwd_plan's pieces, with room for the sums of grad_hidden whatever the rows
-// worked on are: splits times row tiles as for all rows.
+// bwd_plan's pieces, with room for the sums of grad_hidden of whatever rows are
+// worked on: `cap` row tiles times splits.
 struct BackwardLayout {
-  int64_t vp, splits, cap;
+  int64_t vp, cap;
   int64_t scale, plan, rows, col, dh, G, entries, bytes;
 };
 BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep, bool bias) {
@@ -1095,13 +1140,15 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
   };
   const int64_t nmt = ceil_div(M, MM_T);
   b.vp = pl.vp;
-  b.splits = pl.splits;
-  b.cap = pl.splits * nmt;
+  // fewer rows than the call's take more splits: with three fifths of 4096 rows
+  // (H = 4096) 160 tiles would leave 96 of 256 CUs without one; three splits of
+  // them fill 94%
+  b.cap = pl.splits > 3 ? pl.splits * nmt : 3 * nmt;
   b.scale = take(8);
   b.plan = take(sizeof(SplitPlan));
   b.rows = take(16 * M);
   b.col = take(bias ? 4 * (keep ? ceil_div(M, kept_rows(M)) : nmt) * b.vp : 0);
-  b.dh = take(4 * H * (M > LR_DIRECT ? b.cap * MM_T : pl.splits * M));
+  b.dh = take(4 * H * b.cap * (M > LR_DIRECT ? MM_T : M));  // not packed: one row tile
   b.G = take(2 * M * b.vp);
   b.entries = take(bias && K ? 8 * V : 0);
   b.bytes = at;
@@ -1245,12 +1292,23 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
                         c.mem.keep ? kept_rows(h.M) : (int)MM_T, lay.vp, nv,
                         sums ? reinterpret_cast<const long long *>(entries) + v0 : nullptr, static_cast<const float *>(scale),
                         unit, h.temperature, c.grad_bias + v0);
-    // the last piece may have fewer splits with work in them; `cap` tiles is the most there are
-    const int64_t ta = nht * (st.count != nullptr ? lay.cap : lay.splits);
+    const int64_t ta = nht * lay.cap, tb = nht * (p.np / MM_T);  // ta: the most there are
+    if (e == hipSuccess && c.grad_hidden != nullptr && c.grad_W != nullptr && ta + tb <= device_cus()) {
+      e = launch_kernel(loss_products_kernel<ET>, dim3((unsigned)(ta + tb)), dim3(MM_THREADS), s, p, dev, (uint32_t)ta);
+      continue;
+    }
     if (e == hipSuccess && c.grad_hidden != nullptr)
       e = launch_kernel(loss_dhidden_kernel<ET>, mm_grid(ta), dim3(MM_THREADS), s, p, dev);
-    if (e == hipSuccess && c.grad_W != nullptr)
-      e = launch_kernel(loss_dweight_kernel<ET>, mm_grid(nht * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
+    if (e == hipSuccess && c.grad_W != nullptr) {
+      if (h.M <= XO_ROWS) {
+        // three work-groups per CU, spread over the slabs of hidden's columns
+        const int64_t slots = ceil_div(3 * (int64_t)device_cus(), nht), n = ceil_div(nv, 128);
+        const int64_t per_slab = n < slots ? n : slots;
+        e = launch_kernel(loss_outer_kernel<ET>, dim3((unsigned)(nht * per_slab)), dim3(64 * XO_WAVES), s, p, per_slab);
+      } else {
+        e = launch_kernel(loss_dweight_kernel<ET>, mm_grid(tb), dim3(MM_THREADS), s, p, dev);
+      }
+    }
   }
   if (e == hipSuccess && c.grad_hidden != nullptr)
     e = launch_kernel(loss_dhidden_out_kernel<ET>, numbered_grid(ceil_div(h.M * h.H, 2048)), dim3(256), s,

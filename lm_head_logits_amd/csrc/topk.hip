@@ -8,15 +8,15 @@
 //
 // A work-group each row. The K-th largest of the first stretch's group maxima
 // (a group: some of one thread's logits) is a bound that at least K logits
-// reach, and only logits that reach it become keys in LDS: of logits in no order,
+// reach; only logits that reach it become keys in LDS: of logits in no order,
 // with G of them a group and n groups, about K / (n G) of the row. The first
-// stretch is read once more for its keys (from the caches), the rest once. The
-// keys are sorted (bitonic, in LDS) when there are many or they do not fit, and
-// at the end; the K largest are kept, the bound rises to the last of them. The
-// sum of exponentials is carried along per thread.
+// stretch is read once more for its keys (from the caches), the rest once. When
+// there are many keys, or they do not fit, and at the end, the K largest are
+// sorted out and the bound rises to the last of them. The sum of exponentials is
+// carried along per thread. Logits of -inf never become keys that way; where
+// fewer than K others are there, the first of them fill up.
 //
-// Few rows are cut into segments, whose sorted lists a second kernel merges two
-// and two: the larger of a[i] and b[K - 1 - i] are the K largest of both.
+// Few rows are cut into segments, whose sorted lists a second kernel merges.
 #include "group_launch.hpp"
 #include "losses_launch.hpp"
 #include "mma256.hpp"
@@ -25,8 +25,13 @@ namespace lmhead {
 
 namespace {
 
-constexpr int TK_THREADS = 256, TK_CAP = 4096, TK_FIRST = 8, TK_TILE = 4, TK_SOFT = 512;
+constexpr int TK_THREADS = 256;
+constexpr int TK_CAP = 4096;   // keys in LDS
+constexpr int TK_TILE = 4;     // 16-byte pieces a thread in flight
+constexpr int TK_FIRST = 8;    // ... in the first stretch
+constexpr int TK_COUNT = 512;  // keys up to which places are counted, not sorted
 constexpr float TK_NEG_INF = -__builtin_inff();
+constexpr float TK_LOWEST = -__FLT_MAX__;
 
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);  // -0 to 0
@@ -39,16 +44,32 @@ __device__ __forceinline__ float of_order(uint32_t o) {
 // The elements of a 16-byte piece.
 template <typename T>
 struct Piece {
-  static constexpr int N = 16 / sizeof(T);
+  static constexpr int N = 16 / sizeof(T), PER_WORD = 4 / sizeof(T);
+  static constexpr uint32_t NEG_INF = sizeof(T) == 4 ? 0xFF800000u : std::is_same_v<T, _Float16> ? 0xFC00u : 0xFF80u;
   static __device__ __forceinline__ float at(const u32x4 &v, int i) {
     // (a bit cast of a vector's element itself would take the first one)
-    const uint32_t word = v[i / (N / 4)];
+    const uint32_t word = v[i / PER_WORD];
     if constexpr (sizeof(T) == 4)
       return __builtin_bit_cast(float, word);
     else if constexpr (std::is_same_v<T, _Float16>)
-      return (float)__builtin_bit_cast(f16x2, word)[i & 1];
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? word >> 16 : word));
     else
       return __builtin_bit_cast(float, i & 1 ? word & 0xFFFF0000u : word << 16);
+  }
+  // -inf in the places of a piece that begins at element `first` of `V` that are not there
+  static __device__ __forceinline__ u32x4 cut(const u32x4 &v, int first, int V) {
+    u32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t word = v[j];
+#pragma unroll
+      for (int h = 0; h < PER_WORD; ++h) {
+        const uint32_t mask = sizeof(T) == 4 ? 0xFFFFFFFFu : 0xFFFFu << (16 * h), inf = NEG_INF << (16 * h);
+        word = (uint32_t)(first + j * PER_WORD + h) < (uint32_t)V ? word : (word & ~mask) | inf;
+      }
+      r[j] = word;
+    }
+    return r;
   }
 };
 
@@ -74,6 +95,33 @@ __device__ __forceinline__ void sort_keys(uint64_t *key, int n) {
       else sched_fence();
     }
 }
+// The K largest of n keys (at most TK_COUNT) to their places: keys are distinct
+// (but for those of nothing, 0), and a key's place is the number of larger ones.
+// For that few a third of a sort's steps: each of those is a round trip to LDS.
+__device__ __forceinline__ void count_places(uint64_t *key, int n, int K) {
+  constexpr int Q = TK_COUNT / TK_THREADS;
+  const int tid = threadIdx.x;
+  __syncthreads();
+  uint64_t mine[Q];
+  int place[Q] = {};
+#pragma unroll
+  for (int q = 0; q < Q; ++q) mine[q] = q * TK_THREADS + tid < n ? key[q * TK_THREADS + tid] : 0;
+  if (n <= TK_THREADS) {
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) place[0] += key[i] > mine[0] ? 1 : 0;
+  } else {
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const uint64_t other = key[i];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) place[q] += other > mine[q] ? 1 : 0;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (mine[q] != 0 && place[q] < K) key[place[q]] = mine[q];
+}
 __device__ __forceinline__ int power_of_two(int n, int least) {
   while (least < n) least <<= 1;
   return least;
@@ -82,14 +130,14 @@ __device__ __forceinline__ int power_of_two(int n, int least) {
 struct TopkPart {
   const uint8_t *logits;
   int64_t M, V, row_bytes;
-  int K, lists_K;      // lists_K: K as a power of two
+  int K;
   int segments;
   float c;             // log2(e) / temperature
   float temperature;
   void *values;        // [M, K], segments == 1
   int32_t *ids;
   float *lse;
-  uint64_t *lists;     // [M, segments, lists_K]
+  uint64_t *lists;     // [M, segments, K]
   float2 *sums;        // [M, segments] {largest, sum of exp((x - largest) / temperature)}
 };
 
@@ -119,6 +167,7 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
   constexpr int N = Piece<T>::N;
   __shared__ uint64_t key[TK_CAP];
   __shared__ int count;
+  __shared__ uint32_t kth;  // the group maximum of that place
   __shared__ float2 wave_sums[TK_THREADS / 64];
   const int64_t g = group_number(), row = g / p.segments;
   if (row >= p.M) return;
@@ -129,234 +178,299 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
   const u32x4 *const base = reinterpret_cast<const u32x4 *>(start - off);
   const int V = (int)p.V, pieces = (V + shift + N - 1) / N;
   const int per = (pieces + p.segments - 1) / p.segments;
-  const int lo = seg * per, hi = lo + per < pieces ? lo + per : pieces;
+  const int lo = seg * per < pieces ? seg * per : pieces, hi = lo + per < pieces ? lo + per : pieces;
 
-  float top = TK_NEG_INF, sum = 0.0f;  // this thread's largest logit, and its sum
-  uint64_t bound = 0;                  // keys above it are wanted
-  float bound_x = TK_NEG_INF;          // no logit below it has one
+  float ref = TK_NEG_INF, sum = 0.0f;  // this thread's sum of exp((x - ref) / temperature)
+  float bound = TK_LOWEST;             // no logit below it is wanted; never -inf
+  int sorted = 0;                      // the keys up to there are; behind them {column, logit}
 
-  // a piece's logits; EDGE: what lies outside the row or the segment is -inf,
-  // which adds nothing
-  auto unpack = [&](auto edge, const u32x4 &v, int i, float (&x)[N]) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      x[e] = Piece<T>::at(v, e);
-      if constexpr (decltype(edge)::value) x[e] = (uint32_t)(i * N - shift + e) < (uint32_t)V && i < hi ? x[e] : TK_NEG_INF;
-    }
-  };
-  // Tiles of TK_TILE pieces a thread from piece `from` to `to`, the next in flight.
+  // Tiles of TK_TILE pieces a thread from piece `from` to `to`, the next in
+  // flight; -inf where there is nothing, which adds nothing and is not wanted.
   auto tiles = [&](int from, int to, auto &&f) {
     u32x4 w[TK_TILE], next[TK_TILE];
     auto load = [&](int i0) {
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k) {
         const int i = i0 + k * TK_THREADS + tid;
-        next[k] = i < to ? base[i] : u32x4{0, 0, 0, 0};
+        next[k] = base[i < to ? i : from];
       }
     };
-    load(from);
+    if (from < to) load(from);
 #pragma unroll 1
     for (int i0 = from; i0 < to; i0 += TK_TILE * TK_THREADS) {
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k) w[k] = next[k];
-      load(i0 + TK_TILE * TK_THREADS);
+      if (i0 + TK_TILE * TK_THREADS < to) load(i0 + TK_TILE * TK_THREADS);
       // nearly every tile lies whole inside the row
-      if (i0 * N >= shift && (i0 + TK_TILE * TK_THREADS) * N - shift <= V && i0 + TK_TILE * TK_THREADS <= hi)
-        f(std::false_type{}, w, i0 + tid);
-      else
-        f(std::true_type{}, w, i0 + tid);
+      if (i0 * N < shift || (i0 + TK_TILE * TK_THREADS) * N - shift > V || i0 + TK_TILE * TK_THREADS > to)
+#pragma unroll
+        for (int k = 0; k < TK_TILE; ++k) {
+          const int i = i0 + k * TK_THREADS + tid;
+          w[k] = Piece<T>::cut(w[k], i < to ? i * N - shift : V, V);
+        }
+      f(w, i0 + tid);
     }
   };
-  // adds a tile to the thread's sum, with its maxima by piece
-  auto add = [&](auto edge, const u32x4 (&w)[TK_TILE], int i, float (&most)[TK_TILE]) {
-    float x[TK_TILE][N], m = TK_NEG_INF;
-#pragma unroll
-    for (int k = 0; k < TK_TILE; ++k) {
-      unpack(edge, w[k], i + k * TK_THREADS, x[k]);
-      most[k] = x[k][0];
-#pragma unroll
-      for (int e = 1; e < N; ++e) most[k] = fmaxf(most[k], x[k][e]);
-      m = fmaxf(m, most[k]);
+  auto raise = [&](float x) {
+    if (x > ref) {
+      sum = sum == 0.0f ? 0.0f : __fmul_rn(sum, __builtin_amdgcn_exp2f(__fmul_rn(p.c, __fsub_rn(ref, x))));
+      ref = x;
     }
-    if (m > top) {
-      sum = sum == 0.0f ? 0.0f : __fmul_rn(sum, __builtin_amdgcn_exp2f(__fmul_rn(p.c, __fsub_rn(top, m))));
-      top = m;
-    }
-    const float ref = top == TK_NEG_INF ? 0.0f : top;
+  };
+  // {column, logit} of the logits of P pieces that reach the bound. A wave
+  // counts its own and reserves their places at once; the writes need no answer.
+  auto take = [&](auto pc, const u32x4 *w, int i) {
+    constexpr int P = decltype(pc)::value;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+#pragma unroll
+      for (int e = 0; e < N; ++e) n += __popcll(__ballot(!(Piece<T>::at(w[k], e) < bound)));
+    if (n == 0) return;
+    int at = 0;
+    if ((tid & 63) == 0) at = atomicAdd(&count, n);
+    at = __builtin_amdgcn_readfirstlane(at);
+    float most = TK_NEG_INF;
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float x = Piece<T>::at(w[k], e);
+        const uint64_t all = __ballot(!(x < bound));
+        if (all == 0) continue;
+        if (!(x < bound)) {
+          most = fmaxf(most, x);
+          const int place = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+          if (place < TK_CAP) key[place] = (uint64_t)__builtin_bit_cast(uint32_t, x) << 32 | (uint32_t)((i + k * TK_THREADS) * N - shift + e);
+        }
+        at += __popcll(all);
+      }
+    raise(most);
+  };
+  // adds a tile to the thread's sum: none of its logits is above ref
+  auto add = [&](const u32x4 (&w)[TK_TILE]) {
+    const float r = ref == TK_NEG_INF ? 0.0f : ref;
 #pragma unroll
     for (int k = 0; k < TK_TILE; ++k)
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        sum = __fadd_rn(sum, __builtin_amdgcn_exp2f(__fmul_rn(p.c, __fsub_rn(x[k][e], ref))));
+        sum = __fadd_rn(sum, __builtin_amdgcn_exp2f(__fmul_rn(p.c, __fsub_rn(Piece<T>::at(w[k], e), r))));
   };
-  // the keys of a piece that are above the bound
-  auto take = [&](auto edge, const u32x4 &v, int i) {
-    float x[N];
-    unpack(edge, v, i, x);
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (!(x[e] < bound_x)) {
-        const uint32_t col = (uint32_t)(i * N - shift + e);
-        const uint64_t k = (uint64_t)order_of(x[e]) << 32 | (uint32_t)~col;
-        if (k > bound && (!decltype(edge)::value || (col < (uint32_t)V && i < hi))) {
-          const int at = atomicAdd(&count, 1);
-          if (at < TK_CAP) key[at] = k;
-        }
-      }
-  };
-  // the K largest of the keys so far; all threads
-  auto compact = [&]() {
-    __syncthreads();
-    const int c = count, n = power_of_two(c, 128);
-    for (int i = c + tid; i < n; i += TK_THREADS) key[i] = 0;
-    sort_keys(key, n);
-    if (c >= K) {
-      bound = key[K - 1];
-      bound_x = of_order((uint32_t)(bound >> 32));
+  // The first n keys, of which K at most stay, sorted; all threads, after a
+  // barrier. What comes later has larger columns, so a logit equal to the last
+  // of K is not wanted any more.
+  auto compact = [&](int n) {
+    for (int i = sorted + tid; i < n; i += TK_THREADS) {
+      const uint64_t raw = key[i];
+      key[i] = (uint64_t)order_of(__builtin_bit_cast(float, (uint32_t)(raw >> 32))) << 32 | ~(uint32_t)raw;
     }
+    if (n <= TK_COUNT) {
+      count_places(key, n, K);
+    } else {
+      const int all = power_of_two(n, 128);
+      for (int i = n + tid; i < all; i += TK_THREADS) key[i] = 0;
+      sort_keys(key, all);
+    }
+    sorted = n < K ? n : K;
+    if (tid == 0) count = sorted;
     __syncthreads();
-    if (tid == 0) count = c < K ? c : K;
-    __syncthreads();
-  };
-  // a tile's keys: all at once, or, where they do not fit, piece by piece
-  auto take_tile = [&](auto edge, const u32x4 (&w)[TK_TILE], int i) {
-    const int before = count;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < TK_TILE; ++k) take(edge, w[k], i + k * TK_THREADS);
-    __syncthreads();
-    if (count > TK_CAP) {
-      __syncthreads();
-      if (tid == 0) count = before;
-      __syncthreads();
-#pragma unroll 1
-      for (int k = 0; k < TK_TILE; ++k) {
-        if (count > TK_CAP - TK_THREADS * N) compact();
-        __syncthreads();
-        take(edge, k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3], i + k * TK_THREADS);
-        __syncthreads();
-      }
-    } else if (count > TK_SOFT && count > 4 * K) {
-      compact();
+    if (n >= K) {
+      const uint32_t last = (uint32_t)(key[K - 1] >> 32), infinite = order_of(__builtin_inff());
+      bound = fmaxf(last < infinite ? of_order(last + 1) : __builtin_inff(), TK_LOWEST);
+      raise(bound);
     }
   };
 
-  if (tid == 0) count = 0;
-  // the first stretch's sum, and the bound from its groups' maxima
+  if (tid == 0) {
+    count = 0;
+    kth = 0;
+  }
+  // the bound from the first stretch's group maxima: of a thread's every piece,
+  // half of them, or each
   const int mid = lo + TK_FIRST * TK_THREADS < hi ? lo + TK_FIRST * TK_THREADS : hi;
-  const int group = K <= TK_THREADS / 4 ? TK_FIRST : K <= TK_THREADS ? TK_FIRST / 4 : 1;  // pieces of one thread
-  for (int k = tid; k < TK_FIRST / group * TK_THREADS; k += TK_THREADS) key[k] = 0;
+  const int group = K <= TK_THREADS / 4 ? TK_FIRST : K <= TK_THREADS ? TK_FIRST / 2 : 1, groups = TK_FIRST / group * TK_THREADS;
   {
     float gm = TK_NEG_INF;
     int done = 0;
-    tiles(lo, mid, [&](auto edge, const u32x4 (&w)[TK_TILE], int i) {
-      float most[TK_TILE];
-      add(edge, w, i, most);
+    for (int k = tid; k < groups; k += TK_THREADS) key[k] = 0;
+    // a maximum's last bits make it one of its own; without them it is a bound as well
+    auto put_group = [&](int q) {
+      const uint32_t o = order_of(gm);
+      key[q] = group == 1 ? (uint64_t)o << 32 : (o & ~511u) | (uint32_t)(511 - q);
+      gm = TK_NEG_INF;
+    };
+    tiles(lo, mid, [&](const u32x4 (&w)[TK_TILE], int) {
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k) {
-        gm = fmaxf(gm, most[k]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) gm = fmaxf(gm, Piece<T>::at(w[k], e));
         ++done;
-        // a group of no logits is one of -inf: any logit reaches that
-        if (done % group == 0) {
-          key[(done / group - 1) * TK_THREADS + tid] = (uint64_t)order_of(gm) << 32;
-          gm = TK_NEG_INF;
-        }
+        if (done % group == 0) put_group((done / group - 1) * TK_THREADS + tid);
       }
     });
-    if (done % group != 0) key[done / group * TK_THREADS + tid] = (uint64_t)order_of(gm) << 32;
+    if (done % group != 0) put_group(done / group * TK_THREADS + tid);
   }
-  sort_keys(key, TK_FIRST / group * TK_THREADS);
-  if (key[K - 1] != 0) {
-    bound = key[K - 1] - 1;
-    bound_x = of_order((uint32_t)(key[K - 1] >> 32));
+  if (group > 1) {
+    __syncthreads();
+    uint32_t mine[2];
+    int place[2] = {};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) mine[q] = q * TK_THREADS + tid < groups ? (uint32_t)key[q * TK_THREADS + tid] : 0;
+#pragma unroll 8
+    for (int i = 0; i < groups; ++i) {
+      const uint32_t other = (uint32_t)key[i];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) place[q] += other > mine[q] ? 1 : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (mine[q] != 0 && place[q] == K - 1) kth = mine[q] & ~511u;
+  } else {
+    sort_keys(key, groups);
+    if (tid == 0) kth = (uint32_t)(key[K - 1] >> 32);
   }
   __syncthreads();
-  tiles(lo, mid, take_tile);
-  tiles(mid, hi, [&](auto edge, const u32x4 (&w)[TK_TILE], int i) {
-    float most[TK_TILE];
-    add(edge, w, i, most);
-    take_tile(edge, w, i);
+  // (a group of no logits is one of -inf: any other reaches that)
+  if (kth != 0) bound = fmaxf(of_order(kth), TK_LOWEST);
+  raise(bound);
+  __syncthreads();
+  tiles(lo, hi, [&](const u32x4 (&w)[TK_TILE], int i) {
+    const int before = count;
+    __syncthreads();
+    constexpr int P = 16 / N;  // the ballots of 16 logits at a time stay in scalar registers
+#pragma unroll
+    for (int k = 0; k < TK_TILE; k += P) take(std::integral_constant<int, P>{}, w + k, i + k * TK_THREADS);
+    __syncthreads();
+    int n = count;
+    if (n > 2 * K + 64) {
+      // sorted out; where the tile's keys did not fit, piece by piece
+      const bool fits = n <= TK_CAP;
+      if (!fits) n = before;
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+        __syncthreads();
+        compact(n);
+        if (fits || k == TK_TILE) break;
+        const u32x4 one = k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3];
+        take(std::integral_constant<int, 1>{}, &one, i + k * TK_THREADS);
+        __syncthreads();
+        n = count;
+      }
+    }
+    add(w);
+    __syncthreads();
   });
-  compact();
+  {
+    int n = count;
+    __syncthreads();
+    compact(n);
+    n = count;
+    // the first logits of -inf, where there are not enough others
+    for (int64_t c0 = (int64_t)lo * N - shift; n < K && c0 < (int64_t)hi * N - shift; c0 += TK_THREADS) {
+      const int64_t col = c0 + tid;
+      const bool mine = col >= 0 && col < V && col < (int64_t)hi * N - shift &&
+                        (float)reinterpret_cast<const T *>(start)[col] == TK_NEG_INF;
+      const uint64_t all = __ballot(mine);
+      if ((tid & 63) == 0) reinterpret_cast<int *>(wave_sums)[tid >> 6] = __popcll(all);
+      __syncthreads();
+      int at = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+#pragma unroll
+      for (int w = 0; w < TK_THREADS / 64; ++w) {
+        const int c = reinterpret_cast<int *>(wave_sums)[w];
+        if (w < (tid >> 6)) at += c;
+        n += c;
+      }
+      if (mine && at < K) key[at] = (uint64_t)order_of(TK_NEG_INF) << 32 | ~(uint32_t)col;
+      __syncthreads();
+    }
+    if (tid == 0) count = n < K ? n : K;
+    __syncthreads();
+  }
 
   // the sums: lanes by exchanges, then the waves
 #pragma unroll
-  for (int d = 32; d; d >>= 1) fold_sum(top, sum, __shfl_xor(top, d), __shfl_xor(sum, d), p.c);
-  if ((tid & 63) == 0) wave_sums[tid >> 6] = float2{top, sum};
+  for (int d = 32; d; d >>= 1) fold_sum(ref, sum, __shfl_xor(ref, d), __shfl_xor(sum, d), p.c);
+  if ((tid & 63) == 0) wave_sums[tid >> 6] = float2{ref, sum};
   __syncthreads();
   if (tid == 0)
 #pragma unroll
-    for (int k = 1; k < TK_THREADS / 64; ++k) fold_sum(top, sum, wave_sums[k].x, wave_sums[k].y, p.c);
+    for (int k = 1; k < TK_THREADS / 64; ++k) fold_sum(ref, sum, wave_sums[k].x, wave_sums[k].y, p.c);
   if (p.segments == 1) {
     for (int k = tid; k < K; k += TK_THREADS) put<T>(p, row, k, key[k]);
-    if (tid == 0) p.lse[row] = lse_of(top, sum, p.temperature);
+    if (tid == 0) p.lse[row] = lse_of(ref, sum, p.temperature);
   } else {
-    for (int k = tid; k < p.lists_K; k += TK_THREADS) p.lists[g * p.lists_K + k] = k < count ? key[k] : 0;
-    if (tid == 0) p.sums[g] = float2{top, sum};
+    for (int k = tid; k < K; k += TK_THREADS) p.lists[g * K + k] = k < count ? key[k] : 0;
+    if (tid == 0) p.sums[g] = float2{ref, sum};
   }
 }
 
-// Merges a row's lists.
+// Merges a row's lists. With S lists, the smallest of their q-th largest keys,
+// q = ceil(K / S), is a bound that K keys reach; those that do, about 2 K, are
+// sorted out.
 template <typename T>
 __global__ __launch_bounds__(TK_THREADS) void topk_merge_kernel(TopkPart p) {
-  __shared__ uint64_t key[TK_CAP];
+  __shared__ uint64_t out[TK_CAP];
+  __shared__ uint64_t bound;
+  __shared__ int count;
   const int64_t row = group_number();
   if (row >= p.M) return;
-  const int tid = threadIdx.x, L = p.lists_K;
-  int lists = power_of_two(p.segments, 2);
-  for (int i = tid; i < lists * L; i += TK_THREADS)
-    key[i] = i < p.segments * L ? p.lists[row * p.segments * L + i] : 0;
-  __syncthreads();
-  for (; lists > 1; lists >>= 1) {
-    // list l of the next round from lists l and l + lists / 2
-    const int n = lists / 2 * L;
-    for (int i = tid; i < n; i += TK_THREADS) {
-      const uint64_t a = key[i], b = key[n + (i | (L - 1)) - (i & (L - 1))];
-      if (a < b) key[i] = b;
+  const int tid = threadIdx.x, K = p.K, S = p.segments, all = S * K;
+  const uint64_t *const in = p.lists + row * all;
+  if (tid < 64) {  // at most 64 segments
+    uint64_t least = tid < S ? in[tid * K + (K + S - 1) / S - 1] : ~0ull;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      const uint64_t other = __shfl_xor(least, d);
+      least = other < least ? other : least;
     }
-    __syncthreads();
-    for (int j = L >> 1; j; j >>= 1) {
-      for (int q = tid; q < n / 2; q += TK_THREADS) {
-        const int i = ((q & ~(j - 1)) << 1) | (q & (j - 1));
-        const uint64_t a = key[i], b = key[i | j];
-        if (a < b) {
-          key[i] = b;
-          key[i | j] = a;
-        }
-      }
-      __syncthreads();
+    if (tid == 0) {
+      bound = least;
+      count = 0;
     }
   }
-  for (int k = tid; k < p.K; k += TK_THREADS) put<T>(p, row, k, key[k]);
-  if (tid == 0) {
-    float m = TK_NEG_INF, s = 0.0f;
-    for (int k = 0; k < p.segments; ++k) {
-      const float2 e = p.sums[row * p.segments + k];
-      fold_sum(m, s, e.x, e.y, p.c);
-    }
-    p.lse[row] = lse_of(m, s, p.temperature);
+  __syncthreads();
+  const uint64_t least = bound;
+  for (int i = tid; i < all; i += TK_THREADS) {
+    const uint64_t k = in[i];
+    if (k >= least && k != 0) out[atomicAdd(&count, 1)] = k;  // keys are distinct: their order does not matter
+  }
+  __syncthreads();
+  const int n = count;
+  if (n <= TK_COUNT) {
+    count_places(out, n, K);
+  } else {
+    const int pow2 = power_of_two(n, 128);
+    for (int i = n + tid; i < pow2; i += TK_THREADS) out[i] = 0;
+    sort_keys(out, pow2);
+  }
+  __syncthreads();
+  for (int k = tid; k < K; k += TK_THREADS) put<T>(p, row, k, out[k]);
+  if (tid < 64) {  // at most 64 segments
+    const float2 e = tid < p.segments ? p.sums[row * p.segments + tid] : float2{TK_NEG_INF, 0.0f};
+    float m = e.x, s = e.y;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) fold_sum(m, s, __shfl_xor(m, d), __shfl_xor(s, d), p.c);
+    if (tid == 0) p.lse[row] = lse_of(m, s, p.temperature);
   }
 }
 
 // Segments of a row: enough for four work-groups a CU, of at least two pieces
-// a thread (a segment costs a sort however short it is), and no more lists than
-// the merge holds.
+// a thread (a segment has a bound to find however short it is), and no more
+// than the merge holds.
 struct TopkPlan {
-  int segments, lists_K;
+  int segments;
   int64_t lists, sums, bytes;
 };
 TopkPlan topk_plan(int64_t M, int64_t V, int64_t K, int size) {
   TopkPlan p;
-  p.lists_K = 1;
-  while (p.lists_K < K) p.lists_K *= 2;
   int64_t s = M > 0 ? 1024 / M : 1;
-  const int64_t most = V * size / 16 / (2 * TK_THREADS), fit = TK_CAP / p.lists_K;
+  const int64_t most = V * size / 16 / (2 * TK_THREADS);
   if (s > most) s = most;
-  if (s > fit) s = fit;
+  if (s > TK_CAP / K) s = TK_CAP / K;
   if (s > 64) s = 64;
   p.segments = (int)(s > 1 ? s : 1);
   p.lists = 0;
-  p.sums = p.segments > 1 ? 8 * M * p.segments * p.lists_K : 0;
+  p.sums = p.segments > 1 ? 8 * M * p.segments * K : 0;
   p.bytes = p.sums + (p.segments > 1 ? 8 * M * p.segments : 0);
   return p;
 }
@@ -365,8 +479,8 @@ template <typename T>
 hipError_t topk(const TopkArgs &c, hipStream_t s) {
   const TopkPlan pl = topk_plan(c.M, c.V, c.K, sizeof(T));
   uint8_t *const ws = static_cast<uint8_t *>(c.workspace);
-  const TopkPart p{static_cast<const uint8_t *>(c.logits), c.M, c.V, c.ld * (int64_t)sizeof(T), (int)c.K, pl.lists_K,
-                   pl.segments, (float)(1.4426950408889634 / (double)c.temperature), c.temperature, c.values, c.ids, c.lse,
+  const TopkPart p{static_cast<const uint8_t *>(c.logits), c.M, c.V, c.ld * (int64_t)sizeof(T), (int)c.K, pl.segments,
+                   (float)(1.4426950408889634 / (double)c.temperature), c.temperature, c.values, c.ids, c.lse,
                    reinterpret_cast<uint64_t *>(ws + pl.lists), reinterpret_cast<float2 *>(ws + pl.sums)};
   hipError_t e = launch_kernel(topk_part_kernel<T>, numbered_grid(c.M * pl.segments), dim3(TK_THREADS), s, p);
   if (e == hipSuccess && pl.segments > 1)
@@ -376,8 +490,11 @@ hipError_t topk(const TopkArgs &c, hipStream_t s) {
 
 }  // namespace
 
-// Whatever the logits' type: fp32 rows are cut into the most segments.
-int64_t topk_bytes(int64_t M, int64_t V, int64_t K) { return topk_plan(M, V, K, 4).bytes; }
+// Whatever the logits' type.
+int64_t topk_bytes(int64_t M, int64_t V, int64_t K) {
+  const int64_t a = topk_plan(M, V, K, 4).bytes, b = topk_plan(M, V, K, 2).bytes;
+  return a > b ? a : b;
+}
 
 hipError_t launch_topk(const TopkArgs &c, hipStream_t s) {
   return c.logits_type == OUT_F32    ? topk<float>(c, s)
