@@ -11,9 +11,8 @@
 // reach; only logits that reach it become keys in LDS: of logits in no order,
 // with G of them a group and n groups, about K / (n G) of the row. The first
 // stretch is read once more for its keys (from the caches), the rest once. When
-// there are many keys, or they do not fit, and at the end, the K largest are
-// sorted out and the bound rises to the last of them. The sum of exponentials is
-// carried along per thread. Logits of -inf never become keys that way; where
+// there are many keys, or they do not fit, the K largest are kept and the bound
+// rises to the last of them. The sum of exponentials is carried along per thread. Logits of -inf never become keys that way; where
 // fewer than K others are there, the first of them fill up.
 //
 // Few rows are cut into segments, whose sorted lists a second kernel merges.
@@ -122,6 +121,20 @@ __device__ __forceinline__ void count_places(uint64_t *key, int n, int K) {
   for (int q = 0; q < Q; ++q)
     if (mine[q] != 0 && place[q] < K) key[place[q]] = mine[q];
 }
+// The largest v that at least K of the wave's 64 R values reach (0 when there
+// are not as many but of 0), bit by bit.
+template <int R>
+__device__ __forceinline__ uint32_t kth_value(const uint32_t (&x)[R], int K) {
+  uint32_t v = 0;
+#pragma unroll 1
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) n += __popcll(__ballot(x[r] >= (v | bit)));
+    if (n >= K) v |= bit;
+  }
+  return v;
+}
 __device__ __forceinline__ int power_of_two(int n, int least) {
   while (least < n) least <<= 1;
   return least;
@@ -182,7 +195,7 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
 
   float ref = TK_NEG_INF, sum = 0.0f;  // this thread's sum of exp((x - ref) / temperature)
   float bound = TK_LOWEST;             // no logit below it is wanted; never -inf
-  int sorted = 0;                      // the keys up to there are; behind them {column, logit}
+  int keys = 0;                        // entries that are keys; behind them {column, logit}
 
   // Tiles of TK_TILE pieces a thread from piece `from` to `to`, the next in
   // flight; -inf where there is nothing, which adds nothing and is not wanted.
@@ -218,64 +231,111 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
     }
   };
   // {column, logit} of the logits of P pieces that reach the bound. A wave
-  // counts its own and reserves their places at once; the writes need no answer.
+  // counts its own and reserves their places at once (none where they do not
+  // fit: then the tile is taken again); the writes need no answer. The ballots
+  // are kept as scalar numbers, or each test of one would cost vector operations.
   auto take = [&](auto pc, const u32x4 *w, int i) {
     constexpr int P = decltype(pc)::value;
+    uint64_t set[P * N];
     int n = 0;
 #pragma unroll
-    for (int k = 0; k < P; ++k)
-#pragma unroll
-      for (int e = 0; e < N; ++e) n += __popcll(__ballot(!(Piece<T>::at(w[k], e) < bound)));
+    for (int k = 0; k < P * N; ++k) {
+      set[k] = __ballot(!(Piece<T>::at(w[k / N], k % N) < bound));
+      asm("" : "+s"(set[k]));
+      n += __popcll(set[k]);
+    }
     if (n == 0) return;
     int at = 0;
     if ((tid & 63) == 0) at = atomicAdd(&count, n);
     at = __builtin_amdgcn_readfirstlane(at);
+    if (at + n > TK_CAP) return;
     float most = TK_NEG_INF;
 #pragma unroll
-    for (int k = 0; k < P; ++k)
+    for (int k4 = 0; k4 < P * N; k4 += 4) {
+      if ((set[k4] | set[k4 + 1] | set[k4 + 2] | set[k4 + 3]) == 0) continue;
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float x = Piece<T>::at(w[k], e);
-        const uint64_t all = __ballot(!(x < bound));
-        if (all == 0) continue;
-        if (!(x < bound)) {
-          most = fmaxf(most, x);
-          const int place = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
-          if (place < TK_CAP) key[place] = (uint64_t)__builtin_bit_cast(uint32_t, x) << 32 | (uint32_t)((i + k * TK_THREADS) * N - shift + e);
+      for (int k = k4; k < k4 + 4; ++k)
+        if (set[k] != 0) {
+          const float x = Piece<T>::at(w[k / N], k % N);
+          const int place = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(set[k] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)set[k], 0));
+          if (__builtin_amdgcn_inverse_ballot_w64(set[k])) {
+            key[place] = (uint64_t)__builtin_bit_cast(uint32_t, x) << 32 | (uint32_t)((i + k / N * TK_THREADS) * N - shift + k % N);
+            most = x > most ? x : most;
+          }
+          at += __popcll(set[k]);
         }
-        at += __popcll(all);
-      }
+    }
     raise(most);
   };
   // adds a tile to the thread's sum: none of its logits is above ref
   auto add = [&](const u32x4 (&w)[TK_TILE]) {
-    const float r = ref == TK_NEG_INF ? 0.0f : ref;
+    if (fabsf(ref) < 1e30f) {
+      const float rc = -__fmul_rn(ref, p.c);
 #pragma unroll
-    for (int k = 0; k < TK_TILE; ++k)
+      for (int k = 0; k < TK_TILE; ++k)
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        sum = __fadd_rn(sum, __builtin_amdgcn_exp2f(__fmul_rn(p.c, __fsub_rn(Piece<T>::at(w[k], e), r))));
+        for (int e = 0; e < N; ++e)
+          sum = __fadd_rn(sum, __builtin_amdgcn_exp2f(__fmaf_rn(Piece<T>::at(w[k], e), p.c, rc)));
+    } else {  // its product with c may not be finite: the difference first
+#pragma unroll
+      for (int k = 0; k < TK_TILE; ++k)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          sum = __fadd_rn(sum, __builtin_amdgcn_exp2f(__fmul_rn(p.c, __fsub_rn(Piece<T>::at(w[k], e), ref))));
+    }
   };
-  // The first n keys, of which K at most stay, sorted; all threads, after a
-  // barrier. What comes later has larger columns, so a logit equal to the last
-  // of K is not wanted any more.
-  auto compact = [&](int n) {
-    for (int i = sorted + tid; i < n; i += TK_THREADS) {
+  // Of the first n keys those that are among the K largest logits (with all that
+  // equal the last of them); all threads, after a barrier. What comes later has
+  // larger columns, so a logit equal to the last is not wanted any more.
+  auto prune = [&](int n) {
+    constexpr int Q = TK_COUNT / TK_THREADS;
+    for (int i = keys + tid; i < n; i += TK_THREADS) {
       const uint64_t raw = key[i];
       key[i] = (uint64_t)order_of(__builtin_bit_cast(float, (uint32_t)(raw >> 32))) << 32 | ~(uint32_t)raw;
     }
-    if (n <= TK_COUNT) {
-      count_places(key, n, K);
-    } else {
+    keys = n;
+    if (n > TK_COUNT) {
       const int all = power_of_two(n, 128);
       for (int i = n + tid; i < all; i += TK_THREADS) key[i] = 0;
       sort_keys(key, all);
+      keys = n < K ? n : K;
+      if (tid == 0) {
+        count = keys;
+        kth = (uint32_t)(key[K - 1] >> 32);
+      }
+    } else if (n >= K) {
+      __syncthreads();
+      uint64_t mine[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) mine[q] = q * TK_THREADS + tid < n ? key[q * TK_THREADS + tid] : 0;
+      if (tid < 64) {
+        uint32_t x[TK_COUNT / 64];
+#pragma unroll
+        for (int r = 0; r < TK_COUNT / 64; ++r) x[r] = r * 64 + tid < n ? (uint32_t)(key[r * 64 + tid] >> 32) : 0;
+        const uint32_t v = kth_value(x, K);
+        if (tid == 0) {
+          kth = v;
+          count = 0;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const uint64_t all = __ballot(mine[q] != 0 && (uint32_t)(mine[q] >> 32) >= kth);
+        if (all == 0) continue;
+        int at = 0;
+        if ((tid & 63) == 0) at = atomicAdd(&count, __popcll(all));
+        at = __builtin_amdgcn_readfirstlane(at) + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+        if (all >> (tid & 63) & 1) key[at] = mine[q];
+      }
+      __syncthreads();
+      keys = count;
+    } else if (tid == 0) {
+      count = n;  // not what a tile that did not fit has made of it
     }
-    sorted = n < K ? n : K;
-    if (tid == 0) count = sorted;
     __syncthreads();
     if (n >= K) {
-      const uint32_t last = (uint32_t)(key[K - 1] >> 32), infinite = order_of(__builtin_inff());
+      const uint32_t last = kth, infinite = order_of(__builtin_inff());
       bound = fmaxf(last < infinite ? of_order(last + 1) : __builtin_inff(), TK_LOWEST);
       raise(bound);
     }
@@ -285,86 +345,83 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
     count = 0;
     kth = 0;
   }
-  // the bound from the first stretch's group maxima: of a thread's every piece,
-  // half of them, or each
+  // the bound from the first stretch's group maxima: of all of a thread's
+  // pieces, half of them, or each
   const int mid = lo + TK_FIRST * TK_THREADS < hi ? lo + TK_FIRST * TK_THREADS : hi;
-  const int group = K <= TK_THREADS / 4 ? TK_FIRST : K <= TK_THREADS ? TK_FIRST / 2 : 1, groups = TK_FIRST / group * TK_THREADS;
+  const int group = K <= TK_THREADS / 4 ? TK_FIRST : K <= TK_THREADS ? TK_FIRST / 2 : 1;
+  uint32_t *const most = reinterpret_cast<uint32_t *>(key);  // [TK_FIRST / group][TK_THREADS]
   {
     float gm = TK_NEG_INF;
     int done = 0;
-    for (int k = tid; k < groups; k += TK_THREADS) key[k] = 0;
-    // a maximum's last bits make it one of its own; without them it is a bound as well
-    auto put_group = [&](int q) {
-      const uint32_t o = order_of(gm);
-      key[q] = group == 1 ? (uint64_t)o << 32 : (o & ~511u) | (uint32_t)(511 - q);
-      gm = TK_NEG_INF;
-    };
+#pragma unroll
+    for (int k = 0; k < TK_FIRST; ++k) most[k * TK_THREADS + tid] = 0;
     tiles(lo, mid, [&](const u32x4 (&w)[TK_TILE], int) {
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k) {
 #pragma unroll
         for (int e = 0; e < N; ++e) gm = fmaxf(gm, Piece<T>::at(w[k], e));
         ++done;
-        if (done % group == 0) put_group((done / group - 1) * TK_THREADS + tid);
+        if (done % group == 0) {
+          most[(done / group - 1) * TK_THREADS + tid] = order_of(gm);
+          gm = TK_NEG_INF;
+        }
       }
     });
-    if (done % group != 0) put_group(done / group * TK_THREADS + tid);
+    if (done % group != 0) most[done / group * TK_THREADS + tid] = order_of(gm);
   }
-  if (group > 1) {
-    __syncthreads();
-    uint32_t mine[2];
-    int place[2] = {};
+  __syncthreads();
+  if (tid < 64) {
+    constexpr int R = TK_THREADS / 64;
+    auto find = [&](auto rc) {
+      uint32_t x[decltype(rc)::value];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) mine[q] = q * TK_THREADS + tid < groups ? (uint32_t)key[q * TK_THREADS + tid] : 0;
-#pragma unroll 8
-    for (int i = 0; i < groups; ++i) {
-      const uint32_t other = (uint32_t)key[i];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) place[q] += other > mine[q] ? 1 : 0;
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      if (mine[q] != 0 && place[q] == K - 1) kth = mine[q] & ~511u;
-  } else {
-    sort_keys(key, groups);
-    if (tid == 0) kth = (uint32_t)(key[K - 1] >> 32);
+      for (int r = 0; r < decltype(rc)::value; ++r) x[r] = most[r * 64 + tid];
+      return kth_value(x, K);
+    };
+    const uint32_t v = group == TK_FIRST ? find(std::integral_constant<int, R>{})
+                       : group > 1       ? find(std::integral_constant<int, 2 * R>{})
+                                         : find(std::integral_constant<int, TK_FIRST * R>{});
+    if (tid == 0) kth = v;
   }
   __syncthreads();
   // (a group of no logits is one of -inf: any other reaches that)
   if (kth != 0) bound = fmaxf(of_order(kth), TK_LOWEST);
   raise(bound);
   __syncthreads();
+  int total = 0;  // entries so far
   tiles(lo, hi, [&](const u32x4 (&w)[TK_TILE], int i) {
-    const int before = count;
-    __syncthreads();
     constexpr int P = 16 / N;  // the ballots of 16 logits at a time stay in scalar registers
 #pragma unroll
     for (int k = 0; k < TK_TILE; k += P) take(std::integral_constant<int, P>{}, w + k, i + k * TK_THREADS);
     __syncthreads();
     int n = count;
-    if (n > 2 * K + 64) {
-      // sorted out; where the tile's keys did not fit, piece by piece
+    const int before = total;
+    if (n > keys + K + 64) {
+      // pruned; where the tile's keys did not fit, piece by piece
       const bool fits = n <= TK_CAP;
       if (!fits) n = before;
 #pragma unroll 1
       for (int k = 0;; ++k) {
         __syncthreads();
-        compact(n);
+        prune(n);
         if (fits || k == TK_TILE) break;
         const u32x4 one = k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3];
         take(std::integral_constant<int, 1>{}, &one, i + k * TK_THREADS);
         __syncthreads();
         n = count;
       }
+      n = keys;
     }
+    total = n;
     add(w);
     __syncthreads();
   });
   {
-    int n = count;
+    prune(total);
+    int n = keys;
+    if (n <= TK_COUNT) count_places(key, n, K);  // more are sorted already, and K
     __syncthreads();
-    compact(n);
-    n = count;
+    if (n > K) n = K;
     // the first logits of -inf, where there are not enough others
     for (int64_t c0 = (int64_t)lo * N - shift; n < K && c0 < (int64_t)hi * N - shift; c0 += TK_THREADS) {
       const int64_t col = c0 + tid;
