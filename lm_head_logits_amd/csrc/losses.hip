@@ -44,7 +44,7 @@ constexpr int64_t LR_DIRECT = MM_T;
 
 // What the forward pass leaves for the backward pass, in one buffer.
 struct StateLayout {
-  int64_t count, rows, inv, hidden, y, lse, coef, up, bias, ids, p, tk, t, bytes;
+  int64_t count, rows, inv, hidden, y, lse, coef, own, up, bias, ids, p, tk, t, bytes;
 };
 int64_t padded(int64_t V) { return ceil_div(V, MM_T) * MM_T; }
 StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) {
@@ -63,6 +63,7 @@ StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
   s.y = take(4 * M);
   s.lse = take(4 * M);
   s.coef = take(4 * M);
+  s.own = take(K ? 0 : 4 * M);
   s.up = take(4 * M);
   s.bias = take(4 * V);
   s.ids = take(4 * M * K);
@@ -81,6 +82,7 @@ struct State {
   int32_t *y;      // [n] target column or -1
   float *lse;      // [n]
   float *coef;     // [n] d loss / d logp; distill: P
+  float *own;      // [n] coef (1 - q) of the target: d loss / d its t; targets only
   int32_t *up;     // [n] which element of the upstream gradient is the row's
   float *bias;     // [V] bias / T, where T != 1
   int32_t *ids;    // [M, K] the teacher's tokens in ascending order, NO_ID behind the last
@@ -93,7 +95,8 @@ State state_at(void *base, const StateLayout &l, int64_t M) {
   auto ints = [&](int64_t at) { return packed ? reinterpret_cast<int32_t *>(b + at) : nullptr; };
   return State{ints(l.count), ints(l.rows), ints(l.inv), packed ? reinterpret_cast<uint16_t *>(b + l.hidden) : nullptr,
                reinterpret_cast<int32_t *>(b + l.y),    reinterpret_cast<float *>(b + l.lse),
-               reinterpret_cast<float *>(b + l.coef),   reinterpret_cast<int32_t *>(b + l.up),
+               reinterpret_cast<float *>(b + l.coef),   reinterpret_cast<float *>(b + l.own),
+               reinterpret_cast<int32_t *>(b + l.up),
                reinterpret_cast<float *>(b + l.bias),   reinterpret_cast<int32_t *>(b + l.ids),
                reinterpret_cast<float *>(b + l.p),      reinterpret_cast<float *>(b + l.tk),
                reinterpret_cast<float *>(b + l.t)};
@@ -644,6 +647,11 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(Disti
   c.loss[row] = c.P[row] == 0.0f ? 0.0f : __fsub_rn(c.ent[row], sum);
 }
 
+// coef (1 - q) of a target with that log q
+__device__ __forceinline__ float own_share(float coef, float logp) {
+  return coef == 0.0f ? 0.0f : __fmul_rn(coef, -expm1f(logp));
+}
+
 struct TokenRows {
   RowsArgs r;
   int64_t V;
@@ -700,6 +708,7 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void token_rows_kernel(TokenRo
     c.r.st.up[m] = 0;  // preference_pairs_kernel knows the rows' pairs
   }
   c.r.st.coef[m] = coef;
+  c.r.st.own[m] = own_share(coef, logp);
 }
 
 // One pair of sequences, one work-group: their sums in 64 bits in a fixed
@@ -716,7 +725,7 @@ struct Pairs {
   const float *rowlogp, *ref;
   float beta, margin, smoothing;
   int average;
-  float *loss, *logp, *coef;
+  float *loss, *logp, *coef, *own;
   int32_t *up;
   const int32_t *inv;  // State
 };
@@ -780,6 +789,7 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
         const int64_t at = c.inv != nullptr ? c.inv[m] : m;
         if (at < 0) continue;  // bounds that do not ascend
         c.coef[at] = der[w];
+        c.own[at] = own_share(der[w], c.rowlogp[m]);
         c.up[at] = (int32_t)pair;
       }
   }
@@ -789,10 +799,17 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // Backward
 // ---------------------------------------------------------------------------
 
-// The rows' coefficients of G, scaled as in xent.hip: by f = top / the largest
-// finite one. Target losses: a = b = -g c. Distill: a = g P, b = g (the factor of
-// the entries), no target. Every work-group finds the maximum by itself up to
+// The rows' coefficients of G, scaled as in xent.hip: by f, at most top / the
+// largest finite one. Target losses: a = b = -g c. Distill: a = g P, b = g (the
+// factor of the entries), no target. Every work-group finds the scale by itself up to
 // LC_ONE rows; with more, one work-group finds it in a launch of its own.
+//
+// Which f: a row's gradients hang on a few entries of G, its target's or its
+// teacher's largest, and on how those happen to round. Of LC_TRIES factors over
+// an octave that with the smallest error of such
+// entries is taken, over the first LC_SAMPLES of them: with rounded G the error of
+// the gradients is 1.41 times that of their own rounding, and with few rows
+// anything up to 1.6; so it is 1.2 to 1.35 up to some hundred rows.
 // The splits of G W's K (the piece's columns) that fill the last round of
 // work-groups best, at least 256 columns each; chosen as bwd_plan does, from the
 // rows worked on, by one wave. `cap`: row tiles times splits that the sums have
@@ -823,6 +840,8 @@ __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, in
 
 constexpr int LC_THREADS = 256;
 constexpr int64_t LC_ONE = 32768;
+constexpr float LC_STEP = 0.95760328f;  // 2^(-1 / 16)
+constexpr int LC_TRIES = 16, LC_SAMPLES = 4 * LC_THREADS;
 struct LossCoef {
   const float *g;
   int64_t M;
@@ -835,7 +854,12 @@ struct LossCoef {
   int have_scale, write_rows;
   SplitPlan *plan;
   int64_t H, vp, cap;
+  const float *own;               // targets
+  const float *p, *tk;            // teacher's entries
+  const int32_t *inv, *sid;
+  int64_t K, all_rows;            // all_rows: the call's rows
 };
+template <int ET>
 __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
   if (p.count != nullptr) p.M = *p.count;
   if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale) plan_splits((int32_t)p.M, (int32_t)p.H, (int32_t)p.vp, (int32_t)p.cap, p.plan);
@@ -876,7 +900,65 @@ __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
 #pragma unroll
     for (int w = 0; w < LC_THREADS / 64; ++w) mx = fmaxf(mx, sh[w]);
     // f and 1 / f both well inside the normal range, else no scale
-    if (mx > 1e-30f && mx < 1e30f) f = __fdiv_rn(p.top, mx);
+    if (mx > 1e-30f && mx < 1e30f) {
+      f = __fdiv_rn(p.top, mx);
+      __shared__ float err[LC_TRIES][LC_THREADS + 1];
+      float e2[LC_TRIES] = {};
+      auto sample = [&](float g) {  // an entry of G, unscaled
+        float x = __fmul_rn(g, f);
+        if (!(fabsf(x) <= 2.0f * p.top)) x = 0.0f;
+        float back = 1.0f;  // 1 / the factor tried
+#pragma unroll
+        for (int j = 0; j < LC_TRIES; ++j) {
+          const uint32_t r = mm_pack2<ET>(x, 0.0f);
+          float d;
+          if constexpr (ET == ET_F16)
+            d = (float)__builtin_bit_cast(_Float16, (uint16_t)r);
+          else
+            d = __builtin_bit_cast(float, r << 16);
+          d = __fmul_rn(__fsub_rn(d, x), back);
+          e2[j] = __fmaf_rn(d, d, e2[j]);
+          x = __fmul_rn(x, LC_STEP);
+          back = __fmul_rn(back, 1.0f / LC_STEP);
+        }
+      };
+      if (!p.distill) {
+        for (int64_t m = threadIdx.x; m < p.M && m < LC_SAMPLES; m += LC_THREADS) {
+          const float o = p.own[m];
+          sample(o == 0.0f ? 0.0f : __fmul_rn(o, p.g[p.up[m]]));
+        }
+      } else {
+        for (int64_t e = threadIdx.x; e < p.all_rows * p.K && e < LC_SAMPLES; e += LC_THREADS) {
+          const int64_t row = e / p.K, m = p.inv != nullptr ? p.inv[row] : row;
+          if (m < 0 || p.sid[e] == NO_ID || p.coef[m] == 0.0f) continue;
+          sample(__fmul_rn(p.g[row], __fsub_rn(__fmul_rn(p.coef[m], exp_diff(p.tk[e], p.lse[m])), p.p[e])));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < LC_TRIES; ++j) err[j][threadIdx.x] = e2[j];
+      __syncthreads();
+      {
+        const int j = threadIdx.x / 16, part = threadIdx.x % 16;
+        float s = 0.0f;
+        #pragma unroll
+        for (int k = 0; k < LC_THREADS; k += 16) s = __fadd_rn(s, err[j][k + part]);
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) s = __fadd_rn(s, __shfl_xor(s, d));
+        __syncthreads();
+        if (part == 0) err[0][j] = s;
+      }
+      __syncthreads();
+      float least = err[0][0], factor = 1.0f, best = 1.0f;
+#pragma unroll
+      for (int j = 1; j < LC_TRIES; ++j) {
+        factor = __fmul_rn(factor, LC_STEP);
+        if (err[0][j] < least) {
+          least = err[0][j];
+          best = factor;
+        }
+      }
+      f = __fmul_rn(f, best);
+    }
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       p.scale[0] = f;
       p.scale[1] = __fdiv_rn(1.0f, f);
@@ -1238,15 +1320,15 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + lay.rows);
   const float top = ET == ET_F16 ? 16384.0f : 1.0f;
   LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, st.count, c.K > 0, top, scale, rows, 0, 1,
-             plan, h.H, lay.vp, lay.cap};
+             plan, h.H, lay.vp, lay.cap, st.own, st.p, st.tk, st.inv, st.ids, c.K, h.M};
   hipError_t e = hipSuccess;
   if (h.M > LC_ONE) {
     r.write_rows = 0;
-    e = launch_kernel(loss_coef_kernel, dim3(1), dim3(LC_THREADS), s, r);
+    e = launch_kernel(loss_coef_kernel<ET>, dim3(1), dim3(LC_THREADS), s, r);
     r.write_rows = r.have_scale = 1;
   }
   if (e == hipSuccess)
-    e = launch_kernel(loss_coef_kernel, dim3((unsigned)ceil_div(h.M, LC_THREADS)), dim3(LC_THREADS), s, r);
+    e = launch_kernel(loss_coef_kernel<ET>, dim3((unsigned)ceil_div(h.M, LC_THREADS)), dim3(LC_THREADS), s, r);
   XentBwdArgs p{};
   p.hidden = st.hidden != nullptr ? reinterpret_cast<const uint8_t *>(st.hidden) : static_cast<const uint8_t *>(h.hidden);
   p.W = static_cast<const uint8_t *>(h.W);
@@ -1396,7 +1478,7 @@ hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t s) 
     e = launch_kernel(preference_pairs_kernel, dim3((unsigned)c.pairs), dim3(PP_THREADS), s,
                       Pairs{c.starts, c.starts64, c.pairs, c.head.M, c.head.V, c.y.target, c.y.wide, c.y.ignore,
                             rowlogp, c.ref_logp, c.beta, c.margin, c.smoothing, c.average, c.loss, c.logp, u.st.coef,
-                            u.st.up, u.st.inv});
+                            u.st.own, u.st.up, u.st.inv});
   return e;
 }
 
