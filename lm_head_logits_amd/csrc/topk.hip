@@ -195,6 +195,7 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
 
   float ref = TK_NEG_INF, sum = 0.0f;  // this thread's sum of exp((x - ref) / temperature)
   float bound = TK_LOWEST;             // no logit below it is wanted; never -inf
+  float most = TK_NEG_INF;             // the largest logit that became an entry lately
   int keys = 0;                        // entries that are keys; behind them {column, logit}
 
   // Tiles of TK_TILE pieces a thread from piece `from` to `to`, the next in
@@ -249,7 +250,6 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
     if ((tid & 63) == 0) at = atomicAdd(&count, n);
     at = __builtin_amdgcn_readfirstlane(at);
     if (at + n > TK_CAP) return;
-    float most = TK_NEG_INF;
 #pragma unroll
     for (int k4 = 0; k4 < P * N; k4 += 4) {
       if ((set[k4] | set[k4 + 1] | set[k4 + 2] | set[k4 + 3]) == 0) continue;
@@ -265,7 +265,6 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
           at += __popcll(set[k]);
         }
     }
-    raise(most);
   };
   // adds a tile to the thread's sum: none of its logits is above ref
   auto add = [&](const u32x4 (&w)[TK_TILE]) {
@@ -349,12 +348,12 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
   // pieces, half of them, or each
   const int mid = lo + TK_FIRST * TK_THREADS < hi ? lo + TK_FIRST * TK_THREADS : hi;
   const int group = K <= TK_THREADS / 4 ? TK_FIRST : K <= TK_THREADS ? TK_FIRST / 2 : 1;
-  uint32_t *const most = reinterpret_cast<uint32_t *>(key);  // [TK_FIRST / group][TK_THREADS]
+  uint32_t *const maxima = reinterpret_cast<uint32_t *>(key);  // [TK_FIRST / group][TK_THREADS]
   {
     float gm = TK_NEG_INF;
     int done = 0;
 #pragma unroll
-    for (int k = 0; k < TK_FIRST; ++k) most[k * TK_THREADS + tid] = 0;
+    for (int k = 0; k < TK_FIRST; ++k) maxima[k * TK_THREADS + tid] = 0;
     tiles(lo, mid, [&](const u32x4 (&w)[TK_TILE], int) {
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k) {
@@ -362,12 +361,12 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
         for (int e = 0; e < N; ++e) gm = fmaxf(gm, Piece<T>::at(w[k], e));
         ++done;
         if (done % group == 0) {
-          most[(done / group - 1) * TK_THREADS + tid] = order_of(gm);
+          maxima[(done / group - 1) * TK_THREADS + tid] = order_of(gm);
           gm = TK_NEG_INF;
         }
       }
     });
-    if (done % group != 0) most[done / group * TK_THREADS + tid] = order_of(gm);
+    if (done % group != 0) maxima[done / group * TK_THREADS + tid] = order_of(gm);
   }
   __syncthreads();
   if (tid < 64) {
@@ -375,7 +374,7 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
     auto find = [&](auto rc) {
       uint32_t x[decltype(rc)::value];
 #pragma unroll
-      for (int r = 0; r < decltype(rc)::value; ++r) x[r] = most[r * 64 + tid];
+      for (int r = 0; r < decltype(rc)::value; ++r) x[r] = maxima[r * 64 + tid];
       return kth_value(x, K);
     };
     const uint32_t v = group == TK_FIRST ? find(std::integral_constant<int, R>{})
@@ -395,11 +394,13 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
     for (int k = 0; k < TK_TILE; k += P) take(std::integral_constant<int, P>{}, w + k, i + k * TK_THREADS);
     __syncthreads();
     int n = count;
-    const int before = total;
+    const bool fits = n <= TK_CAP;
+    // of a tile that did not fit, which waves found room is chance: as if none had
+    if (fits) raise(most);
+    most = TK_NEG_INF;
     if (n > keys + K + 64) {
       // pruned; where the tile's keys did not fit, piece by piece
-      const bool fits = n <= TK_CAP;
-      if (!fits) n = before;
+      if (!fits) n = total;
 #pragma unroll 1
       for (int k = 0;; ++k) {
         __syncthreads();
@@ -407,6 +408,8 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
         if (fits || k == TK_TILE) break;
         const u32x4 one = k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3];
         take(std::integral_constant<int, 1>{}, &one, i + k * TK_THREADS);
+        raise(most);
+        most = TK_NEG_INF;
         __syncthreads();
         n = count;
       }

@@ -582,3 +582,98 @@ def test_differentiable(op):
     if op != "distill":
         _, logp = apply(h3, c["weight"], c["bias"], return_logp=True)
         assert not logp.requires_grad
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("M", [40, 700, 4500])
+def test_no_row_is_trained_on(op, M):
+    """All left out, then all but one, the last."""
+    c = make(op, 71, M, 64, 500, "bf16", True)
+    name = "teacher_ids" if op == "distill" else "target"
+    was = c[name][-1].clone().clamp(min=3)
+    c[name].fill_(-100)
+    if op == "preference":
+        c["starts"][1:] = M
+    c.update(old=None, ref=None)
+    say("no row", op, M)
+    for k in range(2):
+        got, d = check(c)
+        if k == 0:
+            assert all(bool((t == 0).all()) for t in d)
+            if op != "preference":
+                assert all(bool((t == 0).all()) for t in got)
+        c[name][-1] = was
+
+
+def _step(op, c, h, W, b, kw):
+    if op == "distill":
+        return L.distillation(h, W, c["teacher_ids"], c["teacher_logits"], 0.5, b, **kw)
+    if op == "policy":
+        return L.policy_loss(h, W, c["target"], c["advantage"], c["old"], c["ref"], 0.5, b, **kw)
+    return L.preference_loss(h, W, c["target"], c["starts"], c["ref"], 0.5, b, **kw)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("M", [200, 900])
+def test_differentiable_captured_and_replayed(op, M):
+    """The differentiable forms, with their means and their backward passes, in a
+    graph; the number of rows trained on changes from replay to replay."""
+    H, V, kw = 64, 700, KW[op]
+    c = make(op, 73, M, H, V, "bf16", True, pairs=3)
+    reference(c, 0.5, kw)
+    new = lambda k: c[k].clone().requires_grad_(True)
+
+    def grads(h, W, b):
+        loss = _step(op, c, h, W, b, kw)
+        return (loss.detach(), *torch.autograd.grad(loss, [h, W, b]))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            grads(new("hidden"), new("weight"), new("bias"))
+    torch.cuda.current_stream().wait_stream(s)
+    leaves = [new(k) for k in ("hidden", "weight", "bias")]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = grads(*leaves)
+    for k in range(4):
+        say("replay", op, M, k)
+        c["hidden"].copy_(torch.randn(M, H, device=DEV) * (k + 1))
+        leaves[0].data.copy_(c["hidden"])
+        name = "teacher_ids" if op == "distill" else "target"
+        c[name].copy_(torch.randint(0, V, c[name].shape, device=DEV))
+        c[name][torch.rand(M, device=DEV) < 0.3 * k] = -100
+        want = grads(new("hidden"), new("weight"), new("bias"))
+        torch.cuda.synchronize()
+        for t in out:
+            t.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(out, want):
+            assert torch.equal(p, q)
+
+
+def test_a_policy_step_with_a_tied_embedding():
+    """Rollout, reference and update together: log-probabilities of the policy
+    that sampled, the clipped loss, its gradient in the head's matrix with the
+    embedding's added, and the candidates of the next token."""
+    M, H, V = 300, 64, 2000
+    c = make("policy", 79, M, H, V, "bf16", False)
+    h, W = c["hidden"], c["weight"]
+    zero = torch.zeros(M, device=DEV)
+    _, old, none = L.policy_forward(h, W, c["target"], zero, train=False)
+    xent, _ = L.xent_forward(h, W, c["target"])
+    assert none is None and torch.equal(old, -xent)  # the cross entropy's own bits
+    loss, logp, saved = L.policy_forward(h, W, c["target"], c["advantage"], old, old, kl_coef=0.1)
+    assert torch.equal(logp, old)
+    kept = c["target"] >= 0
+    assert torch.equal(loss[kept], -c["advantage"][kept])  # ratio 1, no divergence
+    dh, dw, _ = L.loss_backward(torch.full((M,), 1.0 / M, device=DEV), W, saved)
+    want = dw.double().index_add_(0, c["target"][kept], dh[kept].double() * 2.0)
+    got = L.embed_backward(dh[kept].contiguous(), c["target"][kept].contiguous(), V, 2.0, grad_weight=dw.clone())
+    err = (got.double() - want).abs()
+    # one more rounding of the sum, and of fp32 sums of at most M terms
+    assert bool((err <= 2.0 ** -8 * want.abs() + M * 2.0 ** -24 * dh.double().abs().max() * 2 + 2.0 ** -126).all())
+    values, ids, lse = L.logits_topk(L.logits(h, W), 5)
+    assert float((values[:, 0] - lse).max()) <= 1e-6 and torch.equal(ids[:, 0], L.logits_rowreduce(h, W)[1])
