@@ -279,7 +279,7 @@ struct Select {
     return m >= lo && m < hi ? target_of(target, target64, m, ignore, V) : -1;
   }
 };
-constexpr int LR_THREADS = 256, LR_ROWS = 16;
+constexpr int LR_THREADS = 256, LR_ROWS = 4;
 __device__ __forceinline__ int block_sum(int x, int (&sh)[LR_THREADS / 64]) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
@@ -300,8 +300,9 @@ __global__ __launch_bounds__(LR_THREADS) void loss_count_kernel(Select c, int32_
   n = block_sum(n, sh);
   if (threadIdx.x == 0) chunks[blockIdx.x] = n;
 }
-// 16 rows a work-group, which counts the rows before them by itself; copies
-// the hidden rows that are worked on, clears the outputs of the others.
+// Four rows a work-group, which counts the rows before them by itself; copies
+// the hidden rows that are worked on, clears the outputs of the others. (4096 rows,
+// H = 4096: 17.6 us; sixteen a work-group, whose copies then follow each other: 21.)
 struct Gather {
   Select sel;
   const int32_t *chunks;
@@ -811,9 +812,12 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // the gradients is 1.41 times that of their own rounding, and with few rows
 // anything up to 1.6; so it is 1.2 to 1.35 up to some hundred rows.
 // The splits of G W's K (the piece's columns) that fill the last round of
-// work-groups best, at least 256 columns each; chosen as bwd_plan does, from the
-// rows worked on, by one wave. `cap`: row tiles times splits that the sums have
-// room for.
+// work-groups best, at least 256 columns each; chosen much as bwd_plan does, from
+// the rows worked on, by one wave. More splits have to fill 10% more: every one is
+// a sum of grad_hidden to write and to read again (764 rows, H = 2048, ten splits
+// against 32 that fill 6% more: the product 200 us against 247, the sums joined in
+// 12 against 42).
+// `cap`: row tiles times splits that the sums have room for.
 struct SplitPlan {
   int32_t ksplit, splits;
 };
@@ -827,7 +831,7 @@ __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, in
 #pragma unroll
   for (int k = 0; k < 64; ++k) {
     const float u = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, use), k));
-    if (u > best * 1.06f) {
+    if (u > best * 1.1f) {
       best = u;
       splits = k + 1;
     }
