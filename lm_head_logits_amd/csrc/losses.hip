@@ -862,126 +862,134 @@ struct LossCoef {
   const float *p, *tk;            // teacher's entries
   const int32_t *inv, *sid;
   int64_t K, all_rows;            // all_rows: the call's rows
-};
-template <int ET>
-__global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
-  if (p.count != nullptr) p.M = *p.count;
-  if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale) plan_splits((int32_t)p.M, (int32_t)p.H, (int32_t)p.vp, (int32_t)p.cap, p.plan);
   // c = 0: nothing, whatever g is (rows of no sequence have no upstream gradient)
-  auto coef_of = [&](float c, float g, float &a, float &b) {
-    a = c == 0.0f ? 0.0f : __fmul_rn(p.distill ? c : -c, g);
-    b = p.distill && c != 0.0f ? g : a;
-  };
+  __device__ __forceinline__ void of(float c, float g, float &a, float &b) const {
+    a = c == 0.0f ? 0.0f : __fmul_rn(distill ? c : -c, g);
+    b = distill && c != 0.0f ? g : a;
+  }
+  __device__ __forceinline__ RowCoef row(int64_t m, float f) const {
+    float a, b;
+    const float c = coef[m];
+    of(c, c == 0.0f ? 0.0f : g[up[m]], a, b);
+    return RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), lse[m], distill ? -1 : y[m]};
+  }
+};
+// The scale: all threads of a work-group, all rows.
+template <int ET>
+__device__ __forceinline__ float find_scale(const LossCoef &p) {
   float f = 1.0f;
-  if (p.have_scale) {
-    f = p.scale[0];
-  } else {
-    __shared__ float sh[LC_THREADS / 64];
-    float mx = 0.0f;
-    for (int64_t m0 = threadIdx.x; m0 < p.M; m0 += 8 * LC_THREADS) {
-      float c[8], g[8];
-      int32_t u[8];
+  __shared__ float sh[LC_THREADS / 64];
+  float mx = 0.0f;
+  for (int64_t m0 = threadIdx.x; m0 < p.M; m0 += 8 * LC_THREADS) {
+    float c[8], g[8];
+    int32_t u[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {  // past the last: the last again
-        const int64_t m = m0 + k * LC_THREADS < p.M ? m0 + k * LC_THREADS : p.M - 1;
-        c[k] = p.coef[m];
-        u[k] = p.up[m];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = c[k] == 0.0f ? 0.0f : p.g[u[k]];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float a, b;
-        coef_of(c[k], g[k], a, b);
-        a = fabsf(a);
-        b = fabsf(b);
-        mx = fmaxf(mx, fmaxf(a < __builtin_inff() ? a : 0.0f, b < __builtin_inff() ? b : 0.0f));
-      }
+    for (int k = 0; k < 8; ++k) {  // past the last: the last again
+      const int64_t m = m0 + k * LC_THREADS < p.M ? m0 + k * LC_THREADS : p.M - 1;
+      c[k] = p.coef[m];
+      u[k] = p.up[m];
     }
-    for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
-    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < LC_THREADS / 64; ++w) mx = fmaxf(mx, sh[w]);
-    // f and 1 / f both well inside the normal range, else no scale
-    if (mx > 1e-30f && mx < 1e30f) {
-      f = __fdiv_rn(p.top, mx);
-      __shared__ float err[LC_TRIES][LC_THREADS + 1];
-      float e2[LC_TRIES] = {};
-      auto sample = [&](float g) {  // an entry of G, unscaled
-        float x = __fmul_rn(g, f);
-        if (!(fabsf(x) <= 2.0f * p.top)) x = 0.0f;
-        float back = 1.0f;  // 1 / the factor tried
+    for (int k = 0; k < 8; ++k) g[k] = c[k] == 0.0f ? 0.0f : p.g[u[k]];
 #pragma unroll
-        for (int j = 0; j < LC_TRIES; ++j) {
-          const uint32_t r = mm_pack2<ET>(x, 0.0f);
-          float d;
-          if constexpr (ET == ET_F16)
-            d = (float)__builtin_bit_cast(_Float16, (uint16_t)r);
-          else
-            d = __builtin_bit_cast(float, r << 16);
-          d = __fmul_rn(__fsub_rn(d, x), back);
-          e2[j] = __fmaf_rn(d, d, e2[j]);
-          x = __fmul_rn(x, LC_STEP);
-          back = __fmul_rn(back, 1.0f / LC_STEP);
-        }
-      };
-      if (!p.distill) {
-        for (int64_t m = threadIdx.x; m < p.M && m < LC_SAMPLES; m += LC_THREADS) {
-          const float o = p.own[m];
-          sample(o == 0.0f ? 0.0f : __fmul_rn(o, p.g[p.up[m]]));
-        }
-      } else {
-        for (int64_t e = threadIdx.x; e < p.all_rows * p.K && e < LC_SAMPLES; e += LC_THREADS) {
-          const int64_t row = e / p.K, m = p.inv != nullptr ? p.inv[row] : row;
-          if (m < 0 || p.sid[e] == NO_ID || p.coef[m] == 0.0f) continue;
-          sample(__fmul_rn(p.g[row], __fsub_rn(__fmul_rn(p.coef[m], exp_diff(p.tk[e], p.lse[m])), p.p[e])));
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < LC_TRIES; ++j) err[j][threadIdx.x] = e2[j];
-      __syncthreads();
-      {
-        const int j = threadIdx.x / 16, part = threadIdx.x % 16;
-        float s = 0.0f;
-        #pragma unroll
-        for (int k = 0; k < LC_THREADS; k += 16) s = __fadd_rn(s, err[j][k + part]);
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2) s = __fadd_rn(s, __shfl_xor(s, d));
-        __syncthreads();
-        if (part == 0) err[0][j] = s;
-      }
-      __syncthreads();
-      float least = err[0][0], factor = 1.0f, best = 1.0f;
-#pragma unroll
-      for (int j = 1; j < LC_TRIES; ++j) {
-        factor = __fmul_rn(factor, LC_STEP);
-        if (err[0][j] < least) {
-          least = err[0][j];
-          best = factor;
-        }
-      }
-      f = __fmul_rn(f, best);
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.scale[0] = f;
-      p.scale[1] = __fdiv_rn(1.0f, f);
+    for (int k = 0; k < 8; ++k) {
+      float a, b;
+      p.of(c[k], g[k], a, b);
+      a = fabsf(a);
+      b = fabsf(b);
+      mx = fmaxf(mx, fmaxf(a < __builtin_inff() ? a : 0.0f, b < __builtin_inff() ? b : 0.0f));
     }
   }
+  for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < LC_THREADS / 64; ++w) mx = fmaxf(mx, sh[w]);
+  // f and 1 / f both well inside the normal range, else no scale
+  if (mx > 1e-30f && mx < 1e30f) {
+    f = __fdiv_rn(p.top, mx);
+    __shared__ float err[LC_TRIES][LC_THREADS + 1];
+    float e2[LC_TRIES] = {};
+    auto sample = [&](float g) {  // an entry of G, unscaled
+      float x = __fmul_rn(g, f);
+      if (!(fabsf(x) <= 2.0f * p.top)) x = 0.0f;
+      float back = 1.0f;  // 1 / the factor tried
+#pragma unroll
+      for (int j = 0; j < LC_TRIES; ++j) {
+        const uint32_t r = mm_pack2<ET>(x, 0.0f);
+        float d;
+        if constexpr (ET == ET_F16)
+          d = (float)__builtin_bit_cast(_Float16, (uint16_t)r);
+        else
+          d = __builtin_bit_cast(float, r << 16);
+        d = __fmul_rn(__fsub_rn(d, x), back);
+        e2[j] = __fmaf_rn(d, d, e2[j]);
+        x = __fmul_rn(x, LC_STEP);
+        back = __fmul_rn(back, 1.0f / LC_STEP);
+      }
+    };
+    if (!p.distill) {
+      for (int64_t m = threadIdx.x; m < p.M && m < LC_SAMPLES; m += LC_THREADS) {
+        const float o = p.own[m];
+        sample(o == 0.0f ? 0.0f : __fmul_rn(o, p.g[p.up[m]]));
+      }
+    } else {
+      for (int64_t e = threadIdx.x; e < p.all_rows * p.K && e < LC_SAMPLES; e += LC_THREADS) {
+        const int64_t row = e / p.K, m = p.inv != nullptr ? p.inv[row] : row;
+        if (m < 0 || p.sid[e] == NO_ID || p.coef[m] == 0.0f) continue;
+        sample(__fmul_rn(p.g[row], __fsub_rn(__fmul_rn(p.coef[m], exp_diff(p.tk[e], p.lse[m])), p.p[e])));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < LC_TRIES; ++j) err[j][threadIdx.x] = e2[j];
+    __syncthreads();
+    {
+      const int j = threadIdx.x / 16, part = threadIdx.x % 16;
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < LC_THREADS; k += 16) s = __fadd_rn(s, err[j][k + part]);
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) s = __fadd_rn(s, __shfl_xor(s, d));
+      __syncthreads();
+      if (part == 0) err[0][j] = s;
+    }
+    __syncthreads();
+    float least = err[0][0], factor = 1.0f, best = 1.0f;
+#pragma unroll
+    for (int j = 1; j < LC_TRIES; ++j) {
+      factor = __fmul_rn(factor, LC_STEP);
+      if (err[0][j] < least) {
+        least = err[0][j];
+        best = factor;
+      }
+    }
+    f = __fmul_rn(f, best);
+  }
+  return f;
+}
+template <int ET>
+__global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
+  if (p.count != nullptr) {
+    p.M = *p.count;
+    if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale)
+      plan_splits((int32_t)p.M, (int32_t)p.H, (int32_t)p.vp, (int32_t)p.cap, p.plan);
+  }
+  const float f = p.have_scale ? p.scale[0] : find_scale<ET>(p);
+  if (!p.have_scale && blockIdx.x == 0 && threadIdx.x == 0) {
+    p.scale[0] = f;
+    p.scale[1] = __fdiv_rn(1.0f, f);
+  }
   const int64_t m = (int64_t)blockIdx.x * LC_THREADS + threadIdx.x;
-  if (!p.write_rows || m >= p.M) return;
-  float a, b;
-  const float c = p.coef[m];
-  coef_of(c, c == 0.0f ? 0.0f : p.g[p.up[m]], a, b);
-  p.rows[m] = RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), p.lse[m], p.distill ? -1 : p.y[m]};
+  if (p.write_rows && m < p.M) p.rows[m] = p.row(m, f);
 }
 
 // Packed rows: their number is known on the device.
 struct OnDevice {
-  const int32_t *count;
+  const int32_t *count;   // nullptr: not packed, and the splits are known
   const SplitPlan *plan;
   __device__ __forceinline__ void apply(XentBwdArgs &p) const {
-    if (count != nullptr) p.M = mm_uni(*count);
+    if (count == nullptr) return;
+    p.M = mm_uni(*count);
     p.ksplit = (int64_t)mm_uni((uint32_t)plan->ksplit);
   }
 };
@@ -995,70 +1003,120 @@ __global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p,
   mm_run<ET, false, false>(prob, mm_buf);
 }
 
+// G at entry k of a row's teacher, over what the product's epilogue or the kept t
+// left there: a q - b p from the entry's t, the dense value's own fp32 operations,
+// rounded once. An id that a row has more than once is written by each of them
+// with the sum of their p.
+template <int ET>
+__device__ __forceinline__ uint16_t entry_of_G(const RowCoef &r, const int32_t *sid, const float *p, const float *tk, int64_t row,
+                                               int64_t K, int64_t k) {
+  const int64_t at = row * K;
+  const int32_t id = sid[at + k];
+  int64_t first = k;
+  while (first > 0 && sid[at + first - 1] == id) --first;
+  float sum = 0.0f;
+  for (int64_t j = first; j < K && sid[at + j] == id; ++j) sum = __fadd_rn(sum, p[at + j]);
+  const float q = exp_diff(tk[at + k], r.lse == NEG_INF ? 0.0f : r.lse);
+  return (uint16_t)mm_pack2<ET>(__fsub_rn(__fmul_rn(r.a, q), __fmul_rn(r.b, sum)), 0.0f);
+}
+
 // G of a piece from the kept t: the same operations on the same values as the
 // product's epilogue, so the same bits. 2048 columns and R rows a work-group,
 // eight columns a thread; four rows' loads in flight. grad_bias: the column sums
 // of R rows.
-template <int ET, bool DB, int R>
-__global__ __launch_bounds__(256) void loss_kept_kernel(XentBwdArgs p, OnDevice dev, const float *t, int64_t ldt) {
-  if (dev.count != nullptr) p.M = mm_uni(*dev.count);
-  const int64_t chunks = (p.np + 2047) / 2048, g = group_number(), rt = g / chunks;
-  const int64_t m0 = rt * R, c = (g - rt * chunks) * 2048 + 8 * threadIdx.x;
-  if (m0 >= p.M || c >= p.np) return;  // np is a multiple of 256
-  const int rows = (int)(p.M - m0 < R ? p.M - m0 : R);
-  float sum[8] = {};
-  const float *at = t + m0 * ldt + p.v0 + c;
-  uint16_t *out = reinterpret_cast<uint16_t *>(p.G) + m0 * p.ldg + c;
-  for (int r0 = 0; r0 < rows; r0 += 4) {
-    f32x4 v[4][2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[k][h] = __builtin_nontemporal_load(
-            reinterpret_cast<const f32x4 *>(at + (r0 + k < rows ? r0 + k : rows - 1) * ldt + 4 * h));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (r0 + k >= rows) break;
-      RowCoef r = p.rows[m0 + r0 + k];
-      if (r.lse == NEG_INF) r.lse = 0.0f;
-      float g8[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) g8[q] = __fmul_rn(r.a, exp_diff(v[k][q >> 2][q & 3], r.lse));
-      const int64_t y = r.y - p.v0 - c;
-      if (y >= 0 && y < 8)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (y == q) g8[q] = __fsub_rn(g8[q], r.b);
-      if constexpr (DB)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) sum[q] = __fadd_rn(sum[q], g8[q]);
-      *reinterpret_cast<u32x4 *>(out + (r0 + k) * p.ldg) =
-          u32x4{mm_pack2<ET>(g8[0], g8[1]), mm_pack2<ET>(g8[2], g8[3]), mm_pack2<ET>(g8[4], g8[5]), mm_pack2<ET>(g8[6], g8[7])};
+//
+// FEW (a small G of rows that are not packed): the rows' coefficients and their
+// scale are found here, by every work-group, and the teacher's entries are
+// written here where grad_bias does not want their sums; both are launches of
+// their own otherwise (a step of 37 rows, H = 256, V = 4096: 53.8 -> 50.0 us).
+constexpr int KEPT_FEW = 4, KEPT_MANY = 32;  // rows a work-group: few where there are few, for the sake of work-groups
+constexpr int64_t KEPT_GROUPS = 1024;        // work-groups up to which each finds the scale: one round of them
+int kept_rows(int64_t M) { return M <= LR_DIRECT ? KEPT_FEW : KEPT_MANY; }
+bool kept_few(int64_t M, int64_t V) {
+  return M <= LR_DIRECT && ceil_div(M, KEPT_FEW) * ceil_div(V, 2048) <= KEPT_GROUPS;
+}
+template <int ET, bool DB, int R, bool FEW>
+__global__ __launch_bounds__(256) void loss_kept_kernel(XentBwdArgs p, OnDevice dev, const float *t, int64_t ldt, LossCoef few,
+                                                        int entries) {
+  if (!FEW) dev.apply(p);
+  const int64_t chunks = (p.np + 2047) / 2048, g = group_number(), rt = g / chunks, c0 = (g - rt * chunks) * 2048;
+  const int64_t m0 = rt * R, c = c0 + 8 * threadIdx.x;
+  if (m0 >= p.M) return;
+  float f = 1.0f;
+  if constexpr (FEW) {
+    f = find_scale<ET>(few);
+    if (g == 0 && threadIdx.x == 0) {
+      few.scale[0] = f;
+      few.scale[1] = __fdiv_rn(1.0f, f);
     }
   }
-  if constexpr (DB) {
-    const float f = p.scale[1];
+  const int rows = (int)(p.M - m0 < R ? p.M - m0 : R);
+  if (c < p.np) {  // np is a multiple of 256
+    float sum[8] = {};
+    const float *at = t + m0 * ldt + p.v0 + c;
+    uint16_t *out = reinterpret_cast<uint16_t *>(p.G) + m0 * p.ldg + c;
+    for (int r0 = 0; r0 < rows; r0 += 4) {
+      f32x4 v[4][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<f32x4 *>(p.colpart + rt * p.ldg + c + 4 * h) =
-          f32x4{__fmul_rn(f, sum[4 * h]), __fmul_rn(f, sum[4 * h + 1]), __fmul_rn(f, sum[4 * h + 2]), __fmul_rn(f, sum[4 * h + 3])};
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[k][h] = __builtin_nontemporal_load(
+              reinterpret_cast<const f32x4 *>(at + (r0 + k < rows ? r0 + k : rows - 1) * ldt + 4 * h));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (r0 + k >= rows) break;
+        RowCoef r;
+        if constexpr (FEW) r = few.row(m0 + r0 + k, f);
+        else r = p.rows[m0 + r0 + k];
+        if (r.lse == NEG_INF) r.lse = 0.0f;
+        float g8[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) g8[q] = __fmul_rn(r.a, exp_diff(v[k][q >> 2][q & 3], r.lse));
+        const int64_t y = r.y - p.v0 - c;
+        if (y >= 0 && y < 8)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (y == q) g8[q] = __fsub_rn(g8[q], r.b);
+        if constexpr (DB)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) sum[q] = __fadd_rn(sum[q], g8[q]);
+        *reinterpret_cast<u32x4 *>(out + (r0 + k) * p.ldg) = u32x4{
+            mm_pack2<ET>(g8[0], g8[1]), mm_pack2<ET>(g8[2], g8[3]), mm_pack2<ET>(g8[4], g8[5]), mm_pack2<ET>(g8[6], g8[7])};
+      }
+    }
+    if constexpr (DB) {
+      const float back = FEW ? __fdiv_rn(1.0f, f) : p.scale[1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<f32x4 *>(p.colpart + rt * p.ldg + c + 4 * h) = f32x4{
+            __fmul_rn(back, sum[4 * h]), __fmul_rn(back, sum[4 * h + 1]), __fmul_rn(back, sum[4 * h + 2]), __fmul_rn(back, sum[4 * h + 3])};
+    }
+  }
+  if constexpr (FEW && !DB) {
+    if (entries) {
+      dma_barrier();  // what the entries lie over has been written
+      for (int64_t e = threadIdx.x; e < rows * few.K; e += 256) {
+        const int64_t m = m0 + e / few.K, k = m * few.K + e % few.K;
+        const int32_t id = few.sid[k];
+        const int64_t col = id - p.v0;
+        if (id == NO_ID || col < c0 || col >= c0 + 2048 || col >= p.np) continue;
+        reinterpret_cast<uint16_t *>(p.G)[m * p.ldg + col] = entry_of_G<ET>(few.row(m, f), few.sid, few.p, few.tk, m, few.K, e % few.K);
+      }
+    }
   }
 }
-// rows a work-group of it: few where there are few, for the sake of work-groups
-constexpr int KEPT_FEW = 4, KEPT_MANY = 32;
-int kept_rows(int64_t M) { return M <= MM_T ? KEPT_FEW : KEPT_MANY; }
 template <int ET, bool DB>
-hipError_t kept_grad(const XentBwdArgs &p, const OnDevice &dev, const float *t, int64_t ldt, hipStream_t s) {
+hipError_t kept_grad(const XentBwdArgs &p, const OnDevice &dev, const float *t, int64_t ldt, const LossCoef &few, bool entries,
+                     hipStream_t s) {
   const int R = kept_rows(p.M);
-  return launch_kernel(R == KEPT_FEW ? loss_kept_kernel<ET, DB, KEPT_FEW> : loss_kept_kernel<ET, DB, KEPT_MANY>,
-                       numbered_grid(ceil_div(p.M, R) * ceil_div(p.np, 2048)), dim3(256), s, p, dev, t, ldt);
+  return launch_kernel(kept_few(p.M, p.V)  ? loss_kept_kernel<ET, DB, KEPT_FEW, true>
+                       : R == KEPT_FEW ? loss_kept_kernel<ET, DB, KEPT_FEW, false>
+                                       : loss_kept_kernel<ET, DB, KEPT_MANY, false>,
+                       numbered_grid(ceil_div(p.M, R) * ceil_div(p.np, 2048)), dim3(256), s, p, dev, t, ldt, few, entries ? 1 : 0);
 }
 
-// G at the teacher's entries of a piece, over what the product's epilogue left
-// there: a q - b p from the entry's t, the dense value's own fp32 operations,
-// rounded once. An id that a row has more than once is written by each of them
-// with the sum of their p.
+// The entries of a piece.
 //
 // grad_bias: what the entries add to it, as whole numbers of 2^-shift of the
 // largest coefficient, so that the order of the additions does not matter.
@@ -1079,13 +1137,7 @@ __global__ __launch_bounds__(256) void distill_entries_kernel(DistillEntries c) 
   const int64_t row = e / c.K, k = e - row * c.K, m = c.inv != nullptr ? c.inv[row] : row;
   if (m < 0) return;
   const RowCoef r = c.b.rows[m];
-  const float lse = r.lse == NEG_INF ? 0.0f : r.lse;
-  int64_t first = k;
-  while (first > 0 && c.sid[e - k + first - 1] == id) --first;
-  float p = 0.0f;
-  for (int64_t j = first; j < c.K && c.sid[e - k + j] == id; ++j) p = __fadd_rn(p, c.p[e - k + j]);
-  const float g = __fsub_rn(__fmul_rn(r.a, exp_diff(c.tk[e], lse)), __fmul_rn(r.b, p));
-  reinterpret_cast<uint16_t *>(c.b.G)[m * c.b.ldg + (id - c.b.v0)] = (uint16_t)mm_pack2<ET>(g, 0.0f);
+  reinterpret_cast<uint16_t *>(c.b.G)[m * c.b.ldg + (id - c.b.v0)] = entry_of_G<ET>(r, c.sid, c.p, c.tk, row, c.K, k);
   if (c.bias != nullptr) {
     const double x = -(double)r.b * (double)c.p[e] * c.unit;
     // what is not finite makes the whole row of G so, and with it every sum
@@ -1164,6 +1216,7 @@ struct DHiddenOut {
   int64_t M, H;
   const int32_t *count, *inv;
   const SplitPlan *plan;
+  int splits;       // not packed
   float alpha;
   const float *scale;
   uint16_t *out;
@@ -1178,7 +1231,7 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
     return;
   }
   const int64_t n = (c.count != nullptr ? *c.count : c.M) * c.H, at = m * c.H + (e - row * c.H);
-  const int splits = c.plan->splits;
+  const int splits = c.count != nullptr ? c.plan->splits : c.splits;
   f32x4 s[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) s[h] = *reinterpret_cast<const f32x4 *>(c.dh + at + 4 * h);
@@ -1212,7 +1265,8 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
 // bwd_plan's pieces, with room for the sums of grad_hidden of whatever rows are
 // worked on: `cap` row tiles times splits.
 struct BackwardLayout {
-  int64_t vp, cap;
+  int64_t vp, cap, ksplit;
+  int splits;
   int64_t scale, plan, rows, col, dh, G, entries, bytes;
 };
 BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep, bool bias) {
@@ -1226,10 +1280,12 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
   };
   const int64_t nmt = ceil_div(M, MM_T);
   b.vp = pl.vp;
+  b.ksplit = pl.ksplit;
+  b.splits = (int)pl.splits;
   // fewer rows than the call's take more splits: with three fifths of 4096 rows
   // (H = 4096) 160 tiles would leave 96 of 256 CUs without one; three splits of
   // them fill 94%
-  b.cap = pl.splits > 3 ? pl.splits * nmt : 3 * nmt;
+  b.cap = pl.splits > 3 || M <= LR_DIRECT ? pl.splits * nmt : 3 * nmt;
   b.scale = take(8);
   b.plan = take(sizeof(SplitPlan));
   b.rows = take(16 * M);
@@ -1331,7 +1387,8 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
     e = launch_kernel(loss_coef_kernel<ET>, dim3(1), dim3(LC_THREADS), s, r);
     r.write_rows = r.have_scale = 1;
   }
-  if (e == hipSuccess)
+  const bool few = c.mem.keep != 0 && kept_few(h.M, h.V);  // loss_kept_kernel finds them itself
+  if (e == hipSuccess && (!few || (c.K > 0 && c.grad_bias != nullptr)))
     e = launch_kernel(loss_coef_kernel<ET>, dim3((unsigned)ceil_div(h.M, LC_THREADS)), dim3(LC_THREADS), s, r);
   XentBwdArgs p{};
   p.hidden = st.hidden != nullptr ? reinterpret_cast<const uint8_t *>(st.hidden) : static_cast<const uint8_t *>(h.hidden);
@@ -1348,6 +1405,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + lay.col) : nullptr;
   p.dh = reinterpret_cast<float *>(ws + lay.dh);
   p.dw = static_cast<uint16_t *>(c.grad_W);
+  p.ksplit = lay.ksplit;
   const OnDevice dev{st.count, plan};
   const int64_t nmt = ceil_div(h.M, MM_T), nht = ceil_div(h.H, MM_T);
   // whole numbers of 2^-shift: their sum over all rows stays below 2^62
@@ -1364,12 +1422,12 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
     const int64_t nv = h.V - v0 < lay.vp ? h.V - v0 : lay.vp;
     p.np = ceil_div(nv, MM_T) * MM_T;
     if (c.mem.keep)
-      e = c.grad_bias != nullptr ? kept_grad<ET, true>(p, dev, st.t, padded(h.V), s)
-                                 : kept_grad<ET, false>(p, dev, st.t, padded(h.V), s);
+      e = c.grad_bias != nullptr ? kept_grad<ET, true>(p, dev, st.t, padded(h.V), r, false, s)
+                                 : kept_grad<ET, false>(p, dev, st.t, padded(h.V), r, c.K > 0, s);
     else
       e = launch_kernel(c.grad_bias != nullptr ? loss_grad_kernel<ET, true> : loss_grad_kernel<ET, false>,
                         mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
-    if (e == hipSuccess && c.K > 0)
+    if (e == hipSuccess && c.K > 0 && (!few || c.grad_bias != nullptr))
       e = launch_kernel(distill_entries_kernel<ET>, numbered_grid(ceil_div(h.M * c.K, 256)), dim3(256), s,
                         DistillEntries{p, c.K, st.ids, st.inv, st.p, st.tk, entries, unit});
     if (e == hipSuccess && c.grad_bias != nullptr)
@@ -1398,7 +1456,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   }
   if (e == hipSuccess && c.grad_hidden != nullptr)
     e = launch_kernel(loss_dhidden_out_kernel<ET>, numbered_grid(ceil_div(h.M * h.H, 2048)), dim3(256), s,
-                      DHiddenOut{p.dh, h.M, h.H, st.count, st.inv, plan, p.alpha, scale, static_cast<uint16_t *>(c.grad_hidden)});
+                      DHiddenOut{p.dh, h.M, h.H, st.count, st.inv, plan, lay.splits, p.alpha, scale, static_cast<uint16_t *>(c.grad_hidden)});
   return e;
 }
 
