@@ -379,7 +379,8 @@ size_t lmhead_logits_topk_workspace_bytes(int64_t M, int64_t V, int64_t K);
  * K is the teacher's logits per row for lmhead_distill_forward and 0 for the others. What
  * is said of lmhead_xent_forward about -inf, the lowest value, +inf and NaN
  * holds, as does its independence of the call's other rows (preference: of the
- * other pairs). Returns as lmhead_xent_forward.
+ * other pairs). What stands in the hidden rows that are left out reaches no result, not
+ * grad_W either. Returns as lmhead_xent_forward.
  * ------------------------------------------------------------------------- */
 
 /* The divergence from a teacher's top logits. A row's entries k are those whose
@@ -443,7 +444,8 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
 
 /* Gradients of sum_m grad_loss[m] loss[m] (preference: over the pairs) of one of the
  * three calls above, whose state is given and whose other arguments are the same
- * (K: 0 but for lmhead_distill_forward).
+ * (K: 0 but for lmhead_distill_forward). hidden's values are not read again: the state
+ * has the rows that are worked on.
  *   grad_loss   fp32 [M], or [pairs]                            (device, read)
  *   grad_hidden, grad_W, grad_bias, workspace   as in lmhead_xent_backward, with
  *               lmhead_loss_backward_workspace_bytes(M, H, V, K, keep_logits, grad_bias != NULL)

@@ -27,6 +27,17 @@
 // from memory.
 //
 // 1 / T: alpha / T and a copy of the bias divided by T go into the products.
+//
+// Bound by the matrix pipes (mma256.hpp) but for few rows, where the weight's
+// bytes bind, and short products (H = 2048, some hundred rows), whose tiles'
+// epilogues show. 4096 rows, H = 4096, V = 128256, 64 teacher's logits a row: forward
+// 3.3 ms (0.25 of it t's stores), per piece of 32256 columns G from t 0.143 ms (792
+// MB at 5.5 TB/s), G W 0.68-0.73 ms (1.46-1.57 PFLOP/s), G^T hidden 0.77-0.81 (1.31-1.38);
+// 10.0-10.2 ms in all, 12.5 with t made again.
+//
+// Roundings: t, the statistics, probabilities, coefficients and grad_bias are
+// fp32, sums over a sequence and pairs' margins fp64. G is rounded to the inputs'
+// 16-bit type, scaled (loss_coef_kernel).
 #include "losses_launch.hpp"
 #include "xent_core.hpp"
 
@@ -39,7 +50,11 @@ constexpr int32_t NO_ID = 0x7FFFFFFF;
 // Rows that are not trained on are left out of the work. With more than
 // LR_DIRECT rows, one row tile, the others' hidden rows are copied one behind
 // the other and their number stays on the device, where every kernel reads it;
-// with fewer nothing would be saved by it.
+// with fewer nothing would be saved by it. (Their rows are then copied for the
+// backward pass by the kernel that makes the rows' losses, with zeros in those
+// left out: what stands there does not reach grad_W as 0 times infinity.)
+// (4096 rows, H = 4096, two fifths left out: the step 12.0 -> 8.4 ms, of which the
+// copies are 0.02.)
 constexpr int64_t LR_DIRECT = MM_T;
 
 // What the forward pass leaves for the backward pass, in one buffer.
@@ -59,7 +74,7 @@ StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
   s.count = take(4);
   s.rows = take(packed ? 4 * M : 0);
   s.inv = take(packed ? 4 * M : 0);
-  s.hidden = take(packed ? 2 * M * H : 0);
+  s.hidden = take(2 * M * H);
   s.y = take(4 * M);
   s.lse = take(4 * M);
   s.coef = take(4 * M);
@@ -78,9 +93,9 @@ struct State {
   int32_t *count;  // n; nullptr without packing
   int32_t *rows;   // [n] the call's row; nullptr
   int32_t *inv;    // [M] the packed row, -1 where left out; nullptr
-  uint16_t *hidden;  // [n, H]; nullptr
+  uint16_t *hidden;  // [n, H]; without packing zeros in the rows left out
   int32_t *y;      // [n] target column or -1
-  float *lse;      // [n]
+  float *lse;      // [n]; +inf in rows left out
   float *coef;     // [n] d loss / d logp; distill: P
   float *own;      // [n] coef (1 - q) of the target: d loss / d its t; targets only
   int32_t *up;     // [n] which element of the upstream gradient is the row's
@@ -93,7 +108,7 @@ State state_at(void *base, const StateLayout &l, int64_t M) {
   uint8_t *const b = static_cast<uint8_t *>(base);
   const bool packed = M > LR_DIRECT;
   auto ints = [&](int64_t at) { return packed ? reinterpret_cast<int32_t *>(b + at) : nullptr; };
-  return State{ints(l.count), ints(l.rows), ints(l.inv), packed ? reinterpret_cast<uint16_t *>(b + l.hidden) : nullptr,
+  return State{ints(l.count), ints(l.rows), ints(l.inv), reinterpret_cast<uint16_t *>(b + l.hidden),
                reinterpret_cast<int32_t *>(b + l.y),    reinterpret_cast<float *>(b + l.lse),
                reinterpret_cast<float *>(b + l.coef),   reinterpret_cast<float *>(b + l.own),
                reinterpret_cast<int32_t *>(b + l.up),
@@ -396,7 +411,8 @@ struct LossFwdArgs {
 // PICK: t at the rows' entries in the tile instead of at one target. Through
 // LDS, 32 rows at a time: all 256 columns of the rows are written, then 16
 // threads a row take that row's entries from it. Groups of rows without an
-// entry are left out.
+// entry are left out. What 64 entries a row add to a tile of H = 4096 (92 us) is
+// not seen between cards.
 //
 // KEEP: t of the whole tile to memory, for the backward pass.
 template <int ET, bool PICK, bool KEEP>
@@ -614,6 +630,23 @@ struct RowsArgs {
   const float2 *part;
   int64_t M, nvt;
   State st;
+  Select sel;               // without packing
+  const uint16_t *hidden;   // ... and [M, H] to be copied, or nullptr
+  int64_t H;
+  __device__ __forceinline__ int64_t column(int64_t m) const {
+    return sel.column(m, sel.starts != nullptr ? sel.bound(0) : 0, sel.starts != nullptr ? sel.bound(sel.last) : M);
+  }
+  // the work-group's 16 rows, a wave each
+  __device__ __forceinline__ void copy(int64_t m0) const {
+    static_assert(XC_SLICES * XC_ROWS == 64 * XC_ROWS);
+    const int64_t m = m0 + threadIdx.x / 64, per = H / 8;
+    if (hidden == nullptr || m >= M) return;
+    const bool worked_on = column(m) >= 0;
+    const u32x4 *const from = reinterpret_cast<const u32x4 *>(hidden) + m * per;
+    u32x4 *const to = reinterpret_cast<u32x4 *>(st.hidden) + m * per;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x % 64; i < per; i += 64) to[i] = worked_on ? from[i] : u32x4{0, 0, 0, 0};
+  }
   __device__ __forceinline__ int64_t rows() const { return st.count != nullptr ? *st.count : M; }
   __device__ __forceinline__ int64_t row(int64_t m) const { return st.rows != nullptr ? st.rows[m] : m; }
 };
@@ -628,6 +661,7 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(Disti
   const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
   const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r, n = c.r.rows();
   if (m - r >= n) return;  // the whole work-group
+  c.r.copy(m - r);
   const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
   const float ls = logf(f.y);
   const int64_t row = m < n ? c.r.row(m) : 0;
@@ -641,7 +675,7 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(Disti
   __syncthreads();
   if (sl != 0 || m >= n) return;
   for (int k = 1; k < XC_SLICES; ++k) sum = __fadd_rn(sum, sh[k][r].x);
-  c.r.st.lse[m] = row_lse(f, ls);
+  c.r.st.lse[m] = c.P[row] == 0.0f ? __builtin_inff() : row_lse(f, ls);
   c.r.st.y[m] = -1;
   c.r.st.up[m] = (int32_t)row;
   c.r.st.coef[m] = c.P[row];
@@ -655,11 +689,7 @@ __device__ __forceinline__ float own_share(float coef, float logp) {
 
 struct TokenRows {
   RowsArgs r;
-  int64_t V;
   const float *tlogit;
-  const void *target;  // without packing
-  int target64;
-  int64_t ignore;
   float *logp;     // [M]
   // policy
   const float *advantage, *old_logp, *ref_logp;
@@ -690,14 +720,15 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void token_rows_kernel(TokenRo
   const int r = threadIdx.x % XC_ROWS, sl = threadIdx.x / XC_ROWS;
   const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r, n = c.r.rows();
   if (m - r >= n) return;  // the whole work-group
+  c.r.copy(m - r);
   const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
   if (sl != 0 || m >= n) return;
   const float ls = logf(f.y);
   const int64_t row = c.r.row(m);
   const bool packed = c.r.st.rows != nullptr;
-  const int64_t y = packed ? c.r.st.y[m] : target_of(c.target, c.target64, m, c.ignore, c.V);
+  const int64_t y = packed ? c.r.st.y[m] : c.r.column(m);
   const float logp = y >= 0 ? log_q(c.tlogit[m], f, ls) : 0.0f;
-  c.r.st.lse[m] = row_lse(f, ls);
+  c.r.st.lse[m] = y >= 0 ? row_lse(f, ls) : __builtin_inff();
   if (!packed) c.r.st.y[m] = (int32_t)y;
   c.logp[row] = logp;
   float loss = 0.0f, coef = 0.0f;
@@ -1016,14 +1047,14 @@ __device__ __forceinline__ uint16_t entry_of_G(const RowCoef &r, const int32_t *
   while (first > 0 && sid[at + first - 1] == id) --first;
   float sum = 0.0f;
   for (int64_t j = first; j < K && sid[at + j] == id; ++j) sum = __fadd_rn(sum, p[at + j]);
-  const float q = exp_diff(tk[at + k], r.lse == NEG_INF ? 0.0f : r.lse);
+  const float q = r.a == 0.0f ? 0.0f : exp_diff(tk[at + k], r.lse == NEG_INF ? 0.0f : r.lse);
   return (uint16_t)mm_pack2<ET>(__fsub_rn(__fmul_rn(r.a, q), __fmul_rn(r.b, sum)), 0.0f);
 }
 
 // G of a piece from the kept t: the same operations on the same values as the
 // product's epilogue, so the same bits. 2048 columns and R rows a work-group,
-// eight columns a thread; four rows' loads in flight. grad_bias: the column sums
-// of R rows.
+// eight columns a thread; four rows' loads in flight: 5.5 TB/s of reads and writes.
+// grad_bias: the column sums of R rows.
 //
 // FEW (a small G of rows that are not packed): the rows' coefficients and their
 // scale are found here, by every work-group, and the teacher's entries are
@@ -1072,7 +1103,7 @@ __global__ __launch_bounds__(256) void loss_kept_kernel(XentBwdArgs p, OnDevice 
         if (r.lse == NEG_INF) r.lse = 0.0f;
         float g8[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) g8[q] = __fmul_rn(r.a, exp_diff(v[k][q >> 2][q & 3], r.lse));
+        for (int q = 0; q < 8; ++q) g8[q] = r.a == 0.0f ? 0.0f : __fmul_rn(r.a, exp_diff(v[k][q >> 2][q & 3], r.lse));
         const int64_t y = r.y - p.v0 - c;
         if (y >= 0 && y < 8)
 #pragma unroll
@@ -1310,7 +1341,7 @@ hipError_t set_up(const LossHead &h, const LossMemory &mem, int64_t K, hipStream
   u.st = state_at(mem.state != nullptr ? mem.state : u.ws + u.lay.state, state_layout(h.M, h.H, h.V, K, mem.keep != 0),
                   h.M);
   u.a = LossFwdArgs{};
-  u.a.hidden = u.st.hidden != nullptr ? reinterpret_cast<const uint8_t *>(u.st.hidden) : static_cast<const uint8_t *>(h.hidden);
+  u.a.hidden = static_cast<const uint8_t *>(u.st.rows != nullptr ? u.st.hidden : h.hidden);
   u.a.W = static_cast<const uint8_t *>(h.W);
   u.a.M = h.M;
   u.a.H = h.H;
@@ -1356,16 +1387,9 @@ void set_targets(LossFwdArgs &a, const LossTargets &y) {
   a.target64 = y.wide;
   a.ignore = y.ignore;
 }
-RowsArgs rows_args(const Setup &u) { return RowsArgs{u.a.part, u.a.M, ceil_div(u.a.V, MM_T), u.st}; }
-TokenRows token_rows(const Setup &u, const LossTargets &y) {
-  TokenRows r{};
-  r.r = rows_args(u);
-  r.V = u.a.V;
-  r.tlogit = u.a.tlogit;
-  r.target = y.target;
-  r.target64 = y.wide;
-  r.ignore = y.ignore;
-  return r;
+RowsArgs rows_args(const LossHead &h, const LossMemory &mem, const Setup &u, const Select &sel) {
+  return RowsArgs{u.a.part, h.M, ceil_div(h.V, MM_T), u.st, sel,
+                  mem.state != nullptr && u.st.rows == nullptr ? static_cast<const uint16_t *>(h.hidden) : nullptr, h.H};
 }
 dim3 rows_grid(int64_t M) { return dim3((unsigned)ceil_div(M, XC_ROWS)); }
 
@@ -1391,7 +1415,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   if (e == hipSuccess && (!few || (c.K > 0 && c.grad_bias != nullptr)))
     e = launch_kernel(loss_coef_kernel<ET>, dim3((unsigned)ceil_div(h.M, LC_THREADS)), dim3(LC_THREADS), s, r);
   XentBwdArgs p{};
-  p.hidden = st.hidden != nullptr ? reinterpret_cast<const uint8_t *>(st.hidden) : static_cast<const uint8_t *>(h.hidden);
+  p.hidden = reinterpret_cast<const uint8_t *>(st.hidden);
   p.W = static_cast<const uint8_t *>(h.W);
   p.M = h.M;
   p.H = h.H;
@@ -1493,7 +1517,7 @@ hipError_t launch_distill_forward(const DistillForward &c, hipStream_t s) {
   if (e == hipSuccess) e = stats<true>(h, u.a, c.mem.keep != 0, s);
   if (e == hipSuccess)
     e = launch_kernel(distill_rows_kernel, rows_grid(h.M), dim3(XC_ROWS * XC_SLICES), s,
-                      DistillRows{rows_args(u), c.K, ent, P, c.loss});
+                      DistillRows{rows_args(h, c.mem, u, sel), c.K, ent, P, c.loss});
   return e;
 }
 
@@ -1505,7 +1529,9 @@ hipError_t launch_policy_forward(const PolicyForward &c, hipStream_t s) {
   Select sel{nullptr, c.y.target, c.y.wide, c.y.ignore, c.head.M, c.head.V, nullptr, 0, 0};
   e = gather(c.head, u, sel, c.loss, c.logp, s);
   if (e == hipSuccess) e = stats<false>(c.head, u.a, c.mem.keep != 0, s);
-  TokenRows r = token_rows(u, c.y);
+  TokenRows r{};
+  r.r = rows_args(c.head, c.mem, u, sel);
+  r.tlogit = u.a.tlogit;
   r.logp = c.logp;
   r.advantage = c.advantage;
   r.old_logp = c.old_logp;
@@ -1531,7 +1557,9 @@ hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t s) 
                c.starts64, 2 * c.pairs};
     e = gather(c.head, u, sel, nullptr, nullptr, s);
     if (e == hipSuccess) e = stats<false>(c.head, u.a, c.mem.keep != 0, s);
-    TokenRows r = token_rows(u, c.y);
+    TokenRows r{};
+    r.r = rows_args(c.head, c.mem, u, sel);
+    r.tlogit = u.a.tlogit;
     r.logp = rowlogp;
     if (e == hipSuccess)
       e = launch_kernel(token_rows_kernel<false>, rows_grid(c.head.M), dim3(XC_ROWS * XC_SLICES), s, r);

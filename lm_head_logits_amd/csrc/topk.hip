@@ -12,10 +12,16 @@
 // with G of them a group and n groups, about K / (n G) of the row. The first
 // stretch is read once more for its keys (from the caches), the rest once. When
 // there are many keys, or they do not fit, the K largest are kept and the bound
-// rises to the last of them. The sum of exponentials is carried along per thread. Logits of -inf never become keys that way; where
-// fewer than K others are there, the first of them fill up.
+// rises to the last of them. The sum of exponentials is carried along per
+// thread. Logits of -inf never become keys that way; where fewer than K others
+// are there, the first of them fill up.
 //
 // Few rows are cut into segments, whose sorted lists a second kernel merges.
+//
+// 4096 rows of 128256 bf16, K = 64: 255 us, 4.1 TB/s; vector instructions take 57%
+// of the cycles (ten a logit: conversion, comparison, one multiply-add, the
+// exponential, its sum, and what the keys cost), the rest is waits at barriers and
+// for loads. One row of 151936 fp32, K = 20: 22 us in two launches.
 #include "group_launch.hpp"
 #include "losses_launch.hpp"
 #include "mma256.hpp"

@@ -236,6 +236,8 @@ def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossStat
     if need_bias is None:
         need_bias = bias is not None
     _need(not need_bias or bias is not None, "there is no bias to differentiate")
+    _need(saved.state.numel() == loss_state_bytes(M, H, V, saved.K, saved.keep_logits),
+          "saved is of a head of another size than weight")
     dev = hidden.device
     with _alloc_on(stream):
         dh = torch.empty_like(hidden) if need_hidden else None
@@ -292,15 +294,17 @@ def _check_reduction(reduction):
 
 def distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                  alpha: float = 1.0, bias=None, *, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
-                 reduction: str = "mean") -> torch.Tensor:
+                 keep_logits: bool | None = None, reduction: str = "mean") -> torch.Tensor:
     """Differentiable distill_forward. reduction: "none" (fp32 [M]), "sum", or
     "mean" over the rows that have entries (NaN when there are none). Losses at a
-    temperature T are usually weighted by T * T; that is left to the caller."""
+    temperature T are usually weighted by T * T; that is left to the caller.
+    keep_logits as there, here and in the functions below: False saves fp32 [M, V]
+    between the passes, the gradients stay as they are."""
     _check_reduction(reduction)
 
     def call(h, w, b, train):
         return distill_forward(h, w, teacher_ids, teacher_logits, alpha, b, temperature=temperature,
-                               teacher_lse=teacher_lse, train=train)
+                               teacher_lse=teacher_lse, train=train, keep_logits=keep_logits)
 
     (loss,) = _HeadLoss.apply(hidden, weight, bias, call)
     return _reduce(loss, reduction, lambda: ((teacher_ids >= 0) & (teacher_ids < weight.shape[0])
@@ -310,7 +314,8 @@ def distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.
 def policy_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, advantage: torch.Tensor,
                 old_logp: torch.Tensor | None = None, ref_logp: torch.Tensor | None = None, alpha: float = 1.0, bias=None,
                 *, temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
-                ignore_index: int = -100, reduction: str = "mean", return_logp: bool = False):
+                ignore_index: int = -100, keep_logits: bool | None = None, reduction: str = "mean",
+                return_logp: bool = False):
     """Differentiable policy_forward. reduction: "none" (fp32 [M]), "sum", or
     "mean" over the rows that are not left out. With return_logp also the tokens'
     log-probabilities [M], without a gradient (for the ratio's and the KL's
@@ -320,7 +325,7 @@ def policy_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor
     def call(h, w, b, train):
         return policy_forward(h, w, target, advantage, old_logp, ref_logp, alpha, b, temperature=temperature,
                               clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, ignore_index=ignore_index,
-                              train=train)
+                              train=train, keep_logits=keep_logits)
 
     loss, logp = _HeadLoss.apply(hidden, weight, bias, call)
     loss = _reduce(loss, reduction, lambda: (target != ignore_index) & (target >= 0) & (target < weight.shape[0]))
@@ -330,7 +335,8 @@ def policy_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor
 def preference_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, starts: torch.Tensor,
                     ref_logp: torch.Tensor | None = None, alpha: float = 1.0, bias=None, *, beta: float = 0.1,
                     margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False, temperature: float = 1.0,
-                    ignore_index: int = -100, reduction: str = "mean", return_logp: bool = False):
+                    ignore_index: int = -100, keep_logits: bool | None = None, reduction: str = "mean",
+                    return_logp: bool = False):
     """Differentiable preference_forward. reduction: "none" (fp32 [P]), "sum",
     or "mean" over the pairs. With return_logp also the sequences'
     log-probabilities [2 P], without a gradient (for the implicit rewards)."""
@@ -339,7 +345,7 @@ def preference_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Te
     def call(h, w, b, train):
         return preference_forward(h, w, target, starts, ref_logp, alpha, b, beta=beta, margin=margin,
                                   label_smoothing=label_smoothing, average=average, temperature=temperature,
-                                  ignore_index=ignore_index, train=train)
+                                  ignore_index=ignore_index, train=train, keep_logits=keep_logits)
 
     loss, logp = _HeadLoss.apply(hidden, weight, bias, call)
     loss = _reduce(loss, reduction, lambda: torch.ones_like(loss))

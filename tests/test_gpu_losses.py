@@ -677,3 +677,73 @@ def test_a_policy_step_with_a_tied_embedding():
     assert bool((err <= 2.0 ** -8 * want.abs() + M * 2.0 ** -24 * dh.double().abs().max() * 2 + 2.0 ** -126).all())
     values, ids, lse = L.logits_topk(L.logits(h, W), 5)
     assert float((values[:, 0] - lse).max()) <= 1e-6 and torch.equal(ids[:, 0], L.logits_rowreduce(h, W)[1])
+
+
+def left_out(c):
+    """The rows that a call leaves out."""
+    V, M = c["weight"].shape[0], c["hidden"].shape[0]
+    if c["op"] == "distill":
+        return ~((c["teacher_ids"] >= 0) & (c["teacher_ids"] < V)).any(1)
+    out = c["target"] == -100
+    if c["op"] == "preference":
+        at = torch.arange(M, device=DEV)
+        out = out | (at < c["starts"][0]) | (at >= c["starts"][-1])
+    return out
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M", [40, 64, 200, 300])
+@pytest.mark.parametrize("op", OPS)
+def test_what_stands_in_rows_that_are_left_out(op, M, bias, bad):
+    """... does not matter, to the gradients either: hidden states of padding."""
+    say(f"left out {op} M={M} bias={bias} {bad}")
+    c = make(op, 40 + M, M, 96, 1300, "bf16", bias, K=70)
+    if bias:
+        c["bias"][5] = 120.0  # its exponential alone is none
+    kw = KW[op]
+    reference(c, 0.5, kw)
+    spoilt = dict(c, hidden=c["hidden"].clone())
+    out = left_out(c)
+    assert 0 < int(out.sum()) < M
+    spoilt["hidden"][out] = bad
+    for keep in (True, False):
+        *a, sa = call(c, 0.5, kw, keep_logits=keep)
+        *b, sb = call(spoilt, 0.5, kw, keep_logits=keep)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        for x, y in zip(L.loss_backward(c["grad"], c["weight"], sa), L.loss_backward(c["grad"], c["weight"], sb)):
+            assert x is y is None or (bool(torch.isfinite(y).all()) and torch.equal(x, y))
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("M,V", [(200, 50001), (256, 41000), (256, 32769)])
+def test_few_rows_on_a_large_vocabulary(op, M, V, bias):
+    """Either side of where the rows' coefficients are found in a launch of their own."""
+    say(f"{op} M={M} V={V} bias={bias}")
+    check(make(op, M + V, M, 64, V, "bf16", bias, K=9))
+
+
+def test_a_state_belongs_to_its_sizes():
+    c = make("policy", 3, 20, 64, 1000, "bf16", False)
+    reference(c, 0.5, KW["policy"])
+    *_, saved = call(c, 0.5, KW["policy"])
+    for V in (500, 1500):
+        with pytest.raises(ValueError, match="saved"):
+            L.loss_backward(c["grad"], torch.zeros(V, 64, dtype=torch.bfloat16, device=DEV), saved)
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("op", OPS)
+def test_differentiable_with_and_without_kept_logits(op, keep):
+    c = make(op, 9, 50, 64, 700, "bf16", False)
+    reference(c, 1.0, KW[op])
+    fn = dict(distill=L.distillation, policy=L.policy_loss, preference=L.preference_loss)[op]
+    args = dict(distill=("teacher_ids", "teacher_logits"), policy=("target", "advantage", "old", "ref"),
+                preference=("target", "starts", "ref"))[op]
+    got = []
+    for more in (dict(), dict(keep_logits=keep)):
+        h, w = c["hidden"].clone().requires_grad_(), c["weight"].clone().requires_grad_()
+        fn(h, w, *[c[k] for k in args], reduction="sum", **KW[op], **more).backward()
+        got.append((h.grad, w.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
