@@ -167,7 +167,7 @@ struct DistillPrep {
   float T;
   int32_t *sid;    // [M, K]
   float *sp;       // [M, K]
-  uint16_t *ptr;   // [M, nvt + 1] entries before each tile
+  uint16_t *ptr;   // [M, nvt + 1] entries before each tile; nullptr where t is kept
   float *ent;      // [M] sum p log p
   float *P;        // [M] sum p
 };
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * DP_WAVES) void distill_prep_kernel(DistillPrep
     }
   sched_fence();
   const int64_t nvt = (c.V + MM_T - 1) / MM_T;
-  for (int64_t t = lane; t <= nvt; t += 64) {
+  for (int64_t t = lane; c.ptr != nullptr && t <= nvt; t += 64) {
     int lo = 0, hi = count;  // the first of the present entries at or past the tile's first column
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -393,10 +393,10 @@ struct LossFwdArgs {
   int target64;
   int64_t ignore;
   float2 *part;        // [vocabulary tile][M] {largest t, sum of exp(t - largest)}
-  float *tlogit;       // [M] t at the target (rows with one)
+  float *tlogit;       // neither: [M] t at the target (rows with one)
   const int32_t *sid;  // PICK: the teacher's entries (distill_prep_kernel)
   const uint16_t *ptr;
-  float *tk;           // [M, K] t at the entries
+  float *tk;           // ... [M, K] t at them
   int64_t K;
   float *t;            // KEEP: [M, padded V]
   __device__ __forceinline__ void set_rows() {
@@ -411,10 +411,13 @@ struct LossFwdArgs {
 // PICK: t at the rows' entries in the tile instead of at one target. Through
 // LDS, 32 rows at a time: all 256 columns of the rows are written, then 16
 // threads a row take that row's entries from it. Groups of rows without an
-// entry are left out. What 64 entries a row add to a tile of H = 4096 (92 us) is
-// not seen between cards.
+// entry are left out. (4096 rows with 64 entries, H = 4096, V = 128256: 0.16 ms of
+// 3.08.)
 //
-// KEEP: t of the whole tile to memory, for the backward pass.
+// KEEP: t of the whole tile to memory, for the backward pass (0.18 ms). The
+// kernels that make the rows' losses read from it what else is picked here: with
+// those entries picked here all the same a forward pass took 0.27 ms longer than
+// one with a target a row, so 0.03 ms.
 template <int ET, bool PICK, bool KEEP>
 struct LossStats {
   LossFwdArgs p;
@@ -468,7 +471,7 @@ struct LossStats {
                   __builtin_bit_cast(u32x4, tile.c[x][y][i][j]), rs,
                   row < rows ? (uint32_t)((row * ldt + MmTile<ET>::col(at.wn, at.lg, y, j)) * 4) : OFF_NONE, 0, LOAD_DEFAULT);
         }
-        if constexpr (!PICK) {
+        if constexpr (!PICK && !KEEP) {
           const int32_t yt = m < p.M ? p.column(m) - (int32_t)n0 : -1;
           if (has_column<ET>(at, 0, yt) || has_column<ET>(at, 1, yt)) {
             float v = 0.0f;
@@ -649,6 +652,7 @@ struct RowsArgs {
   }
   __device__ __forceinline__ int64_t rows() const { return st.count != nullptr ? *st.count : M; }
   __device__ __forceinline__ int64_t row(int64_t m) const { return st.rows != nullptr ? st.rows[m] : m; }
+  int64_t ldt;              // of the kept t; 0 where it is not
 };
 struct DistillRows {
   RowsArgs r;
@@ -662,9 +666,16 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(Disti
   const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r, n = c.r.rows();
   if (m - r >= n) return;  // the whole work-group
   c.r.copy(m - r);
+  const int64_t row = m < n ? c.r.row(m) : 0;
+  if (c.r.ldt != 0 && m < n) {
+#pragma unroll 1
+    for (int64_t k = sl; k < c.K; k += XC_SLICES) {  // the thread's own, below
+      const int32_t id = c.r.st.ids[row * c.K + k];
+      if (id != NO_ID) c.r.st.tk[row * c.K + k] = c.r.st.t[m * c.r.ldt + id];
+    }
+  }
   const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
   const float ls = logf(f.y);
-  const int64_t row = m < n ? c.r.row(m) : 0;
   float sum = 0.0f;
   if (m < n)
     for (int64_t k = sl; k < c.K; k += XC_SLICES) {
@@ -721,13 +732,18 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void token_rows_kernel(TokenRo
   const int64_t m = (int64_t)blockIdx.x * XC_ROWS + r, n = c.r.rows();
   if (m - r >= n) return;  // the whole work-group
   c.r.copy(m - r);
+  const bool packed = c.r.st.rows != nullptr;
+  int64_t y = -1;
+  float t = 0.0f;
+  if (sl == 0 && m < n) {
+    y = packed ? c.r.st.y[m] : c.r.column(m);
+    if (y >= 0) t = c.r.ldt != 0 ? c.r.st.t[m * c.r.ldt + y] : c.tlogit[m];
+  }
   const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
   if (sl != 0 || m >= n) return;
   const float ls = logf(f.y);
   const int64_t row = c.r.row(m);
-  const bool packed = c.r.st.rows != nullptr;
-  const int64_t y = packed ? c.r.st.y[m] : c.r.column(m);
-  const float logp = y >= 0 ? log_q(c.tlogit[m], f, ls) : 0.0f;
+  const float logp = y >= 0 ? log_q(t, f, ls) : 0.0f;
   c.r.st.lse[m] = y >= 0 ? row_lse(f, ls) : __builtin_inff();
   if (!packed) c.r.st.y[m] = (int32_t)y;
   c.logp[row] = logp;
@@ -1380,7 +1396,7 @@ hipError_t stats(const LossHead &h, const LossFwdArgs &a, hipStream_t s) {
 }
 template <bool PICK>
 hipError_t stats(const LossHead &h, const LossFwdArgs &a, bool keep, hipStream_t s) {
-  return keep ? stats<PICK, true>(h, a, s) : stats<PICK, false>(h, a, s);
+  return keep ? stats<false, true>(h, a, s) : stats<PICK, false>(h, a, s);
 }
 void set_targets(LossFwdArgs &a, const LossTargets &y) {
   a.target = y.target;
@@ -1389,7 +1405,8 @@ void set_targets(LossFwdArgs &a, const LossTargets &y) {
 }
 RowsArgs rows_args(const LossHead &h, const LossMemory &mem, const Setup &u, const Select &sel) {
   return RowsArgs{u.a.part, h.M, ceil_div(h.V, MM_T), u.st, sel,
-                  mem.state != nullptr && u.st.rows == nullptr ? static_cast<const uint16_t *>(h.hidden) : nullptr, h.H};
+                  mem.state != nullptr && u.st.rows == nullptr ? static_cast<const uint16_t *>(h.hidden) : nullptr, h.H,
+                  mem.keep != 0 ? padded(h.V) : 0};
 }
 dim3 rows_grid(int64_t M) { return dim3((unsigned)ceil_div(M, XC_ROWS)); }
 
@@ -1504,7 +1521,7 @@ hipError_t launch_distill_forward(const DistillForward &c, hipStream_t s) {
   uint16_t *const ptr = reinterpret_cast<uint16_t *>(u.ws + u.lay.ptr);
   float *const ent = reinterpret_cast<float *>(u.ws + u.lay.ent), *const P = reinterpret_cast<float *>(u.ws + u.lay.P);
   const DistillPrep d{c.ids, c.ids64, h.M, h.V, c.K, c.logits, c.logits_type, c.teacher_lse, h.temperature,
-                      u.st.ids, u.st.p, ptr, ent, P};
+                      u.st.ids, u.st.p, c.mem.keep != 0 ? nullptr : ptr, ent, P};
   e = launch_kernel(c.K <= 64 ? distill_prep_kernel<1> : c.K <= 256 ? distill_prep_kernel<4> : distill_prep_kernel<16>,
                     numbered_grid(ceil_div(h.M, DP_WAVES)), dim3(64 * DP_WAVES), s, d);
   Select sel{};
