@@ -866,8 +866,12 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // 12 against 42).
 // `cap`: row tiles times splits that the sums have room for.
 struct SplitPlan {
-  int32_t ksplit, splits;
+  int32_t splits;
 };
+// The columns of a split of a piece of np: those of the shorter, last piece are shorter.
+__host__ __device__ __forceinline__ int64_t split_of(int64_t np, int64_t splits) {
+  return ((np + splits - 1) / splits + 63) / 64 * 64;
+}
 __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, int32_t cap, SplitPlan *out) {
   const uint32_t nmt = (n + MM_T - 1) / MM_T, tiles = nmt * ((H + MM_T - 1) / MM_T), cus = 256;
   const uint32_t s = threadIdx.x + 1;
@@ -884,8 +888,8 @@ __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, in
     }
   }
   if (threadIdx.x == 0) {
-    out->ksplit = ((vp + splits - 1) / splits + 63) / 64 * 64;
-    out->splits = (vp + out->ksplit - 1) / out->ksplit;
+    const int32_t k = (int32_t)split_of(vp, splits);
+    out->splits = (vp + k - 1) / k;
   }
 }
 
@@ -1037,7 +1041,7 @@ struct OnDevice {
   __device__ __forceinline__ void apply(XentBwdArgs &p) const {
     if (count == nullptr) return;
     p.M = mm_uni(*count);
-    p.ksplit = (int64_t)mm_uni((uint32_t)plan->ksplit);
+    p.ksplit = split_of(p.np, (int64_t)mm_uni((uint32_t)plan->splits));
   }
 };
 
@@ -1309,10 +1313,20 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
                                                 mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
 }
 
+// Pieces of up to an eighth more columns, where G^T hidden then takes fewer
+// rounds of work-groups in all: 594 tiles of columns by 8 of H (V = 151936, H = 2048)
+// in two pieces of 297 are twice ten rounds for 256 CUs, in 320 and 274 ten and nine.
+int64_t whole_rounds(int64_t vp, int64_t H, int64_t V) {
+  const int64_t nht = ceil_div(H, MM_T), all = ceil_div(V, MM_T), n = vp / MM_T, unit = ceil_div(256, nht);
+  auto rounds = [&](int64_t per) { return all / per * ceil_div(per * nht, 256) + ceil_div(all % per * nht, 256); };
+  const int64_t more = ceil_div(n, unit) * unit;
+  return n < all && more < all && more <= n + n / 8 && rounds(more) < rounds(n) ? more * MM_T : vp;
+}
+
 // bwd_plan's pieces, with room for the sums of grad_hidden of whatever rows are
 // worked on: `cap` row tiles times splits.
 struct BackwardLayout {
-  int64_t vp, cap, ksplit;
+  int64_t vp, cap;
   int splits;
   int64_t scale, plan, rows, col, dh, G, entries, bytes;
 };
@@ -1326,9 +1340,8 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
     return o;
   };
   const int64_t nmt = ceil_div(M, MM_T);
-  b.vp = pl.vp;
-  b.ksplit = pl.ksplit;
-  b.splits = (int)pl.splits;
+  b.vp = whole_rounds(pl.vp, H, V);
+  b.splits = (int)ceil_div(b.vp, split_of(b.vp, pl.splits));
   // fewer rows than the call's take more splits: with three fifths of 4096 rows
   // (H = 4096) 160 tiles would leave 96 of 256 CUs without one; three splits of
   // them fill 94%
@@ -1446,7 +1459,6 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   p.colpart = c.grad_bias != nullptr ? reinterpret_cast<float *>(ws + lay.col) : nullptr;
   p.dh = reinterpret_cast<float *>(ws + lay.dh);
   p.dw = static_cast<uint16_t *>(c.grad_W);
-  p.ksplit = lay.ksplit;
   const OnDevice dev{st.count, plan};
   const int64_t nmt = ceil_div(h.M, MM_T), nht = ceil_div(h.H, MM_T);
   // whole numbers of 2^-shift: their sum over all rows stays below 2^62
@@ -1462,6 +1474,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
     p.first = v0 == 0;
     const int64_t nv = h.V - v0 < lay.vp ? h.V - v0 : lay.vp;
     p.np = ceil_div(nv, MM_T) * MM_T;
+    p.ksplit = split_of(p.np, lay.splits);
     if (c.mem.keep)
       e = c.grad_bias != nullptr ? kept_grad<ET, true>(p, dev, st.t, padded(h.V), r, false, s)
                                  : kept_grad<ET, false>(p, dev, st.t, padded(h.V), r, c.K > 0, s);
