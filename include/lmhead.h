@@ -446,7 +446,7 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
  * three calls above, whose state is given and whose other arguments are the same
  * (K: 0 but for lmhead_distill_forward). hidden's values are not read again: the state
  * has the rows that are worked on.
- *   grad_loss   fp32 [M], or [pairs]                            (device, read)
+ *   grad_loss   fp32 [M], or [pairs]; NULL: zeros               (device, read)
  *   grad_hidden, grad_W, grad_bias, workspace   as in lmhead_xent_backward, with
  *               lmhead_loss_backward_workspace_bytes(M, H, V, K, keep_logits, grad_bias != NULL)
  *               bytes

@@ -930,6 +930,47 @@ template <int ET>
 __device__ __forceinline__ float find_scale(const LossCoef &p) {
   float f = 1.0f;
   __shared__ float sh[LC_THREADS / 64];
+  // The samples, unscaled entries of G: their loads go out before the rows'.
+  constexpr int S = LC_SAMPLES / LC_THREADS;
+  float entry[S];
+  const int64_t all = p.distill ? p.all_rows * p.K : p.M;
+  const int samples = (int)(all < LC_SAMPLES ? all : LC_SAMPLES);
+  if (!p.distill) {
+    float o[S];
+    int32_t u[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int m = threadIdx.x + k * LC_THREADS;
+      o[k] = m < samples ? p.own[m] : 0.0f;
+      u[k] = m < samples ? p.up[m] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) entry[k] = o[k] == 0.0f ? 0.0f : __fmul_rn(o[k], p.g[u[k]]);
+  } else {
+    int32_t id[S];
+    int64_t m[S];
+    float g[S], t[S], pk[S], c[S], lse[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int e = threadIdx.x + k * LC_THREADS;
+      const int64_t row = (uint32_t)(e < samples ? e : 0) / (uint32_t)p.K;
+      id[k] = e < samples ? p.sid[e] : NO_ID;
+      m[k] = p.inv != nullptr ? (int64_t)p.inv[row] : row;
+      g[k] = p.g[row];
+      t[k] = e < samples ? p.tk[e] : 0.0f;
+      pk[k] = e < samples ? p.p[e] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      c[k] = m[k] < 0 ? 0.0f : p.coef[m[k]];
+      lse[k] = m[k] < 0 ? 0.0f : p.lse[m[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+      entry[k] = id[k] == NO_ID || c[k] == 0.0f
+                     ? 0.0f
+                     : __fmul_rn(g[k], __fsub_rn(__fmul_rn(c[k], exp_diff(t[k], lse[k])), pk[k]));
+  }
   float mx = 0.0f;
   for (int64_t m0 = threadIdx.x; m0 < p.M; m0 += 8 * LC_THREADS) {
     float c[8], g[8];
@@ -979,18 +1020,9 @@ __device__ __forceinline__ float find_scale(const LossCoef &p) {
         back = __fmul_rn(back, 1.0f / LC_STEP);
       }
     };
-    if (!p.distill) {
-      for (int64_t m = threadIdx.x; m < p.M && m < LC_SAMPLES; m += LC_THREADS) {
-        const float o = p.own[m];
-        sample(o == 0.0f ? 0.0f : __fmul_rn(o, p.g[p.up[m]]));
-      }
-    } else {
-      for (int64_t e = threadIdx.x; e < p.all_rows * p.K && e < LC_SAMPLES; e += LC_THREADS) {
-        const int64_t row = e / p.K, m = p.inv != nullptr ? p.inv[row] : row;
-        if (m < 0 || p.sid[e] == NO_ID || p.coef[m] == 0.0f) continue;
-        sample(__fmul_rn(p.g[row], __fsub_rn(__fmul_rn(p.coef[m], exp_diff(p.tk[e], p.lse[m])), p.p[e])));
-      }
-    }
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+      if (k * LC_THREADS < samples) sample(entry[k]);
 #pragma unroll
     for (int j = 0; j < LC_TRIES; ++j) err[j][threadIdx.x] = e2[j];
     __syncthreads();
@@ -1603,9 +1635,10 @@ hipError_t launch_preference_forward(const PreferenceForward &c, hipStream_t s) 
 }
 
 hipError_t launch_loss_backward(const LossBackward &c, hipStream_t s) {
-  if (c.head.M == 0) {  // sums over no rows
+  if (c.head.M == 0 || c.grad_loss == nullptr) {  // sums over no rows, or of zeros
     hipError_t e = hipSuccess;
-    if (c.grad_W != nullptr) e = zero_words(c.grad_W, c.head.V * c.head.H / 2, s);
+    if (c.grad_hidden != nullptr && c.head.M > 0) e = zero_words(c.grad_hidden, c.head.M * c.head.H / 2, s);
+    if (e == hipSuccess && c.grad_W != nullptr) e = zero_words(c.grad_W, c.head.V * c.head.H / 2, s);
     if (e == hipSuccess && c.grad_bias != nullptr) e = zero_words(c.grad_bias, c.head.V, s);
     return e;
   }

@@ -195,7 +195,6 @@ lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, con
   if (!teacher_count_ok(K)) return LMHEAD_ERR_INVALID;
   if (grad_hidden == nullptr && grad_W == nullptr && grad_bias == nullptr) return LMHEAD_OK;
   if (M > 0) {
-    // grad_loss may be NULL where there is no pair: then no row reads it
     if (hidden == nullptr || W == nullptr || state == nullptr ||
         state_bytes < lmhead_loss_state_bytes(M, H, V, K, keep_logits) || workspace == nullptr ||
         workspace_bytes < lmhead_loss_backward_workspace_bytes(M, H, V, K, keep_logits, grad_bias != nullptr))

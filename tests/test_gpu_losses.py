@@ -747,3 +747,20 @@ def test_differentiable_with_and_without_kept_logits(op, keep):
         fn(h, w, *[c[k] for k in args], reduction="sum", **KW[op], **more).backward()
         got.append((h.grad, w.grad))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_no_upstream_gradient_is_zeros(M):
+    """The C call with grad_loss NULL."""
+    from lm_head_logits_amd import _lib
+    H, V = 64, 333
+    c = make("policy", M, M, H, V, "bf16", True)
+    reference(c, 0.5, KW["policy"])
+    *_, s = call(c, 0.5, KW["policy"])
+    dh, dw, db = torch.ones_like(c["hidden"]), torch.ones_like(c["weight"]), torch.ones_like(c["bias"])
+    ws = torch.empty(L.loss_backward_workspace_bytes(M, H, V, 0, True, True), dtype=torch.uint8, device=DEV)
+    st = _lib.load().lmhead_loss_backward(c["hidden"].data_ptr(), M, H, c["weight"].data_ptr(), V, 0.5, c["bias"].data_ptr(),
+                                          _lib.LMHEAD_BF16, 1.0, 0, None, s.state.data_ptr(), s.state.numel(), 1,
+                                          dh.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel(),
+                                          torch.cuda.current_stream().cuda_stream)
+    assert st == _lib.OK and all(bool((t == 0).all()) for t in (dh, dw, db))
