@@ -31,9 +31,9 @@
 // Bound by the matrix pipes (mma256.hpp) but for few rows, where the weight's
 // bytes bind, and short products (H = 2048, some hundred rows), whose tiles'
 // epilogues show. 4096 rows, H = 4096, V = 128256, 64 teacher's logits a row: forward
-// 3.3 ms (0.25 of it t's stores), per piece of 32256 columns G from t 0.143 ms (792
-// MB at 5.5 TB/s), G W 0.68-0.73 ms (1.46-1.57 PFLOP/s), G^T hidden 0.77-0.81 (1.31-1.38);
-// 10.0-10.2 ms in all, 12.5 with t made again.
+// 3.17-3.24 ms (0.13-0.28 of it t's stores), per piece of 32256 columns G from t 0.144 ms
+// (800 MB at 5.5 TB/s), G W 0.68-0.73 ms (1.46-1.57 PFLOP/s), G^T hidden 0.77-0.81
+// (1.31-1.38); 9.7-9.95 ms in all, 12.5 with t made again.
 //
 // Roundings: t, the statistics, probabilities, coefficients and grad_bias are
 // fp32, sums over a sequence and pairs' margins fp64. G is rounded to the inputs'
@@ -414,7 +414,7 @@ struct LossFwdArgs {
 // entry are left out. (4096 rows with 64 entries, H = 4096, V = 128256: 0.16 ms of
 // 3.08.)
 //
-// KEEP: t of the whole tile to memory, for the backward pass (0.18 ms). The
+// KEEP: t of the whole tile to memory, for the backward pass (0.13-0.28 ms). The
 // kernels that make the rows' losses read from it what else is picked here: with
 // those entries picked here all the same a forward pass took 0.27 ms longer than
 // one with a target a row, so 0.03 ms.
@@ -1105,13 +1105,14 @@ __device__ __forceinline__ uint16_t entry_of_G(const RowCoef &r, const int32_t *
 
 // G of a piece from the kept t: the same operations on the same values as the
 // product's epilogue, so the same bits. 2048 columns and R rows a work-group,
-// eight columns a thread; four rows' loads in flight: 5.5 TB/s of reads and writes.
+// eight columns a thread; four rows' loads in flight: 5.5 TB/s of reads and writes (as with R = 8 or 16).
 // grad_bias: the column sums of R rows.
 //
 // FEW (a small G of rows that are not packed): the rows' coefficients and their
 // scale are found here, by every work-group, and the teacher's entries are
 // written here where grad_bias does not want their sums; both are launches of
-// their own otherwise (a step of 37 rows, H = 256, V = 4096: 53.8 -> 50.0 us).
+// their own otherwise (a step of 37 rows, H = 256, V = 4096: 53.8 -> 50.0 us, and
+// 48.1 with the scale's loads at once).
 constexpr int KEPT_FEW = 4, KEPT_MANY = 32;  // rows a work-group: few where there are few, for the sake of work-groups
 constexpr int64_t KEPT_GROUPS = 1024;        // work-groups up to which each finds the scale: one round of them
 int kept_rows(int64_t M) { return M <= LR_DIRECT ? KEPT_FEW : KEPT_MANY; }
