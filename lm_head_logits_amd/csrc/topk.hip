@@ -342,7 +342,9 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
     if (n >= K) {
       const uint32_t last = kth, infinite = order_of(__builtin_inff());
       bound = fmaxf(last < infinite ? of_order(last + 1) : __builtin_inff(), TK_LOWEST);
-      raise(bound);
+      // (not the bound, which may lie above the row's largest logit: where a step of
+      // fp32 there is an exponent of 128 or more, no term would be left)
+      raise(of_order(last));
     }
   };
 

@@ -1,0 +1,30 @@
+"""logits_topk: the log-sum-exp of rows whose logits, divided by the temperature, are
+so large that one step of fp32 there is a factor of e^88 and more. The row's largest
+term is 1 and nothing is above it, so that lse is that of the largest logit whatever
+the steps below it; it is infinite only past fp32's range. Bounds: test_gpu_topk.py."""
+import pytest
+import torch
+
+from gpu_util import DEV, say
+from test_gpu_topk import DT, check, logits
+
+pytestmark = pytest.mark.gpu
+V = 20011
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("M", [1, 515])
+@pytest.mark.parametrize("T", [1.0, 2.0])
+def test_rows_of_one_low_value(dt, M, T):
+    """Rows of nothing but the type's lowest value, or of -1e9, as a mask leaves them:
+    several segments a row, and one."""
+    for k in (1, 2, 64, 300, 1024):
+        say(f"topk lowest {dt} M={M} T={T} k={k}")
+        lse = check(torch.full((M, V), torch.finfo(DT[dt]).min, dtype=DT[dt], device=DEV), k, T)[2]
+        assert bool(lse.isfinite().all())
+        if dt != "f16":
+            assert bool(check(torch.full((M, V), -1e9, dtype=DT[dt], device=DEV), k, 0.7)[2].isfinite().all())
+            x = logits(k, M, V, dt)  # ... with one row of numbers among them, and the mask over half of another
+            x[1:] = torch.finfo(DT[dt]).min
+            x[0, ::2] = torch.finfo(DT[dt]).min
+            assert bool(check(x, k, T)[2].isfinite().all())
