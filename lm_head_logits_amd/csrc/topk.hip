@@ -35,6 +35,10 @@ constexpr int TK_CAP = 4096;   // keys in LDS
 constexpr int TK_TILE = 4;     // 16-byte pieces a thread in flight
 constexpr int TK_FIRST = 8;    // ... in the first stretch
 constexpr int TK_COUNT = 512;  // keys up to which places are counted, not sorted
+// Up to this ref / temperature (in powers of 2) x c - ref c is one multiply-add: what the
+// product's rounding adds to the exponent, 2^-5, is no more than lse's own rounding. Past
+// 2^31 it would be 128: every term 0, or infinite.
+constexpr float TK_PRODUCT = 1048576.0f;
 constexpr float TK_NEG_INF = -__builtin_inff();
 constexpr float TK_LOWEST = -__FLT_MAX__;
 
@@ -274,14 +278,14 @@ __global__ __launch_bounds__(TK_THREADS, 4) void topk_part_kernel(TopkPart p) {
   };
   // adds a tile to the thread's sum: none of its logits is above ref
   auto add = [&](const u32x4 (&w)[TK_TILE]) {
-    if (fabsf(ref) < 1e30f) {
-      const float rc = -__fmul_rn(ref, p.c);
+    const float rc = -__fmul_rn(ref, p.c);
+    if (fabsf(rc) < TK_PRODUCT) {
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k)
 #pragma unroll
         for (int e = 0; e < N; ++e)
           sum = __fadd_rn(sum, __builtin_amdgcn_exp2f(__fmaf_rn(Piece<T>::at(w[k], e), p.c, rc)));
-    } else {  // its product with c may not be finite: the difference first
+    } else {  // the difference first
 #pragma unroll
       for (int k = 0; k < TK_TILE; ++k)
 #pragma unroll

@@ -28,3 +28,22 @@ def test_rows_of_one_low_value(dt, M, T):
             x[1:] = torch.finfo(DT[dt]).min
             x[0, ::2] = torch.finfo(DT[dt]).min
             assert bool(check(x, k, T)[2].isfinite().all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 600])
+def test_large_quotients(dt, M):
+    """The largest logit's product with log2(e) / T past 2^31: half a step of it is
+    an exponent of 128."""
+    for top, T in ((5e9, 1.0), (5.3e9, 0.7), (7.7e9, 1.0), (1e12, 1.0), (-9e9, 1.0), (100.0, 1e-8), (93.7, 3e-9), (9e29, 1e-8),
+                   (3e38, 1.0), (-3e38, 1.0), (9e29, 1e-9), (-9e29, 1e-9)):
+        for k in (1, 20, 300):
+            say(f"topk top={top} T={T} {dt} M={M} k={k}")
+            x = logits(k, M, V, dt)
+            if top < 0:  # every logit far below 0
+                x = x.float().abs().mul_(top * 1e-2).add_(top).to(DT[dt])
+            else:
+                at = torch.arange(M, device=DEV)
+                x[at, (at * 7919 + 40) % V] = top
+                x[at, (at * 104729 + 19000) % V] = top * 0.99
+            check(x, k, T)
