@@ -551,8 +551,10 @@ template <typename T>
 hipError_t topk(const TopkArgs &c, hipStream_t s) {
   const TopkPlan pl = topk_plan(c.M, c.V, c.K, sizeof(T));
   uint8_t *const ws = static_cast<uint8_t *>(c.workspace);
+  // (a temperature below fp32's normal numbers: a difference of 0 stays one)
+  const double factor = 1.4426950408889634 / (double)c.temperature;
   const TopkPart p{static_cast<const uint8_t *>(c.logits), c.M, c.V, c.ld * (int64_t)sizeof(T), (int)c.K, pl.segments,
-                   (float)(1.4426950408889634 / (double)c.temperature), c.temperature, c.values, c.ids, c.lse,
+                   (float)(factor < __FLT_MAX__ ? factor : __FLT_MAX__), c.temperature, c.values, c.ids, c.lse,
                    reinterpret_cast<uint64_t *>(ws + pl.lists), reinterpret_cast<float2 *>(ws + pl.sums)};
   hipError_t e = launch_kernel(topk_part_kernel<T>, numbered_grid(c.M * pl.segments), dim3(TK_THREADS), s, p);
   if (e == hipSuccess && pl.segments > 1)

@@ -2,6 +2,8 @@
 so large that one step of fp32 there is a factor of e^88 and more. The row's largest
 term is 1 and nothing is above it, so that lse is that of the largest logit whatever
 the steps below it; it is infinite only past fp32's range. Bounds: test_gpu_topk.py."""
+import math
+
 import pytest
 import torch
 
@@ -47,3 +49,16 @@ def test_large_quotients(dt, M):
                 x[at, (at * 7919 + 40) % V] = top
                 x[at, (at * 104729 + 19000) % V] = top * 0.99
             check(x, k, T)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_the_least_temperatures(dt):
+    """log2(e) / T past fp32's range."""
+    for T in (1e-38, 1e-39, 1e-40):
+        for M in (1, 600):
+            say("topk T", T, dt, M)
+            lse = check(torch.zeros(M, V, dtype=DT[dt], device=DEV), 7, T)[2]
+            assert bool(((lse - math.log(V)).abs() < 1e-4).all())
+            x = logits(5, M, V, dt)
+            for y in (x, -x.abs() - 1):  # -1.0005 / 1e-38 is a number yet; the others are infinite
+                check(y, 7, T)
