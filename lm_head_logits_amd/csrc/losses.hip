@@ -897,6 +897,7 @@ constexpr int LC_THREADS = 256;
 constexpr int64_t LC_ONE = 32768;
 constexpr float LC_STEP = 0.95760328f;  // 2^(-1 / 16)
 constexpr int LC_TRIES = 16, LC_SAMPLES = 4 * LC_THREADS;
+constexpr int F16_TOP = 14;  // fp16 G is scaled to 2^14 at most, bf16 G to 1
 struct LossCoef {
   const float *g;
   int64_t M;
@@ -904,7 +905,7 @@ struct LossCoef {
   const int32_t *y, *up, *count;
   int distill;
   float top;
-  float *scale;
+  float *scale;                   // {the scale f, 1 / f, find_scale's exponent}
   RowCoef *rows;
   int have_scale, write_rows;
   SplitPlan *plan;
@@ -925,9 +926,10 @@ struct LossCoef {
     return RowCoef{__fmul_rn(a, f), __fmul_rn(b, f), lse[m], distill ? -1 : y[m]};
   }
 };
-// The scale: all threads of a work-group, all rows.
+// The scale: all threads of a work-group, all rows. exponent: no finite coefficient times
+// the scale is above 2^exponent.
 template <int ET>
-__device__ __forceinline__ float find_scale(const LossCoef &p) {
+__device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
   float f = 1.0f;
   __shared__ float sh[LC_THREADS / 64];
   // The samples, unscaled entries of G: their loads go out before the rows'.
@@ -997,8 +999,10 @@ __device__ __forceinline__ float find_scale(const LossCoef &p) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < LC_THREADS / 64; ++w) mx = fmaxf(mx, sh[w]);
+  exponent = ilogbf(mx > 0.0f ? mx : 1.0f) + 1;
   // f and 1 / f both well inside the normal range, else no scale
   if (mx > 1e-30f && mx < 1e30f) {
+    exponent = ET == ET_F16 ? F16_TOP : 0;
     f = __fdiv_rn(p.top, mx);
     __shared__ float err[LC_TRIES][LC_THREADS + 1];
     float e2[LC_TRIES] = {};
@@ -1057,10 +1061,12 @@ __global__ __launch_bounds__(LC_THREADS) void loss_coef_kernel(LossCoef p) {
     if (blockIdx.x == 0 && threadIdx.x < 64 && !p.have_scale)
       plan_splits((int32_t)p.M, (int32_t)p.H, (int32_t)p.vp, (int32_t)p.cap, p.plan);
   }
-  const float f = p.have_scale ? p.scale[0] : find_scale<ET>(p);
+  int exponent = 0;
+  const float f = p.have_scale ? p.scale[0] : find_scale<ET>(p, exponent);
   if (!p.have_scale && blockIdx.x == 0 && threadIdx.x == 0) {
     p.scale[0] = f;
     p.scale[1] = __fdiv_rn(1.0f, f);
+    p.scale[2] = (float)exponent;
   }
   const int64_t m = (int64_t)blockIdx.x * LC_THREADS + threadIdx.x;
   if (p.write_rows && m < p.M) p.rows[m] = p.row(m, f);
@@ -1128,7 +1134,8 @@ __global__ __launch_bounds__(256) void loss_kept_kernel(XentBwdArgs p, OnDevice 
   if (m0 >= p.M) return;
   float f = 1.0f;
   if constexpr (FEW) {
-    f = find_scale<ET>(few);
+    int exponent;  // loss_coef_kernel leaves it, where the entries' sums want it
+    f = find_scale<ET>(few, exponent);
     if (g == 0 && threadIdx.x == 0) {
       few.scale[0] = f;
       few.scale[1] = __fdiv_rn(1.0f, f);
@@ -1203,14 +1210,18 @@ hipError_t kept_grad(const XentBwdArgs &p, const OnDevice &dev, const float *t, 
 // The entries of a piece.
 //
 // grad_bias: what the entries add to it, as whole numbers of 2^-shift of the
-// largest coefficient, so that the order of the additions does not matter.
+// largest coefficient, so that the order of the additions does not matter. (Of the
+// power of two above it, scaled or, outside the scale's range, as it is.)
+__device__ __forceinline__ double entry_unit(const float *scale, int shift) {
+  return ldexp(1.0, shift - (int)scale[2]);
+}
 struct DistillEntries {
   XentBwdArgs b;
   int64_t K;
   const int32_t *sid, *inv;
   const float *p, *tk;
   unsigned long long *bias;  // [V] or nullptr
-  double unit;               // 2^shift / top
+  int shift;
 };
 template <int ET>
 __global__ __launch_bounds__(256) void distill_entries_kernel(DistillEntries c) {
@@ -1223,8 +1234,9 @@ __global__ __launch_bounds__(256) void distill_entries_kernel(DistillEntries c) 
   const RowCoef r = c.b.rows[m];
   reinterpret_cast<uint16_t *>(c.b.G)[m * c.b.ldg + (id - c.b.v0)] = entry_of_G<ET>(r, c.sid, c.p, c.tk, row, c.K, k);
   if (c.bias != nullptr) {
-    const double x = -(double)r.b * (double)c.p[e] * c.unit;
-    // what is not finite makes the whole row of G so, and with it every sum
+    const double x = -(double)r.b * (double)c.p[e] * entry_unit(c.b.scale, c.shift);
+    // (below 2^(shift + 1) but for what is not finite, which makes the whole row of G so,
+    // and with it every sum)
     if (fabs(x) < 0x1p62) atomicAdd(c.bias + id, (unsigned long long)llrint(x));
   }
 }
@@ -1242,7 +1254,7 @@ hipError_t zero_words(void *p, int64_t n, hipStream_t s) {
 // ascending order, the entries' share, and 1 / T.
 __global__ __launch_bounds__(256) void loss_bias_kernel(const float *__restrict__ colpart, int64_t M,
                                                         const int32_t *__restrict__ count, int tile, int64_t vp, int64_t n, const long long *__restrict__ entries,
-                                                        const float *__restrict__ scale, double unit, float T,
+                                                        const float *__restrict__ scale, int shift, float T,
                                                         float *__restrict__ db) {
   const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (v >= n) return;
@@ -1250,7 +1262,7 @@ __global__ __launch_bounds__(256) void loss_bias_kernel(const float *__restrict_
   const int64_t nmt = ((count != nullptr ? *count : M) + tile - 1) / tile;
 #pragma unroll 8
   for (int64_t t = 0; t < nmt; ++t) s = __fadd_rn(s, colpart[t * vp + v]);
-  if (entries != nullptr) s = (float)((double)s + (double)entries[v] / unit * (double)scale[1]);
+  if (entries != nullptr) s = (float)((double)s + (double)entries[v] / entry_unit(scale, shift) * (double)scale[1]);
   db[v] = __fdiv_rn(s, T);
 }
 
@@ -1379,7 +1391,7 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
   // (H = 4096) 160 tiles would leave 96 of 256 CUs without one; three splits of
   // them fill 94%
   b.cap = pl.splits > 3 || M <= LR_DIRECT ? pl.splits * nmt : 3 * nmt;
-  b.scale = take(8);
+  b.scale = take(12);
   b.plan = take(sizeof(SplitPlan));
   b.rows = take(16 * M);
   b.col = take(bias ? 4 * (keep ? ceil_div(M, kept_rows(M)) : nmt) * b.vp : 0);
@@ -1465,7 +1477,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   float *const scale = reinterpret_cast<float *>(ws + lay.scale);
   SplitPlan *const plan = reinterpret_cast<SplitPlan *>(ws + lay.plan);
   RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + lay.rows);
-  const float top = ET == ET_F16 ? 16384.0f : 1.0f;
+  const float top = ET == ET_F16 ? (float)(1 << F16_TOP) : 1.0f;
   LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, st.count, c.K > 0, top, scale, rows, 0, 1,
              plan, h.H, lay.vp, lay.cap, st.own, st.p, st.tk, st.inv, st.ids, c.K, h.M};
   hipError_t e = hipSuccess;
@@ -1498,7 +1510,6 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   int shift = 61;
   for (int64_t k = h.M * (c.K > 0 ? c.K : 1); k > 0; k >>= 1) --shift;
   if (shift > 44) shift = 44;
-  const double unit = (double)((int64_t)1 << shift) / (double)top;
   const bool sums = c.grad_bias != nullptr && c.K > 0;
   unsigned long long *const entries = sums ? reinterpret_cast<unsigned long long *>(ws + lay.entries) : nullptr;
   if (e == hipSuccess && sums) e = zero_words(entries, 2 * h.V, s);
@@ -1516,13 +1527,13 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
                         mm_grid(nmt * (p.np / MM_T)), dim3(MM_THREADS), s, p, dev);
     if (e == hipSuccess && c.K > 0 && (!few || c.grad_bias != nullptr))
       e = launch_kernel(distill_entries_kernel<ET>, numbered_grid(ceil_div(h.M * c.K, 256)), dim3(256), s,
-                        DistillEntries{p, c.K, st.ids, st.inv, st.p, st.tk, entries, unit});
+                        DistillEntries{p, c.K, st.ids, st.inv, st.p, st.tk, entries, shift});
     if (e == hipSuccess && c.grad_bias != nullptr)
       e = launch_kernel(loss_bias_kernel, dim3((unsigned)ceil_div(nv, 256)), dim3(256), s,
                         static_cast<const float *>(p.colpart), h.M, static_cast<const int32_t *>(st.count),
                         c.mem.keep ? kept_rows(h.M) : (int)MM_T, lay.vp, nv,
                         sums ? reinterpret_cast<const long long *>(entries) + v0 : nullptr, static_cast<const float *>(scale),
-                        unit, h.temperature, c.grad_bias + v0);
+                        shift, h.temperature, c.grad_bias + v0);
     const int64_t ta = nht * lay.cap, tb = nht * (p.np / MM_T);  // ta: the most there are
     if (e == hipSuccess && c.grad_hidden != nullptr && c.grad_W != nullptr && ta + tb <= device_cus()) {
       e = launch_kernel(loss_products_kernel<ET>, dim3((unsigned)(ta + tb)), dim3(MM_THREADS), s, p, dev, (uint32_t)ta);
