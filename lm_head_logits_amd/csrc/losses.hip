@@ -716,8 +716,8 @@ __device__ __forceinline__ void policy_token(const TokenRows &c, int64_t m, floa
   loss = coef = 0.0f;
   if (A != 0.0f) {  // else 0, also where the ratio has overflowed
     const bool free = ra <= ca;
-    loss = free ? -ra : r != r ? r : -ca;
-    coef = free ? -ra : r != r ? r : 0.0f;
+    loss = free ? -ra : ra != ra ? ra : -ca;  // NaN of any origin
+    coef = free ? -ra : loss != loss ? loss : 0.0f;
   }
   if (c.ref_logp != nullptr && c.kl != 0.0f) {
     const float d = __fsub_rn(c.ref_logp[m], logp), e = expm1f(d);
