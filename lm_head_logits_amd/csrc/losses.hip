@@ -209,19 +209,23 @@ __global__ __launch_bounds__(64 * DP_WAVES) void distill_prep_kernel(DistillPrep
                                            : (float)static_cast<const _Float16 *>(c.logits)[at];
       if (i >= 0 && i < c.V && s != NEG_INF) {
         id[e] = (int32_t)i;
-        v[e] = __fdiv_rn(s, c.T);
+        v[e] = s;
         mx = mx != mx || v[e] != v[e] ? __builtin_nanf("") : fmaxf(mx, v[e]);
       }
       id_w[k] = id[e];
     }
   }
   mx = wave_max(mx);
+  // From here on (s - largest) / T: s / T itself may be past fp32's range (the type's
+  // lowest value at T < 1). Where the teacher's lse is given, s / T.
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = __fdiv_rn(c.teacher_lse != nullptr ? v[e] : __fsub_rn(v[e], mx), c.T);
   float s = 0.0f;
   const float lse_t = c.teacher_lse != nullptr ? c.teacher_lse[m] : 0.0f;
   if (c.teacher_lse == nullptr) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (id[e] != NO_ID) s = __fadd_rn(s, expf(__fsub_rn(v[e], mx)));
+      if (id[e] != NO_ID) s = __fadd_rn(s, expf(v[e]));
     s = wave_sum(s);
   }
   const float ls = logf(s);
@@ -231,7 +235,7 @@ __global__ __launch_bounds__(64 * DP_WAVES) void distill_prep_kernel(DistillPrep
   for (int e = 0; e < E; ++e) {
     p[e] = 0.0f;
     if (id[e] != NO_ID) {
-      const float lp = c.teacher_lse != nullptr ? __fsub_rn(v[e], lse_t) : __fsub_rn(__fsub_rn(v[e], mx), ls);
+      const float lp = c.teacher_lse != nullptr ? __fsub_rn(v[e], lse_t) : __fsub_rn(v[e], ls);
       p[e] = expf(lp);
       if (p[e] != 0.0f) ent = __fadd_rn(ent, __fmul_rn(p[e], lp));
       P = __fadd_rn(P, p[e]);

@@ -44,3 +44,43 @@ def test_an_advantage_that_is_no_number(M, kl):
         assert bool(loss[7].isnan()) and torch.equal(logp, clean[1]) and torch.equal(loss[others], clean[0][others])
         assert bool(gh[7].isnan().all()) and bool(gw.isnan().all()) and bool(gb.isnan().all())
         assert bool(gh[others].isfinite().all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("M", [40, 300])
+def test_teachers_logits_past_the_range_at_the_temperature(dt, M):
+    """Entries whose quotient by the temperature leaves fp32 (a row of the type's
+    lowest value, of its largest) weigh what their differences say."""
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dt]
+    c = make("distill", 31, M, 64, 300, "bf16", True, mask=0.0)
+    c["teacher_ids"][c["teacher_ids"] < 0] = 17
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+
+    def both(fill, plain):
+        got = []
+        for f in (fill, plain):
+            s = c["teacher_logits"].to(dtype).clone()
+            f(s)
+            say("teacher's extremes", dt, M)
+            (loss,), grads = check(dict(c, teacher_logits=s), kw=dict(temperature=0.5))
+            assert bool(loss.isfinite().all()) and all(bool(t.isfinite().all()) for t in grads)
+            got.append((loss, *grads))
+        return got
+
+    def ends(s):
+        s[1], s[2] = low, high
+
+    def zeros(s):
+        s[1:3] = 0.0
+
+    assert all(torch.equal(a, b) for a, b in zip(*both(ends, zeros)))
+
+    def far(s):
+        s[3, ::2], s[4, 1] = low, high
+
+    def absent(s):  # a probability of 0, or none at all
+        s[3, ::2] = -math.inf
+        s[4, 0], s[4, 1], s[4, 2:] = -math.inf, 0.0, -math.inf
+
+    a, b = both(far, absent)
+    assert torch.equal(a[0], b[0])
