@@ -31,6 +31,7 @@ class LossState(NamedTuple):
     K: int                # the teacher's logits a row; 0 for the losses of targets
     elements: int         # of the loss, and so of its upstream gradient
     keep_logits: bool     # the logits are in the state
+    V: int = 0            # rows of the weight (sizes of states are rounded up: others may have the same)
 
 
 # Up to this many bytes of fp32 logits a forward call for training keeps them for
@@ -66,10 +67,11 @@ class _Memory:
         return (st.data_ptr() if st is not None and st.numel() else None, st.numel() if st is not None else 0,
                 int(self.keep), ws.data_ptr(), ws.numel() * ws.element_size())
 
-    def saved(self, hidden, bias, alpha, temperature, K, elements):
+    def saved(self, hidden, weight, bias, alpha, temperature, K, elements):
         if self.state is None:
             return None
-        return LossState(self.state, hidden, bias, float(alpha), float(temperature), K, elements, self.keep)
+        return LossState(self.state, hidden, bias, float(alpha), float(temperature), K, elements, self.keep,
+                         weight.shape[0])
 
 
 def logits_topk_workspace_bytes(M: int, V: int, k: int) -> int:
@@ -147,7 +149,7 @@ def distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: tor
             teacher_ids.data_ptr(), itype, teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], K,
             _ptr(teacher_lse), loss.data_ptr(), *mem.args(), _stream_handle(dev, stream))
     _check(st, "lmhead_distill_forward")
-    return loss, mem.saved(hidden, bias, alpha, temperature, K, M)
+    return loss, mem.saved(hidden, weight, bias, alpha, temperature, K, M)
 
 
 def policy_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, advantage: torch.Tensor,
@@ -179,7 +181,7 @@ def policy_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Ten
             float(clip_low), float(clip_high), float(kl_coef), loss.data_ptr(), logp.data_ptr(),
             *mem.args(), _stream_handle(dev, stream))
     _check(st, "lmhead_policy_forward")
-    return loss, logp, mem.saved(hidden, bias, alpha, temperature, 0, M)
+    return loss, logp, mem.saved(hidden, weight, bias, alpha, temperature, 0, M)
 
 
 def preference_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, starts: torch.Tensor,
@@ -216,7 +218,7 @@ def preference_forward(hidden: torch.Tensor, weight: torch.Tensor, target: torch
             float(margin), float(label_smoothing), int(average), loss.data_ptr(), logp.data_ptr(),
             *mem.args(), _stream_handle(dev, stream))
     _check(st, "lmhead_preference_forward")
-    return loss, logp, mem.saved(hidden, bias, alpha, temperature, 0, P)
+    return loss, logp, mem.saved(hidden, weight, bias, alpha, temperature, 0, P)
 
 
 def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossState, *, need_hidden: bool = True,
@@ -236,7 +238,7 @@ def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossStat
     if need_bias is None:
         need_bias = bias is not None
     _need(not need_bias or bias is not None, "there is no bias to differentiate")
-    _need(saved.state.numel() == loss_state_bytes(M, H, V, saved.K, saved.keep_logits),
+    _need(saved.V == V and saved.state.numel() == loss_state_bytes(M, H, V, saved.K, saved.keep_logits),
           "saved is of a head of another size than weight")
     dev = hidden.device
     with _alloc_on(stream):

@@ -1,5 +1,5 @@
-"""The losses where their inputs leave the ordinary range. Formulas and bounds:
-tests/loss_formulas.py."""
+"""The losses where their inputs leave the ordinary range, and whose state a call takes.
+Formulas and bounds: tests/loss_formulas.py."""
 import math
 
 import pytest
@@ -84,3 +84,16 @@ def test_teachers_logits_past_the_range_at_the_temperature(dt, M):
 
     a, b = both(far, absent)
     assert torch.equal(a[0], b[0])
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("V,others", [(1000, (999, 1001, 961, 1024)), (511, (510, 512))])
+def test_a_state_belongs_to_its_vocabulary(V, others, keep):
+    """Vocabularies whose states are of one size."""
+    c = make("policy", 3, 20, 64, V, "bf16", False)
+    reference(c, 0.5, KW["policy"])
+    *_, saved = call(c, 0.5, KW["policy"], keep_logits=keep)
+    for n in others:
+        assert L.loss_state_bytes(20, 64, n, 0, keep) == saved.state.numel()
+        with pytest.raises(ValueError, match="saved"):
+            L.loss_backward(c["grad"], torch.zeros(n, 64, dtype=torch.bfloat16, device=DEV), saved)
