@@ -258,12 +258,12 @@ def loss_backward(grad_loss: torch.Tensor, weight: torch.Tensor, saved: LossStat
 
 
 class _HeadLoss(torch.autograd.Function):
-    """forward(hidden, weight, bias, call): call(hidden, weight, bias, train) is
-    one of the forward calls above with its other arguments bound."""
+    """forward(hidden, weight, bias, train, call): call(hidden, weight, bias, train)
+    is one of the forward calls above with its other arguments bound."""
 
     @staticmethod
-    def forward(ctx, hidden, weight, bias, call):
-        *out, saved = call(hidden, weight, bias, any(ctx.needs_input_grad))
+    def forward(ctx, hidden, weight, bias, train, call):
+        *out, saved = call(hidden, weight, bias, train)
         if saved is not None:
             ctx.save_for_backward(hidden, weight, bias, saved.state)
             ctx.rest = saved[3:]
@@ -275,12 +275,19 @@ class _HeadLoss(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_loss, *_):
         if grad_loss is None:
-            return None, None, None, None
+            return None, None, None, None, None
         hidden, weight, bias, state = ctx.saved_tensors
         dh, dw, db = loss_backward(grad_loss.contiguous(), weight, LossState(state, hidden, bias, *ctx.rest),
                                    need_hidden=ctx.needs_input_grad[0], need_weight=ctx.needs_input_grad[1],
                                    need_bias=ctx.needs_input_grad[2])
-        return dh, dw, db, None
+        return dh, dw, db, None, None
+
+
+def _apply(hidden, weight, bias, call):
+    """A backward pass is prepared where one can follow: in forward itself grad mode is
+    off, and needs_input_grad is true of a parameter without grad mode too."""
+    train = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (hidden, weight, bias))
+    return _HeadLoss.apply(hidden, weight, bias, train, call)
 
 
 def _reduce(loss, reduction, kept):
@@ -308,7 +315,7 @@ def distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.
         return distill_forward(h, w, teacher_ids, teacher_logits, alpha, b, temperature=temperature,
                                teacher_lse=teacher_lse, train=train, keep_logits=keep_logits)
 
-    (loss,) = _HeadLoss.apply(hidden, weight, bias, call)
+    (loss,) = _apply(hidden, weight, bias, call)
     return _reduce(loss, reduction, lambda: ((teacher_ids >= 0) & (teacher_ids < weight.shape[0])
                                              & (teacher_logits != -torch.inf)).any(1))
 
@@ -329,7 +336,7 @@ def policy_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor
                               clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, ignore_index=ignore_index,
                               train=train, keep_logits=keep_logits)
 
-    loss, logp = _HeadLoss.apply(hidden, weight, bias, call)
+    loss, logp = _apply(hidden, weight, bias, call)
     loss = _reduce(loss, reduction, lambda: (target != ignore_index) & (target >= 0) & (target < weight.shape[0]))
     return (loss, logp) if return_logp else loss
 
@@ -349,6 +356,6 @@ def preference_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Te
                                   label_smoothing=label_smoothing, average=average, temperature=temperature,
                                   ignore_index=ignore_index, train=train, keep_logits=keep_logits)
 
-    loss, logp = _HeadLoss.apply(hidden, weight, bias, call)
+    loss, logp = _apply(hidden, weight, bias, call)
     loss = _reduce(loss, reduction, lambda: torch.ones_like(loss))
     return (loss, logp) if return_logp else loss

@@ -1,5 +1,6 @@
-"""The losses where their inputs leave the ordinary range, and whose state a call takes.
-Formulas and bounds: tests/loss_formulas.py."""
+"""The losses where their inputs leave the ordinary range, whose state a call takes, and
+their differentiable functions without grad mode. Formulas and bounds:
+tests/loss_formulas.py."""
 import math
 
 import pytest
@@ -7,7 +8,7 @@ import torch
 
 import lm_head_logits_amd as L
 from gpu_util import DEV, say
-from test_gpu_losses import KW, call, check, make, reference
+from test_gpu_losses import KW, OPS, call, check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,41 @@ def test_a_state_belongs_to_its_vocabulary(V, others, keep):
         assert L.loss_state_bytes(20, 64, n, 0, keep) == saved.state.numel()
         with pytest.raises(ValueError, match="saved"):
             L.loss_backward(c["grad"], torch.zeros(n, 64, dtype=torch.bfloat16, device=DEV), saved)
+
+
+def apply(c, h, W, b, **kw):
+    kw = {**KW[c["op"]], **kw}
+    if c["op"] == "distill":
+        return L.distillation(h, W, c["teacher_ids"], c["teacher_logits"], 0.5, b, **kw)
+    if c["op"] == "policy":
+        return L.policy_loss(h, W, c["target"], c["advantage"], c["old"], c["ref"], 0.5, b, **kw)
+    return L.preference_loss(h, W, c["target"], c["starts"], c["ref"], 0.5, b, **kw)
+
+
+@pytest.mark.parametrize("off", [torch.no_grad, torch.inference_mode])
+@pytest.mark.parametrize("op", OPS)
+def test_evaluation_leaves_no_state(op, off):
+    """Parameters that require gradients, without grad mode: the loss alone, without
+    the memory of the backward pass (here all logits, 48 MB, and the hidden rows)."""
+    M, H, V = 600, 64, 20000
+    c = make(op, 41, M, H, V, "bf16", True)
+    reference(c, 0.5, KW[op])
+    leaves = [c[k].clone().requires_grad_() for k in ("hidden", "weight", "bias")]
+
+    def peak(fn):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out = fn()
+        return out, torch.cuda.max_memory_allocated() - before
+
+    trained, with_state = peak(lambda: apply(c, *leaves, reduction="none"))
+    with off():
+        (alone, without) = peak(lambda: apply(c, *leaves, reduction="none"))
+    say("peak", op, with_state, without)
+    assert torch.equal(alone, trained.detach()) and not alone.requires_grad
+    assert with_state >= 4 * M * V and without < 2 * L.loss_forward_workspace_bytes(M, H, V, 7, False) < M * V
+    # ... and with grad mode on again, inside it too
+    with off(), torch.inference_mode(False), torch.enable_grad():
+        apply(c, *leaves, reduction="sum").backward()
+    assert leaves[0].grad is not None

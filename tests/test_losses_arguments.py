@@ -1,0 +1,47 @@
+"""The differentiable losses without a GPU: when a backward pass is prepared."""
+import pytest
+import torch
+
+import lm_head_logits_amd as L
+from lm_head_logits_amd import losses
+
+M, H, V, K = 4, 64, 9, 3
+Y, F = torch.zeros(M, dtype=torch.int64), torch.zeros(M)
+IDS, S, CUTS = torch.zeros(M, K, dtype=torch.int64), torch.zeros(M, K), torch.tensor([0, 2, 4])
+
+
+def head(grad=True):
+    return [torch.zeros(*s, dtype=t, requires_grad=grad)
+            for s, t in (((M, H), torch.bfloat16), ((V, H), torch.bfloat16), ((V,), torch.float32))]
+
+
+CALLS = {"distill": lambda h, w, b, **kw: L.distillation(h, w, IDS, S, bias=b, reduction="none", **kw),
+         "policy": lambda h, w, b, **kw: L.policy_loss(h, w, Y, F, bias=b, reduction="none", **kw),
+         "preference": lambda h, w, b, **kw: L.preference_loss(h, w, Y, CUTS, bias=b, reduction="none", **kw)}
+
+
+@pytest.mark.parametrize("op", list(CALLS))
+def test_a_backward_pass_is_prepared_where_one_can_follow(op, monkeypatch):
+    seen = []
+
+    def forward(*args, train=True, **kw):
+        seen.append(train)
+        saved = losses.LossState(torch.zeros(0), args[0], None, 1.0, 1.0, 0, M, False) if train else None
+        return (*[torch.zeros(M) for _ in range(1 if op == "distill" else 2)], saved)
+
+    monkeypatch.setattr(losses, {"distill": "distill_forward", "policy": "policy_forward",
+                                 "preference": "preference_forward"}[op], forward)
+    call = CALLS[op]
+    h, w, b = head()
+    call(h, w, b)
+    for off in (torch.no_grad, torch.inference_mode):
+        with off():
+            call(h, w, b)
+    call(*head(False))
+    for k in range(3):  # any of the three
+        x = head(False)
+        x[k].requires_grad_()
+        assert call(*x).requires_grad
+    with torch.no_grad(), torch.enable_grad():
+        call(h, w, b)
+    assert seen == [True, False, False, False, True, True, True, True]
