@@ -85,7 +85,8 @@ def logits_topk(logits: torch.Tensor, k: int, temperature: float = 1.0, *, works
     in descending order, equal ones by ascending column (lmhead_logits_topk):
     returns (values [M, k] of the logits' type, ids int32 [M, k], lse fp32 [M]),
     lse being the log-sum-exp of the whole row of logits / temperature, so that
-    values / temperature - lse are the candidates' log-probabilities."""
+    values.float() / temperature - lse are the candidates' log-probabilities. It
+    gives no gradient to logits."""
     _need(logits.is_cuda and logits.dtype in _DTYPES and logits.dim() == 2,
           "logits must be a device tensor [M, V], float32, bfloat16 or float16")
     M, V = logits.shape
@@ -301,6 +302,13 @@ def _check_reduction(reduction):
     _need(reduction in ("none", "sum", "mean"), "reduction must be none, sum or mean")
 
 
+def _check_constants(**tensors):
+    """What the losses are not differentiated by must not ask for it: the gradient would be missing in silence."""
+    for name, t in tensors.items():
+        _need(t is None or not t.requires_grad or not torch.is_grad_enabled(),
+              f"there is no gradient for {name}: detach it")
+
+
 def distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
                  alpha: float = 1.0, bias=None, *, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
                  keep_logits: bool | None = None, reduction: str = "mean") -> torch.Tensor:
@@ -308,8 +316,12 @@ def distillation(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.
     "mean" over the rows that have entries (NaN when there are none). Losses at a
     temperature T are usually weighted by T * T; that is left to the caller.
     keep_logits as there, here and in the functions below: False saves fp32 [M, V]
-    between the passes, the gradients stay as they are."""
+    between the passes, the gradients stay as they are. Here and there gradients are
+    those of hidden, weight and bias: without grad mode, or where none of them requires
+    one, only the loss is computed, and any other tensor that requires one is refused
+    (ValueError)."""
     _check_reduction(reduction)
+    _check_constants(teacher_logits=teacher_logits, teacher_lse=teacher_lse)
 
     def call(h, w, b, train):
         return distill_forward(h, w, teacher_ids, teacher_logits, alpha, b, temperature=temperature,
@@ -330,6 +342,7 @@ def policy_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Tensor
     log-probabilities [M], without a gradient (for the ratio's and the KL's
     statistics)."""
     _check_reduction(reduction)
+    _check_constants(advantage=advantage, old_logp=old_logp, ref_logp=ref_logp)
 
     def call(h, w, b, train):
         return policy_forward(h, w, target, advantage, old_logp, ref_logp, alpha, b, temperature=temperature,
@@ -350,6 +363,7 @@ def preference_loss(hidden: torch.Tensor, weight: torch.Tensor, target: torch.Te
     or "mean" over the pairs. With return_logp also the sequences'
     log-probabilities [2 P], without a gradient (for the implicit rewards)."""
     _check_reduction(reduction)
+    _check_constants(ref_logp=ref_logp)
 
     def call(h, w, b, train):
         return preference_forward(h, w, target, starts, ref_logp, alpha, b, beta=beta, margin=margin,

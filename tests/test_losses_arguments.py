@@ -1,4 +1,5 @@
-"""The differentiable losses without a GPU: when a backward pass is prepared."""
+"""The differentiable losses without a GPU: when a backward pass is prepared, which
+arguments may ask for a gradient."""
 import pytest
 import torch
 
@@ -45,3 +46,17 @@ def test_a_backward_pass_is_prepared_where_one_can_follow(op, monkeypatch):
     with torch.no_grad(), torch.enable_grad():
         call(h, w, b)
     assert seen == [True, False, False, False, True, True, True, True]
+
+
+@pytest.mark.parametrize("call,names", [
+    (lambda **kw: L.distillation(*head()[:2], **{"teacher_ids": IDS, "teacher_logits": S, **kw}), ("teacher_logits", "teacher_lse")),
+    (lambda **kw: L.policy_loss(*head()[:2], **{"target": Y, "advantage": F, **kw}), ("advantage", "old_logp", "ref_logp")),
+    (lambda **kw: L.preference_loss(*head()[:2], Y, CUTS, **kw), ("ref_logp",))])
+def test_no_gradient_is_dropped_in_silence(call, names):
+    for name in names:
+        x = (S if name == "teacher_logits" else F).clone().requires_grad_()
+        with pytest.raises(ValueError, match=f"{name}.*detach"):
+            call(**{name: x})
+        for fine in (lambda: call(**{name: x.detach()}), torch.no_grad()(lambda: call(**{name: x}))):
+            with pytest.raises(ValueError, match="device tensor"):  # host tensors: the next check
+                fine()
