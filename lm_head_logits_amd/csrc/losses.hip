@@ -858,10 +858,15 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 //
 // Which f: a row's gradients hang on a few entries of G, its target's or its
 // teacher's largest, and on how those happen to round. Of LC_TRIES factors over
-// an octave that with the smallest error of such
-// entries is taken, over the first LC_SAMPLES of them: with rounded G the error of
-// the gradients is 1.41 times that of their own rounding, and with few rows
-// anything up to 1.6; so it is 1.2 to 1.35 up to some hundred rows.
+// an octave that with the smallest error of such entries is taken, over
+// LC_SAMPLES of them: the targets of the first rows worked on, or all entries of
+// rows spread evenly over those worked on (without packing, over all rows: some
+// may be left out). Error of the gradients over that of a correctly rounded
+// result, which is 1.41 where both roundings weigh the same: with 30 to 130 rows
+// 1.1 to 1.37, without the choice 1.0 to 1.6. Where there are many more targets or
+// entries than samples no factor suits them all, and the choice gains nothing:
+// 1.04 to 1.44.
+//
 // The splits of G W's K (the piece's columns) that fill the last round of
 // work-groups best, at least 256 columns each; chosen much as bwd_plan does, from
 // the rows worked on, by one wave. More splits have to fill 10% more: every one is
@@ -916,8 +921,8 @@ struct LossCoef {
   int64_t H, vp, cap;
   const float *own;               // targets
   const float *p, *tk;            // teacher's entries
-  const int32_t *inv, *sid;
-  int64_t K, all_rows;            // all_rows: the call's rows
+  const int32_t *call_rows, *sid; // call_rows: State's rows
+  int64_t K;
   // c = 0: nothing, whatever g is (rows of no sequence have no upstream gradient)
   __device__ __forceinline__ void of(float c, float g, float &a, float &b) const {
     a = c == 0.0f ? 0.0f : __fmul_rn(distill ? c : -c, g);
@@ -939,8 +944,7 @@ __device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
   // The samples, unscaled entries of G: their loads go out before the rows'.
   constexpr int S = LC_SAMPLES / LC_THREADS;
   float entry[S];
-  const int64_t all = p.distill ? p.all_rows * p.K : p.M;
-  const int samples = (int)(all < LC_SAMPLES ? all : LC_SAMPLES);
+  int samples = (int)(p.M < LC_SAMPLES ? p.M : LC_SAMPLES);
   if (!p.distill) {
     float o[S];
     int32_t u[S];
@@ -953,23 +957,27 @@ __device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
 #pragma unroll
     for (int k = 0; k < S; ++k) entry[k] = o[k] == 0.0f ? 0.0f : __fmul_rn(o[k], p.g[u[k]]);
   } else {
+    // all entries of `take` rows
+    const int n = (int)p.M, K = (int)p.K, most = LC_SAMPLES / K, take = n == 0 ? 1 : n < most ? n : most;
+    const int each = n / take, rest = n % take;
+    samples = n == 0 ? 0 : take * K;
     int32_t id[S];
-    int64_t m[S];
+    int m[S];
     float g[S], t[S], pk[S], c[S], lse[S];
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       const int e = threadIdx.x + k * LC_THREADS;
-      const int64_t row = (uint32_t)(e < samples ? e : 0) / (uint32_t)p.K;
-      id[k] = e < samples ? p.sid[e] : NO_ID;
-      m[k] = p.inv != nullptr ? (int64_t)p.inv[row] : row;
+      const bool ok = e < samples;
+      const int j = ok ? e / K : 0;
+      m[k] = j * each + j * rest / take + each / 2;
+      const int64_t row = ok && p.call_rows != nullptr ? (int64_t)p.call_rows[m[k]] : (int64_t)m[k];
+      const int64_t at = row * K + (ok ? e - j * K : 0);
+      id[k] = ok ? p.sid[at] : NO_ID;
       g[k] = p.g[row];
-      t[k] = e < samples ? p.tk[e] : 0.0f;
-      pk[k] = e < samples ? p.p[e] : 0.0f;
-    }
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      c[k] = m[k] < 0 ? 0.0f : p.coef[m[k]];
-      lse[k] = m[k] < 0 ? 0.0f : p.lse[m[k]];
+      t[k] = ok ? p.tk[at] : 0.0f;
+      pk[k] = ok ? p.p[at] : 0.0f;
+      c[k] = p.coef[m[k]];
+      lse[k] = p.lse[m[k]];
     }
 #pragma unroll
     for (int k = 0; k < S; ++k)
@@ -1483,7 +1491,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + lay.rows);
   const float top = ET == ET_F16 ? (float)(1 << F16_TOP) : 1.0f;
   LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, st.count, c.K > 0, top, scale, rows, 0, 1,
-             plan, h.H, lay.vp, lay.cap, st.own, st.p, st.tk, st.inv, st.ids, c.K, h.M};
+             plan, h.H, lay.vp, lay.cap, st.own, st.p, st.tk, st.rows, st.ids, c.K};
   hipError_t e = hipSuccess;
   if (h.M > LC_ONE) {
     r.write_rows = 0;

@@ -1,6 +1,6 @@
 """The losses where their inputs leave the ordinary range, whose state a call takes, and
-their differentiable functions without grad mode. Formulas and bounds:
-tests/loss_formulas.py."""
+their differentiable functions without grad mode; which rows the scale of G is chosen
+from. Formulas and bounds: tests/loss_formulas.py."""
 import math
 
 import pytest
@@ -8,7 +8,7 @@ import torch
 
 import lm_head_logits_amd as L
 from gpu_util import DEV, say
-from test_gpu_losses import KW, OPS, call, check, make, reference
+from test_gpu_losses import DT, KW, OPS, call, check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +136,27 @@ def test_evaluation_leaves_no_state(op, off):
     with off(), torch.inference_mode(False), torch.enable_grad():
         apply(c, *leaves, reduction="sum").backward()
     assert leaves[0].grad is not None
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_prompts_do_not_reach_the_rounding(seed, dt):
+    """Rows that are left out before those worked on, or behind them: the same
+    gradients, bit for bit, since the scale under which G is rounded is chosen from the
+    rows worked on."""
+    n, H, V, K = 300, 64, 500, 8
+    c = make("distill", seed, n, H, V, dt, False, K=K, mask=0.0)
+    c["teacher_ids"][c["teacher_ids"] < 0] = 17  # no row without entries
+    pad = make("distill", seed + 10, n, H, V, dt, False, K=K, mask=0.0)
+    pad["teacher_ids"][:] = -100
+    got = []
+    for front in (0, n // 2, n):
+        x = dict(c)
+        for k in ("hidden", "teacher_ids", "teacher_logits", "grad"):
+            x[k] = torch.cat([pad[k][:front], c[k], pad[k][front:]])
+        say("prompts", front, dt, seed)
+        loss, saved = call(x, 0.5, KW["distill"])
+        dh, dw, _ = L.loss_backward(x["grad"], c["weight"], saved)
+        got.append((loss[front:front + n], dh[front:front + n], dw))
+    for g in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], g))
