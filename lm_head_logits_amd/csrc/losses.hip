@@ -970,12 +970,14 @@ __device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
       const bool ok = e < samples;
       const int j = ok ? e / K : 0;
       m[k] = j * each + j * rest / take + each / 2;
-      const int64_t row = ok && p.call_rows != nullptr ? (int64_t)p.call_rows[m[k]] : (int64_t)m[k];
+      // (past the last: some entry's, not used)
+      const int64_t row = p.call_rows != nullptr && n != 0 ? (int64_t)p.call_rows[m[k]] : (int64_t)m[k];
       const int64_t at = row * K + (ok ? e - j * K : 0);
-      id[k] = ok ? p.sid[at] : NO_ID;
+      id[k] = p.sid[at];
+      if (!ok) id[k] = NO_ID;
       g[k] = p.g[row];
-      t[k] = ok ? p.tk[at] : 0.0f;
-      pk[k] = ok ? p.p[at] : 0.0f;
+      t[k] = p.tk[at];
+      pk[k] = p.p[at];
       c[k] = p.coef[m[k]];
       lse[k] = p.lse[m[k]];
     }
