@@ -881,10 +881,12 @@ struct SplitPlan {
 __host__ __device__ __forceinline__ int64_t split_of(int64_t np, int64_t splits) {
   return ((np + splits - 1) / splits + 63) / 64 * 64;
 }
+// A split more is looked at where there are fewer tiles without it.
+constexpr int32_t SPLIT_TILES = 4 * 256;
 __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, int32_t cap, SplitPlan *out) {
   const uint32_t nmt = (n + MM_T - 1) / MM_T, tiles = nmt * ((H + MM_T - 1) / MM_T), cus = 256;
   const uint32_t s = threadIdx.x + 1;
-  const bool ok = s == 1 || (s * 256 <= (uint32_t)vp && s * nmt <= (uint32_t)cap && tiles * (s - 1) < cus * 4);
+  const bool ok = s == 1 || (s * 256 <= (uint32_t)vp && s * nmt <= (uint32_t)cap && tiles * (s - 1) < SPLIT_TILES);
   const float use = ok && tiles > 0 ? (float)(tiles * s) / (float)((tiles * s + cus - 1) / cus * cus) : 0.0f;
   float best = 0.0f;
   int32_t splits = 1;
@@ -1382,6 +1384,19 @@ int64_t whole_rounds(int64_t vp, int64_t H, int64_t V) {
   return n < all && more < all && more <= n + n / 8 && rounds(more) < rounds(n) ? more * MM_T : vp;
 }
 
+// Row tiles times splits of the plans (plan_splits) for up to nmt row tiles. (65536 rows,
+// H = 4096: one sum of all rows, 1 GB, where three had been kept.)
+int64_t most_parts(int64_t nmt, int64_t nht, int64_t vp) {
+  int64_t most = nmt;
+  for (int64_t k = 1; k <= nmt && k * nht < SPLIT_TILES; ++k) {
+    int64_t s = (SPLIT_TILES - 1) / (k * nht) + 1;
+    if (s > vp / 256) s = vp / 256;
+    if (s > 64) s = 64;
+    if (s * k > most) most = s * k;
+  }
+  return most;
+}
+
 // bwd_plan's pieces, with room for the sums of grad_hidden of whatever rows are
 // worked on: `cap` row tiles times splits.
 struct BackwardLayout {
@@ -1405,6 +1420,10 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
   // (H = 4096) 160 tiles would leave 96 of 256 CUs without one; three splits of
   // them fill 94%
   b.cap = pl.splits > 3 || M <= LR_DIRECT ? pl.splits * nmt : 3 * nmt;
+  if (M > LR_DIRECT) {
+    const int64_t most = most_parts(nmt, ceil_div(H, MM_T), b.vp);
+    if (most < b.cap) b.cap = most;
+  }
   b.scale = take(12);
   b.plan = take(sizeof(SplitPlan));
   b.rows = take(16 * M);

@@ -1,5 +1,5 @@
 """The differentiable losses without a GPU: when a backward pass is prepared, which
-arguments may ask for a gradient."""
+arguments may ask for a gradient, what is asked of the allocator."""
 import pytest
 import torch
 
@@ -60,3 +60,13 @@ def test_no_gradient_is_dropped_in_silence(call, names):
         for fine in (lambda: call(**{name: x.detach()}), torch.no_grad()(lambda: call(**{name: x}))):
             with pytest.raises(ValueError, match="device tensor"):  # host tensors: the next check
                 fine()
+
+
+@pytest.mark.parametrize("M,H,V", [(65536, 4096, 128256), (1 << 17, 2048, 151936), (8192, 4096, 128256), (8192, 8192, 32000)])
+def test_backward_workspace_of_many_rows(M, H, V):
+    """The cross entropy's, whose sums of grad_hidden are not split for that many rows,
+    and room for the splits of fewer: a split more is taken below 1024 tiles of sums
+    only, so that fewer than 2048 are written. A piece may have an eighth more columns."""
+    tiles = -(-M // 256) * -(-H // 256)
+    room = L.xent_backward_workspace_bytes(M, H, V) + 2 * M * (V // 8 + 256) + max(0, 2048 - tiles) * 4 * 256 * 256 + 4096
+    assert L.loss_backward_workspace_bytes(M, H, V) <= room
