@@ -58,8 +58,15 @@ class _Memory:
 
     def __init__(self, M, H, V, K, train, keep_logits, workspace, dev):
         self.keep = train and (4 * M * V <= KEEP_BYTES if keep_logits is None else bool(keep_logits))
-        self.state = (torch.empty(loss_state_bytes(M, H, V, K, self.keep), dtype=torch.uint8, device=dev) if train
-                      else None)
+        self.state = None
+        if train:
+            try:
+                self.state = torch.empty(loss_state_bytes(M, H, V, K, self.keep), dtype=torch.uint8, device=dev)
+            except torch.OutOfMemoryError:
+                if keep_logits is not None or not self.keep:
+                    raise
+                self.keep = False  # kept by default only, and there is no room for them
+                self.state = torch.empty(loss_state_bytes(M, H, V, K, False), dtype=torch.uint8, device=dev)
         self.workspace = _workspace(workspace, loss_forward_workspace_bytes(M, H, V, K, train), dev)
 
     def args(self):
@@ -129,7 +136,7 @@ def distill_forward(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: tor
     logits / temperature over its whole vocabulary), are those of its whole
     distribution. saved is what loss_backward takes (None where train is
     false); keep_logits: it holds the logits too, fp32 [M, V], which saves making
-    them again there (None: up to 16 GB of them)."""
+    them again there (None: up to 16 GB of them, where they can be allocated)."""
     M, H, V, code = _head_args(hidden, weight, bias)
     _need(teacher_ids.dim() == 2 and teacher_ids.shape[0] == M and teacher_ids.shape[1] >= 1,
           "teacher_ids must be [M, K]")

@@ -1,5 +1,5 @@
-"""The differentiable losses without a GPU: when a backward pass is prepared, which
-arguments may ask for a gradient, what is asked of the allocator."""
+"""The differentiable losses and their memory without a GPU: when a backward pass is
+prepared, which arguments may ask for a gradient, what is asked of the allocator."""
 import pytest
 import torch
 
@@ -60,6 +60,33 @@ def test_no_gradient_is_dropped_in_silence(call, names):
         for fine in (lambda: call(**{name: x.detach()}), torch.no_grad()(lambda: call(**{name: x}))):
             with pytest.raises(ValueError, match="device tensor"):  # host tensors: the next check
                 fine()
+
+
+def test_logits_are_kept_where_there_is_room(monkeypatch):
+    """Without room for the logits the state is one without them; an allocation that
+    the caller asked for, or the lean one, fails as it does."""
+    lean, full = (L.loss_state_bytes(M, H, 5000, 0, k) for k in (False, True))
+    real = torch.empty
+    limit = [1 << 40]
+
+    def empty(n, *args, **kw):
+        if isinstance(n, int) and n > limit[0]:
+            raise torch.OutOfMemoryError("no room")
+        return real(n, *args, **kw)
+
+    monkeypatch.setattr(torch, "empty", empty)
+    memory = lambda keep: losses._Memory(M, H, 5000, 0, True, keep, real(16, dtype=torch.uint8), torch.device("cpu"))
+    monkeypatch.setattr(losses, "_workspace", lambda *a: a[0])
+    assert memory(None).keep and memory(None).state.numel() == full and not memory(False).keep
+    limit[0] = full - 1
+    m = memory(None)
+    assert not m.keep and m.state.numel() == lean and m.args()[2] == 0
+    with pytest.raises(torch.OutOfMemoryError):
+        memory(True)
+    limit[0] = lean - 1
+    for keep in (None, False):
+        with pytest.raises(torch.OutOfMemoryError):
+            memory(keep)
 
 
 @pytest.mark.parametrize("M,H,V", [(65536, 4096, 128256), (1 << 17, 2048, 151936), (8192, 4096, 128256), (8192, 8192, 32000)])
