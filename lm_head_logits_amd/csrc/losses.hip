@@ -1377,11 +1377,17 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
 // Pieces of up to an eighth more columns, where G^T hidden then takes fewer
 // rounds of work-groups in all: 594 tiles of columns by 8 of H (V = 151936, H = 2048)
 // in two pieces of 297 are twice ten rounds for 256 CUs, in 320 and 274 ten and nine.
-int64_t whole_rounds(int64_t vp, int64_t H, int64_t V) {
+// Not past bwd_plan's 256 MiB of G. Backward passes, ms, H, V, rows: 2048, 151936, 1000
+// 1.273 -> 1.257, 4096 rows 4.45 -> 4.38; 4096, 151936, 4096 8.05 -> 7.95; 4096, 200000,
+// 2048 5.48 -> 5.39; 8192, 50257, 8192 10.50 -> 10.23; 8192, 128256, 2048 (a round of 64
+// less) 6.60 -> 6.58; 1024, 262144, 1337 1.688 -> 1.704. With G of 261 and 272 MiB, 1337
+// rows, V = 200000: H = 4096 3.97 -> 4.13, H = 2048 2.15 -> 2.20.
+int64_t whole_rounds(int64_t vp, int64_t M, int64_t H, int64_t V) {
   const int64_t nht = ceil_div(H, MM_T), all = ceil_div(V, MM_T), n = vp / MM_T, unit = ceil_div(256, nht);
   auto rounds = [&](int64_t per) { return all / per * ceil_div(per * nht, 256) + ceil_div(all % per * nht, 256); };
   const int64_t more = ceil_div(n, unit) * unit;
-  return n < all && more < all && more <= n + n / 8 && rounds(more) < rounds(n) ? more * MM_T : vp;
+  const bool fits = 2 * M * more * MM_T <= (int64_t)256 << 20 || more * MM_T <= 8192;
+  return n < all && more < all && more <= n + n / 8 && fits && rounds(more) < rounds(n) ? more * MM_T : vp;
 }
 
 // Row tiles times splits of the plans (plan_splits) for up to nmt row tiles. (65536 rows,
@@ -1414,7 +1420,7 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
     return o;
   };
   const int64_t nmt = ceil_div(M, MM_T);
-  b.vp = whole_rounds(pl.vp, H, V);
+  b.vp = whole_rounds(pl.vp, M, H, V);
   b.splits = (int)ceil_div(b.vp, split_of(b.vp, pl.splits));
   // fewer rows than the call's take more splits: with three fifths of 4096 rows
   // (H = 4096) 160 tiles would leave 96 of 256 CUs without one; three splits of

@@ -97,3 +97,12 @@ def test_backward_workspace_of_many_rows(M, H, V):
     tiles = -(-M // 256) * -(-H // 256)
     room = L.xent_backward_workspace_bytes(M, H, V) + 2 * M * (V // 8 + 256) + max(0, 2048 - tiles) * 4 * 256 * 256 + 4096
     assert L.loss_backward_workspace_bytes(M, H, V) <= room
+
+
+@pytest.mark.parametrize("M,H,V,pieces", [(1337, 4096, 200000, 391), (1337, 2048, 200000, 391), (1000, 2048, 151936, 320),
+                                          (4096, 2048, 151936, 128), (4096, 4096, 128256, 126)])
+def test_pieces_stay_in_the_memory_side_cache(M, H, V, pieces):
+    """G of a piece: whole rounds of work-groups' worth of columns up to 256 MiB, else
+    the cross entropy's pieces. With a bias a row tile's sums take 4 bytes a column more."""
+    col = L.loss_backward_workspace_bytes(M, H, V, grad_bias=True) - L.loss_backward_workspace_bytes(M, H, V)
+    assert col == 4 * -(-M // 256) * pieces * 256 and 2 * M * pieces * 256 <= 256 << 20
