@@ -338,7 +338,8 @@ size_t lmhead_xent_backward_workspace_bytes(int64_t M, int64_t H, int64_t V, int
  *               column; equal logits (zeros of both signs too) by ascending column, NaN
  *               before all others. values are the logits' own bits.
  *   lse[m]      log sum_v exp(logits[m, v] / temperature): -inf for a row of only -inf, NaN
- *               for one with +inf or NaN
+ *               for one with +inf or NaN; infinite else only where the largest logit /
+ *               temperature is past fp32's range
  *   logits      [M, V] of dtype, rows row_stride elements apart (row_stride >= V), any
  *               alignment of an element                          (device, read)
  *   values      [M, K] of dtype; ids int32 [M, K]; lse fp32 [M]  (device, written)
@@ -411,7 +412,8 @@ lmhead_status lmhead_distill_forward(const void *hidden, int64_t M, int64_t H, c
  *   loss[m] = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_coef (exp(d) - d - 1)
  * with A = advantage[m]; the first term is 0 where A is 0, the second where ref_logp
  * is NULL or kl_coef is 0. Its derivative by logp is -r A where the minimum is r A
- * (ties included) and 0 elsewhere, and kl_coef (1 - exp(d)). Rows whose target is
+ * (ties included) and 0 elsewhere, and kl_coef (1 - exp(d)); NaN where the first term
+ * is. Rows whose target is
  * ignore_index or no column of the call have loss and logp 0 and no gradient.
  *   target     [M] of target_type; advantage, old_logp, ref_logp fp32 [M]  (device, read)
  *   loss, logp fp32 [M]                                                    (device, written) */
