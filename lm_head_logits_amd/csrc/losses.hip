@@ -78,7 +78,7 @@ StateLayout state_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep) 
   s.y = take(4 * M);
   s.lse = take(4 * M);
   s.coef = take(4 * M);
-  s.own = take(K ? 0 : 4 * M);
+  s.own = take(4 * M);
   s.up = take(4 * M);
   s.bias = take(4 * V);
   s.ids = take(4 * M * K);
@@ -97,7 +97,8 @@ struct State {
   int32_t *y;      // [n] target column or -1
   float *lse;      // [n]; +inf in rows left out
   float *coef;     // [n] d loss / d logp; distill: P
-  float *own;      // [n] coef (1 - q) of the target: d loss / d its t; targets only
+  float *own;      // [n] G's entry of the row that weighs most, of an upstream gradient of 1: the
+                   // target's, coef (1 - q), or of the teacher's the largest, P q - p
   int32_t *up;     // [n] which element of the upstream gradient is the row's
   float *bias;     // [V] bias / T, where T != 1
   int32_t *ids;    // [M, K] the teacher's tokens in ascending order, NO_ID behind the last
@@ -671,6 +672,7 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(Disti
   if (m - r >= n) return;  // the whole work-group
   c.r.copy(m - r);
   const int64_t row = m < n ? c.r.row(m) : 0;
+  const float P = m < n ? c.P[row] : 0.0f;
   if (c.r.ldt != 0 && m < n) {
 #pragma unroll 1
     for (int64_t k = sl; k < c.K; k += XC_SLICES) {  // the thread's own, below
@@ -680,21 +682,32 @@ __global__ __launch_bounds__(XC_ROWS * XC_SLICES) void distill_rows_kernel(Disti
   }
   const float2 f = fold_row(c.r.part, n, c.r.nvt, m, m < n, sh);
   const float ls = logf(f.y);
-  float sum = 0.0f;
+  float sum = 0.0f, own = 0.0f;
   if (m < n)
     for (int64_t k = sl; k < c.K; k += XC_SLICES) {
       const float p = c.r.st.p[row * c.K + k];
-      if (p != 0.0f) sum = __fadd_rn(sum, __fmul_rn(p, log_q(c.r.st.tk[row * c.K + k], f, ls)));
+      if (p != 0.0f) {
+        const float lq = log_q(c.r.st.tk[row * c.K + k], f, ls), e = __fsub_rn(__fmul_rn(P, expf(lq)), p);
+        sum = __fadd_rn(sum, __fmul_rn(p, lq));
+        own = fabsf(e) > fabsf(own) ? e : own;
+      }
     }
-  sh[sl][r].x = sum;
+  sh[sl][r] = float2{sum, own};
   __syncthreads();
   if (sl != 0 || m >= n) return;
-  for (int k = 1; k < XC_SLICES; ++k) sum = __fadd_rn(sum, sh[k][r].x);
-  c.r.st.lse[m] = c.P[row] == 0.0f ? __builtin_inff() : row_lse(f, ls);
+  const int slices = c.K < XC_SLICES ? (int)c.K : XC_SLICES;  // the others have no entry
+#pragma unroll 8
+  for (int k = 1; k < slices; ++k) {
+    const float2 e = sh[k][r];
+    sum = __fadd_rn(sum, e.x);
+    own = fabsf(e.y) > fabsf(own) ? e.y : own;
+  }
+  c.r.st.lse[m] = P == 0.0f ? __builtin_inff() : row_lse(f, ls);
   c.r.st.y[m] = -1;
   c.r.st.up[m] = (int32_t)row;
-  c.r.st.coef[m] = c.P[row];
-  c.loss[row] = c.P[row] == 0.0f ? 0.0f : __fsub_rn(c.ent[row], sum);
+  c.r.st.coef[m] = P;
+  c.r.st.own[m] = own;
+  c.loss[row] = P == 0.0f ? 0.0f : __fsub_rn(c.ent[row], sum);
 }
 
 // coef (1 - q) of a target with that log q
@@ -856,16 +869,15 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // factor of the entries), no target. Every work-group finds the scale by itself up to
 // LC_ONE rows; with more, one work-group finds it in a launch of its own.
 //
-// Which f: a row's gradients hang on a few entries of G, its target's or its
-// teacher's largest, and on how those happen to round. Of LC_TRIES factors over
-// an octave that with the smallest error of such entries is taken, over
-// LC_SAMPLES of them: the targets of the first rows worked on, or all entries of
-// rows spread evenly over those worked on (without packing, over all rows: some
-// may be left out). Error of the gradients over that of a correctly rounded
-// result, which is 1.41 where both roundings weigh the same: with 30 to 130 rows
-// 1.1 to 1.37, without the choice 1.0 to 1.6. Where there are many more targets or
-// entries than samples no factor suits them all, and the choice gains nothing:
-// 1.04 to 1.44.
+// Which f: a row's gradients hang on a few entries of G and on how those happen to
+// round. Of LC_TRIES factors over an octave that with the smallest error of the
+// entries that weigh most is taken: one a row, its target's or its teacher's largest,
+// of LC_SAMPLES rows spread over those worked on. Error of the gradients over that of a
+// correctly rounded result, over 130 drawn batches of 50 to 4000 rows: 1.01 to 1.42.
+// (Distillation's grad_hidden over forty: without the choice 1.09 to 1.51, the worst
+// factor 1.36 to 2.2, chosen by all entries of the first 1024 / K rows 1.06 to 1.69, so of
+// few rows worse than none, by the largest of each row 1.05 to 1.38, the best factor
+// 1.05 to 1.37.)
 //
 // The splits of G W's K (the piece's columns) that fill the last round of
 // work-groups best, at least 256 columns each; chosen much as bwd_plan does, from
@@ -921,9 +933,9 @@ struct LossCoef {
   int have_scale, write_rows;
   SplitPlan *plan;
   int64_t H, vp, cap;
-  const float *own;               // targets
+  const float *own;
   const float *p, *tk;            // teacher's entries
-  const int32_t *call_rows, *sid; // call_rows: State's rows
+  const int32_t *sid;
   int64_t K;
   // c = 0: nothing, whatever g is (rows of no sequence have no upstream gradient)
   __device__ __forceinline__ void of(float c, float g, float &a, float &b) const {
@@ -946,49 +958,17 @@ __device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
   // The samples, unscaled entries of G: their loads go out before the rows'.
   constexpr int S = LC_SAMPLES / LC_THREADS;
   float entry[S];
-  int samples = (int)(p.M < LC_SAMPLES ? p.M : LC_SAMPLES);
-  if (!p.distill) {
-    float o[S];
-    int32_t u[S];
+  const int samples = (int)(p.M < LC_SAMPLES ? p.M : LC_SAMPLES);
+  float o[S];
+  int32_t o_up[S];
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int m = threadIdx.x + k * LC_THREADS;
-      o[k] = m < samples ? p.own[m] : 0.0f;
-      u[k] = m < samples ? p.up[m] : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < S; ++k) entry[k] = o[k] == 0.0f ? 0.0f : __fmul_rn(o[k], p.g[u[k]]);
-  } else {
-    // all entries of `take` rows
-    const int n = (int)p.M, K = (int)p.K, most = LC_SAMPLES / K, take = n == 0 ? 1 : n < most ? n : most;
-    const int each = n / take, rest = n % take;
-    samples = n == 0 ? 0 : take * K;
-    int32_t id[S];
-    int m[S];
-    float g[S], t[S], pk[S], c[S], lse[S];
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      const int e = threadIdx.x + k * LC_THREADS;
-      const bool ok = e < samples;
-      const int j = ok ? e / K : 0;
-      m[k] = j * each + j * rest / take + each / 2;
-      // (past the last: some entry's, not used)
-      const int64_t row = p.call_rows != nullptr && n != 0 ? (int64_t)p.call_rows[m[k]] : (int64_t)m[k];
-      const int64_t at = row * K + (ok ? e - j * K : 0);
-      id[k] = p.sid[at];
-      if (!ok) id[k] = NO_ID;
-      g[k] = p.g[row];
-      t[k] = p.tk[at];
-      pk[k] = p.p[at];
-      c[k] = p.coef[m[k]];
-      lse[k] = p.lse[m[k]];
-    }
-#pragma unroll
-    for (int k = 0; k < S; ++k)
-      entry[k] = id[k] == NO_ID || c[k] == 0.0f
-                     ? 0.0f
-                     : __fmul_rn(g[k], __fsub_rn(__fmul_rn(c[k], exp_diff(t[k], lse[k])), pk[k]));
+  for (int k = 0; k < S; ++k) {
+    const int j = threadIdx.x + k * LC_THREADS, m = p.M <= LC_SAMPLES ? j : (int)(j * p.M / LC_SAMPLES);
+    o[k] = j < samples ? p.own[m] : 0.0f;
+    o_up[k] = j < samples ? p.up[m] : 0;
   }
+#pragma unroll
+  for (int k = 0; k < S; ++k) entry[k] = o[k] == 0.0f ? 0.0f : __fmul_rn(o[k], p.g[o_up[k]]);
   float mx = 0.0f;
   for (int64_t m0 = threadIdx.x; m0 < p.M; m0 += 8 * LC_THREADS) {
     float c[8], g[8];
@@ -1518,7 +1498,7 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   RowCoef *const rows = reinterpret_cast<RowCoef *>(ws + lay.rows);
   const float top = ET == ET_F16 ? (float)(1 << F16_TOP) : 1.0f;
   LossCoef r{c.grad_loss, h.M, st.lse, st.coef, st.y, st.up, st.count, c.K > 0, top, scale, rows, 0, 1,
-             plan, h.H, lay.vp, lay.cap, st.own, st.p, st.tk, st.rows, st.ids, c.K};
+             plan, h.H, lay.vp, lay.cap, st.own, st.p, st.tk, st.ids, c.K};
   hipError_t e = hipSuccess;
   if (h.M > LC_ONE) {
     r.write_rows = 0;

@@ -1,6 +1,6 @@
 """The losses where their inputs leave the ordinary range, whose state a call takes, and
 their differentiable functions without grad mode; which rows the scale of G is chosen
-from. Formulas and bounds: tests/loss_formulas.py."""
+from, and for which entries. Formulas and bounds: tests/loss_formulas.py."""
 import math
 
 import pytest
@@ -160,3 +160,34 @@ def test_prompts_do_not_reach_the_rounding(seed, dt):
         got.append((loss[front:front + n], dh[front:front + n], dw))
     for g in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], g))
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("M", [200, 300, 3000])
+@pytest.mark.parametrize("p", [0.553, 0.617, 0.68, 0.703, 0.761, 0.822, 0.87, 0.94])
+def test_the_scale_suits_the_entries_that_weigh_most(p, M, dt):
+    """A batch whose rows have one large entry of G each, of the same value, but for some
+    with many small ones (the first rows, and some between): the factor of the scale is the
+    one of the sixteen that rounds the large entry best. With W the unit matrix
+    grad_hidden is G, off by that rounding and by its own: half a step."""
+    V, K, high = 256, 100, 7
+    c = make("distill", 1, M, V, V, dt, False, K=K, mask=0.0)
+    hidden, weight = torch.zeros_like(c["hidden"]), torch.eye(V, device=DEV).to(DT[dt])
+    ids = torch.arange(K, device=DEV).repeat(M, 1)
+    s = torch.zeros(M, K, device=DEV)
+    s[:, high] = math.log(p / (1 - p) * (K - 1))
+    small = torch.arange(M, device=DEV)
+    small = (small < 11) | (small % 30 == 15)
+    s[small] = 0.0
+    g = torch.full((M,), 1.0 / M, device=DEV)
+    say("scale", p, M, dt)
+    _, saved = L.distill_forward(hidden, weight, ids, s)
+    got = L.loss_backward(g, weight, saved)[0][~small, high].double()
+    pk = torch.softmax(s.double(), 1)[~small, high]
+    x = 1.0 / V - float(pk[0])  # the entry over the largest coefficient
+    tries = [2.0 ** (-j / 16) for j in range(16)]
+    rounding = min(abs(float(torch.tensor(x * t).to(DT[dt])) / t - x) for t in tries)
+    want = x * float(g[0])
+    half = 2.0 ** math.floor(math.log2(abs(want))) * torch.finfo(DT[dt]).eps / 2
+    bound = rounding * float(g[0]) + half * (1 + 1e-3)  # and what fp32 adds
+    assert float((got - want).abs().max()) <= bound, (float((got - want).abs().max()) / half, bound / half)
