@@ -871,8 +871,8 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 //
 // Which f: a row's gradients hang on a few entries of G and on how those happen to
 // round. Of LC_TRIES factors over an octave that with the smallest error of the
-// entries that weigh most is taken: one a row, its target's or its teacher's largest,
-// of LC_SAMPLES rows spread over those worked on. Error of the gradients over that of a
+// entries that weigh most is taken: one a row, its target's (where G has it) or its
+// teacher's largest, of LC_SAMPLES rows spread over those worked on. Error of the gradients over that of a
 // correctly rounded result, over 130 drawn batches of 50 to 4000 rows: 1.01 to 1.42.
 // (Distillation's grad_hidden over forty: without the choice 1.09 to 1.51, the worst
 // factor 1.36 to 2.2, chosen by all entries of the first 1024 / K rows 1.06 to 1.69, so of
@@ -916,6 +916,17 @@ __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, in
   }
 }
 
+// The targets' entries of G, g c (1 - q), are the largest by far, and their rounding to
+// bf16 would be most of the gradients' error (1.2 to 1.4 times that of a correctly rounded
+// result; in a frequent token's row of grad_W, a sum of rows of either sign, up to half of
+// grad_W's root mean square). They are kept apart: 0 stands there in G, and
+// loss_out_kernel adds them in fp32, which leaves 1.00 times, and 2^-7 of an element or of
+// the root mean square. (4096 rows on the decode head: 20 to 40 us of 4600 and 6400.) Not for
+// fp16, whose G has three bits more: grad_W's row of a token is rounded before they are
+// added to it, and among fp16's least numbers that shows.
+template <int ET>
+constexpr bool targets_apart = ET == ET_BF16;
+
 constexpr int LC_THREADS = 256;
 constexpr int64_t LC_ONE = 32768;
 constexpr float LC_STEP = 0.95760328f;  // 2^(-1 / 16)
@@ -958,7 +969,8 @@ __device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
   // The samples, unscaled entries of G: their loads go out before the rows'.
   constexpr int S = LC_SAMPLES / LC_THREADS;
   float entry[S];
-  const int samples = (int)(p.M < LC_SAMPLES ? p.M : LC_SAMPLES);
+  const bool apart = targets_apart<ET> && !p.distill;  // then G has no entry that weighs so much
+  const int samples = apart ? 0 : (int)(p.M < LC_SAMPLES ? p.M : LC_SAMPLES);
   float o[S];
   int32_t o_up[S];
 #pragma unroll
@@ -1000,6 +1012,7 @@ __device__ __forceinline__ float find_scale(const LossCoef &p, int &exponent) {
   if (mx > 1e-30f && mx < 1e30f) {
     exponent = ET == ET_F16 ? F16_TOP : 0;
     f = __fdiv_rn(p.top, mx);
+    if (apart) return f;
     __shared__ float err[LC_TRIES][LC_THREADS + 1];
     float e2[LC_TRIES] = {};
     auto sample = [&](float g) {  // an entry of G, unscaled
@@ -1084,7 +1097,7 @@ __global__ __launch_bounds__(MM_THREADS, 1) void loss_grad_kernel(XentBwdArgs p,
   MM_SHARED();
   MM_EPI_SHARED();
   dev.apply(p);
-  const XentGrad<ET, DB> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
+  const XentGrad<ET, DB, targets_apart<ET>> prob{p, mm_epi, (p.M + MM_T - 1) / MM_T, p.np / MM_T};
   mm_run<ET, false, false>(prob, mm_buf);
 }
 
@@ -1164,7 +1177,13 @@ __global__ __launch_bounds__(256) void loss_kept_kernel(XentBwdArgs p, OnDevice 
         if (y >= 0 && y < 8)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (y == q) g8[q] = __fsub_rn(g8[q], r.b);
+            if (y == q) {
+              g8[q] = __fsub_rn(g8[q], r.b);
+              if constexpr (targets_apart<ET>) {  // in the sums only
+                if constexpr (DB) sum[q] = __fadd_rn(sum[q], g8[q]);
+                g8[q] = 0.0f;
+              }
+            }
         if constexpr (DB)
 #pragma unroll
           for (int q = 0; q < 8; ++q) sum[q] = __fadd_rn(sum[q], g8[q]);
@@ -1301,9 +1320,9 @@ __global__ __launch_bounds__(64 * XO_WAVES, 3) void loss_outer_kernel(XentBwdArg
   xent_outer<ET>(p, per_slab, xo_g0, xo_g1, xo_stage);
 }
 
-// grad_hidden: the splits' sums in ascending order, scaled, rounded once; 0 in
-// the rows left out.
-struct DHiddenOut {
+// What the products leave to do: grad_hidden from its sums, and the targets' entries of G
+// (targets_apart).
+struct LossOut {
   const float *dh;  // [splits][n, H]
   int64_t M, H;
   const int32_t *count, *inv;
@@ -1311,12 +1330,128 @@ struct DHiddenOut {
   int splits;       // not packed
   float alpha;
   const float *scale;
-  uint16_t *out;
+  uint16_t *out;          // grad_hidden or nullptr
+  // targets kept apart (else W is nullptr)
+  const uint16_t *W, *hidden;  // hidden: State's
+  const int32_t *y, *up;
+  const float *own, *g;
+  uint16_t *dw;           // grad_W
+  int64_t tokens;         // work-groups of its rows, the first ones: the longest come early
+  int64_t first;          // ... for rows first .. first + OUT_ROWS - 1 of the work
+  __device__ __forceinline__ float entry(int64_t m) const {
+    const float o = own[m];
+    return o == 0.0f ? 0.0f : __fmul_rn(o, g[up[m]]);
+  }
 };
 template <int ET>
-__global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
-  const int64_t e = (group_number() * 256 + threadIdx.x) * 8;
-  if (e >= c.M * c.H) return;
+__device__ __forceinline__ void unpack8(const u32x4 &v, float (&x)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t word = v[q / 2];
+    if constexpr (ET == ET_F16)
+      x[q] = (float)__builtin_bit_cast(_Float16, (uint16_t)(q & 1 ? word >> 16 : word));
+    else
+      x[q] = __builtin_bit_cast(float, q & 1 ? word & 0xFFFF0000u : word << 16);
+  }
+}
+template <int ET>
+__device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
+  return u32x4{mm_pack2<ET>(x[0], x[1]), mm_pack2<ET>(x[2], x[3]), mm_pack2<ET>(x[4], x[5]), mm_pack2<ET>(x[6], x[7])};
+}
+
+// grad_W's row of a token: what the product left there (rounded), and the entries of the
+// rows whose target it is. A work-group a row and slab of columns, of which that of the
+// token's first row does it, in the rows' order; it finds them by looking at all targets
+// (OUT_ROWS at most: more rows take a launch each, and grad_W's rows another rounding).
+constexpr int OUT_SLAB = 2048, OUT_LIST = 256;
+constexpr int64_t OUT_ROWS = 65536;
+template <int ET>
+__device__ __forceinline__ void out_token(const LossOut &c, int64_t group) {
+  __shared__ int32_t rows[OUT_LIST];
+  __shared__ float entries[OUT_LIST];
+  __shared__ int sh[4];
+  const int64_t slabs = (c.H + OUT_SLAB - 1) / OUT_SLAB, n = c.count != nullptr ? *c.count : c.M;
+  const int64_t end = c.first + OUT_ROWS < n ? c.first + OUT_ROWS : n, m = c.first + group / slabs;
+  if (m >= end) return;
+  const int32_t token = c.y[m];
+  if (token < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int64_t m0 = c.first; m0 < m; m0 += 1024) {
+    bool before = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t r = m0 + k * 256 + tid;
+      before |= c.y[r < m ? r : m] == token && r < m;
+    }
+    if (__syncthreads_or(before)) return;
+  }
+  const int64_t col = group % slabs * OUT_SLAB + tid * 8;
+  float sum[8] = {};
+  int listed = 0;  // of the list
+  auto add = [&](auto nc, int e0) {  // that many rows' loads in flight
+    constexpr int N = decltype(nc)::value;
+    u32x4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = *reinterpret_cast<const u32x4 *>(c.hidden + rows[e0 + k] * c.H + col);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float h[8];
+      unpack8<ET>(v[k], h);
+      const float x = entries[e0 + k];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] = __fmaf_rn(x, h[q], sum[q]);
+    }
+  };
+  auto flush = [&]() {
+    __syncthreads();
+    if (col < c.H) {
+      int e0 = 0;
+      for (; e0 + 16 <= listed; e0 += 16) add(std::integral_constant<int, 16>{}, e0);
+      for (; e0 + 4 <= listed; e0 += 4) add(std::integral_constant<int, 4>{}, e0);
+      for (; e0 < listed; ++e0) add(std::integral_constant<int, 1>{}, e0);
+    }
+    __syncthreads();
+    listed = 0;
+  };
+  for (int64_t m0 = m; m0 < end; m0 += 256) {
+    const int64_t r = m0 + tid;
+    const bool mine = r < end && c.y[r < end ? r : m] == token;
+    const uint64_t set = __ballot(mine);
+    if (!__syncthreads_or(mine)) continue;
+    if (lane == 0) sh[wave] = __popcll(set);
+    __syncthreads();
+    const int found = sh[0] + sh[1] + sh[2] + sh[3];
+    if (listed + found > OUT_LIST) flush();
+    int at = listed + __popcll(set & ((1ull << lane) - 1));
+    for (int w = 0; w < wave; ++w) at += sh[w];
+    if (mine) {
+      rows[at] = (int32_t)r;
+      entries[at] = c.entry(r);
+    }
+    listed += found;
+    __syncthreads();
+  }
+  flush();
+  if (col >= c.H) return;
+  u32x4 *const to = reinterpret_cast<u32x4 *>(c.dw + (int64_t)token * c.H + col);
+  float x[8];
+  unpack8<ET>(*to, x);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(c.alpha, sum[q], x[q]);
+  *to = pack8<ET>(x);
+}
+
+// grad_hidden: the splits' sums in ascending order, scaled, with the target's entry,
+// rounded once; 0 in the rows left out.
+template <int ET>
+__global__ __launch_bounds__(256) void loss_out_kernel(LossOut c) {
+  const int64_t group = group_number();
+  if (targets_apart<ET> && group < c.tokens) {
+    out_token<ET>(c, group);
+    return;
+  }
+  const int64_t e = ((group - c.tokens) * 256 + threadIdx.x) * 8;
+  if (c.out == nullptr || e >= c.M * c.H) return;
   const int64_t row = e / c.H, m = c.inv != nullptr ? c.inv[row] : row;
   if (m < 0) {
     *reinterpret_cast<u32x4 *>(c.out + e) = u32x4{0, 0, 0, 0};
@@ -1346,12 +1481,18 @@ __global__ __launch_bounds__(256) void loss_dhidden_out_kernel(DHiddenOut c) {
   for (; k0 + 2 <= splits; k0 += 2) more(std::integral_constant<int, 2>{}, k0);
   if (k0 < splits) more(std::integral_constant<int, 1>{}, k0);
   const float f = __fmul_rn(c.alpha, c.scale[1]);
+  float x[8];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int q = 0; q < 8; ++q) x[q] = __fmul_rn(f, s[q / 4][q % 4]);
+  const int32_t token = targets_apart<ET> && c.W != nullptr ? c.y[m] : -1;
+  if (token >= 0) {
+    float w[8];
+    unpack8<ET>(*reinterpret_cast<const u32x4 *>(c.W + token * c.H + (e - row * c.H)), w);
+    const float entry = __fmul_rn(c.alpha, c.entry(m));
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s[h][q] = __fmul_rn(f, s[h][q]);
-  *reinterpret_cast<u32x4 *>(c.out + e) = u32x4{mm_pack2<ET>(s[0][0], s[0][1]), mm_pack2<ET>(s[0][2], s[0][3]),
-                                                mm_pack2<ET>(s[1][0], s[1][1]), mm_pack2<ET>(s[1][2], s[1][3])};
+    for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(entry, w[q], x[q]);
+  }
+  *reinterpret_cast<u32x4 *>(c.out + e) = pack8<ET>(x);
 }
 
 // Pieces of up to an eighth more columns, where G^T hidden then takes fewer
@@ -1571,9 +1712,18 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
       }
     }
   }
-  if (e == hipSuccess && c.grad_hidden != nullptr)
-    e = launch_kernel(loss_dhidden_out_kernel<ET>, numbered_grid(ceil_div(h.M * h.H, 2048)), dim3(256), s,
-                      DHiddenOut{p.dh, h.M, h.H, st.count, st.inv, plan, lay.splits, p.alpha, scale, static_cast<uint16_t *>(c.grad_hidden)});
+  const bool apart = targets_apart<ET> && c.K == 0;
+  LossOut out{p.dh, h.M, h.H, st.count, st.inv, plan, lay.splits, p.alpha, scale, static_cast<uint16_t *>(c.grad_hidden),
+              apart ? static_cast<const uint16_t *>(h.W) : nullptr, st.hidden, st.y, st.up, st.own, c.grad_loss,
+              static_cast<uint16_t *>(c.grad_W), 0, 0};
+  const int64_t slabs = apart && c.grad_W != nullptr ? ceil_div(h.H, OUT_SLAB) : 0;
+  for (int64_t m0 = 0; m0 < h.M && e == hipSuccess; m0 += OUT_ROWS) {
+    out.first = m0;
+    out.tokens = (h.M - m0 < OUT_ROWS ? h.M - m0 : OUT_ROWS) * slabs;
+    const int64_t groups = out.tokens + (out.out != nullptr ? ceil_div(h.M * h.H, 2048) : 0);
+    if (groups > 0) e = launch_kernel(loss_out_kernel<ET>, numbered_grid(groups), dim3(256), s, out);
+    out.out = nullptr;
+  }
   return e;
 }
 

@@ -117,8 +117,9 @@ struct XentBwdArgs {
   uint16_t *dw;        // [V, H]
 };
 
-// G of one piece; DB: and its column sums.
-template <int ET, bool DB>
+// G of one piece; DB: and its column sums. APART: 0 in the place of a row's target, whose
+// entry is in the column sums only.
+template <int ET, bool DB, bool APART = false>
 struct XentGrad {
   XentBwdArgs p;
   u32x4 *epi;
@@ -172,7 +173,13 @@ struct XentGrad {
               for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                  if (r.y == MmTile<ET>::col(at.wn, at.lg, y, j) + q) g[j][q] = __fsub_rn(g[j][q], r.b);
+                  if (r.y == MmTile<ET>::col(at.wn, at.lg, y, j) + q) {
+                    g[j][q] = __fsub_rn(g[j][q], r.b);
+                    if constexpr (APART) {
+                      if constexpr (DB) colsum[j][q] = __fadd_rn(colsum[j][q], g[j][q]);
+                      g[j][q] = 0.0f;
+                    }
+                  }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               if constexpr (DB)

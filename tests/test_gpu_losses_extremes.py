@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import lm_head_logits_amd as L
+import loss_formulas as F
 from gpu_util import DEV, say
 from test_gpu_losses import DT, KW, OPS, call, check, make, reference
 
@@ -191,3 +192,47 @@ def test_the_scale_suits_the_entries_that_weigh_most(p, M, dt):
     half = 2.0 ** math.floor(math.log2(abs(want))) * torch.finfo(DT[dt]).eps / 2
     bound = rounding * float(g[0]) + half * (1 + 1e-3)  # and what fp32 adds
     assert float((got - want).abs().max()) <= bound, (float((got - want).abs().max()) / half, bound / half)
+
+
+@pytest.mark.parametrize("M,H,V,tokens", [(1, 32, 40, 1), (40, 64, 300, 1), (64, 2080, 300, 2), (200, 64, 500, 1), (256, 4096, 333, 3),
+                                          (300, 64, 500, 1), (700, 2080, 500, 5), (3000, 96, 700, 2), (70000, 32, 300, 3)])
+def test_rows_of_frequent_tokens(M, H, V, tokens):
+    """grad_W's row of a token that is the target of many rows, of either sign: elements in
+    which they cancel are as exact as the others. With no ratio and no KL term the entry of
+    a row is -g A (1 - q). Bound: q is off by what log q is (loss_formulas), 1 - q and the
+    entry by 4 u, a chain of M additions; the token's other logits' share, G rounded to
+    half a step, summed and rounded; the result's own rounding, and one more each 65536 rows.
+    (bf16: fp16's G has three bits more, and the target's entry in it.)"""
+    dt = "bf16"
+    c = make("policy", 11, M, H, V, dt, False, mask=0.1 if M > 1 else 0.0)
+    y = c["target"]
+    y[y >= 0] = y[y >= 0] % tokens  # the first ones
+    kw = dict(KW["policy"], kl_coef=0.0)
+    c.update(old=None, ref=None)
+    loss, logp, saved = call(c, 0.5, kw)
+    say("frequent tokens", M, H, V, tokens, dt)
+    for keep in (True, False):
+        *_, saved = call(c, 0.5, kw, keep_logits=keep)
+        dh, dw, _ = L.loss_backward(c["grad"], c["weight"], saved)
+        head = F.Head(c["hidden"], c["weight"], None, 0.5, 1.0)
+        kept = y >= 0
+        at = torch.where(kept, y, torch.zeros_like(y)).long()[:, None]
+        a = torch.where(kept, c["grad"].double() * c["advantage"].double(), torch.zeros(M, dtype=torch.float64, device=DEV))
+        G = a[:, None] * head.q
+        G.scatter_add_(1, at, -a[:, None])
+        own = torch.zeros_like(G).scatter_(1, at, G.gather(1, at))
+        rest, h = G - own, c["hidden"].double()
+        u, step = F.U, torch.finfo(DT[dt]).eps / 2
+        q = head.q.gather(1, at)[:, 0]
+        err = a.abs() * (q * 2 * head.dlogq.gather(1, at)[:, 0] + 8 * u)  # of the entry
+        spread = torch.zeros_like(G).scatter_(1, at, err[:, None] + (M + 8) * u * own.gather(1, at).abs())
+        want = 0.5 * (G.t() @ h)
+        main = 0.5 * (rest.t() @ h)
+        d = rest.abs() * step + a.abs()[:, None] * head.dq
+        tol = 0.5 * (spread.t() @ h.abs() + d.t() @ h.abs() + 2e-5 * (rest.abs().t() @ h.abs()))
+        windows = -(-M // 65536)
+        tol = tol * (1 + 2 * step) + step * main.abs() + windows * (step * want.abs() + 2.0 ** -126)
+        if windows > 1:  # the sum so far is rounded, which may be larger than the last
+            tol = tol + step * 0.5 * (G.abs().t() @ h.abs())
+        bad = (dw.double() - want)[:tokens].abs() - tol[:tokens]
+        assert float(bad.max()) <= 0, (keep, float(((dw.double() - want)[:tokens].abs() / tol[:tokens]).max()))
