@@ -873,8 +873,9 @@ __global__ __launch_bounds__(PP_THREADS) void preference_pairs_kernel(Pairs c) {
 // Which f: a row's gradients hang on a few entries of G and on how those happen to
 // round. Of LC_TRIES factors over an octave that with the smallest error of the
 // entries that weigh most is taken: one a row, its target's (where G has it) or its
-// teacher's largest, of LC_SAMPLES rows spread over those worked on. Error of the gradients over that of a
-// correctly rounded result, over 130 drawn batches of 50 to 4000 rows: 1.01 to 1.42.
+// teacher's largest, of LC_SAMPLES rows spread over those worked on. Error of the
+// gradients over that of a correctly rounded result, over 130 drawn batches of 50 to
+// 4000 rows: 1.01 to 1.42.
 // (Distillation's grad_hidden over forty: without the choice 1.09 to 1.51, the worst
 // factor 1.36 to 2.2, chosen by all entries of the first 1024 / K rows 1.06 to 1.69, so of
 // few rows worse than none, by the largest of each row 1.05 to 1.38, the best factor
@@ -922,13 +923,13 @@ __device__ __forceinline__ void plan_splits(int32_t n, int32_t H, int32_t vp, in
 // result; in a frequent token's row of grad_W, a sum of rows of either sign, up to half of
 // grad_W's root mean square). They are kept apart: 0 stands there in G, and
 // loss_out_kernel adds them in fp32, which leaves 1.00 times, and 2^-7 of an element or of
-// the root mean square. (4096 rows on the decode head, 2367 of them worked on: 30 us of
-// 6300; 126 rows on a small head: 0.7 us less, since no scale is chosen.) Not for fp16,
-// whose G has three bits more: grad_W's row of a token is rounded before they are
-// added to it, and among fp16's least numbers that shows. Nor for a teacher's largest
-// entries (error 1.00 to 1.09 times, for 0.6% more time of a large step): they are less of
-// their token's row, and that row's two roundings then pass, once in a million elements,
-// what one and G's would be.
+// the root mean square. (A step of 4096 rows on the decode head, 2367 of them worked on:
+// 6265 us against 6240; 126 rows on a small head 50.9 against 51.1, since no scale is
+// chosen.) Not for fp16, whose G has three bits more: grad_W's row of a token is rounded
+// before they are added to it, and among fp16's least numbers that shows. Nor for a
+// teacher's largest entries (error 1.00 to 1.09 times, for 0.6% more time of a large step):
+// they are less of their token's row, and that row's two roundings then pass, once in a
+// million elements, what one and G's would be.
 template <int ET>
 constexpr bool targets_apart = ET == ET_BF16;
 
@@ -1325,6 +1326,14 @@ __global__ __launch_bounds__(64 * XO_WAVES, 3) void loss_outer_kernel(XentBwdArg
   xent_outer<ET>(p, per_slab, xo_g0, xo_g1, xo_stage);
 }
 
+// The rows of each target, where there are more than OUT_CHUNK rows. notes and used from zeros.
+struct TokenLists {
+  int2 *notes;      // [V] {M - a token's first row, its rows}
+  int4 *used;       // {tokens of up to OUT_SHORT rows, places of order, other tokens}
+  int32_t *tokens;  // [M] the tokens, the others from the end on, ...
+  int2 *lists;      // [M] ... and {place in order, rows}
+  int32_t *order;   // [n] the rows, token by token
+};
 // What the products leave to do: grad_hidden from its sums, and the targets' entries of G
 // (targets_apart).
 struct LossOut {
@@ -1341,8 +1350,8 @@ struct LossOut {
   const int32_t *y, *up;
   const float *own, *g;
   uint16_t *dw;           // grad_W
-  int64_t tokens;         // work-groups of its rows, the first ones: the longest come early
-  int64_t first;          // ... for rows first .. first + OUT_ROWS - 1 of the work
+  int64_t tokens;         // work-groups of its rows, the first ones
+  TokenLists lists;       // more than OUT_CHUNK rows
   __device__ __forceinline__ float entry(int64_t m) const {
     const float o = own[m];
     return o == 0.0f ? 0.0f : __fmul_rn(o, g[up[m]]);
@@ -1365,94 +1374,239 @@ __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
 }
 
 // grad_W's row of a token: what the product left there (rounded), and the entries of the
-// rows whose target it is. A work-group a row and slab of columns, of which that of the
-// token's first row does it, in the rows' order; it finds them by looking at all targets
-// (OUT_ROWS at most: more rows take a launch each, and grad_W's rows another rounding).
-constexpr int OUT_SLAB = 2048, OUT_LIST = 256;
-constexpr int64_t OUT_ROWS = 65536;
-template <int ET>
-__device__ __forceinline__ void out_token(const LossOut &c, int64_t group) {
-  __shared__ int32_t rows[OUT_LIST];
-  __shared__ float entries[OUT_LIST];
+// rows whose target it is, in those rows' order. With up to OUT_CHUNK rows there is a
+// work-group a row and slab of columns, which looks at all targets and ends at once where the
+// row is not the token's first. With more, three kernels before make lists (of each token's
+// first row and number of rows, of the lists' places, of the rows), and the work-groups take
+// token after token. With short rows several threads have the same columns: they take a row each.
+// (Backward pass with and without, H = 4096, targets distributed as 1 / rank: 4096 rows,
+// V = 128256, 6633 against 6595 us, all of one target 7078 against 6595; 16384 rows 27.19
+// ms against 27.00; 65536 rows, V = 32000, 28.24 against 27.54, of which the lists 0.3.)
+constexpr int OUT_CHUNK = 4096, OUT_BATCH = 1024, OUT_SLAB_FEW = 2048, OUT_SLAB_MANY = 512, OUT_SHORT = 16;
+// The rows of base .. base + OUT_CHUNK - 1 before n whose target is the token, in order, to
+// LDS as numbers from base on, by 256 threads; how many, or -1 where one lies before `first`.
+__device__ __forceinline__ int find_rows(const int32_t *y, int64_t base, int64_t n, int32_t token, int64_t first,
+                                         uint16_t (&found)[OUT_CHUNK], int (&sh)[4]) {
+  static_assert(OUT_CHUNK == 256 * 16);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t r = base + threadIdx.x * 16;
+  uint32_t mask = 0;
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+    if (r + 4 * h < n) {  // (y's room is whole 256 bytes)
+      const int4 v = *reinterpret_cast<const int4 *>(y + r + 4 * h);
+      mask |= ((v.x == token ? 1u : 0u) | (v.y == token ? 2u : 0u) | (v.z == token ? 4u : 0u) | (v.w == token ? 8u : 0u)) << (4 * h);
+    }
+  if (r + 16 > n) mask &= r < n ? (1u << (n - r)) - 1 : 0u;
+  if (__syncthreads_or(mask != 0 && r + __builtin_ctz(mask | 0x10000u) < first)) return -1;
+  const int mine = __popc(mask);
+  int at = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int other = __shfl_up(at, d);
+    at += lane >= d ? other : 0;
+  }
+  if (lane == 63) sh[wave] = at;
+  __syncthreads();
+  at -= mine;
+  for (int w = 0; w < wave; ++w) at += sh[w];
+  for (; mask != 0; mask &= mask - 1) found[at++] = (uint16_t)(threadIdx.x * 16 + __builtin_ctz(mask));
+  const int all = sh[0] + sh[1] + sh[2] + sh[3];
+  __syncthreads();
+  return all;
+}
+
+struct TokenRowsOf {
+  const int32_t *y, *count;
+  int64_t M;
+  TokenLists to;
+};
+__global__ __launch_bounds__(256) void loss_tokens_kernel(TokenRowsOf c) {
+  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int32_t token = m < *c.count ? c.y[m] : -1;
+  // a frequent token's additions follow each other: one for all of a wave's
+  for (uint64_t todo = __ballot(token >= 0); todo != 0;) {
+    const int lane = __builtin_ctzll(todo);
+    const int32_t one = __builtin_amdgcn_readlane(token, lane);
+    const uint64_t same = __ballot(token == one);
+    if ((int)(threadIdx.x & 63) == lane) {
+      atomicMax(&c.to.notes[one].x, (int32_t)(c.M - m));
+      atomicAdd(&c.to.notes[one].y, __popcll(same));
+    }
+    todo &= ~same;
+  }
+}
+// The tokens' lists and their places, which are chance (what is in a list is not), a wave 64
+// rows: one addition to `used` each, one a token would take 0.3 ms for 20000 tokens.
+__global__ __launch_bounds__(256) void loss_places_kernel(TokenRowsOf c) {
+  const int64_t m = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int32_t token = m < *c.count ? c.y[m] : -1;
+  int2 note = token >= 0 ? c.to.notes[token] : int2{0, 0};
+  if (note.x != (int32_t)(c.M - m)) note.y = 0;  // not the first
+  int place = note.y;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int other = __shfl_up(place, d);
+    place += lane >= d ? other : 0;
+  }
+  const uint64_t few = __ballot(note.y > 0 && note.y <= OUT_SHORT), many = __ballot(note.y > OUT_SHORT), below = (1ull << lane) - 1;
+  const int all = __shfl(place, 63);
+  unsigned long long at = 0;
+  int back = 0;
+  if (lane == 0 && all > 0) {
+    at = atomicAdd(reinterpret_cast<unsigned long long *>(&c.to.used->x), (unsigned long long)all << 32 | __popcll(few));
+    if (many != 0) back = atomicAdd(&c.to.used->z, __popcll(many));
+  }
+  const int first = __shfl((int)(uint32_t)at, 0), base = __shfl((int)(at >> 32), 0);
+  back = __shfl(back, 0);
+  if (note.y == 0) return;
+  place += base - note.y;
+  const int64_t i = note.y <= OUT_SHORT ? first + __popcll(few & below) : c.M - 1 - back - __popcll(many & below);
+  c.to.tokens[i] = token;
+  c.to.lists[i] = int2{place, note.y};
+  if (note.y == 1) c.to.order[place] = (int32_t)m;
+}
+// ... and the rows of those with more than one, the longest first.
+__global__ __launch_bounds__(256) void loss_lists_kernel(TokenRowsOf c) {
+  __shared__ uint16_t found[OUT_CHUNK];
   __shared__ int sh[4];
-  const int64_t slabs = (c.H + OUT_SLAB - 1) / OUT_SLAB, n = c.count != nullptr ? *c.count : c.M;
-  const int64_t end = c.first + OUT_ROWS < n ? c.first + OUT_ROWS : n, m = c.first + group / slabs;
-  if (m >= end) return;
-  const int32_t token = c.y[m];
-  if (token < 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int64_t m0 = c.first; m0 < m; m0 += 1024) {
-    bool before = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t r = m0 + k * 256 + tid;
-      before |= c.y[r < m ? r : m] == token && r < m;
+  const int64_t n = *c.count;
+  const int4 used = *c.to.used;
+  for (int64_t i = blockIdx.x; i < used.x + used.z; i += gridDim.x) {
+    const int64_t t = i < used.z ? c.M - 1 - i : i - used.z;
+    const int2 list = c.to.lists[t];
+    if (list.y == 1) continue;
+    const int32_t token = c.to.tokens[t];
+    int done = 0;
+    for (int64_t base = (c.M - c.to.notes[token].x) / OUT_CHUNK * OUT_CHUNK; done < list.y && base < n; base += OUT_CHUNK) {
+      const int more = find_rows(c.y, base, n, token, 0, found, sh);
+      for (int k = threadIdx.x; k < more; k += 256) c.to.order[list.x + done + k] = (int32_t)(base + found[k]);
+      done += more;
+      __syncthreads();
     }
-    if (__syncthreads_or(before)) return;
   }
-  const int64_t col = group % slabs * OUT_SLAB + tid * 8;
-  float sum[8] = {};
-  int listed = 0;  // of the list
-  auto add = [&](auto nc, int e0) {  // that many rows' loads in flight
-    constexpr int N = decltype(nc)::value;
-    u32x4 v[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = *reinterpret_cast<const u32x4 *>(c.hidden + rows[e0 + k] * c.H + col);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      float h[8];
-      unpack8<ET>(v[k], h);
-      const float x = entries[e0 + k];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) sum[q] = __fmaf_rn(x, h[q], sum[q]);
-    }
-  };
-  auto flush = [&]() {
-    __syncthreads();
-    if (col < c.H) {
-      int e0 = 0;
-      for (; e0 + 16 <= listed; e0 += 16) add(std::integral_constant<int, 16>{}, e0);
-      for (; e0 + 4 <= listed; e0 += 4) add(std::integral_constant<int, 4>{}, e0);
-      for (; e0 < listed; ++e0) add(std::integral_constant<int, 1>{}, e0);
-    }
-    __syncthreads();
-    listed = 0;
-  };
-  for (int64_t m0 = m; m0 < end; m0 += 256) {
-    const int64_t r = m0 + tid;
-    const bool mine = r < end && c.y[r < end ? r : m] == token;
-    const uint64_t set = __ballot(mine);
-    if (!__syncthreads_or(mine)) continue;
-    if (lane == 0) sh[wave] = __popcll(set);
-    __syncthreads();
-    const int found = sh[0] + sh[1] + sh[2] + sh[3];
-    if (listed + found > OUT_LIST) flush();
-    int at = listed + __popcll(set & ((1ull << lane) - 1));
-    for (int w = 0; w < wave; ++w) at += sh[w];
-    if (mine) {
-      rows[at] = (int32_t)r;
-      entries[at] = c.entry(r);
-    }
-    listed += found;
-    __syncthreads();
-  }
-  flush();
-  if (col >= c.H) return;
-  u32x4 *const to = reinterpret_cast<u32x4 *>(c.dw + (int64_t)token * c.H + col);
+}
+
+struct TokenShared {
+  int32_t rows[OUT_BATCH];
+  float entries[OUT_BATCH];
+  float sums[256][8];
+};
+template <int ET>
+__device__ __forceinline__ void put_token(const LossOut &c, u32x4 *to, const u32x4 &main, const float (&sum)[8]) {
   float x[8];
-  unpack8<ET>(*to, x);
+  unpack8<ET>(main, x);
 #pragma unroll
   for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(c.alpha, sum[q], x[q]);
   *to = pack8<ET>(x);
 }
+// row_at(i): the token's rows
+template <int ET, int SLAB, typename F>
+__device__ __forceinline__ void add_token(const LossOut &c, TokenShared &sh, int32_t token, int64_t slab, int count, F &&row_at) {
+  const int tid = threadIdx.x;
+  const int per = c.H < SLAB ? (int)c.H / 8 : SLAB / 8;  // threads a row
+  const int parts = 256 / per, part = tid / per;
+  const int64_t col = slab * SLAB + tid % per * 8;
+  const bool works = part < parts && col < c.H;
+  float sum[8] = {};
+  auto add = [&](auto nc, int e0) {  // that many rows' loads in flight
+    constexpr int N = decltype(nc)::value;
+    u32x4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = *reinterpret_cast<const u32x4 *>(c.hidden + sh.rows[e0 + k * parts] * c.H + col);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float h[8];
+      unpack8<ET>(v[k], h);
+      const float x = sh.entries[e0 + k * parts];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum[q] = __fmaf_rn(x, h[q], sum[q]);
+    }
+  };
+  for (int b = 0; b < count; b += OUT_BATCH) {
+    const int listed = count - b < OUT_BATCH ? count - b : OUT_BATCH;
+    for (int i = tid; i < listed; i += 256) {
+      const int32_t r = row_at(b + i);
+      sh.rows[i] = r;
+      sh.entries[i] = c.entry(r);
+    }
+    __syncthreads();
+    if (works) {
+      int e0 = part;
+      for (; e0 + 7 * parts < listed; e0 += 8 * parts) add(std::integral_constant<int, 8>{}, e0);
+      for (; e0 + parts < listed; e0 += 2 * parts) add(std::integral_constant<int, 2>{}, e0);
+      if (e0 < listed) add(std::integral_constant<int, 1>{}, e0);
+    }
+    __syncthreads();
+  }
+  if (parts > 1) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sh.sums[tid][q] = sum[q];
+    __syncthreads();
+  }
+  if (part != 0 || !works) return;
+  for (int k = 1; k < parts; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q] = __fadd_rn(sum[q], sh.sums[k * per + tid][q]);
+  u32x4 *const to = reinterpret_cast<u32x4 *>(c.dw + token * c.H + col);
+  put_token<ET>(c, to, *to, sum);
+}
+template <int ET, bool MANY>
+__device__ __forceinline__ void out_tokens(const LossOut &c, int64_t group) {
+  __shared__ TokenShared sh;
+  if constexpr (MANY) {
+    const int64_t slabs = (c.H + OUT_SLAB_MANY - 1) / OUT_SLAB_MANY;
+    const int4 used = *c.lists.used;
+    for (int64_t i = group; i < used.z * slabs; i += c.tokens) {
+      const int64_t t = c.M - 1 - i / slabs;
+      const int2 list = c.lists.lists[t];
+      const int32_t *const order = c.lists.order + list.x;
+      add_token<ET, OUT_SLAB_MANY>(c, sh, c.lists.tokens[t], i % slabs, list.y, [&](int k) { return order[k]; });
+    }
+    // most tokens have a row or two: a wave each
+    for (int64_t i = group * 4 + threadIdx.x / 64; i < used.x * slabs; i += 4 * c.tokens) {
+      const int64_t t = i / slabs, col = (i - t * slabs) * OUT_SLAB_MANY + (threadIdx.x & 63) * 8;
+      if (col >= c.H) continue;
+      const int2 list = c.lists.lists[t];
+      u32x4 *const to = reinterpret_cast<u32x4 *>(c.dw + c.lists.tokens[t] * c.H + col);
+      const u32x4 main = *to;
+      float sum[8] = {};
+      for (int k = 0; k < list.y; k += 2) {
+        const int32_t r0 = c.lists.order[list.x + k], r1 = c.lists.order[list.x + (k + 1 < list.y ? k + 1 : k)];
+        const u32x4 v0 = *reinterpret_cast<const u32x4 *>(c.hidden + r0 * c.H + col);
+        const u32x4 v1 = *reinterpret_cast<const u32x4 *>(c.hidden + r1 * c.H + col);
+        const float e0 = c.entry(r0), e1 = k + 1 < list.y ? c.entry(r1) : 0.0f;
+        float h[8];
+        unpack8<ET>(v0, h);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] = __fmaf_rn(e0, h[q], sum[q]);
+        if (k + 1 == list.y) break;
+        unpack8<ET>(v1, h);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] = __fmaf_rn(e1, h[q], sum[q]);
+      }
+      put_token<ET>(c, to, main, sum);
+    }
+  } else {
+    __shared__ uint16_t found[OUT_CHUNK];
+    __shared__ int counts[4];
+    const int64_t slabs = (c.H + OUT_SLAB_FEW - 1) / OUT_SLAB_FEW, n = c.count != nullptr ? *c.count : c.M, m = group / slabs;
+    if (m >= n) return;
+    const int32_t token = c.y[m];
+    if (token < 0) return;
+    const int count = find_rows(c.y, 0, n, token, m, found, counts);
+    if (count > 0) add_token<ET, OUT_SLAB_FEW>(c, sh, token, group % slabs, count, [&](int k) { return (int32_t)found[k]; });
+  }
+}
 
 // grad_hidden: the splits' sums in ascending order, scaled, with the target's entry,
 // rounded once; 0 in the rows left out.
-template <int ET>
-__global__ __launch_bounds__(256) void loss_out_kernel(LossOut c) {
+template <int ET, bool MANY>
+__global__ __launch_bounds__(256, 5) void loss_out_kernel(LossOut c) {
   const int64_t group = group_number();
   if (targets_apart<ET> && group < c.tokens) {
-    out_token<ET>(c, group);
+    out_tokens<ET, MANY>(c, group);
     return;
   }
   const int64_t e = ((group - c.tokens) * 256 + threadIdx.x) * 8;
@@ -1534,7 +1688,7 @@ int64_t most_parts(int64_t nmt, int64_t nht, int64_t vp) {
 struct BackwardLayout {
   int64_t vp, cap;
   int splits;
-  int64_t scale, plan, rows, col, dh, G, entries, bytes;
+  int64_t scale, plan, rows, col, dh, G, entries, lists, bytes;
 };
 BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool keep, bool bias) {
   BackwardLayout b;
@@ -1563,6 +1717,7 @@ BackwardLayout backward_layout(int64_t M, int64_t H, int64_t V, int64_t K, bool 
   b.dh = take(4 * H * b.cap * (M > LR_DIRECT ? MM_T : M));  // not packed: one row tile
   b.G = take(2 * M * b.vp);
   b.entries = take(bias && K ? 8 * V : 0);
+  b.lists = take(K == 0 && M > OUT_CHUNK ? 16 + 8 * (V + M) + 8 * M : 0);
   b.bytes = at;
   return b;
 }
@@ -1720,15 +1875,26 @@ hipError_t backward(const LossBackward &c, hipStream_t s) {
   const bool apart = targets_apart<ET> && c.K == 0;
   LossOut out{p.dh, h.M, h.H, st.count, st.inv, plan, lay.splits, p.alpha, scale, static_cast<uint16_t *>(c.grad_hidden),
               apart ? static_cast<const uint16_t *>(h.W) : nullptr, st.hidden, st.y, st.up, st.own, c.grad_loss,
-              static_cast<uint16_t *>(c.grad_W), 0, 0};
-  const int64_t slabs = apart && c.grad_W != nullptr ? ceil_div(h.H, OUT_SLAB) : 0;
-  for (int64_t m0 = 0; m0 < h.M && e == hipSuccess; m0 += OUT_ROWS) {
-    out.first = m0;
-    out.tokens = (h.M - m0 < OUT_ROWS ? h.M - m0 : OUT_ROWS) * slabs;
-    const int64_t groups = out.tokens + (out.out != nullptr ? ceil_div(h.M * h.H, 2048) : 0);
-    if (groups > 0) e = launch_kernel(loss_out_kernel<ET>, numbered_grid(groups), dim3(256), s, out);
-    out.out = nullptr;
+              static_cast<uint16_t *>(c.grad_W), 0, {}};
+  const bool many = apart && c.grad_W != nullptr && h.M > OUT_CHUNK;
+  if (many) {
+    uint8_t *const lists = ws + lay.lists;
+    int4 *const used = reinterpret_cast<int4 *>(lists);
+    int2 *const notes = reinterpret_cast<int2 *>(used + 1);
+    int32_t *const words = reinterpret_cast<int32_t *>(notes + h.V + h.M);
+    out.lists = TokenLists{notes, used, words, notes + h.V, words + h.M};
+    const TokenRowsOf of{st.y, st.count, h.M, out.lists};
+    if (e == hipSuccess) e = zero_words(lists, 4 + 2 * h.V, s);
+    if (e == hipSuccess) e = launch_kernel(loss_tokens_kernel, dim3((unsigned)ceil_div(h.M, 256)), dim3(256), s, of);
+    if (e == hipSuccess) e = launch_kernel(loss_places_kernel, dim3((unsigned)ceil_div(h.M, 256)), dim3(256), s, of);
+    if (e == hipSuccess) e = launch_kernel(loss_lists_kernel, dim3((unsigned)(8 * device_cus())), dim3(256), s, of);
+    out.tokens = 4 * (int64_t)device_cus();  // as many as there is room for
+  } else if (apart && c.grad_W != nullptr) {
+    out.tokens = h.M * ceil_div(h.H, OUT_SLAB_FEW);
   }
+  const int64_t groups = out.tokens + (out.out != nullptr ? ceil_div(h.M * h.H, 2048) : 0);
+  if (e == hipSuccess && groups > 0)
+    e = launch_kernel(many ? loss_out_kernel<ET, true> : loss_out_kernel<ET, false>, numbered_grid(groups), dim3(256), s, out);
   return e;
 }
 
