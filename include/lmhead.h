@@ -452,7 +452,9 @@ lmhead_status lmhead_preference_forward(const void *hidden, int64_t M, int64_t H
  *   grad_hidden, grad_W, grad_bias, workspace   as in lmhead_xent_backward, with
  *               lmhead_loss_backward_workspace_bytes(M, H, V, K, keep_logits, grad_bias != NULL)
  *               bytes
- * Rounded and scaled as there. */
+ * Rounded and scaled as there, but that in bf16 a target's entry of the logits' gradient, the
+ * row's largest by far, is not rounded: grad_hidden's row takes it in fp32, and grad_W's row
+ * of the token, rounded once, takes its tokens' entries in fp32 and is rounded again. */
 lmhead_status lmhead_loss_backward(const void *hidden, int64_t M, int64_t H, const void *W, int64_t V, float alpha,
                                    const float *bias, lmhead_dtype in_dtype, float temperature, int64_t K,
                                    const float *grad_loss, const void *state, size_t state_bytes, int keep_logits, void *grad_hidden,
